@@ -339,6 +339,87 @@ int muon_pack_plan(const int64_t* ms, const int64_t* ns, const int* owner, int64
 int muon_pack(void* const* mats, const int64_t* ms, const int64_t* ns, const int64_t* offsets,
               int64_t count, int dtype, void* packed, int to_packed, void* stream);
 
+/*
+ * Losses over the vocabulary, each with its gradient in the same call.  The
+ * pages have no counterpart: these are the objectives of post-training whose
+ * backward pass ends in the gradients muon_step and muon_adamw_step take.
+ *
+ * Shared by the three calls:
+ *   logits     rows x vocab logits on the device, row pitch ld >= vocab elements
+ *              (dtype MUON_F32, MUON_BF16 or MUON_F16; any alignment of the
+ *              element; rows whose pitch and base differ from `grad`'s by
+ *              multiples of 16 bytes take vector stores).  vocab in [1, 2^20].
+ *   grad       receives d(sum of loss)/d(logits), same type, row pitch ld_grad;
+ *              may be the logits themselves (ld_grad == ld), else the two must
+ *              not overlap.  Columns beyond vocab are neither read nor written.
+ *   weights    NULL or one fp32 weight per row (per pair in the preference
+ *              loss), a factor of loss and gradient: 1/N of a mean, a loss
+ *              scale, 0 for rows outside the loss.  A row of weight 0 is not
+ *              read (its logits may hold anything): loss and gradient are 0.
+ *   temperature T > 0: z = logits / T.
+ *   index dtypes MUON_I32 or MUON_I64.
+ * Arithmetic is fp32, the gradient rounded once; results do not depend on
+ * scheduling.  Logits of -inf are banned entries (probability 0, gradient 0); a
+ * row without a finite logit has no distribution and gives NaN.  rows == 0
+ * is valid.  Masked rows' outputs are written (zeros).
+ */
+typedef enum { MUON_I32 = 32, MUON_I64 = 64 } muon_index;
+
+/*
+ * Distillation from a teacher's top logits.  Row r of the teacher is k (1 to
+ * 1024) pairs (teacher_idx[r][j], teacher_logits[r][j]); indices outside
+ * [0, vocab) are padding, an index listed twice counts twice.  With q the
+ * student's softmax of z:
+ *   teacher_lse NULL: p = softmax over the k entries of teacher_logits / T,
+ *                     KL = sum_j p_j (log p_j - log q_j)
+ *   else              log p_j = teacher_logits_j / T - teacher_lse[r] (fp32, the
+ *                     log-sum-exp of the teacher's whole row at T), and what is
+ *                     left, p_r = max(0, 1 - sum p), is one more class against
+ *                     q_r, the student's probability outside the listed
+ *                     indices: KL += p_r (log p_r - log q_r).  The term is left
+ *                     out where q_r is 0 in fp32.
+ *   loss[r] = weight T^2 KL  (rows entries, fp32).
+ */
+int muon_distill_loss(const void* logits, int64_t ld, int64_t rows, int64_t vocab, int dtype,
+                      const void* teacher_idx, int idx_dtype, const void* teacher_logits,
+                      int teacher_dtype, int64_t k, const float* teacher_lse, const float* weights,
+                      float temperature, float* loss, void* grad, int64_t ld_grad, void* stream);
+
+/*
+ * Clipped policy loss with a KL term.  Row r's sampled token a = tokens[r] (a
+ * token outside [0, vocab) takes the row out of the loss, like weight 0):
+ *   l = z_a - logsumexp(z), ratio = exp(l - old_logp[r]) (old_logp NULL: 1, the
+ *   gradient still flows through l),
+ *   loss[r] = weight (-min(ratio A, clip(ratio, 1 - clip_low, 1 + clip_high) A)
+ *             + kl_coef (exp(ref_logp[r] - l) - (ref_logp[r] - l) - 1))
+ * with A = advantages[r]; a ratio beyond the clip on the side its advantage
+ * favours has no gradient.  ref_logp may be NULL when kl_coef is 0; clip_low
+ * in [0, 1], clip_high >= 0.  logp[r] receives l (0 for rows outside the loss).
+ */
+int muon_policy_loss(const void* logits, int64_t ld, int64_t rows, int64_t vocab, int dtype,
+                     const void* tokens, int token_dtype, const float* advantages, const float* old_logp,
+                     const float* ref_logp, const float* weights, float temperature, float clip_low,
+                     float clip_high, float kl_coef, float* loss, float* logp, void* grad, int64_t ld_grad,
+                     void* stream);
+
+/*
+ * Preference loss of paired sequences.  seq_bounds holds 2 pairs + 1
+ * non-decreasing row offsets (clamped to [0, rows]); rows
+ * [bounds[2i], bounds[2i+1]) are pair i's chosen sequence, the next range its
+ * rejected one.  tokens[r] is row r's label; labels outside [0, vocab) (prompt,
+ * padding) are left out, and rows outside every sequence too.
+ *   s = sum of the labels' log-probabilities (average != 0: their mean; 0 for a
+ *       sequence without labels), seq_logp[2 pairs] receives it
+ *   h = beta ((s_c - ref_c) - (s_r - ref_r)) - margin   (ref_logp[2 pairs], NULL: 0)
+ *   loss[i] = weight (-(1 - label_smoothing) log sigmoid(h) - label_smoothing log sigmoid(-h))
+ * Sequence sums are fp64.  Keeps 16 bytes per row in the workspace.
+ */
+int muon_preference_loss(const void* logits, int64_t ld, int64_t rows, int64_t vocab, int dtype,
+                         const void* tokens, int token_dtype, const void* seq_bounds, int bounds_dtype,
+                         int64_t pairs, const float* ref_logp, const float* weights, float beta,
+                         float margin, float label_smoothing, int average, float* loss, float* seq_logp,
+                         void* grad, int64_t ld_grad, void* stream);
+
 /* ---- diagnostics (not part of the method) ---------------------------------- */
 
 /* Total kernels this library has launched in this process. */

@@ -26,6 +26,9 @@ MUON_F32 = 0
 MUON_BF16 = 1
 MUON_F16 = 2
 
+MUON_I32 = 32
+MUON_I64 = 64
+
 MUON_PATH_AUTO = 0
 MUON_PATH_PLAIN = 1
 MUON_PATH_GRAM = 2
@@ -43,6 +46,7 @@ EXPORTS = (
     "muon_group_create", "muon_group_step", "muon_group_destroy", "muon_group_set_host_io",
     "muon_owner_plan", "muon_adamw_step",
     "muon_pack_plan", "muon_pack",
+    "muon_distill_loss", "muon_policy_loss", "muon_preference_loss",
 )
 
 _lib = None
@@ -99,6 +103,11 @@ def lib() -> ctypes.CDLL:
                                   i64p, i64, i32, i32, f32, f32, f32, f32, f32, i64, vp]),
         "muon_pack_plan": (i32, [i64p, i64p, ip, i64, i32, i64, i64p, i64p]),
         "muon_pack": (i32, [ctypes.POINTER(vp), i64p, i64p, i64p, i64, i32, vp, i32, vp]),
+        "muon_distill_loss": (i32, [vp, i64, i64, i64, i32, vp, i32, vp, i32, i64, vp, vp, f32, vp, vp, i64, vp]),
+        "muon_policy_loss": (i32, [vp, i64, i64, i64, i32, vp, i32, vp, vp, vp, vp, f32, f32, f32, f32, vp, vp,
+                                   vp, i64, vp]),
+        "muon_preference_loss": (i32, [vp, i64, i64, i64, i32, vp, i32, vp, i32, i64, vp, vp, f32, f32, f32, i32,
+                                       vp, vp, vp, i64, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -479,3 +488,142 @@ def muon_adamw_step(params, grads, exp_avgs, exp_avg_sqs, lr: float, beta1: floa
                                  (ctypes.c_int64 * k)(*[t.numel() for t in params]), k, pd, sd, float(lr),
                                  float(beta1), float(beta2), float(eps), float(wd), int(step),
                                  _stream_ptr(stream)), "muon_adamw_step")
+
+
+# ---------------------------------------------------------------------------
+# losses over the vocabulary, with their gradients
+# ---------------------------------------------------------------------------
+
+def _on_stream(stream):
+    """Context in which new tensors belong to `stream` (None: the current one)."""
+    import contextlib
+
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _index_code(t, name) -> int:
+    import torch
+    if t.dtype == torch.int32:
+        return MUON_I32
+    if t.dtype == torch.int64:
+        return MUON_I64
+    raise TypeError(f"{name}: int32 or int64 required, got {t.dtype}")
+
+
+def _rows_of(t, name):
+    """(pointer, row pitch) of a rows x cols CUDA tensor whose rows are contiguous."""
+    if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-D CUDA tensor with contiguous rows")
+    pitch = t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1])
+    if pitch < t.shape[1]:
+        raise ValueError(f"{name}: rows overlap")
+    return t.data_ptr(), max(pitch, 1)
+
+
+def _vector(t, n, name, dtype=None):
+    """Pointer of a contiguous CUDA vector of n elements; None stays NULL."""
+    if t is None:
+        return None
+    _cuda_contig(t, name)
+    if t.numel() != n:
+        raise ValueError(f"{name}: {n} elements required, got {t.numel()}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: {dtype} required, got {t.dtype}")
+    return t.data_ptr()
+
+
+def _grad_like(logits, grad, stream):
+    import torch
+    if grad is None:
+        with _on_stream(stream):
+            return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    if grad.shape != logits.shape or grad.dtype != logits.dtype:
+        raise ValueError("grad must have the logits' shape and dtype")
+    return grad
+
+
+def _f32_out(n, like, stream):
+    import torch
+    with _on_stream(stream):
+        return torch.empty(n, dtype=torch.float32, device=like.device)
+
+
+def muon_distill_loss(logits, teacher_idx, teacher_logits, teacher_lse=None, weights=None, temperature: float = 1.0,
+                      grad=None, stream=None):
+    """Distillation from a teacher's top logits: teacher_idx (int32 or int64)
+    and teacher_logits, both rows x k; teacher_lse (rows, fp32) keeps the
+    teacher's remaining mass as one more class, None renormalises over the k.
+    Returns (loss per row, gradient of the loss' sum); grad may be a tensor to
+    write into, the logits themselves included."""
+    import torch
+    lp, ld = _rows_of(logits, "logits")
+    rows, vocab = logits.shape
+    if teacher_idx.dim() != 2 or teacher_idx.shape != teacher_logits.shape or teacher_idx.shape[0] != rows:
+        raise ValueError("teacher_idx and teacher_logits must be rows x k")
+    k = teacher_idx.shape[1]
+    ip = _vector(teacher_idx, rows * k, "teacher_idx")
+    tp = _vector(teacher_logits, rows * k, "teacher_logits")
+    grad = _grad_like(logits, grad, stream)
+    gp, ldg = _rows_of(grad, "grad")
+    loss = _f32_out(rows, logits, stream)
+    _check(lib().muon_distill_loss(lp, ld, rows, vocab, _dtype_code(logits), ip,
+                                   _index_code(teacher_idx, "teacher_idx"), tp, _dtype_code(teacher_logits), k,
+                                   _vector(teacher_lse, rows, "teacher_lse", torch.float32),
+                                   _vector(weights, rows, "weights", torch.float32), float(temperature),
+                                   loss.data_ptr(), gp, ldg, _stream_ptr(stream)), "muon_distill_loss")
+    return loss, grad
+
+
+def muon_policy_loss(logits, tokens, advantages, old_logp=None, ref_logp=None, weights=None,
+                     temperature: float = 1.0, clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
+                     grad=None, stream=None):
+    """Clipped policy loss with a KL term towards ref_logp, one sampled token
+    per row.  Returns (loss per row, log-probability per row, gradient of the
+    loss' sum)."""
+    import torch
+    lp, ld = _rows_of(logits, "logits")
+    rows, vocab = logits.shape
+    grad = _grad_like(logits, grad, stream)
+    gp, ldg = _rows_of(grad, "grad")
+    loss, logp = _f32_out(rows, logits, stream), _f32_out(rows, logits, stream)
+    _check(lib().muon_policy_loss(lp, ld, rows, vocab, _dtype_code(logits), _vector(tokens, rows, "tokens"),
+                                  _index_code(tokens, "tokens"),
+                                  _vector(advantages, rows, "advantages", torch.float32),
+                                  _vector(old_logp, rows, "old_logp", torch.float32),
+                                  _vector(ref_logp, rows, "ref_logp", torch.float32),
+                                  _vector(weights, rows, "weights", torch.float32), float(temperature),
+                                  float(clip_low), float(clip_high), float(kl_coef), loss.data_ptr(),
+                                  logp.data_ptr(), gp, ldg, _stream_ptr(stream)), "muon_policy_loss")
+    return loss, logp, grad
+
+
+def muon_preference_loss(logits, tokens, seq_bounds, ref_logp=None, weights=None, beta: float = 0.1,
+                         margin: float = 0.0, label_smoothing: float = 0.0, average: bool = False, grad=None,
+                         stream=None):
+    """Preference loss of paired sequences packed along the rows: seq_bounds
+    (2 pairs + 1 offsets, int32 or int64, on the device) alternates chosen and
+    rejected; tokens are labels, negative ones left out.  Returns (loss per
+    pair, sequence log-probabilities, gradient of the loss' sum)."""
+    import torch
+    lp, ld = _rows_of(logits, "logits")
+    rows, vocab = logits.shape
+    nb = seq_bounds.numel()
+    if nb % 2 != 1:
+        raise ValueError("seq_bounds needs 2 pairs + 1 offsets")
+    pairs = nb // 2
+    grad = _grad_like(logits, grad, stream)
+    gp, ldg = _rows_of(grad, "grad")
+    loss, seq = _f32_out(pairs, logits, stream), _f32_out(2 * pairs, logits, stream)
+    _check(lib().muon_preference_loss(lp, ld, rows, vocab, _dtype_code(logits), _vector(tokens, rows, "tokens"),
+                                      _index_code(tokens, "tokens"), _vector(seq_bounds, nb, "seq_bounds"),
+                                      _index_code(seq_bounds, "seq_bounds"), pairs,
+                                      _vector(ref_logp, 2 * pairs, "ref_logp", torch.float32),
+                                      _vector(weights, pairs, "weights", torch.float32), float(beta), float(margin),
+                                      float(label_smoothing), 1 if average else 0, loss.data_ptr(), seq.data_ptr(),
+                                      gp, ldg, _stream_ptr(stream)), "muon_preference_loss")
+    return loss, seq, grad
