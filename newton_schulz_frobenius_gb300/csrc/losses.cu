@@ -32,9 +32,6 @@ namespace muon {
 
 namespace {
 
-constexpr float LOG2E = 1.4426950408889634f;
-constexpr float LN2 = 0.6931471805599453f;
-
 enum LossMode : int { LM_POLICY = 0, LM_DISTILL = 1, LM_STATS = 2 };
 
 struct RowStats {       // one row of the preference loss between its launches
@@ -87,6 +84,9 @@ struct Vec<float> {
         v[0] = __uint_as_float(q.x); v[1] = __uint_as_float(q.y);
         v[2] = __uint_as_float(q.z); v[3] = __uint_as_float(q.w);
     }
+    static __device__ __forceinline__ float vmax(const uint4& q) {
+        return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)), fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
+    }
     static __device__ __forceinline__ uint4 pack(const float (&v)[4]) {
         return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
     }
@@ -97,6 +97,11 @@ struct Vec<__nv_bfloat16> {
     static __device__ __forceinline__ float ld(const __nv_bfloat16* p) { return __bfloat162float(*p); }
     static __device__ __forceinline__ void st(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
     static __device__ __forceinline__ void unpack(const uint4& q, float (&v)[8]) { unpack8_h(q, v, false); }
+    static __device__ __forceinline__ float vmax(const uint4& q) {
+        auto h = [](const uint32_t& w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+        const __nv_bfloat162 m = __hmax2(__hmax2(h(q.x), h(q.y)), __hmax2(h(q.z), h(q.w)));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
     static __device__ __forceinline__ uint4 pack(const float (&v)[8]) { return pack8_h(v, false); }
 };
 template <>
@@ -105,6 +110,11 @@ struct Vec<__half> {
     static __device__ __forceinline__ float ld(const __half* p) { return __half2float(*p); }
     static __device__ __forceinline__ void st(__half* p, float v) { *p = __float2half_rn(v); }
     static __device__ __forceinline__ void unpack(const uint4& q, float (&v)[8]) { unpack8_h(q, v, true); }
+    static __device__ __forceinline__ float vmax(const uint4& q) {
+        auto h = [](const uint32_t& w) { return *reinterpret_cast<const __half2*>(&w); };
+        const __half2 m = __hmax2(__hmax2(h(q.x), h(q.y)), __hmax2(h(q.z), h(q.w)));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
     static __device__ __forceinline__ uint4 pack(const float (&v)[8]) { return pack8_h(v, true); }
 };
 
@@ -118,14 +128,13 @@ __device__ __forceinline__ int row_shift(const T* row) {
 }
 
 template <typename T>
-__device__ __forceinline__ void load_vec(const T* row, int v0, int vocab, float (&x)[Vec<T>::E]) {
+__device__ __forceinline__ uint4 load_vec(const T* row, int v0, int vocab) {
     constexpr int E = Vec<T>::E;
-    if (v0 >= 0 && v0 + E <= vocab) {
-        Vec<T>::unpack(*reinterpret_cast<const uint4*>(row + v0), x);
-    } else {
+    if (v0 >= 0 && v0 + E <= vocab) return *reinterpret_cast<const uint4*>(row + v0);
+    float x[E];
 #pragma unroll
-        for (int j = 0; j < E; ++j) x[j] = (v0 + j >= 0 && v0 + j < vocab) ? Vec<T>::ld(row + v0 + j) : -INFINITY;
-    }
+    for (int j = 0; j < E; ++j) x[j] = (v0 + j >= 0 && v0 + j < vocab) ? Vec<T>::ld(row + v0 + j) : -INFINITY;
+    return Vec<T>::pack(x);
 }
 
 template <typename T>
@@ -194,126 +203,366 @@ __device__ __forceinline__ void policy_row(const RowLossArgs& a, int64_t row, fl
     }
 }
 
-constexpr int LT = 512;         // threads of a row
-constexpr int LNW = LT / 32;
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
 
-// Two walks over the row, one CTA per row: first the online maximum and sum,
-// then the gradient.
-template <typename T, int MODE>
-__global__ void __launch_bounds__(LT) row_loss_kernel(const __grid_constant__ RowLossArgs a) {
-    constexpr int E = Vec<T>::E;
-    extern __shared__ uint32_t dyn[];       // distillation: bitmap of S, then indices and p
-    __shared__ float red[LNW];
+// v <- exp2((v + nr) c2), two values per add and multiply; returns their sum.
+template <int E>
+__device__ __forceinline__ float exp_vec(float (&v)[E], float nr, float c2) {
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < E; j += 2) {
+        asm("{\n\t.reg .b64 x, r, c;\n\t"
+            "mov.b64 x, {%0, %1};\n\tmov.b64 r, {%2, %2};\n\tmov.b64 c, {%3, %3};\n\t"
+            "add.rn.f32x2 x, x, r;\n\tmul.rn.f32x2 x, x, c;\n\t"
+            "mov.b64 {%0, %1}, x;\n\t}"
+            : "+f"(v[j]), "+f"(v[j + 1])
+            : "f"(nr), "f"(c2));
+        v[j] = ex2(v[j]);
+        v[j + 1] = ex2(v[j + 1]);
+        asm("{\n\t.reg .b64 s, x;\n\tmov.b64 s, {%0, %1};\n\tmov.b64 x, {%2, %3};\n\t"
+            "add.rn.f32x2 s, s, x;\n\tmov.b64 {%0, %1}, s;\n\t}"
+            : "+f"(s.x), "+f"(s.y)
+            : "f"(v[j]), "f"(v[j + 1]));
+    }
+    return s.x + s.y;
+}
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// Every thread of every CTA of the cluster; orders shared and global accesses before and after.
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void st_cluster_f4(uint32_t local, uint32_t rank, const float4& v) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// one reading: the row rests in shared memory between its two walks
+// ---------------------------------------------------------------------------
+//
+// A row belongs to a cluster of C CTAs (C = 1 up to 53248 16-bit logits), CTA r
+// holding its r-th part in shared memory, SLOTS x NT vectors of 16 bytes at
+// most, two CTAs per SM.  The first walk takes the maximum and the sums, the
+// CTAs of a cluster exchange theirs through distributed shared memory, and the
+// second walk takes the exponentials again (cheaper than the registers to keep
+// them in) and stores the gradient, so every logit is read from memory once.
+// Thread t owns the vectors t, t + NT, ... of the part: it copies them in
+// (cp.async), reads them twice, and as soon as the second walk has taken a slot
+// it starts the copy of the next row's vector into it: no barrier guards the
+// slots, and up to a whole part per CTA is in flight.  Copies complete by
+// quarters of the part.
+//
+// The vectors are those aligned in memory; what a row has before the first and
+// after the last of them (odd vocabularies, sliced heads: at most 2 (E - 1)
+// logits) is taken one logit per thread by the first CTA.
+//
+// A thread's exponents are taken against a reference that follows the maximum
+// only when a logit exceeds it by more than 40 powers of two, so the sums stay
+// far from overflow and the rescaling branch is rare; the row's maximum becomes
+// the reference when the threads' sums are brought together.
+constexpr int SLOTS = 13;
+constexpr int MAX_CLUSTER = 16;
+constexpr float REBASE = 40.0f;     // exponent (base 2) beyond which the reference moves
+
+struct Sums {
+    float ref, limit;       // reference (negated), and the logit from which it moves
+    float s, so;            // sum of exponentials, the part outside the teacher's set
+    float top;              // the maximum
+};
+
+__device__ __forceinline__ void follow(Sums& z, float vm, float c2, float step) {
+    z.top = fmaxf(z.top, vm);
+    if (vm > z.limit) {
+        const float f = z.limit == -INFINITY ? 1.0f : ex2((-z.ref - vm) * c2);
+        z.s *= f;
+        z.so *= f;
+        z.ref = -vm;
+        z.limit = vm + step;
+    }
+}
+
+// Partial sums of a warp's lanes, one per lane (maximum, s, so), as one.
+__device__ __forceinline__ float3 merge_lanes(float top, float s, float so, float c2, bool rest) {
+    float3 r;
+    r.x = warp_max(top);
+    const float f = top == -INFINITY ? 0.f : ex2((top - r.x) * c2);     // 0 x NaN stays NaN
+    r.y = warp_sum(s * f);
+    r.z = rest ? warp_sum(so * f) : 0.f;
+    return r;
+}
+
+// Which of the cluster's next 32 rows are in the loss, refreshed every 32 rows.
+struct LiveWindow {
+    uint32_t bits;
+    int n;                  // rows of the cluster's sequence already taken from it
+};
+
+__host__ __device__ constexpr int bit_words(int logits) { return (logits + 31) / 32; }
+
+struct PartArgs {
+    int csize;              // CTAs per row
+    int per;                // vectors of a row per CTA, at most SLOTS NT
+};
+
+template <typename T, int MODE, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT)
+row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ PartArgs pa) {
+    constexpr int E = Vec<T>::E, NW = NT / 32, QUARTERS = 4;
+    constexpr bool GRAD = MODE != LM_STATS;
+    extern __shared__ __align__(16) uint8_t dyn8[];
+    uint4* ring = reinterpret_cast<uint4*>(dyn8);       // [slots][NT]
+    __shared__ float4 red[2][NW];
+    __shared__ float4 part[2][MAX_CLUSTER];
+    __shared__ float tred[NW], tred_m[NW], lred[NW];
+    const int V = a.vocab, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int csize = pa.csize, per = pa.per;
+    const int rank = csize > 1 ? (int)cluster_rank() : 0;
+    const int64_t G = gridDim.x / csize, row0 = blockIdx.x / csize;
+    const int slots = (per + NT - 1) / NT, quarter = (slots + QUARTERS - 1) / QUARTERS;
+    const float c2 = a.c2, step = REBASE / c2;
+    // distillation: the teacher's entries; with a remainder class, the bitmap of its set in this part
+    int* sidx = reinterpret_cast<int*>(dyn8 + (size_t)slots * NT * 16);
+    float* slp = reinterpret_cast<float*>(sidx + a.k);
+    float* sp = slp + a.k;
+    float* sx = sp + a.k;
+    uint32_t* bits = reinterpret_cast<uint32_t*>(sx + a.k);
+    const bool rest_class = MODE == LM_DISTILL && a.tlse != nullptr;
     pdl_wait();
     pdl_trigger();
-    const int V = a.vocab;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const T* x = reinterpret_cast<const T*>(a.logits) + row * a.ld;
-        T* g = reinterpret_cast<T*>(a.grad) + row * a.ldg;
-        const float w = a.weights ? a.weights[row] : 1.0f;
-        int64_t tok = 0;
-        bool live = (w != 0.f);
+    if (rest_class)
+        for (int i = t; i < bit_words(per * E); i += NT) bits[i] = 0;
+    if (csize > 1) cluster_barrier();                   // every CTA of the cluster runs before any writes to it
+
+    auto row_live = [&](int64_t row) -> bool {
+        if (row >= a.rows) return false;
+        bool live = !a.weights || a.weights[row] != 0.f;
         if (MODE != LM_DISTILL) {
-            tok = ld_index(a.tokens, row, a.tok64);
+            const int64_t tok = ld_index(a.tokens, row, a.tok64);
             live = live && tok >= 0 && tok < V;
         }
-        if (!live) {
-            if (MODE != LM_STATS) zero_row<T, LT>(g, V);
-            if (threadIdx.x == 0) {
+        return live;
+    };
+    auto window = [&](LiveWindow& w, int64_t row) -> bool {     // whether `row`, the sequence's next, is live
+        if ((w.n & 31) == 0) w.bits = __ballot_sync(0xffffffffu, row_live(row + (int64_t)lane * G));
+        return (w.bits >> (w.n++ & 31)) & 1;
+    };
+    // geometry of a row: logits before its first vector, vectors of this CTA
+    auto head_of = [&](const T* x) { return min(V, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(T)); };
+    auto count_of = [&](int head) { return max(0, min(per, (V - head) / E - rank * per)); };
+    // this thread's odd logit of a row (the first CTA's threads), -1 if none
+    auto odd_of = [&](int head) -> int {
+        if (rank != 0 || t >= 2 * E) return -1;
+        if (t < head) return t;
+        const int at = head + (V - head) / E * E + (t - head);
+        return at < V ? at : -1;
+    };
+
+    // the row in the loss after the one worked on: its vectors are copied in as slots fall free
+    LiveWindow lw{0, 0}, pw{0, 0};
+    int64_t lrow = row0;
+    const T* lx = nullptr;
+    const T* lp = nullptr;                              // this thread's first vector of it
+    int lcount = 0;                                     // the CTA's vectors of it
+    float lodd = -INFINITY;                             // this thread's odd logit of it
+    auto advance = [&]() {
+        while (lrow < a.rows && !window(lw, lrow)) lrow += G;
+        lcount = 0;
+        lodd = -INFINITY;
+        if (lrow < a.rows) {
+            lx = reinterpret_cast<const T*>(a.logits) + lrow * a.ld;
+            const int head = head_of(lx);
+            lcount = count_of(head);
+            lp = lx + head + (int64_t)(rank * per + t) * E;
+            const int odd = odd_of(head);
+            if (odd >= 0) lodd = Vec<T>::ld(lx + odd);
+        }
+    };
+    const uint32_t slot0 = smem_addr(ring + t);
+    auto issue = [&](int u) {
+        if (t + u * NT < lcount) cp_async16(slot0 + u * (NT * 16), lp + u * (NT * E));
+    };
+    advance();
+#pragma unroll
+    for (int qd = 0; qd < QUARTERS; ++qd) {
+        for (int u = qd * quarter; u < min(slots, (qd + 1) * quarter); ++u) issue(u);
+        cp_async_commit();
+    }
+
+    int par = 0;
+    for (int64_t row = row0; row < a.rows; row += G) {
+        T* g = reinterpret_cast<T*>(a.grad) + row * a.ldg;
+        if (!window(pw, row)) {
+            if (GRAD) {
+                const int head = head_of(g), n = count_of(head), odd = odd_of(head);
+                T* gp = g + head + (int64_t)rank * per * E;
+                for (int i = t; i < n; i += NT) *reinterpret_cast<uint4*>(gp + i * E) = make_uint4(0, 0, 0, 0);
+                if (odd >= 0) Vec<T>::st(g + odd, 0.f);
+            }
+            if (rank == 0 && t == 0) {
                 if (MODE == LM_STATS) a.stats[row] = RowStats{0.f, 0.f, 0.f, 0.f};
                 else a.loss[row] = 0.f;
                 if (MODE == LM_POLICY) a.logp[row] = 0.f;
             }
             continue;
         }
-        const int shift = row_shift(x);
-        const int nv = (V + shift + E - 1) / E;
-        // teacher's set
-        const int words = (V + 31) / 32;
-        uint32_t* bits = dyn;
-        int* sidx = reinterpret_cast<int*>(dyn + words);
-        float* sp = reinterpret_cast<float*>(sidx + a.k);
-        float mass = 0.f, tsub = 0.f;       // sum of p; log p_j = t_j / T - tsub
+        const T* x = lx;                    // the row whose vectors are in the ring
+        const int head = head_of(x), count = lcount;
+        const float odd = lodd;
+        const float w = a.weights ? a.weights[row] : 1.0f;
+        int tok = 0;
+        float xt = 0.f;
+        if (MODE != LM_DISTILL) {
+            tok = (int)ld_index(a.tokens, row, a.tok64);
+            xt = Vec<T>::ld(x + tok);
+        }
+        float tm = 0.f, lse = 0.f;
+        const int part0 = head + rank * per * E;        // the part's first logit; its bit is 0
+        bool odd_in = false;                            // the thread's odd logit is in the teacher's set
         if (MODE == LM_DISTILL) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < words; i += LT) bits[i] = 0;
-            __syncthreads();
-            float tm = -INFINITY;
-            for (int j = threadIdx.x; j < a.k; j += LT) {
+            lse = a.tlse ? a.tlse[row] : 0.f;
+            __syncthreads();                // the previous row's use of the entries is over
+            float wm = -INFINITY;
+            for (int j = t; j < a.k; j += NT) {
                 const int64_t id = ld_index(a.tidx, row * a.k + j, a.tidx64);
                 const bool ok = id >= 0 && id < V;
-                const float t = ld_elem(a.tval, row * a.k + j, a.tval_dtype);
+                const float tv = ok ? ld_elem(a.tval, row * a.k + j, a.tval_dtype) : -INFINITY;
                 sidx[j] = ok ? (int)id : -1;
-                sp[j] = t;
-                if (ok) {
-                    atomicOr(&bits[id >> 5], 1u << (id & 31));
-                    tm = fmaxf(tm, t);
-                }
+                slp[j] = tv;
+                sx[j] = ok ? Vec<T>::ld(x + id) : 0.f;
+                const int at = (int)id - part0;
+                if (ok && rest_class && at >= 0 && at < count * E) atomicOr(&bits[at >> 5], 1u << (at & 31));
+                wm = fmaxf(wm, tv);
             }
-            if (a.tlse) {
-                tm = 0.f;
-                tsub = a.tlse[row];
-            } else {
-                tm = block_max<LNW>(tm, red);
-                float s = 0.f;
-                for (int j = threadIdx.x; j < a.k; j += LT)
-                    if (sidx[j] >= 0) s += expf((sp[j] - tm) * a.inv_t);
-                tsub = ::logf(block_sum<LNW>(s, red));
-            }
-            // sp[j] becomes log p_j (entries that are not in the vocabulary drop out)
+            wm = warp_max(wm);
+            if (lane == 0) tred_m[warp] = wm;
+            __syncthreads();
+            if (!a.tlse) tm = warp_max(lane < NW ? tred_m[lane] : -INFINITY);
             float s = 0.f;
-            for (int j = threadIdx.x; j < a.k; j += LT) {
-                const float lp = sidx[j] >= 0 ? (sp[j] - tm) * a.inv_t - tsub : -INFINITY;
-                sp[j] = lp;
-                s += expf(lp);
-            }
-            mass = block_sum<LNW>(s, red);
+            for (int j = t; j < a.k; j += NT)
+                if (sidx[j] >= 0) s += expf((slp[j] - tm) * a.inv_t - lse);
+            s = warp_sum(s);
+            if (lane == 0) tred[warp] = s;
+            if (rest_class && odd_of(head) >= 0)
+                for (int j = 0; j < a.k; ++j) odd_in = odd_in || sidx[j] == odd_of(head);
         }
-        // maximum and sums
-        float m = -INFINITY;
-        for (int i = threadIdx.x; i < nv; i += LT) {
-            float v[E];
-            load_vec<T>(x, i * E - shift, V, v);
+        lrow += G;
+        advance();
+        // first walk
+        Sums z{0.f, -INFINITY, 0.f, 0.f, -INFINITY};
 #pragma unroll
-            for (int j = 0; j < E; ++j) m = fmaxf(m, v[j]);
-        }
-        m = block_max<LNW>(m, red);
-        float s = 0.f, so = 0.f;
-        for (int i = threadIdx.x; i < nv; i += LT) {
-            const int v0 = i * E - shift;
-            float v[E];
-            load_vec<T>(x, v0, V, v);
+        for (int qd = 0; qd < QUARTERS; ++qd) {
+            // pending behind this quarter: the row's later ones, and (statistics) the next row's earlier ones
+            if (!GRAD || qd == 0) cp_async_wait<3>();
+            else if (qd == 1) cp_async_wait<2>();
+            else if (qd == 2) cp_async_wait<1>();
+            else cp_async_wait<0>();
+            const int end = min(slots, (qd + 1) * quarter);
+#pragma unroll 2
+            for (int u = qd * quarter; u < end; ++u) {
+                if (t + u * NT < count) {
+                    const uint4 raw = ring[u * NT + t];
+                    follow(z, Vec<T>::vmax(raw), c2, step);
+                    float v[E];
+                    Vec<T>::unpack(raw, v);
+                    const float sv = exp_vec<E>(v, z.ref, c2);
+                    z.s += sv;
+                    if (rest_class) {
+                        const int i = (t + u * NT) * E;
+                        const uint32_t k = (bits[i >> 5] >> (i & 31)) & ((1u << E) - 1);
+                        if (k == 0) {
+                            z.so += sv;
+                        } else {
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                const float e = (v0 + j >= 0 && v0 + j < V) ? exp2f((v[j] - m) * a.c2) : 0.f;
-                s += e;
-                if (MODE == LM_DISTILL && v0 + j >= 0 && v0 + j < V && !((bits[(v0 + j) >> 5] >> ((v0 + j) & 31)) & 1))
-                    so += e;
+                            for (int j = 0; j < E; ++j)
+                                if (!((k >> j) & 1)) z.so += v[j];
+                        }
+                    }
+                }
+                if (!GRAD) issue(u);
+            }
+            if (!GRAD) cp_async_commit();
+        }
+        if (t < 2 * E) {
+            follow(z, odd, c2, step);
+            const float e = ex2((odd + z.ref) * c2);
+            z.s += e;
+            if (!odd_in) z.so += e;
+        }
+        float3 q;
+        {
+            const float wm = warp_max(z.top);
+            const float f = z.limit == -INFINITY ? 0.f : ex2((-z.ref - wm) * c2);
+            const float s = warp_sum(z.s * f);
+            const float so = rest_class ? warp_sum(z.so * f) : 0.f;
+            if (lane == 0) red[par][warp] = make_float4(wm, s, so, 0.f);
+            __syncthreads();
+            const float4 r = lane < NW ? red[par][lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+            if (csize == 1) {
+                q = merge_lanes(r.x, r.y, r.z, c2, rest_class);
+            } else {
+                if (warp == 0) {
+                    q = merge_lanes(r.x, r.y, r.z, c2, rest_class);
+                    if (t < csize) st_cluster_f4(smem_addr(&part[par][rank]), (uint32_t)t, make_float4(q.x, q.y, q.z, 0.f));
+                }
+                cluster_barrier();
+                const float4 c = lane < csize ? part[par][lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+                q = merge_lanes(c.x, c.y, c.z, c2, rest_class);
             }
         }
-        s = block_sum<LNW>(s, red);
-        const float log_s = ::logf(s);
-        const float inv_s = 1.0f / s;
+        par ^= 1;
+        const float m = q.x, log_s = ::logf(q.y), inv_s = 1.0f / q.y;
         float in = 0.f, out = 0.f;          // factors of q inside and outside S
-        float scale = 0.f;                  // factor of t
-        if (MODE != LM_DISTILL) {
-            const float lp = (Vec<T>::ld(x + tok) - m) * a.inv_t - log_s;
-            if (MODE == LM_STATS) {
-                if (threadIdx.x == 0) a.stats[row] = RowStats{m, inv_s, lp, 0.f};
-                continue;
-            }
+        float scale = 0.f;                  // factor of the sparse part
+        if (MODE == LM_STATS) {
+            if (rank == 0 && t == 0) a.stats[row] = RowStats{m, inv_s, (xt - m) * a.inv_t - log_s, 0.f};
+            continue;
+        } else if (MODE == LM_POLICY) {
+            const float lp_tok = (xt - m) * a.inv_t - log_s;
             float loss, dl;
-            policy_row(a, row, lp, loss, dl);
-            if (threadIdx.x == 0) {
+            policy_row(a, row, lp_tok, loss, dl);
+            if (rank == 0 && t == 0) {
                 a.loss[row] = w * loss;
-                a.logp[row] = lp;
+                a.logp[row] = lp_tok;
             }
             scale = w * dl * a.inv_t;
-            in = out = -scale;
+            out = -scale * inv_s;
         } else {
+            const float ts = warp_sum(lane < NW ? tred[lane] : 0.f);
+            const float mass = a.tlse ? ts : (ts > 0.f || ts != ts ? 1.0f : 0.f);
+            const float tsub = a.tlse ? lse : ::logf(ts);
             float rest = 0.f, share = 0.f, kl = 0.f;
             if (a.tlse) {
-                const float qr = block_sum<LNW>(so, red) * inv_s;
+                const float qr = q.z * inv_s;
                 rest = 1.0f - mass;
                 if (!(rest > 0.f && qr > 0.f)) rest = 0.f;
                 else {
@@ -321,49 +570,90 @@ __global__ void __launch_bounds__(LT) row_loss_kernel(const __grid_constant__ Ro
                     kl = rest * ::logf(share);
                 }
             }
-            float part = 0.f;
-            for (int j = threadIdx.x; j < a.k; j += LT) {
-                const float lp = sp[j];
-                const float p = expf(lp);
-                if (p > 0.f) part += p * (lp - ((Vec<T>::ld(x + sidx[j]) - m) * a.inv_t - log_s));
-                else if (p != p) part = p;
+            float part_kl = 0.f;
+            for (int j = t; j < a.k; j += NT) {
+                const float lpj = sidx[j] >= 0 ? (slp[j] - tm) * a.inv_t - tsub : -INFINITY;
+                const float p = expf(lpj);
                 sp[j] = p;
+                if (p > 0.f) part_kl += p * (lpj - ((sx[j] - m) * a.inv_t - log_s));
+                else if (p != p) part_kl = p;
             }
-            kl += block_sum<LNW>(part, red);        // also orders the gathers before the gradient's stores
-            if (threadIdx.x == 0) a.loss[row] = w * a.t * a.t * kl;
+            part_kl = warp_sum(part_kl);
+            if (lane == 0) lred[warp] = part_kl;
             scale = w * a.t;
-            in = scale * (mass + rest);
-            out = scale * (mass + rest - share);
-        }
-        __syncthreads();
-        // gradient
-        for (int i = threadIdx.x; i < nv; i += LT) {
-            const int v0 = i * E - shift;
-            float v[E];
-            load_vec<T>(x, v0, V, v);
-#pragma unroll
-            for (int j = 0; j < E; ++j) {
-                const int id = v0 + j;
-                const float q = exp2f((v[j] - m) * a.c2) * inv_s;
-                if (MODE == LM_POLICY) {
-                    v[j] = in * q + (id == (int)tok ? scale : 0.f);
-                } else if (id >= 0 && id < V && ((bits[id >> 5] >> (id & 31)) & 1)) {
-                    float p = 0.f;          // an index the teacher lists twice counts twice
-                    for (int n = 0; n < a.k; ++n)
-                        if (sidx[n] == id) p += sp[n];
-                    v[j] = in * q - scale * p;
-                } else {
-                    v[j] = out * q;
-                }
+            in = scale * (mass + rest) * inv_s;
+            out = scale * (mass + rest - share) * inv_s;
+            __syncthreads();
+            if (rank == 0 && warp == 0) {
+                part_kl = warp_sum(lane < NW ? lred[lane] : 0.f);
+                if (t == 0) a.loss[row] = w * a.t * a.t * (kl + part_kl);
             }
-            store_vec<T>(g, v0, V, v, a.same_align != 0);
+        }
+        // second walk: out q everywhere, the token's entry on the way
+        T* gp = g + part0 + t * E;
+        const int tok_at = tok - part0;     // within the part's vectors, if there
+#pragma unroll
+        for (int qd = 0; qd < QUARTERS; ++qd) {
+            const int end = min(slots, (qd + 1) * quarter);
+#pragma unroll 2
+            for (int u = qd * quarter; u < end; ++u) {
+                const int i = t + u * NT;
+                if (i < count) {
+                    float v[E];
+                    Vec<T>::unpack(ring[i], v);
+                    exp_vec<E>(v, -m, c2);
+#pragma unroll
+                    for (int j = 0; j < E; ++j) v[j] *= out;
+                    if (MODE == LM_POLICY && (unsigned)(tok_at - i * E) < (unsigned)E) {
+#pragma unroll
+                        for (int j = 0; j < E; ++j)
+                            if (i * E + j == tok_at) v[j] += scale;
+                    }
+                    if (a.same_align) {
+                        *reinterpret_cast<uint4*>(gp + u * (NT * E)) = Vec<T>::pack(v);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < E; ++j) Vec<T>::st(gp + u * (NT * E) + j, v[j]);
+                    }
+                }
+                issue(u);
+            }
+            cp_async_commit();
+        }
+        if (odd_of(head) >= 0) {
+            const int at = odd_of(head);
+            Vec<T>::st(g + at, ex2((odd - m) * c2) * out + (MODE == LM_POLICY && at == tok ? scale : 0.f));
+        }
+        if (MODE == LM_DISTILL) {
+            __syncthreads();                // the listed entries' own values go over what the walk stored
+            for (int j = t; j < a.k; j += NT) {
+                const int id = sidx[j], at = id - part0;
+                const bool vec = at >= 0 && at < count * E;
+                // an odd logit (before the vectors, or after the row's last) is the first CTA's
+                const bool end = rank == 0 && (id < head || id >= head + (V - head) / E * E);
+                if (id < 0 || !(vec || end)) continue;
+                float psum = 0.f;           // an index the teacher lists twice counts twice
+                bool leads = true;
+                for (int n = 0; n < a.k; ++n) {
+                    if (sidx[n] == id) {
+                        psum += sp[n];
+                        leads = leads && n >= j;
+                    }
+                }
+                if (leads) Vec<T>::st(g + id, in * ex2((sx[j] - m) * c2) - scale * psum);
+                if (rest_class && vec) bits[at >> 5] = 0;
+            }
         }
     }
+    cp_async_wait<0>();
+    if (csize > 1) cluster_barrier();       // no CTA leaves while another may still write to its shared memory
 }
 
+constexpr int UNROLL = 4;          // vectors of a gradient row in flight per thread
+
 // Gradient rows of the preference loss: coef ([v = token] - q_v).
-template <typename T>
-__global__ void __launch_bounds__(LT) row_grad_kernel(const __grid_constant__ RowLossArgs a) {
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) row_grad_kernel(const __grid_constant__ RowLossArgs a) {
     constexpr int E = Vec<T>::E;
     pdl_wait();
     pdl_trigger();
@@ -373,20 +663,34 @@ __global__ void __launch_bounds__(LT) row_grad_kernel(const __grid_constant__ Ro
         T* g = reinterpret_cast<T*>(a.grad) + row * a.ldg;
         const RowStats st = a.stats[row];
         if (st.coef == 0.f) {
-            zero_row<T, LT>(g, V);
+            zero_row<T, NT>(g, V);
             continue;
         }
         const int tok = (int)ld_index(a.tokens, row, a.tok64);
         const int shift = row_shift(x);
         const int nv = (V + shift + E - 1) / E;
         const float f = -st.coef * st.inv_s;
-        for (int i = threadIdx.x; i < nv; i += LT) {
-            const int v0 = i * E - shift;
-            float v[E];
-            load_vec<T>(x, v0, V, v);
+        for (int i0 = threadIdx.x; i0 < nv; i0 += UNROLL * NT) {
+            uint4 q[UNROLL];
 #pragma unroll
-            for (int j = 0; j < E; ++j) v[j] = fmaf(f, exp2f((v[j] - st.mx) * a.c2), v0 + j == tok ? st.coef : 0.f);
-            store_vec<T>(g, v0, V, v, a.same_align != 0);
+            for (int u = 0; u < UNROLL; ++u)
+                if (i0 + u * NT < nv) q[u] = load_vec<T>(x, (i0 + u * NT) * E - shift, V);
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                const int v0 = (i0 + u * NT) * E - shift;
+                if (i0 + u * NT < nv) {
+                    float v[E];
+                    Vec<T>::unpack(q[u], v);
+#pragma unroll
+                    for (int j = 0; j < E; ++j) v[j] = f * ex2((v[j] - st.mx) * a.c2);
+                    if ((unsigned)(tok - v0) < (unsigned)E) {
+#pragma unroll
+                        for (int j = 0; j < E; ++j)
+                            if (v0 + j == tok) v[j] += st.coef;
+                    }
+                    store_vec<T>(g, v0, V, v, a.same_align != 0);
+                }
+            }
         }
     }
 }
@@ -482,27 +786,92 @@ __global__ void __launch_bounds__(256) pair_kernel(const __grid_constant__ PairA
 // host side
 // ---------------------------------------------------------------------------
 
-constexpr int64_t MAX_VOCAB = 1 << 20;
+constexpr int64_t MAX_VOCAB = (int64_t)MAX_CLUSTER * SLOTS * 512 * 4;   // fp32: 425984
 constexpr int MAX_TEACHER = 1024;
 
-size_t distill_smem(int vocab, int k) { return 4 * ((size_t)(vocab + 31) / 32 + 2 * (size_t)k); }
+constexpr int SMALL_NT = 128;           // threads of a CTA whose whole row fits SLOTS x 128 vectors; else 512
+
+// Shared memory of a row's CTA: its part of the row, and for distillation the
+// teacher's entries and the bitmap of its set.
+template <typename T, int MODE, int NT>
+size_t row_smem(int per, int k, bool rest) {
+    size_t b = (size_t)((per + NT - 1) / NT) * NT * 16;
+    if (MODE == LM_DISTILL) b += 16 * (size_t)k + (rest ? 4 * (size_t)bit_words(per * Vec<T>::E) : 0);
+    return b;
+}
+
+template <typename T, int MODE, int NT>
+cudaError_t launch_part(const RowLossArgs& a, int64_t nv, int csize, cudaStream_t s) {
+    auto kern = row_loss_kernel<T, MODE, NT>;
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    std::call_once(once, [&] {
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   (int)row_smem<T, MODE, NT>(SLOTS * NT, MAX_TEACHER, true));
+        if (err == cudaSuccess) err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    });
+    if (err != cudaSuccess) return err;
+    PartArgs pa;
+    pa.csize = csize;
+    pa.per = (int)((nv + csize - 1) / csize);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)csize);
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = row_smem<T, MODE, NT>(pa.per, a.k, a.tlse != nullptr);
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)csize;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    // clusters resident at once, by cluster size and slots
+    static std::atomic<int> fits[MAX_CLUSTER + 1][SLOTS + 1];
+    std::atomic<int>& fit = fits[csize][(pa.per + NT - 1) / NT];
+    int n = fit.load();
+    if (n == 0) {
+        cfg.attrs = at + 1;
+        cfg.numAttrs = 1;
+        cudaLaunchConfig_t most = cfg;
+        most.dynamicSmemBytes = row_smem<T, MODE, NT>((pa.per + NT - 1) / NT * NT, MODE == LM_DISTILL ? 256 : 0, true);
+        cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kern, &most);
+        if (e != cudaSuccess) return e;
+        if (n < 1) return cudaErrorInvalidConfiguration;
+        fit.store(n);
+    }
+    cfg.gridDim = dim3((unsigned)(csize * std::min<int64_t>(a.rows, n)));
+    cfg.attrs = pdl_enabled() ? at : at + 1;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, pa);
+}
+
+// How a launch divides its rows: 128-thread CTAs for rows of up to 13 x 128
+// vectors; else 512-thread CTAs, as few per row as hold it, twice as many while
+// the rows alone would leave SMs idle and a CTA keeps two vectors per thread.
+template <typename T, int MODE>
+cudaError_t launch_mode(const RowLossArgs& a, int sms, cudaStream_t s) {
+    constexpr int E = Vec<T>::E;
+    const int64_t nv = std::max(1, a.vocab / E);       // whole vectors of a row at most
+    if (nv <= SLOTS * SMALL_NT) return launch_part<T, MODE, SMALL_NT>(a, nv, 1, s);
+    int c = (int)((nv + SLOTS * 512 - 1) / (SLOTS * 512));
+    while (c <= 4 && a.rows * c < sms && nv > (int64_t)c * 1024) c *= 2;
+    return launch_part<T, MODE, 512>(a, nv, c, s);
+}
 
 template <typename T>
 cudaError_t launch_rows(const RowLossArgs& a, int mode, int sms, cudaStream_t s) {
-    const unsigned grid = (unsigned)std::min<int64_t>(a.rows, (int64_t)sms * 4);
-    if (mode == LM_POLICY) return launch_pdl(row_loss_kernel<T, LM_POLICY>, dim3(grid), dim3(LT), 0, s, a);
-    if (mode == LM_STATS) return launch_pdl(row_loss_kernel<T, LM_STATS>, dim3(grid), dim3(LT), 0, s, a);
-    const size_t smem = distill_smem(a.vocab, a.k);
-    cudaError_t e = cudaFuncSetAttribute(row_loss_kernel<T, LM_DISTILL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)distill_smem((int)MAX_VOCAB, MAX_TEACHER));
-    if (e != cudaSuccess) return e;
-    return launch_pdl(row_loss_kernel<T, LM_DISTILL>, dim3(grid), dim3(LT), smem, s, a);
+    if (mode == LM_POLICY) return launch_mode<T, LM_POLICY>(a, sms, s);
+    if (mode == LM_STATS) return launch_mode<T, LM_STATS>(a, sms, s);
+    return launch_mode<T, LM_DISTILL>(a, sms, s);
 }
 
 template <typename T>
 cudaError_t launch_grad(const RowLossArgs& a, int sms, cudaStream_t s) {
-    const unsigned grid = (unsigned)std::min<int64_t>(a.rows, (int64_t)sms * 4);
-    return launch_pdl(row_grad_kernel<T>, dim3(grid), dim3(LT), 0, s, a);
+    if (a.vocab <= SMALL_NT * UNROLL * Vec<T>::E)
+        return launch_pdl(row_grad_kernel<T, 128>, dim3((unsigned)std::min<int64_t>(a.rows, (int64_t)sms * 8)), dim3(128),
+                          0, s, a);
+    return launch_pdl(row_grad_kernel<T, 512>, dim3((unsigned)std::min<int64_t>(a.rows, (int64_t)sms * 2)), dim3(512), 0,
+                      s, a);
 }
 
 cudaError_t dispatch_rows(const RowLossArgs& a, int mode, int dtype, int sms, cudaStream_t s) {
@@ -526,7 +895,7 @@ int row_args(RowLossArgs& a, const void* logits, int64_t ld, int64_t rows, int64
     std::memset(&a, 0, sizeof a);
     if (!valid_dtype(dtype)) return fail(MUON_EDTYPE, "logits dtype %d", dtype);
     if (rows < 0 || rows > INT32_MAX) return fail(MUON_EINVAL, "rows outside [0, 2^31)");
-    if (vocab < 1 || vocab > MAX_VOCAB) return fail(MUON_EINVAL, "vocab outside [1, 2^20]");
+    if (vocab < 1 || vocab > MAX_VOCAB) return fail(MUON_EINVAL, "vocab outside [1, %lld]", (long long)MAX_VOCAB);
     if (ld < vocab || ld_grad < vocab) return fail(MUON_EINVAL, "row pitch below vocab");
     if (ld > INT64_MAX / 8 / std::max<int64_t>(rows, 1) || ld_grad > INT64_MAX / 8 / std::max<int64_t>(rows, 1))
         return fail(MUON_EINVAL, "byte range overflows");
