@@ -421,6 +421,31 @@ int muon_preference_loss(const void* logits, int64_t ld, int64_t rows, int64_t v
                          float margin, float label_smoothing, int average, float* loss, float* seq_logp,
                          void* grad, int64_t ld_grad, void* stream);
 
+/*
+ * Gated feed-forward block with its backward pass: the projections whose
+ * matrices muon_step updates.  All matrices row-major and contiguous, of one
+ * type, MUON_BF16 or MUON_F16 (16-bit tensor-core products, fp32 accumulation;
+ * MUON_EDTYPE for fp32).  x is tokens x hidden, w_gate and w_up ffn x hidden.
+ *   forward:  gate = x w_gate^T, up = x w_up^T, h = act(gate) up   (tokens x ffn)
+ *             h from the unrounded gate and up; gate and up receive them rounded
+ *             (what the backward pass reads), or are both NULL.
+ *   backward: with dh = d/dh and the gate and up the forward pass kept,
+ *             dg = dh up act'(gate), du = dh act(gate) (rounded to the type),
+ *             dx = dg w_gate + du w_up, dw_gate = dg^T x, dw_up = du^T x.
+ *             dx, or dw_gate and dw_up together, may be NULL.
+ * tokens in [0, 2^24] (0: h is empty, the weights' gradients are zero), hidden
+ * and ffn in [1, 2^20].  Outputs must not overlap anything else of the call.
+ * The backward pass keeps dg and du in the workspace (4 bytes per token and ffn
+ * column); rows that do not start on 16 bytes (a size that is not a multiple of
+ * 8, a pointer off it) are copied there padded first.
+ */
+typedef enum { MUON_ACT_SILU = 0, MUON_ACT_GELU = 1 /* exact */, MUON_ACT_GELU_TANH = 2 } muon_act;
+int muon_glu_forward(const void* x, const void* w_gate, const void* w_up, void* h, void* gate, void* up,
+                     int64_t tokens, int64_t hidden, int64_t ffn, int dtype, int act, void* stream);
+int muon_glu_backward(const void* x, const void* w_gate, const void* w_up, const void* gate, const void* up,
+                      const void* dh, void* dx, void* dw_gate, void* dw_up, int64_t tokens, int64_t hidden,
+                      int64_t ffn, int dtype, int act, void* stream);
+
 /* ---- diagnostics (not part of the method) ---------------------------------- */
 
 /* Total kernels this library has launched in this process. */

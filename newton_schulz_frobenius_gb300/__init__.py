@@ -47,6 +47,7 @@ EXPORTS = (
     "muon_owner_plan", "muon_adamw_step",
     "muon_pack_plan", "muon_pack",
     "muon_distill_loss", "muon_policy_loss", "muon_preference_loss",
+    "muon_glu_forward", "muon_glu_backward",
 )
 
 _lib = None
@@ -108,6 +109,8 @@ def lib() -> ctypes.CDLL:
                                    vp, i64, vp]),
         "muon_preference_loss": (i32, [vp, i64, i64, i64, i32, vp, i32, vp, i32, i64, vp, vp, f32, f32, f32, i32,
                                        vp, vp, vp, i64, vp]),
+        "muon_glu_forward": (i32, [vp] * 6 + [i64, i64, i64, i32, i32, vp]),
+        "muon_glu_backward": (i32, [vp] * 9 + [i64, i64, i64, i32, i32, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -627,3 +630,65 @@ def muon_preference_loss(logits, tokens, seq_bounds, ref_logp=None, weights=None
                                       float(label_smoothing), 1 if average else 0, loss.data_ptr(), seq.data_ptr(),
                                       gp, ldg, _stream_ptr(stream)), "muon_preference_loss")
     return loss, seq, grad
+
+
+# ---------------------------------------------------------------------------
+# gated feed-forward block
+# ---------------------------------------------------------------------------
+
+#: activations of the gated feed-forward block
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+def _glu_args(x, w_gate, w_up, act):
+    for t, nm in ((x, "x"), (w_gate, "w_gate"), (w_up, "w_up")):
+        _cuda_contig(t, nm)
+        if t.dim() != 2:
+            raise ValueError(f"{nm} must be 2-D")
+        if t.dtype != x.dtype:
+            raise TypeError(f"{nm}: dtype differs from x")
+    if w_gate.shape != w_up.shape or w_gate.shape[1] != x.shape[1]:
+        raise ValueError("x is tokens x hidden, w_gate and w_up ffn x hidden")
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act {act!r}: one of {sorted(ACTIVATIONS)}")
+    return x.shape[0], x.shape[1], w_gate.shape[0], _dtype_code(x), ACTIVATIONS[act]
+
+
+def muon_glu_forward(x, w_gate, w_up, act: str = "silu", save: bool = True, stream=None):
+    """act(x w_gate^T) * (x w_up^T) in one kernel (bf16 or fp16; x tokens x
+    hidden, weights ffn x hidden).  Returns (h, gate, up) for the backward
+    pass, or h alone with save=False."""
+    import torch
+    tokens, hidden, ffn, dt, code = _glu_args(x, w_gate, w_up, act)
+    with _on_stream(stream):
+        h, gate, up = (torch.empty(tokens, ffn, dtype=x.dtype, device=x.device) if on else None
+                       for on in (True, save, save))
+    _check(lib().muon_glu_forward(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), h.data_ptr(),
+                                  gate.data_ptr() if save else None, up.data_ptr() if save else None, tokens, hidden,
+                                  ffn, dt, code, _stream_ptr(stream)), "muon_glu_forward")
+    return (h, gate, up) if save else h
+
+
+def muon_glu_backward(x, w_gate, w_up, gate, up, dh, act: str = "silu", need_dx: bool = True, dw_gate=None, dw_up=None,
+                      stream=None):
+    """Gradients (dx, dw_gate, dw_up) of muon_glu_forward from dh and the gate
+    and up it returned.  dw_gate and dw_up may be tensors to write into (the
+    gradients a MuonGroup reads); need_dx=False leaves dx out (None)."""
+    import torch
+    tokens, hidden, ffn, dt, code = _glu_args(x, w_gate, w_up, act)
+    for t, nm in ((gate, "gate"), (up, "up"), (dh, "dh")):
+        _cuda_contig(t, nm)
+        if t.shape != (tokens, ffn) or t.dtype != x.dtype:
+            raise ValueError(f"{nm} must be tokens x ffn of x's dtype")
+    with _on_stream(stream):
+        dx = torch.empty_like(x) if need_dx else None
+        outs = [torch.empty_like(w_gate) if t is None else t for t in (dw_gate, dw_up)]
+    for t, nm in zip(outs, ("dw_gate", "dw_up")):
+        _cuda_contig(t, nm)
+        if t.shape != w_gate.shape or t.dtype != x.dtype:
+            raise ValueError(f"{nm} must be ffn x hidden of x's dtype")
+    _check(lib().muon_glu_backward(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), gate.data_ptr(), up.data_ptr(),
+                                   dh.data_ptr(), dx.data_ptr() if need_dx else None, outs[0].data_ptr(),
+                                   outs[1].data_ptr(), tokens, hidden, ffn, dt, code, _stream_ptr(stream)),
+           "muon_glu_backward")
+    return dx, outs[0], outs[1]

@@ -1,0 +1,683 @@
+// Gated feed-forward block: both projections, the activation and the product in
+// one kernel, and its backward pass.  Weights as a training step keeps them for
+// the Muon update: w_gate and w_up are ffn x hidden, row-major.
+//
+//   forward   G = X Wg^T, U = X Wu^T, H = act(G) U
+//   backward  dG = dH U act'(G), dU = dH act(G)
+//             dX = dG Wg + dU Wu, dWg = dG^T X, dWu = dU^T X
+//
+// Products run on 2-SM tcgen05 pairs (M = 256, N = 256, fp32 accumulation in
+// TMEM, two accumulators so that a tile's epilogue runs under the next tile's
+// products), fed by TMA through a ring of six 32 KB stages per CTA.
+//
+// Forward: a pair's tile is 256 tokens x 128 ffn columns of BOTH projections.
+// The even CTA loads the 128 rows of Wg and the odd CTA the same rows of Wu as
+// the two halves of the N = 256 operand, so G occupies accumulator columns
+// 0..127 and U columns 128..255 of the same rows, and the epilogue forms
+// act(G) U from registers; G and U leave rounded only if the caller keeps them.
+//
+// Backward: one elementwise launch writes dG and dU (16-bit: operands of the
+// products; the one rounding beside the results'), then one persistent launch
+// runs all three products: dX as one contraction over 2 ffn (first dG Wg, then
+// dU Wu, in one accumulator), dWg and dWu with both operands read MN-major, so
+// nothing is transposed in memory.
+#include "host.h"
+#include "epilogue.cuh"
+#include "tc_ptx.cuh"
+
+namespace muon {
+
+namespace {
+
+using namespace tc;
+
+constexpr int GM = 128;                     // rows of a CTA's half-tile
+constexpr int GK = 64;                      // k-block: 128 bytes
+constexpr int NEPI = 8;
+constexpr int GT = 64 + 32 * NEPI;
+constexpr int STAGES = 6;
+constexpr int OP_BYTES = GM * GK * 2;       // one operand tile of a stage (A, or this CTA's half of B)
+constexpr int STAGE_BYTES = 2 * OP_BYTES;
+constexpr int OUT_BYTES = 32 * 32 * 2;      // one output chunk of a warp: 32 x 32, 64-byte swizzled rows
+constexpr int NBARS = 2 * STAGES + 5;
+constexpr int GLU_SMEM = STAGES * STAGE_BYTES + NEPI * 2 * OUT_BYTES + NBARS * 8 + 16 + 1024;
+static_assert(GLU_SMEM <= 232448, "shared memory per CTA");
+constexpr int GROUP = 16;                   // row pairs of tiles that share their B tiles in L2
+
+enum Act : int { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
+
+// act(g), and act'(g) where asked for.  Written so that large |g| give 0, 1 or
+// g, never an infinity times zero.
+template <bool GRAD>
+__device__ __forceinline__ float activate(float g, int act, float* grad) {
+    if (act == ACT_GELU) {
+        const float cdf = 0.5f * erfcf(-0.70710678118654752f * g);
+        if (GRAD) *grad = fmaf(g * expf(-0.5f * g * g), 0.3989422804014327f, cdf);
+        return g * cdf;
+    }
+    if (act == ACT_GELU_TANH) {
+        // (1 + tanh u) / 2 = sigmoid(2 u)
+        const float k2 = 1.5957691216057308f;
+        const float s = 1.0f / (1.0f + __expf(-k2 * g * fmaf(0.044715f * g, g, 1.0f)));
+        if (GRAD) {
+            const float c = fminf(fmaxf(g, -30.f), 30.f);
+            *grad = fmaf(c * s * (1.0f - s), k2 * fmaf(0.134145f * c, c, 1.0f), s);
+        }
+        return g * s;
+    }
+    const float s = 1.0f / (1.0f + __expf(-g));
+    if (GRAD) *grad = s * fmaf(g, 1.0f - s, 1.0f);
+    return g * s;
+}
+
+// One output matrix: rows x cols, row-major with pitch ld.
+struct GluOut {
+    void* p;
+    int64_t ld;
+};
+
+// One family of tiles: rows x cols outputs over kblocks k-blocks.
+struct GluTiles {
+    int rows, cols;             // of the output
+    int tiles_m, tiles_n;       // pairs of row blocks, column tiles
+    int seg_blocks, segs;       // k-blocks of one segment (one A and B map each), segments
+    int count;                  // tiles of one output
+};
+
+struct GluArgs {
+    int dtype;
+    int act;
+    int save;                   // forward: G and U leave too
+    int tma_out;                // outputs leave through tile stores
+    GluTiles a, b;              // forward: a; backward: a = dX, b = dWg and dWu
+    int nb;                     // tiles of family b (both outputs)
+    int extra;                  // tiles of b a cluster with one tile of a less takes first
+    GluOut out[3];              // H, G, U or dX, dWg, dWu
+    int* status;
+};
+
+struct GluMaps {
+    CUtensorMap a[2], b[2];     // family a: operands by segment (forward: b = Wg, Wu)
+    CUtensorMap a2[2], b2;      // family b: dG, dU read MN-major; X
+    CUtensorMap out[3];
+};
+
+struct Tile {
+    int family, which;          // 0: a, 1: b; output index
+    int tm, tn;
+};
+
+// j-th tile of cluster c.  Family a's tiles go round-robin, the clusters left
+// with one fewer then take `extra` of family b's, and the rest of family b goes
+// round-robin starting with those: with a's tiles the longer ones, every
+// cluster ends within one tile of b of the others.
+__device__ __forceinline__ bool tile_of(const GluArgs& g, int c, int P, int j, Tile& t) {
+    const int r = g.a.count % P, mine = g.a.count / P + (c < r ? 1 : 0);
+    int l;
+    if (j < mine) {
+        l = c + j * P;
+        t.family = 0;
+        t.which = 0;
+    } else {
+        j -= mine;
+        int id;
+        const int light = r ? P - r : 0, first = light * g.extra;
+        if (light && c >= r) {
+            id = j < g.extra ? (c - r) + j * light : first + (c - r) + (j - g.extra) * P;
+        } else {
+            id = first + (light ? light + c : c) + j * P;
+        }
+        if (id >= g.nb) return false;
+        t.family = 1;
+        t.which = 1 + id / g.b.count;
+        l = id % g.b.count;
+    }
+    const GluTiles& f = t.family ? g.b : g.a;
+    const int per = GROUP * f.tiles_n, grp = l / per, first = grp * GROUP;
+    const int size = min(GROUP, f.tiles_m - first);
+    l -= grp * per;
+    t.tm = first + l % size;
+    t.tn = l / size;
+    return true;
+}
+
+// One warp's 32 x 32 chunk (rows r0 + lane, columns c0 ..) of an output.
+__device__ __forceinline__ void store_chunk(const GluArgs& g, const CUtensorMap* map, const GluOut& o, int rows, int cols,
+                                            int r0, int c0, const float (&v)[32], uint8_t* stage, int& groups) {
+    const int lane = threadIdx.x & 31;
+    if (g.tma_out) {
+        if (groups >= 2) {              // the store that last used this buffer has read it
+            if (lane == 0) bulk_wait_read1();
+            __syncwarp();
+        }
+        uint8_t* buf = stage + (groups & 1) * OUT_BYTES;
+        // 64-byte swizzle: 16-byte piece k of row r at k ^ ((r / 2) % 4)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(buf + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) =
+                pack8_h(v + 8 * k, g.dtype == MUON_F16);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d(map, smem_u32(buf), c0, r0, 0);
+            bulk_commit();
+        }
+        ++groups;
+        return;
+    }
+    const int r = r0 + lane;
+    if (r >= rows) return;
+    const int64_t off = (int64_t)r * o.ld + c0;
+    if (c0 + 32 <= cols) {
+        store_row_run<32>(o.p, off, v, g.dtype);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (c0 + j < cols) st_elem(o.p, off + j, v[j], g.dtype);
+    }
+}
+
+template <bool FWD>
+__global__ void __launch_bounds__(GT, 1)
+glu_kernel(const __grid_constant__ GluMaps maps, const __grid_constant__ GluArgs g) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = smem + STAGES * OP_BYTES;
+    uint8_t* sOut = sB + STAGES * OP_BYTES;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + NEPI * 2 * OUT_BYTES);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBARS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, accf0 = empty0 + 8 * STAGES;
+    const uint32_t acce0 = accf0 + 16, drain_bar = acce0 + 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank();
+    const int c = (int)cluster_idx(), P = (int)cluster_count();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full0 + 8 * s, rank == 0 ? 2 : 1);    // own copies (even CTA: and the odd one's relay)
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(accf0 + 8 * i, 1);
+            mbar_init(acce0 + 8 * i, 2 * NEPI);
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc2(smem_u32(tmem_slot), 512);
+        tmem_relinquish2();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_trigger();
+
+    Tile t;
+    if (warp == 0) {
+        // ---------------- TMA producer ----------------
+        if (lane == 0) {
+            int issued[STAGES];
+#pragma unroll
+            for (int s = 0; s < STAGES; ++s) issued[s] = -1;
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int j = 0; ok && tile_of(g, c, P, j, t); ++j) {
+                const GluTiles& f = (!FWD && t.family) ? g.b : g.a;
+                const int m0 = t.tm * 2 * GM + rank * GM;
+                for (int seg = 0; seg < f.segs && ok; ++seg) {
+                    for (int kb = 0; kb < f.seg_blocks; ++kb) {
+                        if (!wait_bounded(empty0 + 8 * stage, phase ^ 1u, abort_flag, g.status)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t fb = full0 + 8 * stage;
+                        const uint32_t a = smem_u32(sA + stage * OP_BYTES), b = smem_u32(sB + stage * OP_BYTES);
+                        const int k0 = kb * GK;
+                        mbar_expect_tx(fb, STAGE_BYTES);
+                        if (FWD) {
+                            tma_load_3d(a, &maps.a[0], fb, k0, m0, 0);
+                            tma_load_3d(b, &maps.b[rank], fb, k0, t.tn * GM, 0);    // 128 rows of Wg or of Wu
+                        } else {
+                            const int n0 = t.tn * 2 * GM + rank * GM;
+                            if (t.family == 0) {
+                                tma_load_3d(a, &maps.a[seg], fb, k0, m0, 0);
+                            } else {
+                                tma_load_3d(a, &maps.a2[t.which - 1], fb, m0, k0, 0);
+                                tma_load_3d(a + OP_BYTES / 2, &maps.a2[t.which - 1], fb, m0 + 64, k0, 0);
+                            }
+                            const CUtensorMap* mb = t.family == 0 ? &maps.b[seg] : &maps.b2;
+                            tma_load_3d(b, mb, fb, n0, k0, 0);
+                            tma_load_3d(b + OP_BYTES / 2, mb, fb, n0 + 64, k0, 0);
+                        }
+                        issued[stage] = (int)phase;
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+            }
+            // this CTA's copies still in flight (after an abort nobody consumes them)
+#pragma unroll
+            for (int s = 0; s < STAGES; ++s)
+                if (issued[s] >= 0) wait_drain(full0 + 8 * s, (uint32_t)issued[s]);
+        }
+        __syncwarp();
+    } else if (warp == 1 && rank == 1) {
+        // ---------------- relay: the odd CTA's filled stages to the even CTA ----------------
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int j = 0; ok && tile_of(g, c, P, j, t); ++j) {
+                const GluTiles& f = (!FWD && t.family) ? g.b : g.a;
+                for (int kb = 0; kb < f.segs * f.seg_blocks; ++kb) {
+                    if (!wait_bounded(full0 + 8 * stage, phase, abort_flag, g.status)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_remote_relaxed(full0 + 8 * stage, 0);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------- MMA issuer (even CTA) ----------------
+        if (lane == 0) {
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, aphase = 0;
+            bool ok = true;
+            for (int j = 0; ok && tile_of(g, c, P, j, t); ++j) {
+                const bool fam_b = !FWD && t.family;
+                const GluTiles& f = fam_b ? g.b : g.a;
+                const uint32_t idesc =
+                    idesc_f16kind(2 * GM, 256, !FWD, g.dtype == MUON_F16) | (fam_b ? (1u << 15) : 0u);
+                if (!wait_bounded(acce0 + 8 * acc, aphase ^ 1u, abort_flag, g.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(acc * 256);
+                for (int kb = 0; kb < f.segs * f.seg_blocks; ++kb) {
+                    if (!wait_bounded(full0 + 8 * stage, phase, abort_flag, g.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = smem_u32(sA + stage * OP_BYTES), b = smem_u32(sB + stage * OP_BYTES);
+#pragma unroll
+                    for (int kk = 0; kk < GK / 16; ++kk) {
+                        const uint64_t ad = fam_b ? sdesc(a + kk * 2048, GK * 128, 1024) : sdesc(a + kk * 32, 16, 1024);
+                        const uint64_t bd = FWD ? sdesc(b + kk * 32, 16, 1024) : sdesc(b + kk * 2048, GK * 128, 1024);
+                        tc_mma2_bf16(d, ad, bd, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    tc_commit2(empty0 + 8 * stage, (uint16_t)0x3);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                tc_commit2(accf0 + 8 * acc, (uint16_t)0x3);
+                acc ^= 1;
+                if (acc == 0) aphase ^= 1u;
+            }
+            if (!ok) {
+                tc_commit2(drain_bar, (uint16_t)0x1);
+                wait_drain(drain_bar, 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------- epilogue (warps 2..9) ----------------
+        const int q = warp & 3, half = (warp - 2) / 4;
+        uint8_t* stage = sOut + (warp - 2) * 2 * OUT_BYTES;
+        int groups = 0, acc = 0;
+        uint32_t aphase = 0;
+        for (int j = 0; tile_of(g, c, P, j, t); ++j) {
+            const GluTiles& f = (!FWD && t.family) ? g.b : g.a;
+            const int r0 = t.tm * 2 * GM + rank * GM + q * 32;
+            const bool ok = wait_bounded(accf0 + 8 * acc, aphase, abort_flag, g.status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
+            if (FWD) {
+#pragma unroll 1
+                for (int ch = 2 * half; ch < 2 * half + 2; ++ch) {
+                    const int c0 = t.tn * GM + ch * 32;
+                    if (c0 >= f.cols || r0 >= f.rows) break;
+                    float gv[32], uv[32];
+                    tmem_ld32(lanes + (uint32_t)(ch * 32), gv);
+                    tmem_ld32(lanes + (uint32_t)(GM + ch * 32), uv);
+                    if (g.save) {
+                        store_chunk(g, &maps.out[1], g.out[1], f.rows, f.cols, r0, c0, gv, stage, groups);
+                        store_chunk(g, &maps.out[2], g.out[2], f.rows, f.cols, r0, c0, uv, stage, groups);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) uv[k] *= activate<false>(gv[k], g.act, nullptr);
+                    store_chunk(g, &maps.out[0], g.out[0], f.rows, f.cols, r0, c0, uv, stage, groups);
+                }
+            } else {
+#pragma unroll 1
+                for (int ch = 4 * half; ch < 4 * half + 4; ++ch) {
+                    const int c0 = t.tn * 2 * GM + ch * 32;
+                    if (c0 >= f.cols || r0 >= f.rows) break;
+                    float v[32];
+                    tmem_ld32(lanes + (uint32_t)(ch * 32), v);
+                    store_chunk(g, &maps.out[t.which], g.out[t.which], f.rows, f.cols, r0, c0, v, stage, groups);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (rank == 1) mbar_arrive_remote(acce0 + 8 * acc, 0);
+                else mbar_arrive(acce0 + 8 * acc);
+            }
+            acc ^= 1;
+            if (acc == 0) aphase ^= 1u;
+        }
+        if (groups > 0 && lane == 0) bulk_wait0();
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc2(tmem, 512);
+    }
+}
+
+// dG = dH U act'(G) and dU = dH act(G), rows of `ffn` elements at pitch ldw.
+// Bound by HBM: three matrices read, two written.
+struct GluGradArgs {
+    const void* dh;
+    const void* gate;
+    const void* up;
+    void* dg;
+    void* du;
+    int64_t rows, ffn, ldw;
+    int dtype, act;
+    int vec;                    // 8-element accesses (ffn a multiple of 8, everything 16-byte aligned)
+};
+
+__global__ void __launch_bounds__(256) glu_grad_kernel(const __grid_constant__ GluGradArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t step = (int64_t)gridDim.x * 256;
+    if (a.vec) {
+        const int64_t n = a.rows * (a.ffn / 8);
+        const bool f16 = a.dtype == MUON_F16;
+        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+            // ldw == ffn: the vector path is dense on both sides
+            float d[8], g[8], u[8];
+            unpack8_h(reinterpret_cast<const uint4*>(a.dh)[i], d, f16);
+            unpack8_h(reinterpret_cast<const uint4*>(a.gate)[i], g, f16);
+            unpack8_h(reinterpret_cast<const uint4*>(a.up)[i], u, f16);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float s;
+                const float act = activate<true>(g[k], a.act, &s);
+                g[k] = d[k] * u[k] * s;
+                u[k] = d[k] * act;
+            }
+            reinterpret_cast<uint4*>(a.dg)[i] = pack8_h(g, f16);
+            reinterpret_cast<uint4*>(a.du)[i] = pack8_h(u, f16);
+        }
+        return;
+    }
+    const int64_t n = a.rows * a.ffn;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+        const int64_t r = i / a.ffn, o = r * a.ldw + (i - r * a.ffn);
+        const float d = ld_elem(a.dh, i, a.dtype), u = ld_elem(a.up, i, a.dtype);
+        float s;
+        const float act = activate<true>(ld_elem(a.gate, i, a.dtype), a.act, &s);
+        st_elem(a.dg, o, d * u * s, a.dtype);
+        st_elem(a.du, o, d * act, a.dtype);
+    }
+}
+
+// Rows of `cols` 16-bit elements to a pitch the copy engine can address.
+__global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* src, uint16_t* dst, int64_t rows, int64_t cols,
+                                                       int64_t ld) {
+    pdl_wait();
+    pdl_trigger();
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (int64_t c = threadIdx.x; c < cols; c += 256) dst[r * ld + c] = src[r * cols + c];
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+constexpr int64_t MAX_SIDE = 1 << 20;
+constexpr int64_t MAX_TOKENS = 1 << 24;
+
+struct Operand {
+    const void* p;
+    int64_t rows, cols, ld;
+};
+
+bool tma_ok(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0; }
+
+// A caller's matrix as the copy engine can read it: itself, or (rows that do not
+// start on 16 bytes) a padded copy at `at` in the workspace.
+size_t padded_bytes(const Operand& o) {
+    return tma_ok(o.p, o.ld) ? 0 : align_up((size_t)o.rows * pad8(o.cols) * 2, 256);
+}
+int pad_operand(Operand& o, char*& at, int sms, cudaStream_t s) {
+    const size_t b = padded_bytes(o);
+    if (!b) return MUON_OK;
+    const int64_t ld = pad8(o.cols);
+    note_launch_begin(KC_OTHER, s);
+    cudaError_t e = launch_pdl(pad_rows_kernel, dim3((unsigned)std::min<int64_t>(o.rows, (int64_t)sms * 8)), dim3(256), 0, s,
+                               static_cast<const uint16_t*>(o.p), reinterpret_cast<uint16_t*>(at), o.rows, o.cols, ld);
+    note_launch_end(KC_OTHER, 0.0, s);
+    if (e != cudaSuccess) return cuda_fail(e, "operand copy launch");
+    o.p = at;
+    o.ld = ld;
+    at += b;
+    return MUON_OK;
+}
+
+bool map_in(CUtensorMap* m, const Operand& o, int dtype, uint32_t box_cols, uint32_t box_rows) {
+    return make_map(m, o.p, dtype, (uint64_t)o.cols, (uint64_t)o.rows, 1, (uint64_t)o.ld, 0, box_cols, box_rows);
+}
+
+// 32 x 32 chunks in 64-byte swizzled rows.
+bool map_out(CUtensorMap* m, const GluOut& o, int dtype, int64_t rows, int64_t cols) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 1};
+    cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2, (cuuint64_t)o.ld * 2 * (cuuint64_t)rows};
+    cuuint32_t box[3] = {32, 32, 1}, elem[3] = {1, 1, 1};
+    return fn(m, dtype == MUON_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, o.p, dims,
+              strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+GluTiles tiles(int64_t rows, int64_t cols, int64_t tile_cols, int64_t k, int segs) {
+    GluTiles t;
+    t.rows = (int)rows;
+    t.cols = (int)cols;
+    t.tiles_m = (int)((rows + 2 * GM - 1) / (2 * GM));
+    t.tiles_n = (int)((cols + tile_cols - 1) / tile_cols);
+    t.seg_blocks = (int)((k + GK - 1) / GK);
+    t.segs = segs;
+    t.count = t.tiles_m * t.tiles_n;
+    return t;
+}
+
+template <bool FWD>
+cudaError_t launch_glu(GluMaps& maps, GluArgs& g, cudaStream_t s) {
+    auto kern = glu_kernel<FWD>;
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    static int most = 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(GT);
+    cfg.dynamicSmemBytes = GLU_SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    std::call_once(once, [&] {
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GLU_SMEM);
+        if (err != cudaSuccess) return;
+        cfg.gridDim = dim3(2);
+        err = cudaOccupancyMaxActiveClusters(&most, kern, &cfg);
+        if (err == cudaSuccess && most < 1) err = cudaErrorInvalidConfiguration;
+    });
+    if (err != cudaSuccess) return err;
+    const int P = (int)std::min<int64_t>(most, (int64_t)g.a.count + g.nb);
+    const int r = g.a.count % P;
+    g.extra = 0;
+    if (r && g.nb) {
+        const int ka = g.a.segs * g.a.seg_blocks, kb = g.b.segs * g.b.seg_blocks;
+        g.extra = std::min(g.nb / (P - r), (ka + kb / 2) / kb);
+    }
+    cfg.gridDim = dim3((unsigned)(2 * P));
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, maps, g);
+}
+
+int glu_check(int64_t tokens, int64_t hidden, int64_t ffn, int dtype, int act) {
+    if (!is_half(dtype)) return fail(MUON_EDTYPE, "dtype %d: MUON_BF16 or MUON_F16", dtype);
+    if (act < ACT_SILU || act > ACT_GELU_TANH) return fail(MUON_EINVAL, "activation %d", act);
+    if (tokens < 0 || tokens > MAX_TOKENS) return fail(MUON_EINVAL, "tokens outside [0, 2^24]");
+    if (hidden < 1 || hidden > MAX_SIDE || ffn < 1 || ffn > MAX_SIDE)
+        return fail(MUON_EINVAL, "hidden and ffn outside [1, 2^20]");
+    return MUON_OK;
+}
+
+}  // namespace
+
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" int muon_glu_forward(const void* x, const void* w_gate, const void* w_up, void* h, void* gate, void* up,
+                                int64_t tokens, int64_t hidden, int64_t ffn, int dtype, int act, void* stream) try {
+    int r = glu_check(tokens, hidden, ffn, dtype, act);
+    if (r) return r;
+    if ((gate == nullptr) != (up == nullptr)) return fail(MUON_EINVAL, "gate and up: both or neither");
+    if (tokens == 0) return MUON_OK;
+    if (!x || !w_gate || !w_up || !h) return fail(MUON_EINVAL, "NULL argument");
+    for (const void* p : {x, w_gate, w_up, (const void*)h, (const void*)gate, (const void*)up})
+        if (reinterpret_cast<uintptr_t>(p) & 1) return fail(MUON_EINVAL, "pointer not aligned to its element");
+    DevCtx dc;
+    if ((r = get_dev(dc))) return r;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    Operand X{x, tokens, hidden, hidden}, G{w_gate, ffn, hidden, hidden}, U{w_up, ffn, hidden, hidden};
+    if (const size_t need = padded_bytes(X) + padded_bytes(G) + padded_bytes(U)) {
+        Workspace* w = nullptr;
+        if ((r = ws_get(dc.device, s, need, &w))) return r;
+        char* at = w->base;
+        for (Operand* o : {&X, &G, &U})
+            if ((r = pad_operand(*o, at, dc.sms, s))) return r;
+    }
+    GluArgs g;
+    GluMaps maps;
+    std::memset(&g, 0, sizeof g);
+    std::memset(&maps, 0, sizeof maps);
+    g.dtype = dtype; g.act = act; g.save = gate != nullptr;
+    g.a = tiles(tokens, ffn, GM, hidden, 1);
+    g.b = g.a;
+    g.status = dc.status;
+    g.out[0] = GluOut{h, ffn}; g.out[1] = GluOut{gate, ffn}; g.out[2] = GluOut{up, ffn};
+    g.tma_out = tma_ok(h, ffn) && tma_ok(gate, ffn) && tma_ok(up, ffn);
+    bool ok = map_in(&maps.a[0], X, dtype, GK, GM) && map_in(&maps.b[0], G, dtype, GK, GM) &&
+              map_in(&maps.b[1], U, dtype, GK, GM);
+    for (int i = 0; ok && g.tma_out && i < (g.save ? 3 : 1); ++i) ok = map_out(&maps.out[i], g.out[i], dtype, tokens, ffn);
+    if (!ok) return fail(MUON_ECUDA, "tensor map creation failed");
+    note_launch_begin(KC_GLU, s);
+    cudaError_t e = launch_glu<true>(maps, g, s);
+    note_launch_end(KC_GLU, 4.0 * (double)tokens * hidden * ffn, s);
+    if (e != cudaSuccess) return cuda_fail(e, "glu forward launch");
+    return MUON_OK;
+} MUON_CATCH_ALL
+
+extern "C" int muon_glu_backward(const void* x, const void* w_gate, const void* w_up, const void* gate, const void* up,
+                                 const void* dh, void* dx, void* dw_gate, void* dw_up, int64_t tokens, int64_t hidden,
+                                 int64_t ffn, int dtype, int act, void* stream) try {
+    int r = glu_check(tokens, hidden, ffn, dtype, act);
+    if (r) return r;
+    if ((dw_gate == nullptr) != (dw_up == nullptr)) return fail(MUON_EINVAL, "dw_gate and dw_up: both or neither");
+    if (!dx && !dw_gate) return MUON_OK;
+    if (tokens > 0 && (!x || !w_gate || !w_up || !gate || !up || !dh)) return fail(MUON_EINVAL, "NULL argument");
+    for (const void* p : {x, w_gate, w_up, gate, up, dh, (const void*)dx, (const void*)dw_gate, (const void*)dw_up})
+        if (reinterpret_cast<uintptr_t>(p) & 1) return fail(MUON_EINVAL, "pointer not aligned to its element");
+    DevCtx dc;
+    if ((r = get_dev(dc))) return r;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (tokens == 0) {                      // no token: the weights' gradients are zero
+        if (dw_gate) {
+            MUON_CUDA(cudaMemsetAsync(dw_gate, 0, (size_t)(ffn * hidden) * 2, s));
+            MUON_CUDA(cudaMemsetAsync(dw_up, 0, (size_t)(ffn * hidden) * 2, s));
+        }
+        return MUON_OK;
+    }
+    Operand X{x, tokens, hidden, hidden}, G{w_gate, ffn, hidden, hidden}, U{w_up, ffn, hidden, hidden};
+    const int64_t ldw = pad8(ffn);
+    const size_t half = align_up((size_t)tokens * ldw * 2, 256);
+    Workspace* w = nullptr;
+    if ((r = ws_get(dc.device, s, 2 * half + padded_bytes(X) + padded_bytes(G) + padded_bytes(U), &w))) return r;
+    char* at = w->base + 2 * half;
+    for (Operand* o : {&X, &G, &U})
+        if ((r = pad_operand(*o, at, dc.sms, s))) return r;
+    GluGradArgs ga;
+    ga.dh = dh; ga.gate = gate; ga.up = up;
+    ga.dg = w->base; ga.du = w->base + half;
+    ga.rows = tokens; ga.ffn = ffn; ga.ldw = ldw;
+    ga.dtype = dtype; ga.act = act;
+    ga.vec = tma_ok(dh, ffn) && tma_ok(gate, ffn) && tma_ok(up, ffn);
+    const int64_t work = ga.vec ? tokens * (ffn / 8) : tokens * ffn;
+    note_launch_begin(KC_GLU, s);
+    cudaError_t e = launch_pdl(glu_grad_kernel, dim3((unsigned)std::min<int64_t>((work + 255) / 256, (int64_t)dc.sms * 8)),
+                               dim3(256), 0, s, ga);
+    note_launch_end(KC_GLU, 0.0, s);
+    if (e != cudaSuccess) return cuda_fail(e, "glu gradient launch");
+    const Operand DG{ga.dg, tokens, ffn, ldw}, DU{ga.du, tokens, ffn, ldw};
+    GluArgs g;
+    GluMaps maps;
+    std::memset(&g, 0, sizeof g);
+    std::memset(&maps, 0, sizeof maps);
+    g.dtype = dtype; g.act = act;
+    g.status = dc.status;
+    g.a = tiles(tokens, hidden, 2 * GM, ffn, 2);
+    if (!dx) g.a.count = 0;
+    g.b = tiles(ffn, hidden, 2 * GM, tokens, 1);
+    g.nb = dw_gate ? 2 * g.b.count : 0;
+    g.out[0] = GluOut{dx, hidden}; g.out[1] = GluOut{dw_gate, hidden}; g.out[2] = GluOut{dw_up, hidden};
+    g.tma_out = tma_ok(dx, hidden) && tma_ok(dw_gate, hidden) && tma_ok(dw_up, hidden);
+    bool ok = map_in(&maps.a[0], DG, dtype, GK, GM) && map_in(&maps.a[1], DU, dtype, GK, GM) &&
+              map_in(&maps.b[0], G, dtype, 64, GK) && map_in(&maps.b[1], U, dtype, 64, GK) &&
+              map_in(&maps.a2[0], DG, dtype, 64, GK) && map_in(&maps.a2[1], DU, dtype, 64, GK) &&
+              map_in(&maps.b2, X, dtype, 64, GK);
+    if (ok && g.tma_out && dx) ok = map_out(&maps.out[0], g.out[0], dtype, tokens, hidden);
+    if (ok && g.tma_out && dw_gate)
+        ok = map_out(&maps.out[1], g.out[1], dtype, ffn, hidden) && map_out(&maps.out[2], g.out[2], dtype, ffn, hidden);
+    if (!ok) return fail(MUON_ECUDA, "tensor map creation failed");
+    note_launch_begin(KC_GLU, s);
+    e = launch_glu<false>(maps, g, s);
+    note_launch_end(KC_GLU, (dx ? 4.0 : 0.0) * tokens * (double)hidden * ffn + (dw_gate ? 4.0 : 0.0) * tokens * (double)hidden * ffn, s);
+    if (e != cudaSuccess) return cuda_fail(e, "glu backward launch");
+    return MUON_OK;
+} MUON_CATCH_ALL

@@ -1,6 +1,6 @@
 // Host-side declarations shared by the library's host translation units
 // (runtime.cu, ns.cu, plan.cu, group.cu, noalloc.cu, owner.cu, adamw.cu,
-// losses.cu):
+// losses.cu, glu.cu):
 // logging and status helpers, per-device state, the workspace, the NS plan
 // and its orchestration, and the tuned per-shape plans.
 #pragma once

@@ -256,7 +256,7 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 enum KernelClass : int {
     KC_PREP = 0, KC_NORM = 1 /* no longer launched: prep finalises */, KC_SYRK = 2, KC_SQUARE = 3, KC_APPLY = 4,
     KC_APPLY_UPDATE = 5, KC_SIMT = 6, KC_OTHER = 7, KC_SMALL = 8, KC_ADAMW = 9, KC_PACK = 10,
-    KC_LOSS = 11, KC_COUNT = 12
+    KC_LOSS = 11, KC_GLU = 12, KC_COUNT = 13
 };
 void note_launch_begin(int kclass, cudaStream_t s);
 void note_launch_end(int kclass, double work, cudaStream_t s);

@@ -195,7 +195,7 @@ static thread_local int t_open = -1;   // index of the launch being recorded
 static const char* kclass_name(int k) {
     static const char* names[KC_COUNT] = {"prep_momentum_norm", "norm_finalize", "gemm_tc_syrk",
                                           "gemm_tc_square", "gemm_tc_apply", "gemm_tc_apply_update",
-                                          "gemm_fp32", "other", "small_ns_fused", "adamw", "pack", "vocab_loss"};
+                                          "gemm_fp32", "other", "small_ns_fused", "adamw", "pack", "vocab_loss", "glu"};
     return (k >= 0 && k < KC_COUNT) ? names[k] : "other";
 }
 
