@@ -348,8 +348,7 @@ int muon_pack(void* const* mats, const int64_t* ms, const int64_t* ns, const int
  *   logits     rows x vocab logits on the device, row pitch ld >= vocab elements
  *              (dtype MUON_F32, MUON_BF16 or MUON_F16; any alignment of the
  *              element; rows whose pitch and base differ from `grad`'s by
- *              multiples of 16 bytes take vector stores).  vocab in [1, 425984]
- *              (an fp32 row rests in the shared memory of 16 CTAs at most).
+ *              multiples of 16 bytes take vector stores).  vocab in [1, 2^19].
  *   grad       receives d(sum of loss)/d(logits), same type, row pitch ld_grad;
  *              may be the logits themselves (ld_grad == ld), else the two must
  *              not overlap.  Columns beyond vocab are neither read nor written.

@@ -81,7 +81,8 @@ struct GluTiles {
     int rows, cols;             // of the output
     int tiles_m, tiles_n;       // pairs of row blocks, column tiles
     int seg_blocks, segs;       // k-blocks of one segment (one A and B map each), segments
-    int count;                  // tiles of one output
+    int count;                  // units of one output: tiles, times splits
+    int splits;                 // parts the k-blocks are cut into (family a only)
 };
 
 struct GluArgs {
@@ -93,6 +94,8 @@ struct GluArgs {
     int nb;                     // tiles of family b (both outputs)
     int extra;                  // tiles of b a cluster with one tile of a less takes first
     GluOut out[3];              // H, G, U or dX, dWg, dWu
+    float* part;                // dX in splits > 1 parts: [splits][rows][ldp] partial sums
+    int64_t ldp;
     int* status;
 };
 
@@ -105,6 +108,7 @@ struct GluMaps {
 struct Tile {
     int family, which;          // 0: a, 1: b; output index
     int tm, tn;
+    int split, kb0, kb1;        // its k-blocks
 };
 
 // j-th tile of cluster c.  Family a's tiles go round-robin, the clusters left
@@ -133,6 +137,11 @@ __device__ __forceinline__ bool tile_of(const GluArgs& g, int c, int P, int j, T
         l = id % g.b.count;
     }
     const GluTiles& f = t.family ? g.b : g.a;
+    const int all = f.tiles_m * f.tiles_n, blocks = f.segs * f.seg_blocks;
+    t.split = l / all;
+    l -= t.split * all;
+    t.kb0 = (int)((int64_t)blocks * t.split / f.splits);
+    t.kb1 = (int)((int64_t)blocks * (t.split + 1) / f.splits);
     const int per = GROUP * f.tiles_n, grp = l / per, first = grp * GROUP;
     const int size = min(GROUP, f.tiles_m - first);
     l -= grp * per;
@@ -165,15 +174,20 @@ __device__ __forceinline__ void store_chunk(const GluArgs& g, const CUtensorMap*
         ++groups;
         return;
     }
-    const int r = r0 + lane;
-    if (r >= rows) return;
-    const int64_t off = (int64_t)r * o.ld + c0;
-    if (c0 + 32 <= cols) {
-        store_row_run<32>(o.p, off, v, g.dtype);
-    } else {
+    // rows that do not start on 16 bytes: through the same buffer, a row's 32 columns per store
+    uint8_t* buf = stage;
+    __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (c0 + j < cols) st_elem(o.p, off + j, v[j], g.dtype);
+    for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint4*>(buf + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = pack8_h(v + 8 * k, g.dtype == MUON_F16);
+    __syncwarp();
+    if (c0 + lane < cols) {
+        uint16_t* p = static_cast<uint16_t*>(o.p) + (int64_t)r0 * o.ld + c0 + lane;
+        const int n = min(32, rows - r0);
+#pragma unroll 8
+        for (int i = 0; i < n; ++i)
+            p[(int64_t)i * o.ld] = *reinterpret_cast<const uint16_t*>(
+                buf + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + (lane & 7) * 2);
     }
 }
 
@@ -232,36 +246,35 @@ glu_kernel(const __grid_constant__ GluMaps maps, const __grid_constant__ GluArgs
             for (int j = 0; ok && tile_of(g, c, P, j, t); ++j) {
                 const GluTiles& f = (!FWD && t.family) ? g.b : g.a;
                 const int m0 = t.tm * 2 * GM + rank * GM;
-                for (int seg = 0; seg < f.segs && ok; ++seg) {
-                    for (int kb = 0; kb < f.seg_blocks; ++kb) {
-                        if (!wait_bounded(empty0 + 8 * stage, phase ^ 1u, abort_flag, g.status)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t fb = full0 + 8 * stage;
-                        const uint32_t a = smem_u32(sA + stage * OP_BYTES), b = smem_u32(sB + stage * OP_BYTES);
-                        const int k0 = kb * GK;
-                        mbar_expect_tx(fb, STAGE_BYTES);
-                        if (FWD) {
-                            tma_load_3d(a, &maps.a[0], fb, k0, m0, 0);
-                            tma_load_3d(b, &maps.b[rank], fb, k0, t.tn * GM, 0);    // 128 rows of Wg or of Wu
+                for (int kb = t.kb0; kb < t.kb1; ++kb) {
+                    if (!wait_bounded(empty0 + 8 * stage, phase ^ 1u, abort_flag, g.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = full0 + 8 * stage;
+                    const uint32_t a = smem_u32(sA + stage * OP_BYTES), b = smem_u32(sB + stage * OP_BYTES);
+                    const int seg = kb >= f.seg_blocks ? 1 : 0;
+                    const int k0 = (kb - seg * f.seg_blocks) * GK;
+                    mbar_expect_tx(fb, STAGE_BYTES);
+                    if (FWD) {
+                        tma_load_3d(a, &maps.a[0], fb, k0, m0, 0);
+                        tma_load_3d(b, &maps.b[rank], fb, k0, t.tn * GM, 0);    // 128 rows of Wg or of Wu
+                    } else {
+                        const int n0 = t.tn * 2 * GM + rank * GM;
+                        if (t.family == 0) {
+                            tma_load_3d(a, &maps.a[seg], fb, k0, m0, 0);
                         } else {
-                            const int n0 = t.tn * 2 * GM + rank * GM;
-                            if (t.family == 0) {
-                                tma_load_3d(a, &maps.a[seg], fb, k0, m0, 0);
-                            } else {
-                                tma_load_3d(a, &maps.a2[t.which - 1], fb, m0, k0, 0);
-                                tma_load_3d(a + OP_BYTES / 2, &maps.a2[t.which - 1], fb, m0 + 64, k0, 0);
-                            }
-                            const CUtensorMap* mb = t.family == 0 ? &maps.b[seg] : &maps.b2;
-                            tma_load_3d(b, mb, fb, n0, k0, 0);
-                            tma_load_3d(b + OP_BYTES / 2, mb, fb, n0 + 64, k0, 0);
+                            tma_load_3d(a, &maps.a2[t.which - 1], fb, m0, k0, 0);
+                            tma_load_3d(a + OP_BYTES / 2, &maps.a2[t.which - 1], fb, m0 + 64, k0, 0);
                         }
-                        issued[stage] = (int)phase;
-                        if (++stage == STAGES) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
+                        const CUtensorMap* mb = t.family == 0 ? &maps.b[seg] : &maps.b2;
+                        tma_load_3d(b, mb, fb, n0, k0, 0);
+                        tma_load_3d(b + OP_BYTES / 2, mb, fb, n0 + 64, k0, 0);
+                    }
+                    issued[stage] = (int)phase;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
                     }
                 }
             }
@@ -278,8 +291,7 @@ glu_kernel(const __grid_constant__ GluMaps maps, const __grid_constant__ GluArgs
             uint32_t phase = 0;
             bool ok = true;
             for (int j = 0; ok && tile_of(g, c, P, j, t); ++j) {
-                const GluTiles& f = (!FWD && t.family) ? g.b : g.a;
-                for (int kb = 0; kb < f.segs * f.seg_blocks; ++kb) {
+                for (int kb = t.kb0; kb < t.kb1; ++kb) {
                     if (!wait_bounded(full0 + 8 * stage, phase, abort_flag, g.status)) {
                         ok = false;
                         break;
@@ -301,7 +313,6 @@ glu_kernel(const __grid_constant__ GluMaps maps, const __grid_constant__ GluArgs
             bool ok = true;
             for (int j = 0; ok && tile_of(g, c, P, j, t); ++j) {
                 const bool fam_b = !FWD && t.family;
-                const GluTiles& f = fam_b ? g.b : g.a;
                 const uint32_t idesc =
                     idesc_f16kind(2 * GM, 256, !FWD, g.dtype == MUON_F16) | (fam_b ? (1u << 15) : 0u);
                 if (!wait_bounded(acce0 + 8 * acc, aphase ^ 1u, abort_flag, g.status)) {
@@ -310,7 +321,7 @@ glu_kernel(const __grid_constant__ GluMaps maps, const __grid_constant__ GluArgs
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(acc * 256);
-                for (int kb = 0; kb < f.segs * f.seg_blocks; ++kb) {
+                for (int kb = t.kb0; kb < t.kb1; ++kb) {
                     if (!wait_bounded(full0 + 8 * stage, phase, abort_flag, g.status)) {
                         ok = false;
                         break;
@@ -321,7 +332,7 @@ glu_kernel(const __grid_constant__ GluMaps maps, const __grid_constant__ GluArgs
                     for (int kk = 0; kk < GK / 16; ++kk) {
                         const uint64_t ad = fam_b ? sdesc(a + kk * 2048, GK * 128, 1024) : sdesc(a + kk * 32, 16, 1024);
                         const uint64_t bd = FWD ? sdesc(b + kk * 32, 16, 1024) : sdesc(b + kk * 2048, GK * 128, 1024);
-                        tc_mma2_bf16(d, ad, bd, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                        tc_mma2_bf16(d, ad, bd, idesc, (kb > t.kb0 || kk > 0) ? 1u : 0u);
                     }
                     tc_commit2(empty0 + 8 * stage, (uint16_t)0x3);
                     if (++stage == STAGES) {
@@ -376,6 +387,11 @@ glu_kernel(const __grid_constant__ GluMaps maps, const __grid_constant__ GluArgs
                     if (c0 >= f.cols || r0 >= f.rows) break;
                     float v[32];
                     tmem_ld32(lanes + (uint32_t)(ch * 32), v);
+                    if (t.family == 0 && f.splits > 1) {
+                        if (r0 + lane < f.rows)     // ldp is a multiple of 32
+                            store_row_run<32>(g.part, ((int64_t)t.split * f.rows + r0 + lane) * g.ldp + c0, v, MUON_F32);
+                        continue;
+                    }
                     store_chunk(g, &maps.out[t.which], g.out[t.which], f.rows, f.cols, r0, c0, v, stage, groups);
                 }
             }
@@ -400,62 +416,296 @@ glu_kernel(const __grid_constant__ GluMaps maps, const __grid_constant__ GluArgs
     }
 }
 
-// dG = dH U act'(G) and dU = dH act(G), rows of `ffn` elements at pitch ldw.
-// Bound by HBM: three matrices read, two written.
+// ---------------------------------------------------------------------------
+// forward for few tokens: the weights are the rows of the products
+// ---------------------------------------------------------------------------
+//
+// With at most FEW_TOKENS tokens the call is a reading of both weights, so they
+// take the M side: a tile is R rows of Wg (accumulator lanes 0 .. R-1) and the
+// same R rows of Wu (lanes 64 ..), the tokens are the N columns (16 .. 128), and
+// up to FEW_STAGES stages of the ring keep the copies of one CTA per SM running.
+// R divides the ffn rows evenly over the SMs: the smallest number of rows per
+// SM over R = 8, 16, ..., 64 (14336 rows on 152 SMs: R = 48, two tiles each).
+// G and U of one ffn row sit in different lanes; U goes through shared memory.
+constexpr int FEW_TOKENS = 128;
+constexpr int FEW_STAGES = 12;
+constexpr int FEW_EPI = 4;
+constexpr int FEW_T = 64 + 32 * FEW_EPI;
+constexpr int FEW_BARS = 2 * FEW_STAGES + 5;
+constexpr int FEW_FIXED = 64 * 33 * 4 + FEW_BARS * 8 + 16 + 1024;
+
+struct FewArgs {
+    int dtype, act, save;
+    int tokens, ffn, kblocks;
+    int n;                      // tokens rounded up to 16
+    int R, tiles, stages;
+    GluOut out[3];              // H, G, U
+    int* status;
+};
+
+__global__ void __launch_bounds__(FEW_T, 1)
+glu_few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg,
+               const __grid_constant__ CUtensorMap mu, const __grid_constant__ FewArgs g) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int stage_bytes = OP_BYTES + g.n * 128, S = g.stages;
+    float(*up)[33] = reinterpret_cast<float(*)[33]>(smem + S * stage_bytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * stage_bytes + 64 * 33 * 4);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + FEW_BARS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * FEW_STAGES, accf0 = empty0 + 8 * FEW_STAGES;
+    const uint32_t acce0 = accf0 + 16, drain_bar = acce0 + 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(accf0 + 8 * i, 1);
+            mbar_init(acce0 + 8 * i, FEW_EPI);
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), 256);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_trigger();
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint32_t bytes = (uint32_t)(2 * g.R * 128 + g.n * 128);
+            uint32_t flight = 0, phases = 0;        // per stage: a copy was issued, and its phase
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < g.tiles && ok; t += gridDim.x) {
+                for (int kb = 0; kb < g.kblocks; ++kb) {
+                    if (!wait_bounded(empty0 + 8 * stage, phase ^ 1u, abort_flag, g.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = full0 + 8 * stage, a = smem_u32(smem + stage * stage_bytes);
+                    mbar_expect_tx(fb, bytes);
+                    tma_load_3d(a, &mg, fb, kb * GK, t * g.R, 0);
+                    tma_load_3d(a + OP_BYTES / 2, &mu, fb, kb * GK, t * g.R, 0);
+                    tma_load_3d(a + OP_BYTES, &mx, fb, kb * GK, 0, 0);
+                    flight |= 1u << stage;
+                    phases = (phases & ~(1u << stage)) | (phase << stage);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            for (int s = 0; s < S; ++s)
+                if ((flight >> s) & 1) wait_drain(full0 + 8 * s, (phases >> s) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_f16kind(GM, g.n, false, g.dtype == MUON_F16);
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, aphase = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < g.tiles && ok; t += gridDim.x) {
+                if (!wait_bounded(acce0 + 8 * acc, aphase ^ 1u, abort_flag, g.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                for (int kb = 0; kb < g.kblocks; ++kb) {
+                    if (!wait_bounded(full0 + 8 * stage, phase, abort_flag, g.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = smem_u32(smem + stage * stage_bytes), b = a + OP_BYTES;
+#pragma unroll
+                    for (int kk = 0; kk < GK / 16; ++kk)
+                        tc_mma_bf16(tmem + (uint32_t)(acc * FEW_TOKENS), sdesc(a + kk * 32, 16, 1024),
+                                    sdesc(b + kk * 32, 16, 1024), idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                    tc_commit(empty0 + 8 * stage);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                tc_commit(accf0 + 8 * acc);
+                acc ^= 1;
+                if (acc == 0) aphase ^= 1u;
+            }
+            if (!ok) {
+                tc_commit(drain_bar);
+                wait_drain(drain_bar, 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        // warps 2 .. 5: lane quarters 2, 3 (U) and 0, 1 (G)
+        const int q = warp & 3, r = (q & 1) * 32 + lane;        // row of the tile
+        const bool is_up = q >= 2, f16 = g.dtype == MUON_F16;
+        auto bar4 = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+        int acc = 0;
+        uint32_t aphase = 0;
+        for (int t = blockIdx.x; t < g.tiles; t += gridDim.x) {
+            // the four warps go on together, whichever of them saw the wait give up
+            const bool got = wait_bounded(accf0 + 8 * acc, aphase, abort_flag, g.status);
+            int all;
+            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                         "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+                         : "=r"(all) : "r"((uint32_t)got) : "memory");
+            if (!all) break;
+            tc_fence_after();
+            const int f = t * g.R + r;
+            const bool mine = r < g.R && f < g.ffn;
+            for (int n0 = 0; n0 < g.tokens; n0 += 32) {
+                float v[32];
+                tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * FEW_TOKENS + n0), v);
+                const int n = min(32, g.tokens - n0);
+                if (is_up) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) up[r][k] = v[k];
+                }
+                bar4();
+                if (g.save && mine) {
+                    const GluOut& o = g.out[is_up ? 2 : 1];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (k < n) st_elem(o.p, (int64_t)(n0 + k) * o.ld + f, v[k], f16 ? MUON_F16 : MUON_BF16);
+                }
+                if (!is_up && mine) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (k < n)
+                            st_elem(g.out[0].p, (int64_t)(n0 + k) * g.out[0].ld + f,
+                                    activate<false>(v[k], g.act, nullptr) * up[r][k], f16 ? MUON_F16 : MUON_BF16);
+                }
+                bar4();                     // U's buffer is free again
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acce0 + 8 * acc);
+            acc ^= 1;
+            if (acc == 0) aphase ^= 1u;
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 256);
+    }
+}
+
+// dG = dH U act'(G) and dU = dH act(G), written at a pitch of whole 16-byte
+// pieces (zeros beyond ffn), eight columns per thread and step.  Bound by HBM:
+// three matrices read, two written.
 struct GluGradArgs {
     const void* dh;
     const void* gate;
     const void* up;
     void* dg;
     void* du;
-    int64_t rows, ffn, ldw;
+    int64_t rows;
+    int ffn, pieces;            // columns, 16-byte pieces of a workspace row
     int dtype, act;
-    int vec;                    // 8-element accesses (ffn a multiple of 8, everything 16-byte aligned)
+    int vec;                    // the inputs' rows start on 16 bytes too
 };
+
+// Eight 16-bit values of a dense row, columns c .. c + 7 (zeros from `cols` on).
+__device__ __forceinline__ uint4 load8(const void* p, int64_t row, int c, int cols, bool vec) {
+    const uint16_t* r = static_cast<const uint16_t*>(p) + row * cols + c;
+    if (vec) return *reinterpret_cast<const uint4*>(r);
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = c + 2 * k < cols ? r[2 * k] : 0u, hi = c + 2 * k + 1 < cols ? r[2 * k + 1] : 0u;
+        w[k] = lo | (hi << 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
 __global__ void __launch_bounds__(256) glu_grad_kernel(const __grid_constant__ GluGradArgs a) {
     pdl_wait();
     pdl_trigger();
-    const int64_t step = (int64_t)gridDim.x * 256;
-    if (a.vec) {
-        const int64_t n = a.rows * (a.ffn / 8);
-        const bool f16 = a.dtype == MUON_F16;
-        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
-            // ldw == ffn: the vector path is dense on both sides
-            float d[8], g[8], u[8];
-            unpack8_h(reinterpret_cast<const uint4*>(a.dh)[i], d, f16);
-            unpack8_h(reinterpret_cast<const uint4*>(a.gate)[i], g, f16);
-            unpack8_h(reinterpret_cast<const uint4*>(a.up)[i], u, f16);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                float s;
-                const float act = activate<true>(g[k], a.act, &s);
-                g[k] = d[k] * u[k] * s;
-                u[k] = d[k] * act;
-            }
-            reinterpret_cast<uint4*>(a.dg)[i] = pack8_h(g, f16);
-            reinterpret_cast<uint4*>(a.du)[i] = pack8_h(u, f16);
-        }
-        return;
-    }
-    const int64_t n = a.rows * a.ffn;
+    const bool f16 = a.dtype == MUON_F16;
+    const int64_t n = a.rows * a.pieces, step = (int64_t)gridDim.x * 256;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
-        const int64_t r = i / a.ffn, o = r * a.ldw + (i - r * a.ffn);
-        const float d = ld_elem(a.dh, i, a.dtype), u = ld_elem(a.up, i, a.dtype);
-        float s;
-        const float act = activate<true>(ld_elem(a.gate, i, a.dtype), a.act, &s);
-        st_elem(a.dg, o, d * u * s, a.dtype);
-        st_elem(a.du, o, d * act, a.dtype);
+        const int64_t row = a.vec ? 0 : i / a.pieces;       // aligned rows are one dense run of pieces
+        const int64_t col = a.vec ? i * 8 : (i - row * a.pieces) * 8;
+        uint4 qd, qg, qu;
+        if (a.vec) {
+            qd = static_cast<const uint4*>(a.dh)[i];
+            qg = static_cast<const uint4*>(a.gate)[i];
+            qu = static_cast<const uint4*>(a.up)[i];
+        } else {
+            qd = load8(a.dh, row, (int)col, a.ffn, false);
+            qg = load8(a.gate, row, (int)col, a.ffn, false);
+            qu = load8(a.up, row, (int)col, a.ffn, false);
+        }
+        float d[8], g[8], u[8];
+        unpack8_h(qd, d, f16);
+        unpack8_h(qg, g, f16);
+        unpack8_h(qu, u, f16);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            float s;
+            const float act = activate<true>(g[k], a.act, &s);
+            g[k] = d[k] * u[k] * s;
+            u[k] = d[k] * act;
+        }
+        static_cast<uint4*>(a.dg)[i] = pack8_h(g, f16);
+        static_cast<uint4*>(a.du)[i] = pack8_h(u, f16);
     }
 }
 
-// Rows of `cols` 16-bit elements to a pitch the copy engine can address.
-__global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* src, uint16_t* dst, int64_t rows, int64_t cols,
-                                                       int64_t ld) {
+// Up to three matrices of 16-bit elements to pitches the copy engine can
+// address (operand blockIdx.y), a 16-byte piece per thread and step.
+struct PadArgs {
+    const void* src[3];
+    void* dst[3];
+    int64_t rows[3];
+    int cols;
+};
+__global__ void __launch_bounds__(256) pad_rows_kernel(const __grid_constant__ PadArgs a) {
     pdl_wait();
     pdl_trigger();
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        for (int64_t c = threadIdx.x; c < cols; c += 256) dst[r * ld + c] = src[r * cols + c];
+    const int o = blockIdx.y, pieces = (a.cols + 7) / 8;
+    const int64_t n = a.rows[o] * pieces, step = (int64_t)gridDim.x * 256;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+        const int64_t row = i / pieces;
+        static_cast<uint4*>(a.dst[o])[i] = load8(a.src[o], row, (int)(i - row * pieces) * 8, a.cols, false);
+    }
+}
+
+// dX from its partial sums, added in the order of the parts.
+struct PartSumArgs {
+    const float* part;
+    void* out;
+    int64_t rows, ldp;
+    int cols, splits, dtype;
+};
+__global__ void __launch_bounds__(256) part_sum_kernel(const __grid_constant__ PartSumArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t n = a.rows * a.cols, step = (int64_t)gridDim.x * 256, plane = a.rows * a.ldp;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+        const int64_t row = i / a.cols, at = row * a.ldp + (i - row * a.cols);
+        float s = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < a.splits; ++k) s += a.part[k * plane + at];
+        st_elem(a.out, i, s, a.dtype);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -464,6 +714,7 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* src, uint
 
 constexpr int64_t MAX_SIDE = 1 << 20;
 constexpr int64_t MAX_TOKENS = 1 << 24;
+constexpr int SPLIT_BLOCKS = 8;     // k-blocks a part of dX keeps at least
 
 struct Operand {
     const void* p;
@@ -477,18 +728,32 @@ bool tma_ok(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) 
 size_t padded_bytes(const Operand& o) {
     return tma_ok(o.p, o.ld) ? 0 : align_up((size_t)o.rows * pad8(o.cols) * 2, 256);
 }
-int pad_operand(Operand& o, char*& at, int sms, cudaStream_t s) {
-    const size_t b = padded_bytes(o);
-    if (!b) return MUON_OK;
-    const int64_t ld = pad8(o.cols);
+// Points the operands that need it at padded copies, made in one launch.
+int pad_operands(Operand* const* ops, char* at, int sms, cudaStream_t s) {
+    PadArgs p;
+    std::memset(&p, 0, sizeof p);
+    unsigned n = 0;
+    int64_t most = 0;
+    for (int i = 0; i < 3; ++i) {
+        Operand& o = *ops[i];
+        const size_t b = padded_bytes(o);
+        if (!b) continue;
+        p.src[n] = o.p;
+        p.dst[n] = at;
+        p.rows[n] = o.rows;
+        p.cols = (int)o.cols;               // the three share it
+        ++n;
+        o.ld = pad8(o.cols);
+        most = std::max(most, o.rows * (o.ld / 8));
+        o.p = at;
+        at += b;
+    }
+    if (!n) return MUON_OK;
     note_launch_begin(KC_OTHER, s);
-    cudaError_t e = launch_pdl(pad_rows_kernel, dim3((unsigned)std::min<int64_t>(o.rows, (int64_t)sms * 8)), dim3(256), 0, s,
-                               static_cast<const uint16_t*>(o.p), reinterpret_cast<uint16_t*>(at), o.rows, o.cols, ld);
+    cudaError_t e = launch_pdl(pad_rows_kernel, dim3((unsigned)std::min<int64_t>((most + 255) / 256, (int64_t)sms * 8), n),
+                               dim3(256), 0, s, p);
     note_launch_end(KC_OTHER, 0.0, s);
     if (e != cudaSuccess) return cuda_fail(e, "operand copy launch");
-    o.p = at;
-    o.ld = ld;
-    at += b;
     return MUON_OK;
 }
 
@@ -517,6 +782,7 @@ GluTiles tiles(int64_t rows, int64_t cols, int64_t tile_cols, int64_t k, int seg
     t.seg_blocks = (int)((k + GK - 1) / GK);
     t.segs = segs;
     t.count = t.tiles_m * t.tiles_n;
+    t.splits = 1;
     return t;
 }
 
@@ -550,12 +816,44 @@ cudaError_t launch_glu(GluMaps& maps, GluArgs& g, cudaStream_t s) {
     const int r = g.a.count % P;
     g.extra = 0;
     if (r && g.nb) {
-        const int ka = g.a.segs * g.a.seg_blocks, kb = g.b.segs * g.b.seg_blocks;
+        // a tile of few k-blocks costs what its 256 x 256 results take to leave, about 8 k-blocks' time
+        const int ka = g.a.segs * g.a.seg_blocks / g.a.splits, kb = std::max(8, g.b.segs * g.b.seg_blocks);
         g.extra = std::min(g.nb / (P - r), (ka + kb / 2) / kb);
     }
     cfg.gridDim = dim3((unsigned)(2 * P));
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, maps, g);
+}
+
+int launch_few(const Operand& X, const Operand& W, const Operand& U, FewArgs& g, int sms, cudaStream_t s) {
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    std::call_once(once, [] {
+        err = cudaFuncSetAttribute(glu_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+    });
+    if (err != cudaSuccess) return cuda_fail(err, "cudaFuncSetAttribute");
+    g.n = (g.tokens + 15) / 16 * 16;
+    int64_t best = INT64_MAX;
+    for (int R = 64; R >= 8; R -= 8) {
+        const int64_t n = ((int64_t)g.ffn + R - 1) / R, rows = (n + sms - 1) / sms * R;
+        if (rows < best) {
+            best = rows;
+            g.R = R;
+            g.tiles = (int)n;
+        }
+    }
+    const int stage_bytes = OP_BYTES + g.n * 128;
+    g.stages = std::min(FEW_STAGES, (232448 - FEW_FIXED) / stage_bytes);
+    CUtensorMap mx, mg, mu;
+    if (!map_in(&mx, X, g.dtype, GK, (uint32_t)g.n) || !map_in(&mg, W, g.dtype, GK, (uint32_t)g.R) ||
+        !map_in(&mu, U, g.dtype, GK, (uint32_t)g.R))
+        return fail(MUON_ECUDA, "tensor map creation failed");
+    note_launch_begin(KC_GLU, s);
+    cudaError_t e = launch_pdl(glu_few_kernel, dim3((unsigned)std::min(g.tiles, sms)), dim3(FEW_T),
+                               (size_t)(g.stages * stage_bytes + FEW_FIXED), s, mx, mg, mu, g);
+    note_launch_end(KC_GLU, 4.0 * g.tokens * (double)X.cols * g.ffn, s);
+    if (e != cudaSuccess) return cuda_fail(e, "glu forward launch");
+    return MUON_OK;
 }
 
 int glu_check(int64_t tokens, int64_t hidden, int64_t ffn, int dtype, int act) {
@@ -589,9 +887,17 @@ extern "C" int muon_glu_forward(const void* x, const void* w_gate, const void* w
     if (const size_t need = padded_bytes(X) + padded_bytes(G) + padded_bytes(U)) {
         Workspace* w = nullptr;
         if ((r = ws_get(dc.device, s, need, &w))) return r;
-        char* at = w->base;
-        for (Operand* o : {&X, &G, &U})
-            if ((r = pad_operand(*o, at, dc.sms, s))) return r;
+        Operand* const ops[3] = {&X, &G, &U};
+        if ((r = pad_operands(ops, w->base, dc.sms, s))) return r;
+    }
+    if (tokens <= FEW_TOKENS) {
+        FewArgs f;
+        std::memset(&f, 0, sizeof f);
+        f.dtype = dtype; f.act = act; f.save = gate != nullptr;
+        f.tokens = (int)tokens; f.ffn = (int)ffn; f.kblocks = (int)((hidden + GK - 1) / GK);
+        f.out[0] = GluOut{h, ffn}; f.out[1] = GluOut{gate, ffn}; f.out[2] = GluOut{up, ffn};
+        f.status = dc.status;
+        return launch_few(X, G, U, f, dc.sms, s);
     }
     GluArgs g;
     GluMaps maps;
@@ -637,34 +943,42 @@ extern "C" int muon_glu_backward(const void* x, const void* w_gate, const void* 
     Operand X{x, tokens, hidden, hidden}, G{w_gate, ffn, hidden, hidden}, U{w_up, ffn, hidden, hidden};
     const int64_t ldw = pad8(ffn);
     const size_t half = align_up((size_t)tokens * ldw * 2, 256);
+    GluArgs g;
+    std::memset(&g, 0, sizeof g);
+    g.dtype = dtype; g.act = act;
+    g.status = dc.status;
+    g.a = tiles(tokens, hidden, 2 * GM, ffn, 2);
+    g.b = tiles(ffn, hidden, 2 * GM, tokens, 1);
+    // dX has few tiles and a long contraction (2 ffn) when the tokens are few:
+    // its k-blocks are then cut into parts, enough of them for the pairs of the
+    // device, at least SPLIT_BLOCKS each
+    const int pairs = dc.sms / 2, blocks = g.a.segs * g.a.seg_blocks;
+    g.a.splits = std::max(1, std::min(pairs / g.a.count, blocks / SPLIT_BLOCKS));
+    g.a.count *= g.a.splits;
+    if (!dx) g.a.count = 0;
+    g.nb = dw_gate ? 2 * g.b.count : 0;
+    g.ldp = (hidden + 31) / 32 * 32;
+    const size_t part = dx && g.a.splits > 1 ? align_up((size_t)g.a.splits * tokens * g.ldp * 4, 256) : 0;
     Workspace* w = nullptr;
-    if ((r = ws_get(dc.device, s, 2 * half + padded_bytes(X) + padded_bytes(G) + padded_bytes(U), &w))) return r;
-    char* at = w->base + 2 * half;
-    for (Operand* o : {&X, &G, &U})
-        if ((r = pad_operand(*o, at, dc.sms, s))) return r;
+    if ((r = ws_get(dc.device, s, 2 * half + part + padded_bytes(X) + padded_bytes(G) + padded_bytes(U), &w))) return r;
+    g.part = reinterpret_cast<float*>(w->base + 2 * half);
+    Operand* const ops[3] = {&X, &G, &U};
+    if ((r = pad_operands(ops, w->base + 2 * half + part, dc.sms, s))) return r;
     GluGradArgs ga;
     ga.dh = dh; ga.gate = gate; ga.up = up;
     ga.dg = w->base; ga.du = w->base + half;
-    ga.rows = tokens; ga.ffn = ffn; ga.ldw = ldw;
+    ga.rows = tokens; ga.ffn = (int)ffn; ga.pieces = (int)(ldw / 8);
     ga.dtype = dtype; ga.act = act;
     ga.vec = tma_ok(dh, ffn) && tma_ok(gate, ffn) && tma_ok(up, ffn);
-    const int64_t work = ga.vec ? tokens * (ffn / 8) : tokens * ffn;
     note_launch_begin(KC_GLU, s);
-    cudaError_t e = launch_pdl(glu_grad_kernel, dim3((unsigned)std::min<int64_t>((work + 255) / 256, (int64_t)dc.sms * 8)),
+    cudaError_t e = launch_pdl(glu_grad_kernel,
+                               dim3((unsigned)std::min<int64_t>((tokens * ga.pieces + 255) / 256, (int64_t)dc.sms * 8)),
                                dim3(256), 0, s, ga);
     note_launch_end(KC_GLU, 0.0, s);
     if (e != cudaSuccess) return cuda_fail(e, "glu gradient launch");
     const Operand DG{ga.dg, tokens, ffn, ldw}, DU{ga.du, tokens, ffn, ldw};
-    GluArgs g;
     GluMaps maps;
-    std::memset(&g, 0, sizeof g);
     std::memset(&maps, 0, sizeof maps);
-    g.dtype = dtype; g.act = act;
-    g.status = dc.status;
-    g.a = tiles(tokens, hidden, 2 * GM, ffn, 2);
-    if (!dx) g.a.count = 0;
-    g.b = tiles(ffn, hidden, 2 * GM, tokens, 1);
-    g.nb = dw_gate ? 2 * g.b.count : 0;
     g.out[0] = GluOut{dx, hidden}; g.out[1] = GluOut{dw_gate, hidden}; g.out[2] = GluOut{dw_up, hidden};
     g.tma_out = tma_ok(dx, hidden) && tma_ok(dw_gate, hidden) && tma_ok(dw_up, hidden);
     bool ok = map_in(&maps.a[0], DG, dtype, GK, GM) && map_in(&maps.a[1], DU, dtype, GK, GM) &&
@@ -679,5 +993,13 @@ extern "C" int muon_glu_backward(const void* x, const void* w_gate, const void* 
     e = launch_glu<false>(maps, g, s);
     note_launch_end(KC_GLU, (dx ? 4.0 : 0.0) * tokens * (double)hidden * ffn + (dw_gate ? 4.0 : 0.0) * tokens * (double)hidden * ffn, s);
     if (e != cudaSuccess) return cuda_fail(e, "glu backward launch");
+    if (part) {
+        PartSumArgs p{g.part, dx, tokens, g.ldp, (int)hidden, g.a.splits, dtype};
+        note_launch_begin(KC_GLU, s);
+        e = launch_pdl(part_sum_kernel,
+                       dim3((unsigned)std::min<int64_t>((tokens * hidden + 255) / 256, (int64_t)dc.sms * 8)), dim3(256), 0, s, p);
+        note_launch_end(KC_GLU, 0.0, s);
+        if (e != cudaSuccess) return cuda_fail(e, "glu partial sum launch");
+    }
     return MUON_OK;
 } MUON_CATCH_ALL

@@ -27,6 +27,7 @@
 // logits are all the type's lowest value stay finite for T < 1.
 #include "host.h"
 #include "epilogue.cuh"
+#include "tc_ptx.cuh"
 
 namespace muon {
 
@@ -38,6 +39,13 @@ struct RowStats {       // one row of the preference loss between its launches
     float mx, inv_s;    // q_v = exp2((x_v - mx) c2) * inv_s
     float logp;
     float coef;         // d loss / d logp, 0 for rows outside the loss
+};
+
+// One entry of a teacher's list as the row kernel needs it.
+struct alignas(16) Listed {
+    int id;                     // -1: padding
+    float p, lp;                // the teacher's probability and its logarithm
+    float psum;                 // p of every entry with this index at its first one, -1 at the others
 };
 
 struct RowLossArgs {
@@ -65,6 +73,8 @@ struct RowLossArgs {
     const void* tval;
     const float* tlse;
     int k, tidx64, tval_dtype;
+    Listed* listed;             // [rows][k], written by teacher_kernel
+    float* mass;                // [rows]: the teacher's listed probability
     // preference
     RowStats* stats;
 };
@@ -186,16 +196,20 @@ __device__ __forceinline__ void zero_row(T* row, int vocab) {
     for (int i = threadIdx.x; i < nv; i += NT) store_vec<T>(row, i * E - shift, vocab, z, true);
 }
 
+// What the policy loss needs of one row besides its logits.
+struct PolicyRow {
+    float w, adv, old, ref;
+};
+
 // The policy loss of one row from its log-probability: loss and dL/dlogp.
-__device__ __forceinline__ void policy_row(const RowLossArgs& a, int64_t row, float lp, float& loss, float& dl) {
-    const float adv = a.adv[row];
-    const float r = a.old_logp ? expf(lp - a.old_logp[row]) : 1.0f;
+__device__ __forceinline__ void policy_row(const RowLossArgs& a, const PolicyRow& p, float lp, float& loss, float& dl) {
+    const float r = a.old_logp ? expf(lp - p.old) : 1.0f;
     const float rc = fminf(fmaxf(r, a.lo), a.hi);
-    const float u = r * adv, uc = rc * adv;
+    const float u = r * p.adv, uc = rc * p.adv;
     loss = -fminf(u, uc);
     dl = (u <= uc || u != u) ? -u : 0.f;
     if (a.kl != 0.f) {
-        const float x = a.ref_logp[row] - lp;
+        const float x = p.ref - lp;
         // exp(x) - x - 1 cancels for small x: expm1 keeps it
         const float em = expm1f(x);
         loss += a.kl * (em - x);
@@ -219,26 +233,51 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// v <- exp2((v + nr) c2), two values per add and multiply; returns their sum.
+// Pairs of fp32 values in one 64-bit register, two per instruction.
+__device__ __forceinline__ uint64_t pair2(float x, float y) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    return p;
+}
+__device__ __forceinline__ float2 unpair(uint64_t p) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// v <- exp2((v + nr) c2)
 template <int E>
-__device__ __forceinline__ float exp_vec(float (&v)[E], float nr, float c2) {
-    float2 s = make_float2(0.f, 0.f);
+__device__ __forceinline__ void exp_vec(uint64_t (&v)[E / 2], uint64_t nr, uint64_t c2) {
 #pragma unroll
-    for (int j = 0; j < E; j += 2) {
-        asm("{\n\t.reg .b64 x, r, c;\n\t"
-            "mov.b64 x, {%0, %1};\n\tmov.b64 r, {%2, %2};\n\tmov.b64 c, {%3, %3};\n\t"
-            "add.rn.f32x2 x, x, r;\n\tmul.rn.f32x2 x, x, c;\n\t"
-            "mov.b64 {%0, %1}, x;\n\t}"
-            : "+f"(v[j]), "+f"(v[j + 1])
-            : "f"(nr), "f"(c2));
-        v[j] = ex2(v[j]);
-        v[j + 1] = ex2(v[j + 1]);
-        asm("{\n\t.reg .b64 s, x;\n\tmov.b64 s, {%0, %1};\n\tmov.b64 x, {%2, %3};\n\t"
-            "add.rn.f32x2 s, s, x;\n\tmov.b64 {%0, %1}, s;\n\t}"
-            : "+f"(s.x), "+f"(s.y)
-            : "f"(v[j]), "f"(v[j + 1]));
+    for (int j = 0; j < E / 2; ++j) {
+        const float2 z = unpair(mul2(add2(v[j], nr), c2));
+        v[j] = pair2(ex2(z.x), ex2(z.y));
     }
-    return s.x + s.y;
+}
+template <typename T>
+__device__ __forceinline__ void unpack_pairs(const uint4& q, uint64_t (&v)[Vec<T>::E / 2]) {
+    float f[Vec<T>::E];
+    Vec<T>::unpack(q, f);
+#pragma unroll
+    for (int j = 0; j < Vec<T>::E / 2; ++j) v[j] = pair2(f[2 * j], f[2 * j + 1]);
+}
+template <int E>
+__device__ __forceinline__ void split_pairs(const uint64_t (&v)[E / 2], float (&f)[E]) {
+#pragma unroll
+    for (int j = 0; j < E / 2; ++j) {
+        const float2 z = unpair(v[j]);
+        f[2 * j] = z.x;
+        f[2 * j + 1] = z.y;
+    }
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -246,23 +285,20 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Waits until at most n (0 .. 3) of the thread's copy groups are pending.
+__device__ __forceinline__ void cp_async_wait(int n) {
+    if (n == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-// Every thread of every CTA of the cluster; orders shared and global accesses before and after.
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void st_cluster_f4(uint32_t local, uint32_t rank, const float4& v) {
-    uint32_t a;
+// 16 bytes to the same shared-memory offset of CTA `rank`, counted on its mbarrier.
+__device__ __forceinline__ void st_async_f4(uint32_t local, uint32_t bar, uint32_t rank, const float4& v) {
+    uint32_t a, b;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(bar), "r"(rank));
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(b)
                  : "memory");
 }
 
@@ -272,10 +308,14 @@ __device__ __forceinline__ void st_cluster_f4(uint32_t local, uint32_t rank, con
 //
 // A row belongs to a cluster of C CTAs (C = 1 up to 53248 16-bit logits), CTA r
 // holding its r-th part in shared memory, SLOTS x NT vectors of 16 bytes at
-// most, two CTAs per SM.  The first walk takes the maximum and the sums, the
-// CTAs of a cluster exchange theirs through distributed shared memory, and the
-// second walk takes the exponentials again (cheaper than the registers to keep
-// them in) and stores the gradient, so every logit is read from memory once.
+// most, two CTAs per SM.  The first walk takes the maximum and the sums; warp 0
+// brings them together, exchanges them with the other CTAs of the cluster
+// (distributed shared memory, an mbarrier per row parity), forms the loss and
+// hands the gradient's factors to the other warps; the second walk takes the
+// exponentials again (cheaper than the registers to keep them in) and stores
+// the gradient, so every logit is read from memory once.  What is per row is
+// done by one warp: at eight vectors per thread and row, a per-row step of every
+// warp costs as many instructions as a vector or two of each thread.
 // Thread t owns the vectors t, t + NT, ... of the part: it copies them in
 // (cp.async), reads them twice, and as soon as the second walk has taken a slot
 // it starts the copy of the next row's vector into it: no barrier guards the
@@ -296,72 +336,89 @@ constexpr float REBASE = 40.0f;     // exponent (base 2) beyond which the refere
 
 struct Sums {
     float ref, limit;       // reference (negated), and the logit from which it moves
-    float s, so;            // sum of exponentials, the part outside the teacher's set
+    float s, si;            // sums of exponentials: outside the teacher's set (or all), inside
     float top;              // the maximum
 };
 
-__device__ __forceinline__ void follow(Sums& z, float vm, float c2, float step) {
+// Takes a new maximum; returns whether the reference moved.
+__device__ __forceinline__ bool follow(Sums& z, float vm, float c2, float step) {
     z.top = fmaxf(z.top, vm);
-    if (vm > z.limit) {
-        const float f = z.limit == -INFINITY ? 1.0f : ex2((-z.ref - vm) * c2);
-        z.s *= f;
-        z.so *= f;
-        z.ref = -vm;
-        z.limit = vm + step;
-    }
+    if (!(vm > z.limit)) return false;
+    const float f = z.limit == -INFINITY ? 1.0f : ex2((-z.ref - vm) * c2);
+    z.s *= f;
+    z.si *= f;
+    z.ref = -vm;
+    z.limit = vm + step;
+    return true;
 }
 
-// Partial sums of a warp's lanes, one per lane (maximum, s, so), as one.
-__device__ __forceinline__ float3 merge_lanes(float top, float s, float so, float c2, bool rest) {
+// Partial sums of a warp's lanes, one per lane (maximum, s, si), as one.
+__device__ __forceinline__ float3 merge_lanes(float top, float s, float si, float c2, bool set) {
     float3 r;
     r.x = warp_max(top);
     const float f = top == -INFINITY ? 0.f : ex2((top - r.x) * c2);     // 0 x NaN stays NaN
     r.y = warp_sum(s * f);
-    r.z = rest ? warp_sum(so * f) : 0.f;
+    r.z = set ? warp_sum(si * f) : 0.f;
     return r;
 }
 
-// Which of the cluster's next 32 rows are in the loss, refreshed every 32 rows.
-struct LiveWindow {
-    uint32_t bits;
-    int n;                  // rows of the cluster's sequence already taken from it
-};
-
-__host__ __device__ constexpr int bit_words(int logits) { return (logits + 31) / 32; }
+// Bytes of a row's listing in shared memory (rows with a remainder class): for
+// each vector of the part the listed logits, a bit each, and for each entry
+// whether it leads its vector.
+__host__ __device__ constexpr int listing_bytes(int per, int k) { return (per + 15) / 16 * 16 + (k + 127) / 128 * 16; }
 
 struct PartArgs {
     int csize;              // CTAs per row
     int per;                // vectors of a row per CTA, at most SLOTS NT
+    int* status;
 };
 
+// In distillation one warp of the CTA is for the listed entries, so that the
+// walks stay free of them: the first walk leaves out whole vectors that hold one
+// (their other logits are summed by that warp), and the second stores all
+// logits alike, the listed ones' gradients following once it is through.
+// Listings are kept for three rows: the one walked, the one listed next, and the
+// one before, which other warps may still be walking.
+constexpr int TEACHERS = 3;
+template <int MODE>
+constexpr int TEACHER = MODE == LM_DISTILL ? 32 : 0;
+
 template <typename T, int MODE, int NT>
-__global__ void __launch_bounds__(NT, 1024 / NT)
+__global__ void __launch_bounds__(NT + TEACHER<MODE>, 1024 / (NT + TEACHER<MODE>))
 row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ PartArgs pa) {
-    constexpr int E = Vec<T>::E, NW = NT / 32, QUARTERS = 4;
-    constexpr bool GRAD = MODE != LM_STATS;
+    constexpr int E = Vec<T>::E, NW = NT / 32, QUARTERS = 4, AHEAD = 4;
+    constexpr bool GRAD = MODE != LM_STATS, SET = MODE == LM_DISTILL;
     extern __shared__ __align__(16) uint8_t dyn8[];
     uint4* ring = reinterpret_cast<uint4*>(dyn8);       // [slots][NT]
-    __shared__ float4 red[2][NW];
-    __shared__ float4 part[2][MAX_CLUSTER];
-    __shared__ float tred[NW], tred_m[NW], lred[NW];
+    __shared__ float4 red[2][NW + 1];
+    __shared__ __align__(16) float4 part[2][MAX_CLUSTER];
+    __shared__ __align__(8) uint64_t bars[2];
+    __shared__ float4 factors;                          // maximum, factors of q inside and outside S, factor of t
+    __shared__ float3 terms;                            // distillation: log of the sum, the rest's term, weight T^2
+    __shared__ uint32_t odd_of_row[TEACHERS];           // which of the row's odd logits are listed
+    __shared__ int abort_flag;
     const int V = a.vocab, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int csize = pa.csize, per = pa.per;
-    const int rank = csize > 1 ? (int)cluster_rank() : 0;
+    const int rank = csize > 1 ? (int)tc::cluster_ctarank() : 0;
     const int64_t G = gridDim.x / csize, row0 = blockIdx.x / csize;
     const int slots = (per + NT - 1) / NT, quarter = (slots + QUARTERS - 1) / QUARTERS;
     const float c2 = a.c2, step = REBASE / c2;
-    // distillation: the teacher's entries; with a remainder class, the bitmap of its set in this part
-    int* sidx = reinterpret_cast<int*>(dyn8 + (size_t)slots * NT * 16);
-    float* slp = reinterpret_cast<float*>(sidx + a.k);
-    float* sp = slp + a.k;
-    float* sx = sp + a.k;
-    uint32_t* bits = reinterpret_cast<uint32_t*>(sx + a.k);
-    const bool rest_class = MODE == LM_DISTILL && a.tlse != nullptr;
+    const uint64_t c22 = pair2(c2, c2);
+    const bool rest_class = SET && a.tlse != nullptr;
+    float* sx = reinterpret_cast<float*>(dyn8 + (size_t)slots * NT * 16);    // [k] the row's listed logits
+    auto listing = [&](int buf) {
+        return reinterpret_cast<uint8_t*>(sx) + (a.k + 3) / 4 * 16 + (size_t)buf * listing_bytes(per, a.k);
+    };
+    if (t == 0) {
+        tc::mbar_init(smem_addr(&bars[0]), 1);
+        tc::mbar_init(smem_addr(&bars[1]), 1);
+        abort_flag = 0;
+        tc::fence_mbar_init();
+    }
+    __syncthreads();
+    if (csize > 1) tc::cluster_sync();                  // the cluster's barriers exist before anything targets them
     pdl_wait();
     pdl_trigger();
-    if (rest_class)
-        for (int i = t; i < bit_words(per * E); i += NT) bits[i] = 0;
-    if (csize > 1) cluster_barrier();                   // every CTA of the cluster runs before any writes to it
 
     auto row_live = [&](int64_t row) -> bool {
         if (row >= a.rows) return false;
@@ -372,14 +429,17 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
         }
         return live;
     };
-    auto window = [&](LiveWindow& w, int64_t row) -> bool {     // whether `row`, the sequence's next, is live
-        if ((w.n & 31) == 0) w.bits = __ballot_sync(0xffffffffu, row_live(row + (int64_t)lane * G));
-        return (w.bits >> (w.n++ & 31)) & 1;
+    // whether `row`, the sequence's next, is live: 32 rows are looked up at a time
+    uint32_t window = 0;
+    int taken = 0;
+    auto live_next = [&](int64_t row) -> bool {
+        if ((taken & 31) == 0) window = __ballot_sync(0xffffffffu, row_live(row + (int64_t)lane * G));
+        return (window >> (taken++ & 31)) & 1;
     };
     // geometry of a row: logits before its first vector, vectors of this CTA
     auto head_of = [&](const T* x) { return min(V, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(T)); };
     auto count_of = [&](int head) { return max(0, min(per, (V - head) / E - rank * per)); };
-    // this thread's odd logit of a row (the first CTA's threads), -1 if none
+    // an odd logit of a row (the first CTA's first threads), -1 if none
     auto odd_of = [&](int head) -> int {
         if (rank != 0 || t >= 2 * E) return -1;
         if (t < head) return t;
@@ -388,265 +448,427 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
     };
 
     // the row in the loss after the one worked on: its vectors are copied in as slots fall free
-    LiveWindow lw{0, 0}, pw{0, 0};
-    int64_t lrow = row0;
     const T* lx = nullptr;
     const T* lp = nullptr;                              // this thread's first vector of it
-    int lcount = 0;                                     // the CTA's vectors of it
-    float lodd = -INFINITY;                             // this thread's odd logit of it
-    auto advance = [&]() {
-        while (lrow < a.rows && !window(lw, lrow)) lrow += G;
-        lcount = 0;
-        lodd = -INFINITY;
-        if (lrow < a.rows) {
-            lx = reinterpret_cast<const T*>(a.logits) + lrow * a.ld;
-            const int head = head_of(lx);
-            lcount = count_of(head);
-            lp = lx + head + (int64_t)(rank * per + t) * E;
-            const int odd = odd_of(head);
-            if (odd >= 0) lodd = Vec<T>::ld(lx + odd);
-        }
-    };
+    int lhead = 0, lcount = 0;                          // its odd logits in front, the CTA's vectors of it
+    float lodd = -INFINITY;                             // this thread's odd logit of it (warp 0)
+    int64_t lrow = row0 - G;
     const uint32_t slot0 = smem_addr(ring + t);
     auto issue = [&](int u) {
         if (t + u * NT < lcount) cp_async16(slot0 + u * (NT * 16), lp + u * (NT * E));
     };
-    advance();
+    const bool walker = !SET || warp < NW;
+    // The entries' warp holds the indices of the first AHEAD x 32 entries of this
+    // row and of the next in registers, so that its loads of one pass wait for
+    // memory once; longer lists are read as they are worked through.
+    int rid[AHEAD], nid[AHEAD];
 #pragma unroll
-    for (int qd = 0; qd < QUARTERS; ++qd) {
-        for (int u = qd * quarter; u < min(slots, (qd + 1) * quarter); ++u) issue(u);
-        cp_async_commit();
-    }
+    for (int n = 0; n < AHEAD; ++n) rid[n] = nid[n] = -1;
+    // lists entry j0 + lane of row lrow, of index id, in buffer buf
+    auto list = [&](int buf, int j0, int id) {
+        uint8_t* flags = listing(buf);
+        uint32_t* leads = reinterpret_cast<uint32_t*>(flags + (per + 15) / 16 * 16);
+        const int part0 = lhead + rank * per * E, tail = lhead + (V - lhead) / E * E, at = id - part0;
+        const bool in = id >= 0 && at >= 0 && at < lcount * E;
+        const int vec = in ? at / E : 0;
+        const uint32_t same = __match_any_sync(0xffffffffu, in ? vec : -1 - lane);
+        const bool lead = in && flags[vec] == 0 && lane == __ffs(same) - 1;
+        const uint32_t word = __ballot_sync(0xffffffffu, lead);
+        if (lane == 0) leads[j0 >> 5] = word;
+        if (in) atomicOr(reinterpret_cast<uint32_t*>(flags) + (vec >> 2), 1u << ((vec & 3) * 8 + at % E));
+        else if (id >= 0 && rank == 0 && (id < lhead || id >= tail))
+            atomicOr(&odd_of_row[buf], 1u << (id < lhead ? id : lhead + id - tail));
+        __syncwarp();
+    };
 
-    int par = 0;
-    for (int64_t row = row0; row < a.rows; row += G) {
-        T* g = reinterpret_cast<T*>(a.grad) + row * a.ldg;
-        if (!window(pw, row)) {
-            if (GRAD) {
-                const int head = head_of(g), n = count_of(head), odd = odd_of(head);
-                T* gp = g + head + (int64_t)rank * per * E;
-                for (int i = t; i < n; i += NT) *reinterpret_cast<uint4*>(gp + i * E) = make_uint4(0, 0, 0, 0);
-                if (odd >= 0) Vec<T>::st(g + odd, 0.f);
-            }
-            if (rank == 0 && t == 0) {
-                if (MODE == LM_STATS) a.stats[row] = RowStats{0.f, 0.f, 0.f, 0.f};
-                else a.loss[row] = 0.f;
-                if (MODE == LM_POLICY) a.logp[row] = 0.f;
-            }
-            continue;
-        }
-        const T* x = lx;                    // the row whose vectors are in the ring
-        const int head = head_of(x), count = lcount;
+    // One pass per row in the loss, and one before the first that only fetches:
+    // the row after the current one is found, the rows between, which are not
+    // in the loss, get their zeros, and every per-row step appears once.
+    int par = 1, nbuf = 0;
+    uint32_t phase[2] = {0, 0};
+    int64_t row = -1;
+    do {
+        par ^= 1;
+        const int head = lhead, count = lcount;     // the row whose vectors are in the ring
+        const int part0 = head + rank * per * E;    // the part's first logit
         const float odd = lodd;
-        const float w = a.weights ? a.weights[row] : 1.0f;
+        T* g = reinterpret_cast<T*>(a.grad) + row * a.ldg;
         int tok = 0;
         float xt = 0.f;
-        if (MODE != LM_DISTILL) {
-            tok = (int)ld_index(a.tokens, row, a.tok64);
-            xt = Vec<T>::ld(x + tok);
-        }
-        float tm = 0.f, lse = 0.f;
-        const int part0 = head + rank * per * E;        // the part's first logit; its bit is 0
-        bool odd_in = false;                            // the thread's odd logit is in the teacher's set
-        if (MODE == LM_DISTILL) {
-            lse = a.tlse ? a.tlse[row] : 0.f;
-            __syncthreads();                // the previous row's use of the entries is over
-            float wm = -INFINITY;
-            for (int j = t; j < a.k; j += NT) {
-                const int64_t id = ld_index(a.tidx, row * a.k + j, a.tidx64);
-                const bool ok = id >= 0 && id < V;
-                const float tv = ok ? ld_elem(a.tval, row * a.k + j, a.tval_dtype) : -INFINITY;
-                sidx[j] = ok ? (int)id : -1;
-                slp[j] = tv;
-                sx[j] = ok ? Vec<T>::ld(x + id) : 0.f;
-                const int at = (int)id - part0;
-                if (ok && rest_class && at >= 0 && at < count * E) atomicOr(&bits[at >> 5], 1u << (at & 31));
-                wm = fmaxf(wm, tv);
+        float mass = 0.f;
+        PolicyRow pr{1.0f, 0.f, 0.f, 0.f};
+        if (row >= 0) {
+            if (MODE != LM_DISTILL) tok = (int)ld_index(a.tokens, row, a.tok64);
+            if (warp == 0) {                // under the first walk, for the step between the barriers
+                if (MODE != LM_DISTILL) xt = Vec<T>::ld(lx + tok);
+                if (MODE != LM_STATS && a.weights) pr.w = a.weights[row];
+                if (SET) mass = a.mass[row];
+                if (MODE == LM_POLICY) {
+                    pr.adv = a.adv[row];
+                    if (a.old_logp) pr.old = a.old_logp[row];
+                    if (a.kl != 0.f) pr.ref = a.ref_logp[row];
+                }
             }
-            wm = warp_max(wm);
-            if (lane == 0) tred_m[warp] = wm;
-            __syncthreads();
-            if (!a.tlse) tm = warp_max(lane < NW ? tred_m[lane] : -INFINITY);
-            float s = 0.f;
-            for (int j = t; j < a.k; j += NT)
-                if (sidx[j] >= 0) s += expf((slp[j] - tm) * a.inv_t - lse);
-            s = warp_sum(s);
-            if (lane == 0) tred[warp] = s;
-            if (rest_class && odd_of(head) >= 0)
-                for (int j = 0; j < a.k; ++j) odd_in = odd_in || sidx[j] == odd_of(head);
         }
-        lrow += G;
-        advance();
-        // first walk
-        Sums z{0.f, -INFINITY, 0.f, 0.f, -INFINITY};
+        const int buf = nbuf;                       // of the teacher's buffers
+        nbuf = nbuf == TEACHERS - 1 ? 0 : nbuf + 1;
+        const uint8_t* flags = listing(SET ? buf : 0);
+        for (lrow += G; lrow < a.rows && !live_next(lrow); lrow += G) {
+            if (GRAD && walker) {
+                T* z = reinterpret_cast<T*>(a.grad) + lrow * a.ldg;
+                const int h = head_of(z), n = count_of(h), at = odd_of(h);
+                z += h + (int64_t)rank * per * E;
+                for (int i = t; i < n; i += NT) *reinterpret_cast<uint4*>(z + i * E) = make_uint4(0, 0, 0, 0);
+                if (at >= 0) Vec<T>::st(reinterpret_cast<T*>(a.grad) + lrow * a.ldg + at, 0.f);
+            }
+            if (rank == 0 && t == 0) {
+                if (MODE == LM_STATS) a.stats[lrow] = RowStats{0.f, 0.f, 0.f, 0.f};
+                else a.loss[lrow] = 0.f;
+                if (MODE == LM_POLICY) a.logp[lrow] = 0.f;
+            }
+        }
+        lcount = 0;
+        if (lrow < a.rows) {
+            lx = reinterpret_cast<const T*>(a.logits) + lrow * a.ld;
+            lhead = head_of(lx);
+            lcount = count_of(lhead);
+            lp = lx + lhead + (int64_t)(rank * per + t) * E;
+            if (warp == 0) {
+                const int at = odd_of(lhead);
+                lodd = at >= 0 ? Vec<T>::ld(lx + at) : -INFINITY;
+            }
+        }
+        auto put_sums = [&](const Sums& z) {
+            const float wm = warp_max(z.top);
+            const float f = z.limit == -INFINITY ? 0.f : ex2((-z.ref - wm) * c2);
+            const float s = warp_sum(z.s * f);
+            const float si = SET ? warp_sum(z.si * f) : 0.f;
+            if (lane == 0) red[par][warp] = make_float4(wm, s, si, 0.f);
+        };
+        if (!walker) {
+            if (lrow < a.rows) {
 #pragma unroll
-        for (int qd = 0; qd < QUARTERS; ++qd) {
-            // pending behind this quarter: the row's later ones, and (statistics) the next row's earlier ones
-            if (!GRAD || qd == 0) cp_async_wait<3>();
-            else if (qd == 1) cp_async_wait<2>();
-            else if (qd == 2) cp_async_wait<1>();
-            else cp_async_wait<0>();
-            const int end = min(slots, (qd + 1) * quarter);
-#pragma unroll 2
-            for (int u = qd * quarter; u < end; ++u) {
-                if (t + u * NT < count) {
-                    const uint4 raw = ring[u * NT + t];
+                for (int n = 0; n < AHEAD; ++n)
+                    nid[n] = n * 32 + lane < a.k ? a.listed[lrow * a.k + n * 32 + lane].id : -1;
+            }
+            if (row >= 0) {
+                // this row's listed logits, before anything replaces them, and the
+                // sums of the vectors that the walk leaves out
+                const T* x = reinterpret_cast<const T*>(a.logits) + row * a.ld;
+                const uint32_t* leads = reinterpret_cast<const uint32_t*>(flags + (per + 15) / 16 * 16);
+                Sums z{0.f, -INFINITY, 0.f, 0.f, -INFINITY};
+                auto leads_vec = [&](int j0) { return rest_class && j0 < a.k && ((leads[j0 >> 5] >> lane) & 1); };
+                auto vec_of = [&](int id) { return *reinterpret_cast<const uint4*>(x + part0 + (int64_t)((id - part0) / E) * E); };
+                auto sum_vec = [&](int id, const uint4& raw) {
+                    const uint32_t f = flags[(id - part0) / E];
                     follow(z, Vec<T>::vmax(raw), c2, step);
                     float v[E];
                     Vec<T>::unpack(raw, v);
-                    const float sv = exp_vec<E>(v, z.ref, c2);
-                    z.s += sv;
-                    if (rest_class) {
-                        const int i = (t + u * NT) * E;
-                        const uint32_t k = (bits[i >> 5] >> (i & 31)) & ((1u << E) - 1);
-                        if (k == 0) {
-                            z.so += sv;
-                        } else {
 #pragma unroll
-                            for (int j = 0; j < E; ++j)
-                                if (!((k >> j) & 1)) z.so += v[j];
-                        }
+                    for (int j = 0; j < E; ++j) {
+                        const float ev = ex2((v[j] + z.ref) * c2);
+                        if ((f >> j) & 1) z.si += ev;
+                        else z.s += ev;
+                    }
+                };
+                T xr[AHEAD];
+                uint4 raw[AHEAD];
+#pragma unroll
+                for (int n = 0; n < AHEAD; ++n) {
+                    if (rid[n] >= 0) xr[n] = x[rid[n]];
+                    if (leads_vec(32 * n)) raw[n] = vec_of(rid[n]);
+                }
+#pragma unroll
+                for (int n = 0; n < AHEAD; ++n) {
+                    if (rid[n] >= 0) sx[32 * n + lane] = Vec<T>::ld(&xr[n]);
+                    if (leads_vec(32 * n)) sum_vec(rid[n], raw[n]);
+                }
+#pragma unroll 1
+                for (int j0 = 32 * AHEAD; j0 < a.k; j0 += 32) {
+                    const int id = j0 + lane < a.k ? a.listed[row * a.k + j0 + lane].id : -1;
+                    if (id >= 0) sx[j0 + lane] = Vec<T>::ld(x + id);
+                    if (leads_vec(j0)) sum_vec(id, vec_of(id));
+                }
+                put_sums(z);
+            }
+        }
+        if (row >= 0) {
+        if (walker) {
+        // first walk
+        Sums z{0.f, -INFINITY, 0.f, 0.f, -INFINITY};
+        uint64_t ref2 = pair2(0.f, 0.f), sum2 = ref2;
+#pragma unroll
+        for (int qd = 0; qd < QUARTERS; ++qd) {
+            // pending behind this quarter: the row's later ones, and (statistics) the next row's earlier ones
+            cp_async_wait(GRAD ? QUARTERS - 1 - qd : QUARTERS - 1);
+            const int end = min(slots, (qd + 1) * quarter);
+#pragma unroll 1
+            for (int u = qd * quarter; u < end; ++u) {
+                if (t + u * NT < count) {
+                    const uint4 raw = ring[u * NT + t];
+                    const float vm = Vec<T>::vmax(raw);
+                    z.top = fmaxf(z.top, vm);
+                    if (vm > z.limit) {
+                        const float2 h = unpair(sum2);
+                        z.s = h.x + h.y;
+                        follow(z, vm, c2, step);
+                        sum2 = pair2(z.s, 0.f);
+                        ref2 = pair2(z.ref, z.ref);
+                    }
+                    uint64_t v[E / 2];
+                    unpack_pairs<T>(raw, v);
+                    exp_vec<E>(v, ref2, c22);
+                    if (!rest_class || flags[t + u * NT] == 0) {
+#pragma unroll
+                        for (int j = 0; j < E / 2; ++j) sum2 = add2(sum2, v[j]);
                     }
                 }
                 if (!GRAD) issue(u);
             }
             if (!GRAD) cp_async_commit();
         }
-        if (t < 2 * E) {
+        {
+            const float2 h = unpair(sum2);
+            z.s = h.x + h.y;
+        }
+        if (t < 2 * E && rank == 0) {
             follow(z, odd, c2, step);
             const float e = ex2((odd + z.ref) * c2);
-            z.s += e;
-            if (!odd_in) z.so += e;
+            if (rest_class && ((odd_of_row[buf] >> t) & 1)) z.si += e;
+            else z.s += e;
         }
-        float3 q;
-        {
-            const float wm = warp_max(z.top);
-            const float f = z.limit == -INFINITY ? 0.f : ex2((-z.ref - wm) * c2);
-            const float s = warp_sum(z.s * f);
-            const float so = rest_class ? warp_sum(z.so * f) : 0.f;
-            if (lane == 0) red[par][warp] = make_float4(wm, s, so, 0.f);
-            __syncthreads();
-            const float4 r = lane < NW ? red[par][lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-            if (csize == 1) {
-                q = merge_lanes(r.x, r.y, r.z, c2, rest_class);
-            } else {
-                if (warp == 0) {
-                    q = merge_lanes(r.x, r.y, r.z, c2, rest_class);
-                    if (t < csize) st_cluster_f4(smem_addr(&part[par][rank]), (uint32_t)t, make_float4(q.x, q.y, q.z, 0.f));
-                }
-                cluster_barrier();
+        put_sums(z);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            const float4 r = lane < NW + (SET ? 1 : 0) ? red[par][lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+            float3 q = merge_lanes(r.x, r.y, r.z, c2, SET);
+            if (csize > 1) {
+                // the token's logit travels along: it has been read before any CTA's gradient can replace it
+                const uint32_t bar = smem_addr(&bars[par]);
+                if (lane == 0) tc::mbar_expect_tx(bar, (uint32_t)(16 * csize));
+                __syncwarp();
+                if (lane < csize) st_async_f4(smem_addr(&part[par][rank]), bar, (uint32_t)lane, make_float4(q.x, q.y, q.z, xt));
+                tc::wait_bounded(bar, phase[par], &abort_flag, pa.status);
+                phase[par] ^= 1u;
+                __syncwarp();
                 const float4 c = lane < csize ? part[par][lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-                q = merge_lanes(c.x, c.y, c.z, c2, rest_class);
+                q = merge_lanes(c.x, c.y, c.z, c2, SET);
             }
-        }
-        par ^= 1;
-        const float m = q.x, log_s = ::logf(q.y), inv_s = 1.0f / q.y;
-        float in = 0.f, out = 0.f;          // factors of q inside and outside S
-        float scale = 0.f;                  // factor of the sparse part
-        if (MODE == LM_STATS) {
-            if (rank == 0 && t == 0) a.stats[row] = RowStats{m, inv_s, (xt - m) * a.inv_t - log_s, 0.f};
-            continue;
-        } else if (MODE == LM_POLICY) {
-            const float lp_tok = (xt - m) * a.inv_t - log_s;
-            float loss, dl;
-            policy_row(a, row, lp_tok, loss, dl);
-            if (rank == 0 && t == 0) {
-                a.loss[row] = w * loss;
-                a.logp[row] = lp_tok;
-            }
-            scale = w * dl * a.inv_t;
-            out = -scale * inv_s;
-        } else {
-            const float ts = warp_sum(lane < NW ? tred[lane] : 0.f);
-            const float mass = a.tlse ? ts : (ts > 0.f || ts != ts ? 1.0f : 0.f);
-            const float tsub = a.tlse ? lse : ::logf(ts);
-            float rest = 0.f, share = 0.f, kl = 0.f;
-            if (a.tlse) {
-                const float qr = q.z * inv_s;
-                rest = 1.0f - mass;
-                if (!(rest > 0.f && qr > 0.f)) rest = 0.f;
-                else {
-                    share = rest / qr;
-                    kl = rest * ::logf(share);
+            const float m = q.x, all = q.y + q.z, log_s = ::logf(all), inv_s = 1.0f / all;
+            const bool writes = rank == 0 && lane == 0;
+            if (MODE == LM_STATS) {
+                if (writes) a.stats[row] = RowStats{m, inv_s, (xt - m) * a.inv_t - log_s, 0.f};
+            } else {
+                const float w = pr.w;
+                if (MODE == LM_POLICY) {
+                    const float lt = (xt - m) * a.inv_t - log_s;
+                    float loss, dl;
+                    policy_row(a, pr, lt, loss, dl);
+                    if (writes) {
+                        a.loss[row] = w * loss;
+                        a.logp[row] = lt;
+                    }
+                    const float scale = w * dl * a.inv_t;
+                    if (lane == 0) factors = make_float4(m, 0.f, -scale * inv_s, scale);
+                } else {
+                    float rest = 0.f, share = 0.f, kl = 0.f;
+                    if (rest_class) {
+                        const float qr = q.y * inv_s;
+                        rest = 1.0f - mass;
+                        if (!(rest > 0.f && qr > 0.f)) rest = 0.f;
+                        else {
+                            share = rest / qr;
+                            kl = rest * ::logf(share);
+                        }
+                    }
+                    const float scale = w * a.t;
+                    if (lane == 0) {
+                        factors = make_float4(m, scale * (mass + rest) * inv_s, scale * (mass + rest - share) * inv_s, scale);
+                        terms = make_float3(log_s, kl, w * a.t * a.t);
+                    }
                 }
             }
-            float part_kl = 0.f;
-            for (int j = t; j < a.k; j += NT) {
-                const float lpj = sidx[j] >= 0 ? (slp[j] - tm) * a.inv_t - tsub : -INFINITY;
-                const float p = expf(lpj);
-                sp[j] = p;
-                if (p > 0.f) part_kl += p * (lpj - ((sx[j] - m) * a.inv_t - log_s));
-                else if (p != p) part_kl = p;
+        }
+        }
+        if (!walker && rest_class && lrow < a.rows) {
+            // the next row's listing, while warp 0 brings this row's sums together
+            uint8_t* to = listing(nbuf);
+            for (int i = lane; i < (per + 15) / 16; i += 32) reinterpret_cast<uint4*>(to)[i] = make_uint4(0, 0, 0, 0);
+            if (lane == 0) odd_of_row[nbuf] = 0;
+            __syncwarp();
+#pragma unroll
+            for (int n = 0; n < AHEAD; ++n)
+                if (32 * n < a.k) list(nbuf, 32 * n, nid[n]);
+#pragma unroll 1
+            for (int j0 = 32 * AHEAD; j0 < a.k; j0 += 32)
+                list(nbuf, j0, j0 + lane < a.k ? a.listed[lrow * a.k + j0 + lane].id : -1);
+        }
+        if (GRAD) __syncthreads();
+        const float4 fac = factors;
+        const float m = fac.x, scale = fac.w;
+        if (!walker) {
+            if (row >= 0) {
+                const Listed* e = a.listed + row * a.k;
+                const int tail = head + (V - head) / E * E;
+                float kl = 0.f, psum[AHEAD];
+                // of an entry: its term of the loss, and its p if this part stores it (an index listed
+                // twice counts twice, at its first entry)
+                auto take = [&](int j) {
+                    const Listed q = e[j];
+                    if (q.p > 0.f) kl += q.p * (q.lp - ((sx[j] - m) * a.inv_t - terms.x));
+                    else if (q.p != q.p) kl = q.p;
+                    const int at = q.id - part0;
+                    const bool mine = (at >= 0 && at < count * E) || (rank == 0 && (q.id < head || q.id >= tail));
+                    return q.id >= 0 && mine ? q.psum : -1.0f;
+                };
+                auto store = [&](int id, int j, float p) {
+                    if (!(p < 0.f)) Vec<T>::st(g + id, fac.y * ex2((sx[j] - m) * c2) - scale * p);
+                };
+#pragma unroll
+                for (int n = 0; n < AHEAD; ++n) psum[n] = 32 * n + lane < a.k ? take(32 * n + lane) : -1.0f;
+#pragma unroll 1
+                for (int j = 32 * AHEAD + lane; j < a.k; j += 32) take(j);
+                if (rank == 0) {            // the row's loss
+                    kl = warp_sum(kl);
+                    if (lane == 0) a.loss[row] = terms.z * (terms.y + kl);
+                }
+                asm volatile("bar.sync 1, %0;" ::"n"(NT + 32) : "memory");      // the second walk is through
+#pragma unroll
+                for (int n = 0; n < AHEAD; ++n) store(rid[n], 32 * n + lane, psum[n]);
+#pragma unroll 1
+                for (int j = 32 * AHEAD + lane; j < a.k; j += 32) store(e[j].id, j, take(j));
             }
-            part_kl = warp_sum(part_kl);
-            if (lane == 0) lred[warp] = part_kl;
-            scale = w * a.t;
-            in = scale * (mass + rest) * inv_s;
-            out = scale * (mass + rest - share) * inv_s;
-            __syncthreads();
-            if (rank == 0 && warp == 0) {
-                part_kl = warp_sum(lane < NW ? lred[lane] : 0.f);
-                if (t == 0) a.loss[row] = w * a.t * a.t * (kl + part_kl);
-            }
+#pragma unroll
+            for (int n = 0; n < AHEAD; ++n) rid[n] = nid[n];
+            row = lrow;
+            continue;
         }
         // second walk: out q everywhere, the token's entry on the way
+        const uint64_t out2 = pair2(fac.z, fac.z);
+        const uint64_t ref2 = pair2(-m, -m);
         T* gp = g + part0 + t * E;
         const int tok_at = tok - part0;     // within the part's vectors, if there
 #pragma unroll
-        for (int qd = 0; qd < QUARTERS; ++qd) {
+        for (int qd = 0; qd < QUARTERS && (GRAD || row < 0); ++qd) {
             const int end = min(slots, (qd + 1) * quarter);
-#pragma unroll 2
+#pragma unroll 1
             for (int u = qd * quarter; u < end; ++u) {
                 const int i = t + u * NT;
-                if (i < count) {
-                    float v[E];
-                    Vec<T>::unpack(ring[i], v);
-                    exp_vec<E>(v, -m, c2);
+                if (GRAD && row >= 0 && i < count) {
+                    uint64_t v[E / 2];
+                    float f[E];
+                    unpack_pairs<T>(ring[i], v);
+                    exp_vec<E>(v, ref2, c22);
 #pragma unroll
-                    for (int j = 0; j < E; ++j) v[j] *= out;
+                    for (int j = 0; j < E / 2; ++j) v[j] = mul2(v[j], out2);
+                    split_pairs<E>(v, f);
                     if (MODE == LM_POLICY && (unsigned)(tok_at - i * E) < (unsigned)E) {
 #pragma unroll
                         for (int j = 0; j < E; ++j)
-                            if (i * E + j == tok_at) v[j] += scale;
+                            if (i * E + j == tok_at) f[j] += scale;
                     }
                     if (a.same_align) {
-                        *reinterpret_cast<uint4*>(gp + u * (NT * E)) = Vec<T>::pack(v);
+                        *reinterpret_cast<uint4*>(gp + u * (NT * E)) = Vec<T>::pack(f);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < E; ++j) Vec<T>::st(gp + u * (NT * E) + j, v[j]);
+                        for (int j = 0; j < E; ++j) Vec<T>::st(gp + u * (NT * E) + j, f[j]);
                     }
                 }
                 issue(u);
             }
             cp_async_commit();
         }
-        if (odd_of(head) >= 0) {
+        if (GRAD && warp == 0 && row >= 0) {
             const int at = odd_of(head);
-            Vec<T>::st(g + at, ex2((odd - m) * c2) * out + (MODE == LM_POLICY && at == tok ? scale : 0.f));
+            if (at >= 0)
+                Vec<T>::st(g + at, ex2((odd - m) * c2) * fac.z + (MODE == LM_POLICY && at == tok ? scale : 0.f));
         }
-        if (MODE == LM_DISTILL) {
-            __syncthreads();                // the listed entries' own values go over what the walk stored
-            for (int j = t; j < a.k; j += NT) {
-                const int id = sidx[j], at = id - part0;
-                const bool vec = at >= 0 && at < count * E;
-                // an odd logit (before the vectors, or after the row's last) is the first CTA's
-                const bool end = rank == 0 && (id < head || id >= head + (V - head) / E * E);
-                if (id < 0 || !(vec || end)) continue;
-                float psum = 0.f;           // an index the teacher lists twice counts twice
-                bool leads = true;
+        if (SET && row >= 0) asm volatile("bar.arrive 1, %0;" ::"n"(NT + 32) : "memory");
+        row = lrow;
+    } while (row < a.rows);
+    cp_async_wait(0);
+    if (csize > 1) {
+        __syncthreads();
+        tc::cluster_sync();                 // no CTA leaves while another may still write to its shared memory
+    }
+}
+
+// The teacher's side of every row, a warp per row: its softmax over the listed
+// entries (or against its own log-sum-exp), and repeated indices brought
+// together (looked for only where two entries of a row share a bit of a 32768-bit
+// map).  The student's logits at the entries are left to the row's own CTAs,
+// which read them while they read the row: gathered here, from all over the
+// logits at once, they took 0.4 ms for 9155 x 64.
+constexpr int TW = 4;                       // warps of a CTA
+__global__ void __launch_bounds__(32 * TW) teacher_kernel(const __grid_constant__ RowLossArgs a) {
+    __shared__ __align__(16) uint32_t seen[TW][1024];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();
+    pdl_trigger();
+    for (int64_t row = (int64_t)blockIdx.x * TW + warp; row < a.rows; row += (int64_t)gridDim.x * TW) {
+        if (a.weights && a.weights[row] == 0.f) continue;
+        auto entry = [&](int j, float& v) {
+            const int64_t id = ld_index(a.tidx, row * a.k + j, a.tidx64);
+            const bool ok = id >= 0 && id < a.vocab;
+            v = ok ? ld_elem(a.tval, row * a.k + j, a.tval_dtype) : -INFINITY;
+            return ok ? (int)id : -1;
+        };
+        float tm = 0.f, lse = 0.f, v;
+        if (a.tlse) {
+            lse = a.tlse[row];
+        } else {
+            tm = -INFINITY;
+            for (int j = lane; j < a.k; j += 32) {
+                entry(j, v);
+                tm = fmaxf(tm, v);
+            }
+            tm = warp_max(tm);
+        }
+        for (int i = lane; i < 256; i += 32) reinterpret_cast<uint4*>(seen[warp])[i] = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+        float s = 0.f;
+        bool again = false;
+        for (int j = lane; j < a.k; j += 32) {
+            const int id = entry(j, v);
+            if (id < 0) continue;
+            s += expf((v - tm) * a.inv_t - lse);
+            const uint32_t bit = 1u << (id & 31);
+            again = (atomicOr(&seen[warp][(id >> 5) & 1023], bit) & bit) || again;
+        }
+        s = warp_sum(s);
+        again = __any_sync(0xffffffffu, again);
+        if (!a.tlse) {
+            lse = ::logf(s);
+            s = s > 0.f || s != s ? 1.0f : 0.f;         // nothing listed: no distribution, no loss
+        }
+        Listed* out = a.listed + row * a.k;
+        for (int j = lane; j < a.k; j += 32) {
+            Listed e;
+            e.id = entry(j, v);
+            e.lp = e.id >= 0 ? (v - tm) * a.inv_t - lse : -INFINITY;
+            e.p = expf(e.lp);
+            e.psum = e.p;
+            out[j] = e;
+        }
+        if (again) {
+            __syncwarp();
+            for (int j = lane; j < a.k; j += 32) {
+                const int id = out[j].id;
+                float sum = 0.f;
+                bool first = true;
                 for (int n = 0; n < a.k; ++n) {
-                    if (sidx[n] == id) {
-                        psum += sp[n];
-                        leads = leads && n >= j;
+                    if (out[n].id == id) {
+                        sum += out[n].p;
+                        first = first && n >= j;
                     }
                 }
-                if (leads) Vec<T>::st(g + id, in * ex2((sx[j] - m) * c2) - scale * psum);
-                if (rest_class && vec) bits[at >> 5] = 0;
+                out[j].psum = first ? sum : -1.0f;
             }
         }
+        if (lane == 0) a.mass[row] = s;
+        __syncwarp();
     }
-    cp_async_wait<0>();
-    if (csize > 1) cluster_barrier();       // no CTA leaves while another may still write to its shared memory
 }
 
 constexpr int UNROLL = 4;          // vectors of a gradient row in flight per thread
@@ -786,38 +1008,40 @@ __global__ void __launch_bounds__(256) pair_kernel(const __grid_constant__ PairA
 // host side
 // ---------------------------------------------------------------------------
 
-constexpr int64_t MAX_VOCAB = (int64_t)MAX_CLUSTER * SLOTS * 512 * 4;   // fp32: 425984
+constexpr int64_t MAX_VOCAB = 1 << 19;
 constexpr int MAX_TEACHER = 1024;
 
-constexpr int SMALL_NT = 128;           // threads of a CTA whose whole row fits SLOTS x 128 vectors; else 512
-
 // Shared memory of a row's CTA: its part of the row, and for distillation the
-// teacher's entries and the bitmap of its set.
+// listings of three rows.
 template <typename T, int MODE, int NT>
-size_t row_smem(int per, int k, bool rest) {
+size_t row_smem(int per, int k) {
     size_t b = (size_t)((per + NT - 1) / NT) * NT * 16;
-    if (MODE == LM_DISTILL) b += 16 * (size_t)k + (rest ? 4 * (size_t)bit_words(per * Vec<T>::E) : 0);
+    if (MODE == LM_DISTILL) b += (size_t)TEACHERS * listing_bytes(per, k) + (size_t)(k + 3) / 4 * 16;
     return b;
 }
 
+// Shared memory up to which four CTAs share an SM, and what a CTA may have.
+constexpr size_t QUARTER_SM = 55500, MAX_SMEM = 220000;
+
 template <typename T, int MODE, int NT>
-cudaError_t launch_part(const RowLossArgs& a, int64_t nv, int csize, cudaStream_t s) {
+cudaError_t launch_part(const RowLossArgs& a, int64_t nv, int csize, int* status, cudaStream_t s) {
     auto kern = row_loss_kernel<T, MODE, NT>;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     std::call_once(once, [&] {
         err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   (int)row_smem<T, MODE, NT>(SLOTS * NT, MAX_TEACHER, true));
+                                   (int)MAX_SMEM);
         if (err == cudaSuccess) err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     });
     if (err != cudaSuccess) return err;
     PartArgs pa;
     pa.csize = csize;
     pa.per = (int)((nv + csize - 1) / csize);
+    pa.status = status;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)csize);
-    cfg.blockDim = dim3(NT);
-    cfg.dynamicSmemBytes = row_smem<T, MODE, NT>(pa.per, a.k, a.tlse != nullptr);
+    cfg.blockDim = dim3(NT + TEACHER<MODE>);
+    cfg.dynamicSmemBytes = row_smem<T, MODE, NT>(pa.per, a.k);
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -826,58 +1050,70 @@ cudaError_t launch_part(const RowLossArgs& a, int64_t nv, int csize, cudaStream_
     at[1].val.clusterDim.x = (unsigned)csize;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     // clusters resident at once, by cluster size and slots
-    static std::atomic<int> fits[MAX_CLUSTER + 1][SLOTS + 1];
+    static std::atomic<int> fits[MAX_CLUSTER + 1][64];
     std::atomic<int>& fit = fits[csize][(pa.per + NT - 1) / NT];
     int n = fit.load();
     if (n == 0) {
         cfg.attrs = at + 1;
         cfg.numAttrs = 1;
         cudaLaunchConfig_t most = cfg;
-        most.dynamicSmemBytes = row_smem<T, MODE, NT>((pa.per + NT - 1) / NT * NT, MODE == LM_DISTILL ? 256 : 0, true);
+        most.dynamicSmemBytes = row_smem<T, MODE, NT>((pa.per + NT - 1) / NT * NT, MODE == LM_DISTILL ? 256 : 0);
         cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kern, &most);
         if (e != cudaSuccess) return e;
         if (n < 1) return cudaErrorInvalidConfiguration;
         fit.store(n);
+        muon::logf(2, "row loss mode %d: %d threads, %d CTAs per row, %d vectors each, %zu bytes, %d clusters", MODE, NT, csize, pa.per, most.dynamicSmemBytes, n);
     }
     cfg.gridDim = dim3((unsigned)(csize * std::min<int64_t>(a.rows, n)));
-    cfg.attrs = pdl_enabled() ? at : at + 1;
-    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    // A launch whose clusters walk several rows each waits for the one before it
+    // to end: placed beside its last CTAs, clusters may leave holes that one of
+    // them does not fit, and its rows then follow as a wave of their own (measured
+    // behind teacher_kernel: 0.64 ms became 1.0).
+    const bool early = pdl_enabled() && a.rows <= n;
+    cfg.attrs = early ? at : at + 1;
+    cfg.numAttrs = early ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, a, pa);
 }
 
-// How a launch divides its rows: 128-thread CTAs for rows of up to 13 x 128
-// vectors; else 512-thread CTAs, as few per row as hold it, twice as many while
-// the rows alone would leave SMs idle and a CTA keeps two vectors per thread.
+
+// How a launch divides its rows: 128-thread CTAs for rows of up to SLOTS vectors
+// per thread of theirs; else 256-thread CTAs, as few per row as hold it with four
+// CTAs on an SM (16 at most, then with more shared memory each), twice as many
+// while the rows alone would leave SMs idle and a thread keeps four vectors.
+// Four CTAs of 256 threads beat two of 512 (a CTA's wait between its walks is
+// hidden by the others): 131072 bf16 logits 530 -> 482 us for 1.2 GB of logits,
+// fp32 459 -> 423; eight of 128 with twice the slots took 567 and 501.
 template <typename T, int MODE>
-cudaError_t launch_mode(const RowLossArgs& a, int sms, cudaStream_t s) {
-    constexpr int E = Vec<T>::E;
-    const int64_t nv = std::max(1, a.vocab / E);       // whole vectors of a row at most
-    if (nv <= SLOTS * SMALL_NT) return launch_part<T, MODE, SMALL_NT>(a, nv, 1, s);
-    int c = (int)((nv + SLOTS * 512 - 1) / (SLOTS * 512));
-    while (c <= 4 && a.rows * c < sms && nv > (int64_t)c * 1024) c *= 2;
-    return launch_part<T, MODE, 512>(a, nv, c, s);
+cudaError_t launch_mode(const RowLossArgs& a, const DevCtx& dc, cudaStream_t s) {
+    constexpr int NT = 256 - TEACHER<MODE>, SMALL = 128 - TEACHER<MODE>;
+    const int64_t nv = std::max(1, a.vocab / Vec<T>::E);       // whole vectors of a row at most
+    if (nv <= SLOTS * SMALL) return launch_part<T, MODE, SMALL>(a, nv, 1, dc.status, s);
+    int c = (int)std::min<int64_t>(MAX_CLUSTER, (nv + SLOTS * NT - 1) / (SLOTS * NT));
+    while (c < MAX_CLUSTER && row_smem<T, MODE, NT>((int)((nv + c - 1) / c), a.k) > QUARTER_SM && nv > (int64_t)c * 4 * NT) ++c;
+    while (c <= 4 && a.rows * c < dc.sms && nv > (int64_t)c * 4 * NT) c *= 2;
+    return launch_part<T, MODE, NT>(a, nv, c, dc.status, s);
 }
 
 template <typename T>
-cudaError_t launch_rows(const RowLossArgs& a, int mode, int sms, cudaStream_t s) {
-    if (mode == LM_POLICY) return launch_mode<T, LM_POLICY>(a, sms, s);
-    if (mode == LM_STATS) return launch_mode<T, LM_STATS>(a, sms, s);
-    return launch_mode<T, LM_DISTILL>(a, sms, s);
+cudaError_t launch_rows(const RowLossArgs& a, int mode, const DevCtx& dc, cudaStream_t s) {
+    if (mode == LM_POLICY) return launch_mode<T, LM_POLICY>(a, dc, s);
+    if (mode == LM_STATS) return launch_mode<T, LM_STATS>(a, dc, s);
+    return launch_mode<T, LM_DISTILL>(a, dc, s);
 }
 
 template <typename T>
 cudaError_t launch_grad(const RowLossArgs& a, int sms, cudaStream_t s) {
-    if (a.vocab <= SMALL_NT * UNROLL * Vec<T>::E)
+    if (a.vocab <= 128 * UNROLL * Vec<T>::E)
         return launch_pdl(row_grad_kernel<T, 128>, dim3((unsigned)std::min<int64_t>(a.rows, (int64_t)sms * 8)), dim3(128),
                           0, s, a);
     return launch_pdl(row_grad_kernel<T, 512>, dim3((unsigned)std::min<int64_t>(a.rows, (int64_t)sms * 2)), dim3(512), 0,
                       s, a);
 }
 
-cudaError_t dispatch_rows(const RowLossArgs& a, int mode, int dtype, int sms, cudaStream_t s) {
-    if (dtype == MUON_F32) return launch_rows<float>(a, mode, sms, s);
-    if (dtype == MUON_BF16) return launch_rows<__nv_bfloat16>(a, mode, sms, s);
-    return launch_rows<__half>(a, mode, sms, s);
+cudaError_t dispatch_rows(const RowLossArgs& a, int mode, int dtype, const DevCtx& dc, cudaStream_t s) {
+    if (dtype == MUON_F32) return launch_rows<float>(a, mode, dc, s);
+    if (dtype == MUON_BF16) return launch_rows<__nv_bfloat16>(a, mode, dc, s);
+    return launch_rows<__half>(a, mode, dc, s);
 }
 
 cudaError_t dispatch_grad(const RowLossArgs& a, int dtype, int sms, cudaStream_t s) {
@@ -895,7 +1131,7 @@ int row_args(RowLossArgs& a, const void* logits, int64_t ld, int64_t rows, int64
     std::memset(&a, 0, sizeof a);
     if (!valid_dtype(dtype)) return fail(MUON_EDTYPE, "logits dtype %d", dtype);
     if (rows < 0 || rows > INT32_MAX) return fail(MUON_EINVAL, "rows outside [0, 2^31)");
-    if (vocab < 1 || vocab > MAX_VOCAB) return fail(MUON_EINVAL, "vocab outside [1, %lld]", (long long)MAX_VOCAB);
+    if (vocab < 1 || vocab > MAX_VOCAB) return fail(MUON_EINVAL, "vocab outside [1, 2^19]");
     if (ld < vocab || ld_grad < vocab) return fail(MUON_EINVAL, "row pitch below vocab");
     if (ld > INT64_MAX / 8 / std::max<int64_t>(rows, 1) || ld_grad > INT64_MAX / 8 / std::max<int64_t>(rows, 1))
         return fail(MUON_EINVAL, "byte range overflows");
@@ -944,8 +1180,18 @@ extern "C" int muon_distill_loss(const void* logits, int64_t ld, int64_t rows, i
     a.tval = teacher_logits; a.tval_dtype = teacher_dtype;
     a.tlse = teacher_lse; a.k = (int)k;
     a.weights = weights; a.loss = loss;
+    const size_t listed = align_up(sizeof(Listed) * (size_t)rows * (size_t)k, 256);
+    Workspace* w = nullptr;
+    if ((r = ws_get(dc.device, s, listed + sizeof(float) * (size_t)rows, &w))) return r;
+    a.listed = reinterpret_cast<Listed*>(w->base);
+    a.mass = reinterpret_cast<float*>(w->base + listed);
+    const dim3 tg((unsigned)std::min<int64_t>((rows + TW - 1) / TW, (int64_t)dc.sms * 12));
     note_launch_begin(KC_LOSS, s);
-    cudaError_t e = dispatch_rows(a, LM_DISTILL, dtype, dc.sms, s);
+    cudaError_t e = launch_pdl(teacher_kernel, tg, dim3(32 * TW), 0, s, a);
+    note_launch_end(KC_LOSS, 0.0, s);
+    if (e != cudaSuccess) return cuda_fail(e, "teacher launch");
+    note_launch_begin(KC_LOSS, s);
+    e = dispatch_rows(a, LM_DISTILL, dtype, dc, s);
     note_launch_end(KC_LOSS, 2.0 * (double)rows * vocab * esize(dtype), s);
     if (e != cudaSuccess) return cuda_fail(e, "distillation launch");
     return MUON_OK;
@@ -974,7 +1220,7 @@ extern "C" int muon_policy_loss(const void* logits, int64_t ld, int64_t rows, in
     a.lo = (float)(1.0 - (double)clip_low); a.hi = (float)(1.0 + (double)clip_high); a.kl = kl_coef;
     a.loss = loss; a.logp = logp;
     note_launch_begin(KC_LOSS, s);
-    cudaError_t e = dispatch_rows(a, LM_POLICY, dtype, dc.sms, s);
+    cudaError_t e = dispatch_rows(a, LM_POLICY, dtype, dc, s);
     note_launch_end(KC_LOSS, 2.0 * (double)rows * vocab * esize(dtype), s);
     if (e != cudaSuccess) return cuda_fail(e, "policy loss launch");
     return MUON_OK;
@@ -1007,7 +1253,7 @@ extern "C" int muon_preference_loss(const void* logits, int64_t ld, int64_t rows
     cudaError_t e;
     if (rows > 0) {
         note_launch_begin(KC_LOSS, s);
-        e = dispatch_rows(a, LM_STATS, dtype, dc.sms, s);
+        e = dispatch_rows(a, LM_STATS, dtype, dc, s);
         note_launch_end(KC_LOSS, bytes, s);
         if (e != cudaSuccess) return cuda_fail(e, "preference statistics launch");
     }

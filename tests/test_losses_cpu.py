@@ -39,7 +39,7 @@ def preference(mg, **kw):
 
 NAN, INF = float("nan"), float("inf")
 SHARED = [dict(logits=None), dict(grad=None), dict(rows=-1), dict(rows=1 << 31), dict(vocab=0),
-          dict(vocab=(1 << 20) + 1, ld=1 << 21, ldg=1 << 21), dict(ld=63), dict(ldg=63), dict(ld=65),
+          dict(vocab=(1 << 19) + 1, ld=1 << 21, ldg=1 << 21), dict(ld=63), dict(ldg=63), dict(ld=65),
           dict(ld=1 << 61, ldg=1 << 61), dict(logits=P + 1), dict(grad=P + 64), dict(loss=None)]
 
 
