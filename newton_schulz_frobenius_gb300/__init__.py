@@ -149,8 +149,11 @@ def _dtype_code(t) -> int:
 
 
 def _stream_ptr(stream) -> int:
-    import torch
     if stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and torch.cuda.is_initialized():
+            return raw(torch.cuda.current_device())     # the handle without a Stream object around it
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -520,7 +523,11 @@ def _index_code(t, name) -> int:
 
 def _rows_of(t, name):
     """(pointer, row pitch) of a rows x cols CUDA tensor whose rows are contiguous."""
-    if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor with contiguous rows")
+    if t.is_contiguous():
+        return t.data_ptr(), max(1, t.shape[1])
+    if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must be a 2-D CUDA tensor with contiguous rows")
     pitch = t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1])
     if pitch < t.shape[1]:
@@ -543,8 +550,10 @@ def _vector(t, n, name, dtype=None):
 def _grad_like(logits, grad, stream):
     import torch
     if grad is None:
+        if stream is None:
+            return torch.empty_like(logits, memory_format=torch.contiguous_format)
         with _on_stream(stream):
-            return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+            return torch.empty_like(logits, memory_format=torch.contiguous_format)
     if grad.shape != logits.shape or grad.dtype != logits.dtype:
         raise ValueError("grad must have the logits' shape and dtype")
     return grad
@@ -552,6 +561,8 @@ def _grad_like(logits, grad, stream):
 
 def _f32_out(n, like, stream):
     import torch
+    if stream is None:
+        return torch.empty(n, dtype=torch.float32, device=like.device)
     with _on_stream(stream):
         return torch.empty(n, dtype=torch.float32, device=like.device)
 

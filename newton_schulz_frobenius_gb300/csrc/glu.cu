@@ -428,7 +428,8 @@ glu_kernel(const __grid_constant__ GluMaps maps, const __grid_constant__ GluArgs
 // SM over R = 8, 16, ..., 64 (14336 rows on 152 SMs: R = 48, two tiles each).
 // G and U of one ffn row sit in different lanes; U goes through shared memory.
 constexpr int FEW_TOKENS = 128;
-constexpr int FEW_STAGES = 12;
+constexpr int FEW_SUB = 2;           // k-blocks of a stage
+constexpr int FEW_STAGES = 6;
 constexpr int FEW_EPI = 4;
 constexpr int FEW_T = 64 + 32 * FEW_EPI;
 constexpr int FEW_BARS = 2 * FEW_STAGES + 5;
@@ -448,7 +449,7 @@ glu_few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
                const __grid_constant__ CUtensorMap mu, const __grid_constant__ FewArgs g) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int stage_bytes = OP_BYTES + g.n * 128, S = g.stages;
+    const int block_bytes = OP_BYTES + g.n * 128, stage_bytes = FEW_SUB * block_bytes, S = g.stages;
     float(*up)[33] = reinterpret_cast<float(*)[33]>(smem + S * stage_bytes);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * stage_bytes + 64 * 33 * 4);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + FEW_BARS);
@@ -481,7 +482,7 @@ glu_few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
     pdl_trigger();
     if (warp == 0) {
         if (lane == 0) {
-            const uint32_t bytes = (uint32_t)(2 * g.R * 128 + g.n * 128);
+            const uint32_t bytes = (uint32_t)(FEW_SUB * (2 * g.R * 128 + g.n * 128));
             uint32_t flight = 0, phases = 0;        // per stage: a copy was issued, and its phase
             int stage = 0;
             uint32_t phase = 0;
@@ -494,9 +495,14 @@ glu_few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
                     }
                     const uint32_t fb = full0 + 8 * stage, a = smem_u32(smem + stage * stage_bytes);
                     mbar_expect_tx(fb, bytes);
-                    tma_load_3d(a, &mg, fb, kb * GK, t * g.R, 0);
-                    tma_load_3d(a + OP_BYTES / 2, &mu, fb, kb * GK, t * g.R, 0);
-                    tma_load_3d(a + OP_BYTES, &mx, fb, kb * GK, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < FEW_SUB; ++i) {
+                        const uint32_t at = a + i * block_bytes;
+                        const int k0 = (kb * FEW_SUB + i) * GK;
+                        tma_load_3d(at, &mg, fb, k0, t * g.R, 0);
+                        tma_load_3d(at + OP_BYTES / 2, &mu, fb, k0, t * g.R, 0);
+                        tma_load_3d(at + OP_BYTES, &mx, fb, k0, 0, 0);
+                    }
                     flight |= 1u << stage;
                     phases = (phases & ~(1u << stage)) | (phase << stage);
                     if (++stage == S) {
@@ -527,11 +533,14 @@ glu_few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a = smem_u32(smem + stage * stage_bytes), b = a + OP_BYTES;
 #pragma unroll
-                    for (int kk = 0; kk < GK / 16; ++kk)
-                        tc_mma_bf16(tmem + (uint32_t)(acc * FEW_TOKENS), sdesc(a + kk * 32, 16, 1024),
-                                    sdesc(b + kk * 32, 16, 1024), idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                    for (int i = 0; i < FEW_SUB; ++i) {
+                        const uint32_t a = smem_u32(smem + stage * stage_bytes + i * block_bytes), b = a + OP_BYTES;
+#pragma unroll
+                        for (int kk = 0; kk < GK / 16; ++kk)
+                            tc_mma_bf16(tmem + (uint32_t)(acc * FEW_TOKENS), sdesc(a + kk * 32, 16, 1024),
+                                        sdesc(b + kk * 32, 16, 1024), idesc, (kb > 0 || i > 0 || kk > 0) ? 1u : 0u);
+                    }
                     tc_commit(empty0 + 8 * stage);
                     if (++stage == S) {
                         stage = 0;
@@ -842,7 +851,7 @@ int launch_few(const Operand& X, const Operand& W, const Operand& U, FewArgs& g,
             g.tiles = (int)n;
         }
     }
-    const int stage_bytes = OP_BYTES + g.n * 128;
+    const int stage_bytes = FEW_SUB * (OP_BYTES + g.n * 128);
     g.stages = std::min(FEW_STAGES, (232448 - FEW_FIXED) / stage_bytes);
     CUtensorMap mx, mg, mu;
     if (!map_in(&mx, X, g.dtype, GK, (uint32_t)g.n) || !map_in(&mg, W, g.dtype, GK, (uint32_t)g.R) ||
@@ -894,7 +903,7 @@ extern "C" int muon_glu_forward(const void* x, const void* w_gate, const void* w
         FewArgs f;
         std::memset(&f, 0, sizeof f);
         f.dtype = dtype; f.act = act; f.save = gate != nullptr;
-        f.tokens = (int)tokens; f.ffn = (int)ffn; f.kblocks = (int)((hidden + GK - 1) / GK);
+        f.tokens = (int)tokens; f.ffn = (int)ffn; f.kblocks = (int)((hidden + FEW_SUB * GK - 1) / (FEW_SUB * GK));
         f.out[0] = GluOut{h, ffn}; f.out[1] = GluOut{gate, ffn}; f.out[2] = GluOut{up, ffn};
         f.status = dc.status;
         return launch_few(X, G, U, f, dc.sms, s);

@@ -88,6 +88,7 @@ struct Vec;
 template <>
 struct Vec<float> {
     static constexpr int E = 4;
+    static constexpr uint32_t NONE = 0xFF800000u;       // a word of -inf
     static __device__ __forceinline__ float ld(const float* p) { return *p; }
     static __device__ __forceinline__ void st(float* p, float v) { *p = v; }
     static __device__ __forceinline__ void unpack(const uint4& q, float (&v)[4]) {
@@ -104,6 +105,7 @@ struct Vec<float> {
 template <>
 struct Vec<__nv_bfloat16> {
     static constexpr int E = 8;
+    static constexpr uint32_t NONE = 0xFF80FF80u;
     static __device__ __forceinline__ float ld(const __nv_bfloat16* p) { return __bfloat162float(*p); }
     static __device__ __forceinline__ void st(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
     static __device__ __forceinline__ void unpack(const uint4& q, float (&v)[8]) { unpack8_h(q, v, false); }
@@ -117,6 +119,7 @@ struct Vec<__nv_bfloat16> {
 template <>
 struct Vec<__half> {
     static constexpr int E = 8;
+    static constexpr uint32_t NONE = 0xFC00FC00u;
     static __device__ __forceinline__ float ld(const __half* p) { return __half2float(*p); }
     static __device__ __forceinline__ void st(__half* p, float v) { *p = __float2half_rn(v); }
     static __device__ __forceinline__ void unpack(const uint4& q, float (&v)[8]) { unpack8_h(q, v, true); }
@@ -281,8 +284,11 @@ __device__ __forceinline__ void split_pairs(const uint64_t (&v)[E / 2], float (&
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes into shared memory if `on` (predicated: no branch in the walks)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst),
+                 "l"(src), "r"((int)on)
+                 : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits until at most n (0 .. 3) of the thread's copy groups are pending.
@@ -393,7 +399,8 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
     __shared__ float4 red[2][NW + 1];
     __shared__ __align__(16) float4 part[2][MAX_CLUSTER];
     __shared__ __align__(8) uint64_t bars[2];
-    __shared__ float4 factors;                          // maximum, factors of q inside and outside S, factor of t
+    __shared__ float4 factors;                          // maximum, factors of e inside and outside S (policy: the token's
+                                                        // gradient, factor of e), factor of t
     __shared__ float3 terms;                            // distillation: log of the sum, the rest's term, weight T^2
     __shared__ uint32_t odd_of_row[TEACHERS];           // which of the row's odd logits are listed
     __shared__ int abort_flag;
@@ -447,6 +454,12 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
         return at < V ? at : -1;
     };
 
+    // the thread that has logit `at` as its odd one, -1: none
+    auto odd_thread = [&](int head, int at) {
+        const int tail = head + (V - head) / E * E;
+        return at < head ? at : at >= tail ? head + at - tail : -1;
+    };
+
     // the row in the loss after the one worked on: its vectors are copied in as slots fall free
     const T* lx = nullptr;
     const T* lp = nullptr;                              // this thread's first vector of it
@@ -455,7 +468,7 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
     int64_t lrow = row0 - G;
     const uint32_t slot0 = smem_addr(ring + t);
     auto issue = [&](int u) {
-        if (t + u * NT < lcount) cp_async16(slot0 + u * (NT * 16), lp + u * (NT * E));
+        cp_async16(slot0 + u * (NT * 16), lp + u * (NT * E), t + u * NT < lcount);
     };
     const bool walker = !SET || warp < NW;
     // The entries' warp holds the indices of the first AHEAD x 32 entries of this
@@ -597,6 +610,9 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
         // first walk
         Sums z{0.f, -INFINITY, 0.f, 0.f, -INFINITY};
         uint64_t ref2 = pair2(0.f, 0.f), sum2 = ref2;
+        // slots beyond the part read as -inf
+        for (int u = count / NT; u < slots; ++u)
+            if (t + u * NT >= count) ring[u * NT + t] = make_uint4(Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE);
 #pragma unroll
         for (int qd = 0; qd < QUARTERS; ++qd) {
             // pending behind this quarter: the row's later ones, and (statistics) the next row's earlier ones
@@ -604,24 +620,23 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
             const int end = min(slots, (qd + 1) * quarter);
 #pragma unroll 1
             for (int u = qd * quarter; u < end; ++u) {
-                if (t + u * NT < count) {
-                    const uint4 raw = ring[u * NT + t];
-                    const float vm = Vec<T>::vmax(raw);
-                    z.top = fmaxf(z.top, vm);
-                    if (vm > z.limit) {
-                        const float2 h = unpair(sum2);
-                        z.s = h.x + h.y;
-                        follow(z, vm, c2, step);
-                        sum2 = pair2(z.s, 0.f);
-                        ref2 = pair2(z.ref, z.ref);
-                    }
-                    uint64_t v[E / 2];
-                    unpack_pairs<T>(raw, v);
-                    exp_vec<E>(v, ref2, c22);
-                    if (!rest_class || flags[t + u * NT] == 0) {
+                const uint4 raw = ring[u * NT + t];
+                const float vm = Vec<T>::vmax(raw);
+                z.top = fmaxf(z.top, vm);
+                if (vm > z.limit) {
+                    const float2 h = unpair(sum2);
+                    z.s = h.x + h.y;
+                    follow(z, vm, c2, step);
+                    sum2 = pair2(z.s, 0.f);
+                    ref2 = pair2(z.ref, z.ref);
+                }
+                uint64_t v[E / 2];
+                unpack_pairs<T>(raw, v);
+                exp_vec<E>(v, ref2, c22);
+                // (flags beyond the part are another listing's bytes: those slots add nothing either way)
+                if (!rest_class || flags[min(t + u * NT, per - 1)] == 0) {
 #pragma unroll
-                        for (int j = 0; j < E / 2; ++j) sum2 = add2(sum2, v[j]);
-                    }
+                    for (int j = 0; j < E / 2; ++j) sum2 = add2(sum2, v[j]);
                 }
                 if (!GRAD) issue(u);
             }
@@ -670,7 +685,9 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
                         a.logp[row] = lt;
                     }
                     const float scale = w * dl * a.inv_t;
-                    if (lane == 0) factors = make_float4(m, 0.f, -scale * inv_s, scale);
+                    // the token's gradient, everyone's factor of e
+                    if (lane == 0)
+                        factors = make_float4(m, fmaf(-scale * inv_s, ex2((xt - m) * c2), scale), -scale * inv_s, scale);
                 } else {
                     float rest = 0.f, share = 0.f, kl = 0.f;
                     if (rest_class) {
@@ -748,14 +765,13 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
         const uint64_t out2 = pair2(fac.z, fac.z);
         const uint64_t ref2 = pair2(-m, -m);
         T* gp = g + part0 + t * E;
-        const int tok_at = tok - part0;     // within the part's vectors, if there
 #pragma unroll
         for (int qd = 0; qd < QUARTERS && (GRAD || row < 0); ++qd) {
             const int end = min(slots, (qd + 1) * quarter);
 #pragma unroll 1
             for (int u = qd * quarter; u < end; ++u) {
                 const int i = t + u * NT;
-                if (GRAD && row >= 0 && i < count) {
+                if (GRAD && row >= 0) {
                     uint64_t v[E / 2];
                     float f[E];
                     unpack_pairs<T>(ring[i], v);
@@ -763,14 +779,10 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
 #pragma unroll
                     for (int j = 0; j < E / 2; ++j) v[j] = mul2(v[j], out2);
                     split_pairs<E>(v, f);
-                    if (MODE == LM_POLICY && (unsigned)(tok_at - i * E) < (unsigned)E) {
-#pragma unroll
-                        for (int j = 0; j < E; ++j)
-                            if (i * E + j == tok_at) f[j] += scale;
-                    }
+                    const uint4 packed = Vec<T>::pack(f);
                     if (a.same_align) {
-                        *reinterpret_cast<uint4*>(gp + u * (NT * E)) = Vec<T>::pack(f);
-                    } else {
+                        if (i < count) *reinterpret_cast<uint4*>(gp + u * (NT * E)) = packed;
+                    } else if (i < count) {
 #pragma unroll
                         for (int j = 0; j < E; ++j) Vec<T>::st(gp + u * (NT * E) + j, f[j]);
                     }
@@ -781,8 +793,13 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
         }
         if (GRAD && warp == 0 && row >= 0) {
             const int at = odd_of(head);
-            if (at >= 0)
-                Vec<T>::st(g + at, ex2((odd - m) * c2) * fac.z + (MODE == LM_POLICY && at == tok ? scale : 0.f));
+            if (at >= 0) Vec<T>::st(g + at, ex2((odd - m) * c2) * fac.z);
+        }
+        if (MODE == LM_POLICY && row >= 0) {
+            // the token's own entry over what its thread stored
+            const int at = tok - part0;
+            const bool vec = at >= 0 && at < count * E;
+            if (vec ? t == at / E % NT : rank == 0 && t == odd_thread(head, tok)) Vec<T>::st(g + tok, fac.y);
         }
         if (SET && row >= 0) asm volatile("bar.arrive 1, %0;" ::"n"(NT + 32) : "memory");
         row = lrow;
@@ -871,48 +888,70 @@ __global__ void __launch_bounds__(32 * TW) teacher_kernel(const __grid_constant_
     }
 }
 
-constexpr int UNROLL = 4;          // vectors of a gradient row in flight per thread
-
-// Gradient rows of the preference loss: coef ([v = token] - q_v).
-template <typename T, int NT>
-__global__ void __launch_bounds__(NT, 1024 / NT) row_grad_kernel(const __grid_constant__ RowLossArgs a) {
+// Gradient rows of the preference loss, coef ([v = token] - q_v): a stream over
+// all logits, a CTA per GC vectors of a row.  Rows are taken last first: the
+// statistics' launch read them in order, so the last ones are still in L2.
+constexpr int GC = 2048, GU = 4;        // vectors per CTA, in flight per thread
+template <typename T>
+__global__ void __launch_bounds__(256, 4) row_grad_kernel(const __grid_constant__ RowLossArgs a, int chunks) {
     constexpr int E = Vec<T>::E;
+    const int V = a.vocab, t = threadIdx.x;
+    const uint64_t c22 = pair2(a.c2, a.c2);
     pdl_wait();
     pdl_trigger();
-    const int V = a.vocab;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    for (int64_t b = blockIdx.x; b < a.rows * chunks; b += gridDim.x) {
+        const int64_t back = b / chunks, row = a.rows - 1 - back;
+        const int chunk = (int)(b - back * chunks);
         const T* x = reinterpret_cast<const T*>(a.logits) + row * a.ld;
         T* g = reinterpret_cast<T*>(a.grad) + row * a.ldg;
         const RowStats st = a.stats[row];
-        if (st.coef == 0.f) {
-            zero_row<T, NT>(g, V);
-            continue;
-        }
-        const int tok = (int)ld_index(a.tokens, row, a.tok64);
-        const int shift = row_shift(x);
-        const int nv = (V + shift + E - 1) / E;
+        const bool on = st.coef != 0.f;     // also where it is NaN
+        // the aligned vectors of the row that is read (of the gradient's where it is only cleared)
+        const int head = min(V, (int)((16 - (reinterpret_cast<uintptr_t>(on ? x : g) & 15)) & 15) / (int)sizeof(T));
+        const int nv = (V - head) / E, end = min(nv, (chunk + 1) * GC);
+        const int tok = on ? (int)ld_index(a.tokens, row, a.tok64) : -1;
         const float f = -st.coef * st.inv_s;
-        for (int i0 = threadIdx.x; i0 < nv; i0 += UNROLL * NT) {
-            uint4 q[UNROLL];
+        const uint64_t f2 = pair2(f, f), ref2 = pair2(-st.mx, -st.mx);
+        const bool vec = !on || a.same_align;
+        for (int i0 = chunk * GC + t; i0 < end; i0 += GU * 256) {
+            uint4 q[GU];
 #pragma unroll
-            for (int u = 0; u < UNROLL; ++u)
-                if (i0 + u * NT < nv) q[u] = load_vec<T>(x, (i0 + u * NT) * E - shift, V);
+            for (int u = 0; u < GU; ++u)
+                if (on && i0 + u * 256 < end) q[u] = *reinterpret_cast<const uint4*>(x + head + (int64_t)(i0 + u * 256) * E);
 #pragma unroll
-            for (int u = 0; u < UNROLL; ++u) {
-                const int v0 = (i0 + u * NT) * E - shift;
-                if (i0 + u * NT < nv) {
-                    float v[E];
-                    Vec<T>::unpack(q[u], v);
+            for (int u = 0; u < GU; ++u) {
+                const int v0 = head + (i0 + u * 256) * E;
+                if (i0 + u * 256 < end) {
+                    float r[E];
+                    if (on) {
+                        uint64_t v[E / 2];
+                        unpack_pairs<T>(q[u], v);
+                        exp_vec<E>(v, ref2, c22);
 #pragma unroll
-                    for (int j = 0; j < E; ++j) v[j] = f * ex2((v[j] - st.mx) * a.c2);
-                    if ((unsigned)(tok - v0) < (unsigned)E) {
+                        for (int j = 0; j < E / 2; ++j) v[j] = mul2(v[j], f2);
+                        split_pairs<E>(v, r);
+                        if ((unsigned)(tok - v0) < (unsigned)E) {
 #pragma unroll
-                        for (int j = 0; j < E; ++j)
-                            if (v0 + j == tok) v[j] += st.coef;
+                            for (int j = 0; j < E; ++j)
+                                if (v0 + j == tok) r[j] += st.coef;
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < E; ++j) r[j] = 0.f;
                     }
-                    store_vec<T>(g, v0, V, v, a.same_align != 0);
+                    if (vec) {
+                        *reinterpret_cast<uint4*>(g + v0) = Vec<T>::pack(r);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < E; ++j) Vec<T>::st(g + v0 + j, r[j]);
+                    }
                 }
             }
+        }
+        // what the row has before and after its vectors
+        if (chunk == 0 && t < 2 * E) {
+            const int at = t < head ? t : head + nv * E + (t - head);
+            if (at < V) Vec<T>::st(g + at, on ? fmaf(f, ex2((Vec<T>::ld(x + at) - st.mx) * a.c2), at == tok ? st.coef : 0.f) : 0.f);
         }
     }
 }
@@ -1102,12 +1141,10 @@ cudaError_t launch_rows(const RowLossArgs& a, int mode, const DevCtx& dc, cudaSt
 }
 
 template <typename T>
-cudaError_t launch_grad(const RowLossArgs& a, int sms, cudaStream_t s) {
-    if (a.vocab <= 128 * UNROLL * Vec<T>::E)
-        return launch_pdl(row_grad_kernel<T, 128>, dim3((unsigned)std::min<int64_t>(a.rows, (int64_t)sms * 8)), dim3(128),
-                          0, s, a);
-    return launch_pdl(row_grad_kernel<T, 512>, dim3((unsigned)std::min<int64_t>(a.rows, (int64_t)sms * 2)), dim3(512), 0,
-                      s, a);
+cudaError_t launch_grad(const RowLossArgs& a, cudaStream_t s) {
+    const int chunks = std::max(1, (a.vocab / Vec<T>::E + GC - 1) / GC);
+    return launch_pdl(row_grad_kernel<T>, dim3((unsigned)std::min<int64_t>(a.rows * chunks, 1 << 30)), dim3(256), 0, s, a,
+                      chunks);
 }
 
 cudaError_t dispatch_rows(const RowLossArgs& a, int mode, int dtype, const DevCtx& dc, cudaStream_t s) {
@@ -1116,10 +1153,10 @@ cudaError_t dispatch_rows(const RowLossArgs& a, int mode, int dtype, const DevCt
     return launch_rows<__half>(a, mode, dc, s);
 }
 
-cudaError_t dispatch_grad(const RowLossArgs& a, int dtype, int sms, cudaStream_t s) {
-    if (dtype == MUON_F32) return launch_grad<float>(a, sms, s);
-    if (dtype == MUON_BF16) return launch_grad<__nv_bfloat16>(a, sms, s);
-    return launch_grad<__half>(a, sms, s);
+cudaError_t dispatch_grad(const RowLossArgs& a, int dtype, cudaStream_t s) {
+    if (dtype == MUON_F32) return launch_grad<float>(a, s);
+    if (dtype == MUON_BF16) return launch_grad<__nv_bfloat16>(a, s);
+    return launch_grad<__half>(a, s);
 }
 
 bool valid_index(int d) { return d == MUON_I32 || d == MUON_I64; }
@@ -1272,7 +1309,7 @@ extern "C" int muon_preference_loss(const void* logits, int64_t ld, int64_t rows
     }
     if (rows > 0) {
         note_launch_begin(KC_LOSS, s);
-        e = dispatch_grad(a, dtype, dc.sms, s);
+        e = dispatch_grad(a, dtype, s);
         note_launch_end(KC_LOSS, 2.0 * bytes, s);
         if (e != cudaSuccess) return cuda_fail(e, "preference gradient launch");
     }
