@@ -44,8 +44,9 @@ struct RowStats {       // one row of the preference loss between its launches
 // One entry of a teacher's list as the row kernel needs it.
 struct alignas(16) Listed {
     int id;                     // -1: padding
-    float p, lp;                // the teacher's probability and its logarithm
+    float p;                    // the teacher's probability
     float psum;                 // p of every entry with this index at its first one, -1 at the others
+    int pad;
 };
 
 struct RowLossArgs {
@@ -74,7 +75,7 @@ struct RowLossArgs {
     const float* tlse;
     int k, tidx64, tval_dtype;
     Listed* listed;             // [rows][k], written by teacher_kernel
-    float* mass;                // [rows]: the teacher's listed probability
+    float2* teacher;            // [rows]: the listed probability, sum p log p
     // preference
     RowStats* stats;
 };
@@ -392,16 +393,16 @@ constexpr int TEACHER = MODE == LM_DISTILL ? 32 : 0;
 template <typename T, int MODE, int NT>
 __global__ void __launch_bounds__(NT + TEACHER<MODE>, 1024 / (NT + TEACHER<MODE>))
 row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ PartArgs pa) {
-    constexpr int E = Vec<T>::E, NW = NT / 32, QUARTERS = 4, AHEAD = 4;
+    constexpr int E = Vec<T>::E, NW = NT / 32, QUARTERS = 4;
     constexpr bool GRAD = MODE != LM_STATS, SET = MODE == LM_DISTILL;
     extern __shared__ __align__(16) uint8_t dyn8[];
     uint4* ring = reinterpret_cast<uint4*>(dyn8);       // [slots][NT]
     __shared__ float4 red[2][NW + 1];
-    __shared__ __align__(16) float4 part[2][MAX_CLUSTER];
+    __shared__ __align__(16) float4 part[2][MAX_CLUSTER * (SET ? 2 : 1)];
     __shared__ __align__(8) uint64_t bars[2];
     __shared__ float4 factors;                          // maximum, factors of e inside and outside S (policy: the token's
                                                         // gradient, factor of e), factor of t
-    __shared__ float3 terms;                            // distillation: log of the sum, the rest's term, weight T^2
+    __shared__ float3 cross;                            // distillation: of this part, sum p (x - ref), sum p, ref
     __shared__ uint32_t odd_of_row[TEACHERS];           // which of the row's odd logits are listed
     __shared__ int abort_flag;
     const int V = a.vocab, t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -412,7 +413,10 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
     const float c2 = a.c2, step = REBASE / c2;
     const uint64_t c22 = pair2(c2, c2);
     const bool rest_class = SET && a.tlse != nullptr;
-    float* sx = reinterpret_cast<float*>(dyn8 + (size_t)slots * NT * 16);    // [k] the row's listed logits
+    // of the row's entries: themselves (two rows), the vectors that hold their logits, the logits
+    Listed* entries = reinterpret_cast<Listed*>(dyn8 + (size_t)slots * NT * 16);
+    uint4* vecs = reinterpret_cast<uint4*>(entries + 2 * a.k);
+    float* sx = reinterpret_cast<float*>(vecs + a.k);
     auto listing = [&](int buf) {
         return reinterpret_cast<uint8_t*>(sx) + (a.k + 3) / 4 * 16 + (size_t)buf * listing_bytes(per, a.k);
     };
@@ -471,12 +475,6 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
         cp_async16(slot0 + u * (NT * 16), lp + u * (NT * E), t + u * NT < lcount);
     };
     const bool walker = !SET || warp < NW;
-    // The entries' warp holds the indices of the first AHEAD x 32 entries of this
-    // row and of the next in registers, so that its loads of one pass wait for
-    // memory once; longer lists are read as they are worked through.
-    int rid[AHEAD], nid[AHEAD];
-#pragma unroll
-    for (int n = 0; n < AHEAD; ++n) rid[n] = nid[n] = -1;
     // lists entry j0 + lane of row lrow, of index id, in buffer buf
     auto list = [&](int buf, int j0, int id) {
         uint8_t* flags = listing(buf);
@@ -508,14 +506,14 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
         T* g = reinterpret_cast<T*>(a.grad) + row * a.ldg;
         int tok = 0;
         float xt = 0.f;
-        float mass = 0.f;
+        float2 teacher = make_float2(0.f, 0.f);
         PolicyRow pr{1.0f, 0.f, 0.f, 0.f};
         if (row >= 0) {
             if (MODE != LM_DISTILL) tok = (int)ld_index(a.tokens, row, a.tok64);
             if (warp == 0) {                // under the first walk, for the step between the barriers
                 if (MODE != LM_DISTILL) xt = Vec<T>::ld(lx + tok);
                 if (MODE != LM_STATS && a.weights) pr.w = a.weights[row];
-                if (SET) mass = a.mass[row];
+                if (SET) teacher = a.teacher[row];
                 if (MODE == LM_POLICY) {
                     pr.adv = a.adv[row];
                     if (a.old_logp) pr.old = a.old_logp[row];
@@ -555,54 +553,65 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
             const float wm = warp_max(z.top);
             const float f = z.limit == -INFINITY ? 0.f : ex2((-z.ref - wm) * c2);
             const float s = warp_sum(z.s * f);
-            const float si = SET ? warp_sum(z.si * f) : 0.f;
+            const float si = rest_class ? warp_sum(z.si * f) : 0.f;
             if (lane == 0) red[par][warp] = make_float4(wm, s, si, 0.f);
         };
+        // The entries' warp: the next row's entries start to come in; this row's
+        // entries and the vectors of their logits have, since the last pass.
+        const int tail = head + (V - head) / E * E;
+        const Listed* here = entries + par * a.k;
+        Listed* next_entries = entries + (par ^ 1) * a.k;
+        // whether this CTA holds logit id: in its vectors, or (the first CTA) beside them
+        auto held = [&](int id) {
+            return (id >= part0 && id < part0 + count * E) || (rank == 0 && id >= 0 && (id < head || id >= tail));
+        };
         if (!walker) {
-            if (lrow < a.rows) {
-#pragma unroll
-                for (int n = 0; n < AHEAD; ++n)
-                    nid[n] = n * 32 + lane < a.k ? a.listed[lrow * a.k + n * 32 + lane].id : -1;
-            }
+            if (lrow < a.rows)
+                for (int j = lane; j < a.k; j += 32) cp_async16(smem_addr(next_entries + j), a.listed + lrow * a.k + j, true);
+            cp_async_commit();
+            cp_async_wait(1);
             if (row >= 0) {
-                // this row's listed logits, before anything replaces them, and the
-                // sums of the vectors that the walk leaves out
                 const T* x = reinterpret_cast<const T*>(a.logits) + row * a.ld;
                 const uint32_t* leads = reinterpret_cast<const uint32_t*>(flags + (per + 15) / 16 * 16);
-                Sums z{0.f, -INFINITY, 0.f, 0.f, -INFINITY};
-                auto leads_vec = [&](int j0) { return rest_class && j0 < a.k && ((leads[j0 >> 5] >> lane) & 1); };
-                auto vec_of = [&](int id) { return *reinterpret_cast<const uint4*>(x + part0 + (int64_t)((id - part0) / E) * E); };
-                auto sum_vec = [&](int id, const uint4& raw) {
-                    const uint32_t f = flags[(id - part0) / E];
-                    follow(z, Vec<T>::vmax(raw), c2, step);
-                    float v[E];
-                    Vec<T>::unpack(raw, v);
-#pragma unroll
-                    for (int j = 0; j < E; ++j) {
-                        const float ev = ex2((v[j] + z.ref) * c2);
-                        if ((f >> j) & 1) z.si += ev;
-                        else z.s += ev;
+                Sums z{0.f, -INFINITY, 0.f, 0.f, -INFINITY};    // of the vectors that the walk leaves out
+                float top = -INFINITY;
+                for (int j0 = 0; j0 < a.k; j0 += 32) {
+                    const int j = j0 + lane, id = j < a.k ? here[j].id : -1;
+                    if (held(id)) {
+                        const float xj = Vec<T>::ld(id >= part0 && id < part0 + count * E
+                                                        ? reinterpret_cast<const T*>(vecs + j) + (id - part0) % E : x + id);
+                        sx[j] = xj;
+                        top = fmaxf(top, xj);
                     }
-                };
-                T xr[AHEAD];
-                uint4 raw[AHEAD];
+                    if (rest_class && ((leads[j0 >> 5] >> lane) & 1)) {
+                        const uint32_t f = flags[(id - part0) / E];
+                        const uint4 raw = vecs[j];
+                        follow(z, Vec<T>::vmax(raw), c2, step);
+                        float v[E];
+                        Vec<T>::unpack(raw, v);
 #pragma unroll
-                for (int n = 0; n < AHEAD; ++n) {
-                    if (rid[n] >= 0) xr[n] = x[rid[n]];
-                    if (leads_vec(32 * n)) raw[n] = vec_of(rid[n]);
+                        for (int i = 0; i < E; ++i) {
+                            const float ev = ex2((v[i] + z.ref) * c2);
+                            if ((f >> i) & 1) z.si += ev;
+                            else z.s += ev;
+                        }
+                    }
                 }
-#pragma unroll
-                for (int n = 0; n < AHEAD; ++n) {
-                    if (rid[n] >= 0) sx[32 * n + lane] = Vec<T>::ld(&xr[n]);
-                    if (leads_vec(32 * n)) sum_vec(rid[n], raw[n]);
+                top = warp_max(top);
+                const float ref = top == -INFINITY ? 0.f : top;
+                float d = 0.f, ps = 0.f;
+                for (int j = lane; j < a.k; j += 32) {
+                    const float p = here[j].p;
+                    if (p != 0.f && held(here[j].id)) {     // also where it is NaN
+                        d += p * (sx[j] - ref);
+                        ps += p;
+                    }
                 }
-#pragma unroll 1
-                for (int j0 = 32 * AHEAD; j0 < a.k; j0 += 32) {
-                    const int id = j0 + lane < a.k ? a.listed[row * a.k + j0 + lane].id : -1;
-                    if (id >= 0) sx[j0 + lane] = Vec<T>::ld(x + id);
-                    if (leads_vec(j0)) sum_vec(id, vec_of(id));
-                }
-                put_sums(z);
+                d = warp_sum(d);
+                ps = warp_sum(ps);
+                if (lane == 0) cross = make_float3(d, ps, ref);
+                if (rest_class) put_sums(z);
+                else if (lane == 0) red[par][NW] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
             }
         }
         if (row >= 0) {
@@ -658,17 +667,29 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
         if (warp == 0) {
             const float4 r = lane < NW + (SET ? 1 : 0) ? red[par][lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
             float3 q = merge_lanes(r.x, r.y, r.z, c2, SET);
+            float3 dp = SET ? cross : make_float3(0.f, 0.f, 0.f);
             if (csize > 1) {
                 // the token's logit travels along: it has been read before any CTA's gradient can replace it
                 const uint32_t bar = smem_addr(&bars[par]);
-                if (lane == 0) tc::mbar_expect_tx(bar, (uint32_t)(16 * csize));
+                if (lane == 0) tc::mbar_expect_tx(bar, (uint32_t)((SET ? 32 : 16) * csize));
                 __syncwarp();
-                if (lane < csize) st_async_f4(smem_addr(&part[par][rank]), bar, (uint32_t)lane, make_float4(q.x, q.y, q.z, xt));
+                if (lane < csize) {
+                    st_async_f4(smem_addr(&part[par][rank]), bar, (uint32_t)lane, make_float4(q.x, q.y, q.z, xt));
+                    if (SET)
+                        st_async_f4(smem_addr(&part[par][MAX_CLUSTER + rank]), bar, (uint32_t)lane,
+                                    make_float4(dp.x, dp.y, dp.z, 0.f));
+                }
                 tc::wait_bounded(bar, phase[par], &abort_flag, pa.status);
                 phase[par] ^= 1u;
                 __syncwarp();
                 const float4 c = lane < csize ? part[par][lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+                if (SET) {
+                    const float4 e = lane < csize ? part[par][MAX_CLUSTER + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    dp = make_float3(e.x, e.y, e.z);
+                }
                 q = merge_lanes(c.x, c.y, c.z, c2, SET);
+            } else if (SET && lane > 0) {
+                dp = make_float3(0.f, 0.f, 0.f);
             }
             const float m = q.x, all = q.y + q.z, log_s = ::logf(all), inv_s = 1.0f / all;
             const bool writes = rank == 0 && lane == 0;
@@ -690,6 +711,7 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
                         factors = make_float4(m, fmaf(-scale * inv_s, ex2((xt - m) * c2), scale), -scale * inv_s, scale);
                 } else {
                     float rest = 0.f, share = 0.f, kl = 0.f;
+                    const float mass = teacher.x;
                     if (rest_class) {
                         const float qr = q.y * inv_s;
                         rest = 1.0f - mass;
@@ -699,65 +721,54 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
                             kl = rest * ::logf(share);
                         }
                     }
+                    // sum p (log p - log q) = sum p log p - sum p ((x - m) / T - log s), the parts' sums
+                    // taken against references of their own
+                    float dm = 0.f;
+                    if (dp.y != 0.f) dm = dp.x + dp.y * (dp.z - m);
+                    dm = warp_sum(dm);
+                    const float ps = warp_sum(dp.y);
+                    if (writes) a.loss[row] = w * a.t * a.t * (kl + (ps != 0.f ? teacher.y - dm * a.inv_t + ps * log_s : 0.f));
                     const float scale = w * a.t;
-                    if (lane == 0) {
+                    if (lane == 0)
                         factors = make_float4(m, scale * (mass + rest) * inv_s, scale * (mass + rest - share) * inv_s, scale);
-                        terms = make_float3(log_s, kl, w * a.t * a.t);
-                    }
                 }
             }
         }
         }
-        if (!walker && rest_class && lrow < a.rows) {
-            // the next row's listing, while warp 0 brings this row's sums together
-            uint8_t* to = listing(nbuf);
-            for (int i = lane; i < (per + 15) / 16; i += 32) reinterpret_cast<uint4*>(to)[i] = make_uint4(0, 0, 0, 0);
-            if (lane == 0) odd_of_row[nbuf] = 0;
-            __syncwarp();
-#pragma unroll
-            for (int n = 0; n < AHEAD; ++n)
-                if (32 * n < a.k) list(nbuf, 32 * n, nid[n]);
-#pragma unroll 1
-            for (int j0 = 32 * AHEAD; j0 < a.k; j0 += 32)
-                list(nbuf, j0, j0 + lane < a.k ? a.listed[lrow * a.k + j0 + lane].id : -1);
+        if (!walker) {
+            cp_async_wait(0);
+            if (rest_class && lrow < a.rows) {
+                // the next row's listing, while warp 0 brings this row's sums together
+                uint8_t* to = listing(nbuf);
+                for (int i = lane; i < (per + 15) / 16; i += 32) reinterpret_cast<uint4*>(to)[i] = make_uint4(0, 0, 0, 0);
+                if (lane == 0) odd_of_row[nbuf] = 0;
+                __syncwarp();
+                for (int j0 = 0; j0 < a.k; j0 += 32) list(nbuf, j0, j0 + lane < a.k ? next_entries[j0 + lane].id : -1);
+            }
         }
         if (GRAD) __syncthreads();
         const float4 fac = factors;
         const float m = fac.x, scale = fac.w;
         if (!walker) {
-            if (row >= 0) {
-                const Listed* e = a.listed + row * a.k;
-                const int tail = head + (V - head) / E * E;
-                float kl = 0.f, psum[AHEAD];
-                // of an entry: its term of the loss, and its p if this part stores it (an index listed
-                // twice counts twice, at its first entry)
-                auto take = [&](int j) {
-                    const Listed q = e[j];
-                    if (q.p > 0.f) kl += q.p * (q.lp - ((sx[j] - m) * a.inv_t - terms.x));
-                    else if (q.p != q.p) kl = q.p;
-                    const int at = q.id - part0;
-                    const bool mine = (at >= 0 && at < count * E) || (rank == 0 && (q.id < head || q.id >= tail));
-                    return q.id >= 0 && mine ? q.psum : -1.0f;
-                };
-                auto store = [&](int id, int j, float p) {
-                    if (!(p < 0.f)) Vec<T>::st(g + id, fac.y * ex2((sx[j] - m) * c2) - scale * p);
-                };
-#pragma unroll
-                for (int n = 0; n < AHEAD; ++n) psum[n] = 32 * n + lane < a.k ? take(32 * n + lane) : -1.0f;
-#pragma unroll 1
-                for (int j = 32 * AHEAD + lane; j < a.k; j += 32) take(j);
-                if (rank == 0) {            // the row's loss
-                    kl = warp_sum(kl);
-                    if (lane == 0) a.loss[row] = terms.z * (terms.y + kl);
+            // the vectors that hold the next row's listed logits
+            if (lrow < a.rows) {
+                const int next0 = lhead + rank * per * E;
+                for (int j = lane; j < a.k; j += 32) {
+                    const int at = next_entries[j].id - next0;
+                    cp_async16(smem_addr(vecs + j), lx + next0 + (at >= 0 ? at / E * E : 0), at >= 0 && at < lcount * E);
                 }
-                asm volatile("bar.sync 1, %0;" ::"n"(NT + 32) : "memory");      // the second walk is through
-#pragma unroll
-                for (int n = 0; n < AHEAD; ++n) store(rid[n], 32 * n + lane, psum[n]);
-#pragma unroll 1
-                for (int j = 32 * AHEAD + lane; j < a.k; j += 32) store(e[j].id, j, take(j));
             }
-#pragma unroll
-            for (int n = 0; n < AHEAD; ++n) rid[n] = nid[n];
+            cp_async_commit();
+            if (row >= 0) {
+                // the listed gradients of this part, once the second walk is through (an index listed
+                // twice counts twice, at its first entry)
+                asm volatile("bar.sync 1, %0;" ::"n"(NT + 32) : "memory");
+                for (int j = lane; j < a.k; j += 32) {
+                    const Listed q = here[j];
+                    if (held(q.id) && !(q.psum < 0.f))
+                        Vec<T>::st(g + q.id, fac.y * ex2((sx[j] - m) * c2) - scale * q.psum);
+                }
+            }
             row = lrow;
             continue;
         }
@@ -860,14 +871,17 @@ __global__ void __launch_bounds__(32 * TW) teacher_kernel(const __grid_constant_
             s = s > 0.f || s != s ? 1.0f : 0.f;         // nothing listed: no distribution, no loss
         }
         Listed* out = a.listed + row * a.k;
+        float plp = 0.f;
         for (int j = lane; j < a.k; j += 32) {
             Listed e;
             e.id = entry(j, v);
-            e.lp = e.id >= 0 ? (v - tm) * a.inv_t - lse : -INFINITY;
-            e.p = expf(e.lp);
-            e.psum = e.p;
+            const float lp = e.id >= 0 ? (v - tm) * a.inv_t - lse : -INFINITY;
+            e.p = e.psum = expf(lp);
+            e.pad = 0;
+            if (e.p != 0.f) plp += e.p * lp;
             out[j] = e;
         }
+        plp = warp_sum(plp);
         if (again) {
             __syncwarp();
             for (int j = lane; j < a.k; j += 32) {
@@ -883,7 +897,7 @@ __global__ void __launch_bounds__(32 * TW) teacher_kernel(const __grid_constant_
                 out[j].psum = first ? sum : -1.0f;
             }
         }
-        if (lane == 0) a.mass[row] = s;
+        if (lane == 0) a.teacher[row] = make_float2(s, plp);
         __syncwarp();
     }
 }
@@ -1055,7 +1069,7 @@ constexpr int MAX_TEACHER = 1024;
 template <typename T, int MODE, int NT>
 size_t row_smem(int per, int k) {
     size_t b = (size_t)((per + NT - 1) / NT) * NT * 16;
-    if (MODE == LM_DISTILL) b += (size_t)TEACHERS * listing_bytes(per, k) + (size_t)(k + 3) / 4 * 16;
+    if (MODE == LM_DISTILL) b += (size_t)TEACHERS * listing_bytes(per, k) + 48 * (size_t)k + (size_t)(k + 3) / 4 * 16;
     return b;
 }
 
@@ -1219,9 +1233,9 @@ extern "C" int muon_distill_loss(const void* logits, int64_t ld, int64_t rows, i
     a.weights = weights; a.loss = loss;
     const size_t listed = align_up(sizeof(Listed) * (size_t)rows * (size_t)k, 256);
     Workspace* w = nullptr;
-    if ((r = ws_get(dc.device, s, listed + sizeof(float) * (size_t)rows, &w))) return r;
+    if ((r = ws_get(dc.device, s, listed + sizeof(float2) * (size_t)rows, &w))) return r;
     a.listed = reinterpret_cast<Listed*>(w->base);
-    a.mass = reinterpret_cast<float*>(w->base + listed);
+    a.teacher = reinterpret_cast<float2*>(w->base + listed);
     const dim3 tg((unsigned)std::min<int64_t>((rows + TW - 1) / TW, (int64_t)dc.sms * 12));
     note_launch_begin(KC_LOSS, s);
     cudaError_t e = launch_pdl(teacher_kernel, tg, dim3(32 * TW), 0, s, a);
