@@ -644,37 +644,46 @@ __device__ __forceinline__ uint4 load8(const void* p, int64_t row, int c, int co
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+__device__ __forceinline__ void glu_grad_piece(const GluGradArgs& a, int64_t i, const uint4& qd, const uint4& qg,
+                                               const uint4& qu) {
+    const bool f16 = a.dtype == MUON_F16;
+    float d[8], g[8], u[8];
+    unpack8_h(qd, d, f16);
+    unpack8_h(qg, g, f16);
+    unpack8_h(qu, u, f16);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        float s;
+        const float act = activate<true>(g[k], a.act, &s);
+        g[k] = d[k] * u[k] * s;
+        u[k] = d[k] * act;
+    }
+    static_cast<uint4*>(a.dg)[i] = pack8_h(g, f16);
+    static_cast<uint4*>(a.du)[i] = pack8_h(u, f16);
+}
+
 __global__ void __launch_bounds__(256) glu_grad_kernel(const __grid_constant__ GluGradArgs a) {
     pdl_wait();
     pdl_trigger();
-    const bool f16 = a.dtype == MUON_F16;
     const int64_t n = a.rows * a.pieces, step = (int64_t)gridDim.x * 256;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
-        const int64_t row = a.vec ? 0 : i / a.pieces;       // aligned rows are one dense run of pieces
-        const int64_t col = a.vec ? i * 8 : (i - row * a.pieces) * 8;
-        uint4 qd, qg, qu;
-        if (a.vec) {
-            qd = static_cast<const uint4*>(a.dh)[i];
-            qg = static_cast<const uint4*>(a.gate)[i];
-            qu = static_cast<const uint4*>(a.up)[i];
-        } else {
-            qd = load8(a.dh, row, (int)col, a.ffn, false);
-            qg = load8(a.gate, row, (int)col, a.ffn, false);
-            qu = load8(a.up, row, (int)col, a.ffn, false);
+    int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (a.vec) {                            // aligned rows are one dense run of pieces
+        const uint4 *d = static_cast<const uint4*>(a.dh), *g = static_cast<const uint4*>(a.gate),
+                    *u = static_cast<const uint4*>(a.up);
+        for (; i + step < n; i += 2 * step) {
+            const uint4 d0 = __ldcs(d + i), g0 = __ldcs(g + i), u0 = __ldcs(u + i);
+            const uint4 d1 = __ldcs(d + i + step), g1 = __ldcs(g + i + step), u1 = __ldcs(u + i + step);
+            glu_grad_piece(a, i, d0, g0, u0);
+            glu_grad_piece(a, i + step, d1, g1, u1);
         }
-        float d[8], g[8], u[8];
-        unpack8_h(qd, d, f16);
-        unpack8_h(qg, g, f16);
-        unpack8_h(qu, u, f16);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            float s;
-            const float act = activate<true>(g[k], a.act, &s);
-            g[k] = d[k] * u[k] * s;
-            u[k] = d[k] * act;
-        }
-        static_cast<uint4*>(a.dg)[i] = pack8_h(g, f16);
-        static_cast<uint4*>(a.du)[i] = pack8_h(u, f16);
+        if (i < n) glu_grad_piece(a, i, d[i], g[i], u[i]);
+        return;
+    }
+    for (; i < n; i += step) {
+        const int64_t row = i / a.pieces;
+        const int col = (int)(i - row * a.pieces) * 8;
+        glu_grad_piece(a, i, load8(a.dh, row, col, a.ffn, false), load8(a.gate, row, col, a.ffn, false),
+                       load8(a.up, row, col, a.ffn, false));
     }
 }
 
@@ -690,11 +699,10 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const __grid_constant__ P
     pdl_wait();
     pdl_trigger();
     const int o = blockIdx.y, pieces = (a.cols + 7) / 8;
-    const int64_t n = a.rows[o] * pieces, step = (int64_t)gridDim.x * 256;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
-        const int64_t row = i / pieces;
-        static_cast<uint4*>(a.dst[o])[i] = load8(a.src[o], row, (int)(i - row * pieces) * 8, a.cols, false);
-    }
+    // a warp per row: no division per piece
+    for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < a.rows[o]; row += (int64_t)gridDim.x * 8)
+        for (int i = threadIdx.x & 31; i < pieces; i += 32)
+            static_cast<uint4*>(a.dst[o])[row * pieces + i] = load8(a.src[o], row, i * 8, a.cols, false);
 }
 
 // dX from its partial sums, added in the order of the parts.
@@ -707,13 +715,15 @@ struct PartSumArgs {
 __global__ void __launch_bounds__(256) part_sum_kernel(const __grid_constant__ PartSumArgs a) {
     pdl_wait();
     pdl_trigger();
-    const int64_t n = a.rows * a.cols, step = (int64_t)gridDim.x * 256, plane = a.rows * a.ldp;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
-        const int64_t row = i / a.cols, at = row * a.ldp + (i - row * a.cols);
-        float s = 0.f;
+    const int64_t plane = a.rows * a.ldp;
+    for (int64_t row = (int64_t)blockIdx.x; row < a.rows; row += gridDim.x) {
+        for (int c = blockIdx.y * 256 + threadIdx.x; c < a.cols; c += gridDim.y * 256) {
+            const float* p = a.part + row * a.ldp + c;
+            float s = 0.f;
 #pragma unroll 4
-        for (int k = 0; k < a.splits; ++k) s += a.part[k * plane + at];
-        st_elem(a.out, i, s, a.dtype);
+            for (int k = 0; k < a.splits; ++k) s += p[k * plane];
+            st_elem(a.out, row * a.cols + c, s, a.dtype);
+        }
     }
 }
 
@@ -742,7 +752,7 @@ int pad_operands(Operand* const* ops, char* at, int sms, cudaStream_t s) {
     PadArgs p;
     std::memset(&p, 0, sizeof p);
     unsigned n = 0;
-    int64_t most = 0;
+    int64_t most = 0;       // rows
     for (int i = 0; i < 3; ++i) {
         Operand& o = *ops[i];
         const size_t b = padded_bytes(o);
@@ -753,13 +763,13 @@ int pad_operands(Operand* const* ops, char* at, int sms, cudaStream_t s) {
         p.cols = (int)o.cols;               // the three share it
         ++n;
         o.ld = pad8(o.cols);
-        most = std::max(most, o.rows * (o.ld / 8));
+        most = std::max(most, o.rows);
         o.p = at;
         at += b;
     }
     if (!n) return MUON_OK;
     note_launch_begin(KC_OTHER, s);
-    cudaError_t e = launch_pdl(pad_rows_kernel, dim3((unsigned)std::min<int64_t>((most + 255) / 256, (int64_t)sms * 8), n),
+    cudaError_t e = launch_pdl(pad_rows_kernel, dim3((unsigned)std::min<int64_t>((most + 7) / 8, (int64_t)sms * 8), n),
                                dim3(256), 0, s, p);
     note_launch_end(KC_OTHER, 0.0, s);
     if (e != cudaSuccess) return cuda_fail(e, "operand copy launch");
@@ -1006,7 +1016,8 @@ extern "C" int muon_glu_backward(const void* x, const void* w_gate, const void* 
         PartSumArgs p{g.part, dx, tokens, g.ldp, (int)hidden, g.a.splits, dtype};
         note_launch_begin(KC_GLU, s);
         e = launch_pdl(part_sum_kernel,
-                       dim3((unsigned)std::min<int64_t>((tokens * hidden + 255) / 256, (int64_t)dc.sms * 8)), dim3(256), 0, s, p);
+                       dim3((unsigned)std::min<int64_t>(tokens, 65535), (unsigned)std::min<int64_t>((hidden + 255) / 256, 64)),
+                       dim3(256), 0, s, p);
         note_launch_end(KC_GLU, 0.0, s);
         if (e != cudaSuccess) return cuda_fail(e, "glu partial sum launch");
     }

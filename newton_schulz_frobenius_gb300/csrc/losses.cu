@@ -973,8 +973,6 @@ __global__ void __launch_bounds__(256, 4) row_grad_kernel(const __grid_constant_
 struct PairArgs {
     RowStats* stats;
     int64_t rows;
-    const void* tokens;
-    int tok64, vocab;
     const void* bounds;         // 2 pairs + 1 row offsets
     int bounds64;
     const float* ref_logp;      // per sequence, or null
@@ -985,60 +983,58 @@ struct PairArgs {
     float* loss;
 };
 
-// One CTA per pair: both sequence values (fp64 sums in a fixed order), the
-// pair's loss, and the factor of every row of the pair.
-__global__ void __launch_bounds__(256) pair_kernel(const __grid_constant__ PairArgs a) {
-    __shared__ double rs[8];
-    __shared__ int rn[8];
+// One CTA per pair, half of it per sequence: both sequence values (fp64 sums in
+// a fixed order), the pair's loss, and the factor of every row of the pair.  A
+// row in the loss is one whose statistics say so (inv_s != 0).
+constexpr int PT = 512;
+__global__ void __launch_bounds__(PT) pair_kernel(const __grid_constant__ PairArgs a) {
+    constexpr int HT = PT / 2;
+    __shared__ double rs[PT / 32];
+    __shared__ int rn[PT / 32];
+    const int64_t pair = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = threadIdx.x / HT, t = threadIdx.x % HT;
     pdl_wait();
     pdl_trigger();
-    const int64_t pair = blockIdx.x;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    double val[2];
-    float share[2];
-    int64_t b[3];
-    for (int i = 0; i < 3; ++i) {
-        int64_t v = ld_index(a.bounds, 2 * pair + i, a.bounds64);
-        b[i] = v < 0 ? 0 : (v > a.rows ? a.rows : v);
-    }
-    for (int c = 0; c < 2; ++c) {
-        double s = 0;
-        int n = 0;
-        for (int64_t r = b[c] + threadIdx.x; r < b[c + 1]; r += 256) {
-            const int64_t tok = ld_index(a.tokens, r, a.tok64);
-            if (tok >= 0 && tok < a.vocab) {
-                s += (double)a.stats[r].logp;
-                ++n;
-            }
-        }
-        for (int o = 16; o; o >>= 1) {
-            s += __shfl_xor_sync(0xffffffffu, s, o);
-            n += __shfl_xor_sync(0xffffffffu, n, o);
-        }
-        __syncthreads();
-        if (lane == 0) {
-            rs[warp] = s;
-            rn[warp] = n;
-        }
-        __syncthreads();
-        s = 0;
-        n = 0;
-        for (int i = 0; i < 8; ++i) {
-            s += rs[i];
-            n += rn[i];
-        }
-        share[c] = a.average ? (n > 0 ? 1.0f / (float)n : 0.f) : 1.0f;
-        val[c] = a.average ? (n > 0 ? s / n : 0.0) : s;
-        if (threadIdx.x == 0) a.seq_logp[2 * pair + c] = (float)val[c];
-    }
-    double d = val[0] - val[1];
-    if (a.ref_logp) d -= (double)a.ref_logp[2 * pair] - (double)a.ref_logp[2 * pair + 1];
-    const float h = (float)((double)a.beta * d - (double)a.margin);
+    auto bound = [&](int i) {
+        const int64_t v = ld_index(a.bounds, 2 * pair + i, a.bounds64);
+        return v < 0 ? (int64_t)0 : (v > a.rows ? a.rows : v);
+    };
+    const int64_t b0 = bound(c), b1 = bound(c + 1);
     const float w = a.weights ? a.weights[pair] : 1.0f;
+    double ref = 0.0;
+    if (a.ref_logp) ref = (double)a.ref_logp[2 * pair] - (double)a.ref_logp[2 * pair + 1];
+    double s = 0;
+    int n = 0;
+    for (int64_t r = b0 + t; r < b1; r += HT) {
+        const RowStats st = a.stats[r];
+        if (st.inv_s != 0.f) {
+            s += (double)st.logp;
+            ++n;
+        }
+    }
+    for (int o = 16; o; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        n += __shfl_xor_sync(0xffffffffu, n, o);
+    }
+    if (lane == 0) {
+        rs[warp] = s;
+        rn[warp] = n;
+    }
+    __syncthreads();
+    double val[2] = {0.0, 0.0};
+    int cnt[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < PT / 32; ++i) {
+        val[i / (HT / 32)] += rs[i];
+        cnt[i / (HT / 32)] += rn[i];
+    }
+    if (a.average)
+        for (int i = 0; i < 2; ++i) val[i] = cnt[i] > 0 ? val[i] / cnt[i] : 0.0;
+    const float h = (float)((double)a.beta * (val[0] - val[1] - ref) - (double)a.margin);
     // -log sigmoid(h), and sigmoid(h), sigmoid(-h) without overflow
-    const float t = expf(-fabsf(h));
-    const float soft = fmaxf(-h, 0.f) + log1pf(t);
-    const float big = 1.0f / (1.0f + t), small = t * big;
+    const float e = expf(-fabsf(h));
+    const float soft = fmaxf(-h, 0.f) + log1pf(e);
+    const float big = 1.0f / (1.0f + e), small = e * big;
     const float sp = h >= 0.f ? big : small, sn = h >= 0.f ? small : big;
     float loss = (1.0f - a.smoothing) * soft, dh = -(1.0f - a.smoothing) * sn;
     if (a.smoothing != 0.f) {
@@ -1047,14 +1043,14 @@ __global__ void __launch_bounds__(256) pair_kernel(const __grid_constant__ PairA
     }
     if (h != h) loss = dh = h;
     const bool on = w != 0.f;
-    if (threadIdx.x == 0) a.loss[pair] = on ? w * loss : 0.f;
-    for (int c = 0; c < 2; ++c) {
-        const float coef = on ? (c ? -1.0f : 1.0f) * w * dh * a.beta * share[c] : 0.f;
-        for (int64_t r = b[c] + threadIdx.x; r < b[c + 1]; r += 256) {
-            const int64_t tok = ld_index(a.tokens, r, a.tok64);
-            if (tok >= 0 && tok < a.vocab) a.stats[r].coef = coef;
-        }
+    if (t == 0) {
+        a.seq_logp[2 * pair + c] = (float)val[c];
+        if (c == 0) a.loss[pair] = on ? w * loss : 0.f;
     }
+    const float share = a.average ? (cnt[c] > 0 ? 1.0f / (float)cnt[c] : 0.f) : 1.0f;
+    const float coef = on ? (c ? -1.0f : 1.0f) * w * dh * a.beta * share : 0.f;
+    for (int64_t r = b0 + t; r < b1; r += HT)
+        if (a.stats[r].inv_s != 0.f) a.stats[r].coef = coef;
 }
 
 // ---------------------------------------------------------------------------
@@ -1073,8 +1069,8 @@ size_t row_smem(int per, int k) {
     return b;
 }
 
-// Shared memory up to which four CTAs share an SM, and what a CTA may have.
-constexpr size_t QUARTER_SM = 55500, MAX_SMEM = 220000;
+// Shared memory of a part in distillation, and what a CTA may have.
+constexpr size_t PART_SMEM = 85000, MAX_SMEM = 220000;
 
 template <typename T, int MODE, int NT>
 cudaError_t launch_part(const RowLossArgs& a, int64_t nv, int csize, int* status, cudaStream_t s) {
@@ -1136,13 +1132,21 @@ cudaError_t launch_part(const RowLossArgs& a, int64_t nv, int csize, int* status
 // Four CTAs of 256 threads beat two of 512 (a CTA's wait between its walks is
 // hidden by the others): 131072 bf16 logits 530 -> 482 us for 1.2 GB of logits,
 // fp32 459 -> 423; eight of 128 with twice the slots took 567 and 501.
+// Distillation, with more to keep per CTA, takes powers of two and two or three
+// CTAs on an SM: for the same 1.2 GB, fp32 131072 by 8 CTAs 480 us, by 12 (four
+// on an SM) 503, by 10 584; fp32 65536 by 4 465, by 5 566, by 6 488; bf16 50001
+// by 2 565, by 3 610; bf16 131072 by 4 629, by 6 606, by 8 608.
 template <typename T, int MODE>
 cudaError_t launch_mode(const RowLossArgs& a, const DevCtx& dc, cudaStream_t s) {
     constexpr int NT = 256 - TEACHER<MODE>, SMALL = 128 - TEACHER<MODE>;
     const int64_t nv = std::max(1, a.vocab / Vec<T>::E);       // whole vectors of a row at most
     if (nv <= SLOTS * SMALL) return launch_part<T, MODE, SMALL>(a, nv, 1, dc.status, s);
-    int c = (int)std::min<int64_t>(MAX_CLUSTER, (nv + SLOTS * NT - 1) / (SLOTS * NT));
-    while (c < MAX_CLUSTER && row_smem<T, MODE, NT>((int)((nv + c - 1) / c), a.k) > QUARTER_SM && nv > (int64_t)c * 4 * NT) ++c;
+    auto smem = [&](int c) { return row_smem<T, MODE, NT>((int)((nv + c - 1) / c), a.k); };
+    int c = 1;
+    if (MODE == LM_DISTILL)
+        while (c < MAX_CLUSTER && smem(c) > PART_SMEM) c *= 2;
+    else
+        c = (int)std::min<int64_t>(MAX_CLUSTER, (nv + SLOTS * NT - 1) / (SLOTS * NT));
     while (c <= 4 && a.rows * c < dc.sms && nv > (int64_t)c * 4 * NT) c *= 2;
     return launch_part<T, MODE, NT>(a, nv, c, dc.status, s);
 }
@@ -1311,13 +1315,12 @@ extern "C" int muon_preference_loss(const void* logits, int64_t ld, int64_t rows
     if (pairs > 0) {
         PairArgs p;
         p.stats = a.stats; p.rows = rows;
-        p.tokens = tokens; p.tok64 = a.tok64; p.vocab = (int)vocab;
         p.bounds = seq_bounds; p.bounds64 = bounds_dtype == MUON_I64;
         p.ref_logp = ref_logp; p.weights = weights;
         p.beta = beta; p.margin = margin; p.smoothing = label_smoothing; p.average = average != 0;
         p.seq_logp = seq_logp; p.loss = loss;
         note_launch_begin(KC_LOSS, s);
-        e = launch_pdl(pair_kernel, dim3((unsigned)pairs), dim3(256), 0, s, p);
+        e = launch_pdl(pair_kernel, dim3((unsigned)pairs), dim3(PT), 0, s, p);
         note_launch_end(KC_LOSS, 0.0, s);
         if (e != cudaSuccess) return cuda_fail(e, "preference pair launch");
     }
