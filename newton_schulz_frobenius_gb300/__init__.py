@@ -514,57 +514,55 @@ def _on_stream(stream):
 
 def _index_code(t, name) -> int:
     import torch
-    if t.dtype == torch.int32:
-        return MUON_I32
-    if t.dtype == torch.int64:
+    d = t.dtype
+    if d is torch.int64:
         return MUON_I64
-    raise TypeError(f"{name}: int32 or int64 required, got {t.dtype}")
+    if d is torch.int32:
+        return MUON_I32
+    raise TypeError(f"{name}: int32 or int64 required, got {d}")
 
 
 def _rows_of(t, name):
     """(pointer, row pitch) of a rows x cols CUDA tensor whose rows are contiguous."""
     if not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA tensor with contiguous rows")
+    rows, cols = t.shape
     if t.is_contiguous():
-        return t.data_ptr(), max(1, t.shape[1])
-    if t.shape[1] > 1 and t.stride(1) != 1:
+        return t.data_ptr(), cols or 1
+    if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must be a 2-D CUDA tensor with contiguous rows")
-    pitch = t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1])
-    if pitch < t.shape[1]:
+    pitch = t.stride(0) if rows > 1 else max(1, cols)
+    if pitch < cols:
         raise ValueError(f"{name}: rows overlap")
     return t.data_ptr(), max(pitch, 1)
 
 
 def _vector(t, n, name, dtype=None):
-    """Pointer of a contiguous CUDA vector of n elements; None stays NULL."""
+    """Pointer of a contiguous CUDA tensor of n elements; None stays NULL."""
     if t is None:
         return None
-    _cuda_contig(t, name)
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
     if t.numel() != n:
         raise ValueError(f"{name}: {n} elements required, got {t.numel()}")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name}: {dtype} required, got {t.dtype}")
     return t.data_ptr()
 
 
-def _grad_like(logits, grad, stream):
+def _loss_outputs(logits, grad, stream, *sizes):
+    """The gradient (a new tensor unless one was given) and fp32 vectors of the given sizes."""
     import torch
-    if grad is None:
-        if stream is None:
-            return torch.empty_like(logits, memory_format=torch.contiguous_format)
+    if stream is not None:
         with _on_stream(stream):
-            return torch.empty_like(logits, memory_format=torch.contiguous_format)
-    if grad.shape != logits.shape or grad.dtype != logits.dtype:
+            return _loss_outputs(logits, grad, None, *sizes)
+    dev = logits.device
+    out = [torch.empty(n, dtype=torch.float32, device=dev) for n in sizes]
+    if grad is None:
+        grad = torch.empty_like(logits, memory_format=torch.contiguous_format)
+    elif grad.shape != logits.shape or grad.dtype is not logits.dtype:
         raise ValueError("grad must have the logits' shape and dtype")
-    return grad
-
-
-def _f32_out(n, like, stream):
-    import torch
-    if stream is None:
-        return torch.empty(n, dtype=torch.float32, device=like.device)
-    with _on_stream(stream):
-        return torch.empty(n, dtype=torch.float32, device=like.device)
+    return (grad, *out)
 
 
 def muon_distill_loss(logits, teacher_idx, teacher_logits, teacher_lse=None, weights=None, temperature: float = 1.0,
@@ -575,21 +573,21 @@ def muon_distill_loss(logits, teacher_idx, teacher_logits, teacher_lse=None, wei
     Returns (loss per row, gradient of the loss' sum); grad may be a tensor to
     write into, the logits themselves included."""
     import torch
+    f32 = torch.float32
     lp, ld = _rows_of(logits, "logits")
     rows, vocab = logits.shape
     if teacher_idx.dim() != 2 or teacher_idx.shape != teacher_logits.shape or teacher_idx.shape[0] != rows:
         raise ValueError("teacher_idx and teacher_logits must be rows x k")
     k = teacher_idx.shape[1]
-    ip = _vector(teacher_idx, rows * k, "teacher_idx")
-    tp = _vector(teacher_logits, rows * k, "teacher_logits")
-    grad = _grad_like(logits, grad, stream)
+    args = (lp, ld, rows, vocab, _dtype_code(logits), _vector(teacher_idx, rows * k, "teacher_idx"),
+            _index_code(teacher_idx, "teacher_idx"), _vector(teacher_logits, rows * k, "teacher_logits"),
+            _dtype_code(teacher_logits), k, _vector(teacher_lse, rows, "teacher_lse", f32),
+            _vector(weights, rows, "weights", f32), temperature)
+    grad, loss = _loss_outputs(logits, grad, stream, rows)
     gp, ldg = _rows_of(grad, "grad")
-    loss = _f32_out(rows, logits, stream)
-    _check(lib().muon_distill_loss(lp, ld, rows, vocab, _dtype_code(logits), ip,
-                                   _index_code(teacher_idx, "teacher_idx"), tp, _dtype_code(teacher_logits), k,
-                                   _vector(teacher_lse, rows, "teacher_lse", torch.float32),
-                                   _vector(weights, rows, "weights", torch.float32), float(temperature),
-                                   loss.data_ptr(), gp, ldg, _stream_ptr(stream)), "muon_distill_loss")
+    st = lib().muon_distill_loss(*args, loss.data_ptr(), gp, ldg, _stream_ptr(stream))
+    if st:
+        _check(st, "muon_distill_loss")
     return loss, grad
 
 
@@ -600,19 +598,18 @@ def muon_policy_loss(logits, tokens, advantages, old_logp=None, ref_logp=None, w
     per row.  Returns (loss per row, log-probability per row, gradient of the
     loss' sum)."""
     import torch
+    f32 = torch.float32
     lp, ld = _rows_of(logits, "logits")
     rows, vocab = logits.shape
-    grad = _grad_like(logits, grad, stream)
+    args = (lp, ld, rows, vocab, _dtype_code(logits), _vector(tokens, rows, "tokens"), _index_code(tokens, "tokens"),
+            _vector(advantages, rows, "advantages", f32), _vector(old_logp, rows, "old_logp", f32),
+            _vector(ref_logp, rows, "ref_logp", f32), _vector(weights, rows, "weights", f32), temperature, clip_low,
+            clip_high, kl_coef)
+    grad, loss, logp = _loss_outputs(logits, grad, stream, rows, rows)
     gp, ldg = _rows_of(grad, "grad")
-    loss, logp = _f32_out(rows, logits, stream), _f32_out(rows, logits, stream)
-    _check(lib().muon_policy_loss(lp, ld, rows, vocab, _dtype_code(logits), _vector(tokens, rows, "tokens"),
-                                  _index_code(tokens, "tokens"),
-                                  _vector(advantages, rows, "advantages", torch.float32),
-                                  _vector(old_logp, rows, "old_logp", torch.float32),
-                                  _vector(ref_logp, rows, "ref_logp", torch.float32),
-                                  _vector(weights, rows, "weights", torch.float32), float(temperature),
-                                  float(clip_low), float(clip_high), float(kl_coef), loss.data_ptr(),
-                                  logp.data_ptr(), gp, ldg, _stream_ptr(stream)), "muon_policy_loss")
+    st = lib().muon_policy_loss(*args, loss.data_ptr(), logp.data_ptr(), gp, ldg, _stream_ptr(stream))
+    if st:
+        _check(st, "muon_policy_loss")
     return loss, logp, grad
 
 
@@ -624,22 +621,22 @@ def muon_preference_loss(logits, tokens, seq_bounds, ref_logp=None, weights=None
     rejected; tokens are labels, negative ones left out.  Returns (loss per
     pair, sequence log-probabilities, gradient of the loss' sum)."""
     import torch
+    f32 = torch.float32
     lp, ld = _rows_of(logits, "logits")
     rows, vocab = logits.shape
     nb = seq_bounds.numel()
     if nb % 2 != 1:
         raise ValueError("seq_bounds needs 2 pairs + 1 offsets")
     pairs = nb // 2
-    grad = _grad_like(logits, grad, stream)
+    args = (lp, ld, rows, vocab, _dtype_code(logits), _vector(tokens, rows, "tokens"), _index_code(tokens, "tokens"),
+            _vector(seq_bounds, nb, "seq_bounds"), _index_code(seq_bounds, "seq_bounds"), pairs,
+            _vector(ref_logp, 2 * pairs, "ref_logp", f32), _vector(weights, pairs, "weights", f32), beta, margin,
+            label_smoothing, 1 if average else 0)
+    grad, loss, seq = _loss_outputs(logits, grad, stream, pairs, 2 * pairs)
     gp, ldg = _rows_of(grad, "grad")
-    loss, seq = _f32_out(pairs, logits, stream), _f32_out(2 * pairs, logits, stream)
-    _check(lib().muon_preference_loss(lp, ld, rows, vocab, _dtype_code(logits), _vector(tokens, rows, "tokens"),
-                                      _index_code(tokens, "tokens"), _vector(seq_bounds, nb, "seq_bounds"),
-                                      _index_code(seq_bounds, "seq_bounds"), pairs,
-                                      _vector(ref_logp, 2 * pairs, "ref_logp", torch.float32),
-                                      _vector(weights, pairs, "weights", torch.float32), float(beta), float(margin),
-                                      float(label_smoothing), 1 if average else 0, loss.data_ptr(), seq.data_ptr(),
-                                      gp, ldg, _stream_ptr(stream)), "muon_preference_loss")
+    st = lib().muon_preference_loss(*args, loss.data_ptr(), seq.data_ptr(), gp, ldg, _stream_ptr(stream))
+    if st:
+        _check(st, "muon_preference_loss")
     return loss, seq, grad
 
 
@@ -652,32 +649,44 @@ ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
 
 def _glu_args(x, w_gate, w_up, act):
+    dt = x.dtype
     for t, nm in ((x, "x"), (w_gate, "w_gate"), (w_up, "w_up")):
-        _cuda_contig(t, nm)
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{nm} must be a contiguous CUDA tensor")
         if t.dim() != 2:
             raise ValueError(f"{nm} must be 2-D")
-        if t.dtype != x.dtype:
+        if t.dtype is not dt:
             raise TypeError(f"{nm}: dtype differs from x")
-    if w_gate.shape != w_up.shape or w_gate.shape[1] != x.shape[1]:
+    tokens, hidden = x.shape
+    ffn = w_gate.shape[0]
+    if w_gate.shape[1] != hidden or w_up.shape != w_gate.shape:
         raise ValueError("x is tokens x hidden, w_gate and w_up ffn x hidden")
     if act not in ACTIVATIONS:
         raise ValueError(f"act {act!r}: one of {sorted(ACTIVATIONS)}")
-    return x.shape[0], x.shape[1], w_gate.shape[0], _dtype_code(x), ACTIVATIONS[act]
+    return tokens, hidden, ffn, _dtype_code(x), ACTIVATIONS[act]
+
+
+def _new(stream, *like):
+    """New contiguous tensors of the (shape, tensor to take dtype and device from) pairs given."""
+    import torch
+    if stream is not None:
+        with _on_stream(stream):
+            return _new(None, *like)
+    return [torch.empty(shape, dtype=t.dtype, device=t.device) for shape, t in like]
 
 
 def muon_glu_forward(x, w_gate, w_up, act: str = "silu", save: bool = True, stream=None):
     """act(x w_gate^T) * (x w_up^T) in one kernel (bf16 or fp16; x tokens x
     hidden, weights ffn x hidden).  Returns (h, gate, up) for the backward
     pass, or h alone with save=False."""
-    import torch
     tokens, hidden, ffn, dt, code = _glu_args(x, w_gate, w_up, act)
-    with _on_stream(stream):
-        h, gate, up = (torch.empty(tokens, ffn, dtype=x.dtype, device=x.device) if on else None
-                       for on in (True, save, save))
-    _check(lib().muon_glu_forward(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), h.data_ptr(),
-                                  gate.data_ptr() if save else None, up.data_ptr() if save else None, tokens, hidden,
-                                  ffn, dt, code, _stream_ptr(stream)), "muon_glu_forward")
-    return (h, gate, up) if save else h
+    out = _new(stream, *[((tokens, ffn), x)] * (3 if save else 1))
+    ptrs = [t.data_ptr() for t in out] if save else (out[0].data_ptr(), None, None)
+    st = lib().muon_glu_forward(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), *ptrs, tokens, hidden, ffn, dt, code,
+                                _stream_ptr(stream))
+    if st:
+        _check(st, "muon_glu_forward")
+    return tuple(out) if save else out[0]
 
 
 def muon_glu_backward(x, w_gate, w_up, gate, up, dh, act: str = "silu", need_dx: bool = True, dw_gate=None, dw_up=None,
@@ -685,21 +694,25 @@ def muon_glu_backward(x, w_gate, w_up, gate, up, dh, act: str = "silu", need_dx:
     """Gradients (dx, dw_gate, dw_up) of muon_glu_forward from dh and the gate
     and up it returned.  dw_gate and dw_up may be tensors to write into (the
     gradients a MuonGroup reads); need_dx=False leaves dx out (None)."""
-    import torch
     tokens, hidden, ffn, dt, code = _glu_args(x, w_gate, w_up, act)
     for t, nm in ((gate, "gate"), (up, "up"), (dh, "dh")):
-        _cuda_contig(t, nm)
-        if t.shape != (tokens, ffn) or t.dtype != x.dtype:
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{nm} must be a contiguous CUDA tensor")
+        if t.shape != (tokens, ffn) or t.dtype is not x.dtype:
             raise ValueError(f"{nm} must be tokens x ffn of x's dtype")
-    with _on_stream(stream):
-        dx = torch.empty_like(x) if need_dx else None
-        outs = [torch.empty_like(w_gate) if t is None else t for t in (dw_gate, dw_up)]
-    for t, nm in zip(outs, ("dw_gate", "dw_up")):
-        _cuda_contig(t, nm)
-        if t.shape != w_gate.shape or t.dtype != x.dtype:
-            raise ValueError(f"{nm} must be ffn x hidden of x's dtype")
-    _check(lib().muon_glu_backward(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), gate.data_ptr(), up.data_ptr(),
-                                   dh.data_ptr(), dx.data_ptr() if need_dx else None, outs[0].data_ptr(),
-                                   outs[1].data_ptr(), tokens, hidden, ffn, dt, code, _stream_ptr(stream)),
-           "muon_glu_backward")
-    return dx, outs[0], outs[1]
+    for t, nm in ((dw_gate, "dw_gate"), (dw_up, "dw_up")):
+        if t is not None:
+            _cuda_contig(t, nm)
+            if t.shape != w_gate.shape or t.dtype is not x.dtype:
+                raise ValueError(f"{nm} must be ffn x hidden of x's dtype")
+    want = ([((tokens, hidden), x)] if need_dx else []) + [((ffn, hidden), x)] * ((dw_gate is None) + (dw_up is None))
+    new = _new(stream, *want)
+    dx = new.pop(0) if need_dx else None
+    dw_gate = new.pop(0) if dw_gate is None else dw_gate
+    dw_up = new.pop(0) if dw_up is None else dw_up
+    st = lib().muon_glu_backward(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), gate.data_ptr(), up.data_ptr(),
+                                 dh.data_ptr(), dx.data_ptr() if need_dx else None, dw_gate.data_ptr(),
+                                 dw_up.data_ptr(), tokens, hidden, ffn, dt, code, _stream_ptr(stream))
+    if st:
+        _check(st, "muon_glu_backward")
+    return dx, dw_gate, dw_up

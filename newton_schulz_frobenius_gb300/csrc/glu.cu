@@ -8,7 +8,10 @@
 //
 // Products run on 2-SM tcgen05 pairs (M = 256, N = 256, fp32 accumulation in
 // TMEM, two accumulators so that a tile's epilogue runs under the next tile's
-// products), fed by TMA through a ring of six 32 KB stages per CTA.
+// products), fed by TMA through a ring of six 32 KB stages per CTA.  Bound: the
+// tensor pipe under the power cap.  Forward 8192 x 4096 x 14336 bf16 1.54-1.69
+// PFLOP/s by box and load (0.90-0.99 of the sustained cuBLAS rate), the backward
+// products of 4096 x 2048 x 8192 1.57.
 //
 // Forward: a pair's tile is 256 tokens x 128 ffn columns of BOTH projections.
 // The even CTA loads the 128 rows of Wg and the odd CTA the same rows of Wu as
@@ -42,7 +45,9 @@ constexpr int OUT_BYTES = 32 * 32 * 2;      // one output chunk of a warp: 32 x 
 constexpr int NBARS = 2 * STAGES + 5;
 constexpr int GLU_SMEM = STAGES * STAGE_BYTES + NEPI * 2 * OUT_BYTES + NBARS * 8 + 16 + 1024;
 static_assert(GLU_SMEM <= 232448, "shared memory per CTA");
-constexpr int GROUP = 16;                   // row pairs of tiles that share their B tiles in L2
+// Row pairs of tiles that share their B tiles in L2: forward 8192 x 4096 x 14336
+// 1144 us, with groups of 4, 8 and 32 1172, 1152 and 1201.
+constexpr int GROUP = 16;
 
 enum Act : int { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
 
@@ -422,12 +427,17 @@ glu_kernel(const __grid_constant__ GluMaps maps, const __grid_constant__ GluArgs
 //
 // With at most FEW_TOKENS tokens the call is a reading of both weights, so they
 // take the M side: a tile is R rows of Wg (accumulator lanes 0 .. R-1) and the
-// same R rows of Wu (lanes 64 ..), the tokens are the N columns (16 .. 128), and
-// up to FEW_STAGES stages of the ring keep the copies of one CTA per SM running.
-// R divides the ffn rows evenly over the SMs: the smallest number of rows per
-// SM over R = 8, 16, ..., 64 (14336 rows on 152 SMs: R = 48, two tiles each).
-// G and U of one ffn row sit in different lanes; U goes through shared memory.
-constexpr int FEW_TOKENS = 128;
+// same R rows of Wu (lanes 64 ..), the tokens are the N columns (16 .. 64), and
+// the ring's stages of FEW_SUB k-blocks keep the copies of one CTA per SM
+// running.  R divides the ffn rows evenly over the SMs: the smallest number of
+// rows per SM over R = 8, 16, ..., 64 (14336 rows on 152 SMs: R = 48, two tiles
+// each).  G and U of one ffn row sit in different lanes; U goes through shared
+// memory.  Bound: HBM.  One token through 4096 x 14336 (235 MB): 39 us, 6.0 TB/s,
+// 0.88 of the copy rate; with one k-block per stage 50 us (a stage costs about
+// 340 ns whatever it holds), as 256 x 128 tiles of the other kernel 86 us.  At
+// 128 tokens the other kernel is as fast (72 us) or faster (2048 x 8192: 31
+// against 36 us; at 64 tokens 31 against 29).
+constexpr int FEW_TOKENS = 64;
 constexpr int FEW_SUB = 2;           // k-blocks of a stage
 constexpr int FEW_STAGES = 6;
 constexpr int FEW_EPI = 4;
@@ -471,7 +481,7 @@ glu_few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
         fence_mbar_init();
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_slot), 256);
+        tmem_alloc(smem_u32(tmem_slot), 2 * FEW_TOKENS);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -612,7 +622,7 @@ glu_few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 256);
+        tmem_dealloc(tmem, 2 * FEW_TOKENS);
     }
 }
 
@@ -662,9 +672,7 @@ __device__ __forceinline__ void glu_grad_piece(const GluGradArgs& a, int64_t i, 
     static_cast<uint4*>(a.du)[i] = pack8_h(u, f16);
 }
 
-__global__ void __launch_bounds__(256) glu_grad_kernel(const __grid_constant__ GluGradArgs a) {
-    pdl_wait();
-    pdl_trigger();
+__device__ __forceinline__ void glu_grad(const GluGradArgs& a) {
     const int64_t n = a.rows * a.pieces, step = (int64_t)gridDim.x * 256;
     int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (a.vec) {                            // aligned rows are one dense run of pieces
@@ -687,18 +695,24 @@ __global__ void __launch_bounds__(256) glu_grad_kernel(const __grid_constant__ G
     }
 }
 
-// Up to three matrices of 16-bit elements to pitches the copy engine can
-// address (operand blockIdx.y), a 16-byte piece per thread and step.
+// Up to three matrices of 16-bit elements to pitches the copy engine can address.
 struct PadArgs {
     const void* src[3];
     void* dst[3];
     int64_t rows[3];
-    int cols;
+    int cols, n;
 };
-__global__ void __launch_bounds__(256) pad_rows_kernel(const __grid_constant__ PadArgs a) {
+// What a call needs before its products, in one launch: operands blockIdx.y <
+// pads.n padded, and (backward) blockIdx.y == pads.n dG and dU.
+__global__ void __launch_bounds__(256) glu_prepare_kernel(const __grid_constant__ PadArgs a,
+                                                          const __grid_constant__ GluGradArgs g) {
     pdl_wait();
     pdl_trigger();
     const int o = blockIdx.y, pieces = (a.cols + 7) / 8;
+    if (o == a.n) {
+        glu_grad(g);
+        return;
+    }
     // a warp per row: no division per piece
     for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < a.rows[o]; row += (int64_t)gridDim.x * 8)
         for (int i = threadIdx.x & 31; i < pieces; i += 32)
@@ -747,32 +761,39 @@ bool tma_ok(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) 
 size_t padded_bytes(const Operand& o) {
     return tma_ok(o.p, o.ld) ? 0 : align_up((size_t)o.rows * pad8(o.cols) * 2, 256);
 }
-// Points the operands that need it at padded copies, made in one launch.
-int pad_operands(Operand* const* ops, char* at, int sms, cudaStream_t s) {
+// Points the operands that need it at padded copies and makes these, with dG and
+// dU where `g` is given, in one launch.
+int prepare(Operand* const* ops, char* at, const GluGradArgs* g, int sms, cudaStream_t s) {
     PadArgs p;
+    GluGradArgs ga;
     std::memset(&p, 0, sizeof p);
-    unsigned n = 0;
-    int64_t most = 0;       // rows
+    std::memset(&ga, 0, sizeof ga);
+    int64_t blocks = 1;
     for (int i = 0; i < 3; ++i) {
         Operand& o = *ops[i];
         const size_t b = padded_bytes(o);
         if (!b) continue;
-        p.src[n] = o.p;
-        p.dst[n] = at;
-        p.rows[n] = o.rows;
+        p.src[p.n] = o.p;
+        p.dst[p.n] = at;
+        p.rows[p.n] = o.rows;
         p.cols = (int)o.cols;               // the three share it
-        ++n;
+        ++p.n;
         o.ld = pad8(o.cols);
-        most = std::max(most, o.rows);
+        blocks = std::max(blocks, (o.rows + 7) / 8);
         o.p = at;
         at += b;
     }
-    if (!n) return MUON_OK;
-    note_launch_begin(KC_OTHER, s);
-    cudaError_t e = launch_pdl(pad_rows_kernel, dim3((unsigned)std::min<int64_t>((most + 7) / 8, (int64_t)sms * 8), n),
-                               dim3(256), 0, s, p);
-    note_launch_end(KC_OTHER, 0.0, s);
-    if (e != cudaSuccess) return cuda_fail(e, "operand copy launch");
+    if (g) {
+        ga = *g;
+        blocks = std::max(blocks, (g->rows * g->pieces + 255) / 256);
+    }
+    const unsigned parts = (unsigned)p.n + (g ? 1u : 0u);
+    if (!parts) return MUON_OK;
+    note_launch_begin(g ? KC_GLU : KC_OTHER, s);
+    cudaError_t e = launch_pdl(glu_prepare_kernel, dim3((unsigned)std::min<int64_t>(blocks, (int64_t)sms * 8), parts), dim3(256),
+                               0, s, p, ga);
+    note_launch_end(g ? KC_GLU : KC_OTHER, 0.0, s);
+    if (e != cudaSuccess) return cuda_fail(e, "operand preparation launch");
     return MUON_OK;
 }
 
@@ -907,7 +928,7 @@ extern "C" int muon_glu_forward(const void* x, const void* w_gate, const void* w
         Workspace* w = nullptr;
         if ((r = ws_get(dc.device, s, need, &w))) return r;
         Operand* const ops[3] = {&X, &G, &U};
-        if ((r = pad_operands(ops, w->base, dc.sms, s))) return r;
+        if ((r = prepare(ops, w->base, nullptr, dc.sms, s))) return r;
     }
     if (tokens <= FEW_TOKENS) {
         FewArgs f;
@@ -981,20 +1002,14 @@ extern "C" int muon_glu_backward(const void* x, const void* w_gate, const void* 
     Workspace* w = nullptr;
     if ((r = ws_get(dc.device, s, 2 * half + part + padded_bytes(X) + padded_bytes(G) + padded_bytes(U), &w))) return r;
     g.part = reinterpret_cast<float*>(w->base + 2 * half);
-    Operand* const ops[3] = {&X, &G, &U};
-    if ((r = pad_operands(ops, w->base + 2 * half + part, dc.sms, s))) return r;
     GluGradArgs ga;
     ga.dh = dh; ga.gate = gate; ga.up = up;
     ga.dg = w->base; ga.du = w->base + half;
     ga.rows = tokens; ga.ffn = (int)ffn; ga.pieces = (int)(ldw / 8);
     ga.dtype = dtype; ga.act = act;
     ga.vec = tma_ok(dh, ffn) && tma_ok(gate, ffn) && tma_ok(up, ffn);
-    note_launch_begin(KC_GLU, s);
-    cudaError_t e = launch_pdl(glu_grad_kernel,
-                               dim3((unsigned)std::min<int64_t>((tokens * ga.pieces + 255) / 256, (int64_t)dc.sms * 8)),
-                               dim3(256), 0, s, ga);
-    note_launch_end(KC_GLU, 0.0, s);
-    if (e != cudaSuccess) return cuda_fail(e, "glu gradient launch");
+    Operand* const ops[3] = {&X, &G, &U};
+    if ((r = prepare(ops, w->base + 2 * half + part, &ga, dc.sms, s))) return r;
     const Operand DG{ga.dg, tokens, ffn, ldw}, DU{ga.du, tokens, ffn, ldw};
     GluMaps maps;
     std::memset(&maps, 0, sizeof maps);
@@ -1009,7 +1024,7 @@ extern "C" int muon_glu_backward(const void* x, const void* w_gate, const void* 
         ok = map_out(&maps.out[1], g.out[1], dtype, ffn, hidden) && map_out(&maps.out[2], g.out[2], dtype, ffn, hidden);
     if (!ok) return fail(MUON_ECUDA, "tensor map creation failed");
     note_launch_begin(KC_GLU, s);
-    e = launch_glu<false>(maps, g, s);
+    cudaError_t e = launch_glu<false>(maps, g, s);
     note_launch_end(KC_GLU, (dx ? 4.0 : 0.0) * tokens * (double)hidden * ffn + (dw_gate ? 4.0 : 0.0) * tokens * (double)hidden * ffn, s);
     if (e != cudaSuccess) return cuda_fail(e, "glu backward launch");
     if (part) {

@@ -313,16 +313,29 @@ __device__ __forceinline__ void st_async_f4(uint32_t local, uint32_t bar, uint32
 // one reading: the row rests in shared memory between its two walks
 // ---------------------------------------------------------------------------
 //
-// A row belongs to a cluster of C CTAs (C = 1 up to 53248 16-bit logits), CTA r
-// holding its r-th part in shared memory, SLOTS x NT vectors of 16 bytes at
-// most, two CTAs per SM.  The first walk takes the maximum and the sums; warp 0
+// A row belongs to a cluster of C CTAs (C = 1 up to 26624 16-bit logits), CTA r
+// holding its r-th part in shared memory, SLOTS x NT vectors of 16 bytes as a
+// rule, four CTAs per SM.  The first walk takes the maximum and the sums; warp 0
 // brings them together, exchanges them with the other CTAs of the cluster
 // (distributed shared memory, an mbarrier per row parity), forms the loss and
 // hands the gradient's factors to the other warps; the second walk takes the
 // exponentials again (cheaper than the registers to keep them in) and stores
 // the gradient, so every logit is read from memory once.  What is per row is
-// done by one warp: at eight vectors per thread and row, a per-row step of every
-// warp costs as many instructions as a vector or two of each thread.
+// done by one warp: at ten vectors per thread and row, a per-row step of every
+// warp costs as many instructions as a vector or two of each thread.  For the
+// same reason the walks have no branch per vector (slots beyond the part read
+// as -inf, copies and stores are predicated): 65536 bf16 logits 502 -> 466 us
+// for 9155 rows.
+//
+// Bound: the policy loss by HBM for fp32 (131072 logits: 5.9 TB/s of logits and
+// gradients, 0.87 of the copy rate), by instruction issue for 16-bit types (5.2
+// TB/s, 0.77: twice the logits per byte; issue slots 65-70 % busy, the rest are
+// waits between the walks).  The statistics alone read at 4.3-5.5 TB/s.
+// Other forms measured for 65536 bf16 logits, 1.2 GB: one CTA per row with the
+// second walk reading L2 again 498 us (and 603 at 131072, where the rows in
+// flight no longer fit L2), the exponentials kept in registers over a cluster
+// 819, a ring of eight vectors per thread 590.
+//
 // Thread t owns the vectors t, t + NT, ... of the part: it copies them in
 // (cp.async), reads them twice, and as soon as the second walk has taken a slot
 // it starts the copy of the next row's vector into it: no barrier guards the
@@ -385,7 +398,12 @@ struct PartArgs {
 // (their other logits are summed by that warp), and the second stores all
 // logits alike, the listed ones' gradients following once it is through.
 // Listings are kept for three rows: the one walked, the one listed next, and the
-// one before, which other warps may still be walking.
+// one before, which other warps may still be walking.  The warp's loads run a row
+// ahead (cp.async), since its chain of steps is what the walks would wait for.
+// Measured for 64 entries, 1.2 GB of logits at 65536: bf16 568 us (3.9-4.2 TB/s,
+// the walkers' two or three CTAs per SM and their issue slots bound it), fp32 467
+// (5.1 TB/s).  Listed logits handled inside the walks took 1.0-1.1 ms (branches
+// that a fifth of a warp's vectors take, and partial sectors).
 constexpr int TEACHERS = 3;
 template <int MODE>
 constexpr int TEACHER = MODE == LM_DISTILL ? 32 : 0;
@@ -1213,6 +1231,7 @@ int row_args(RowLossArgs& a, const void* logits, int64_t ld, int64_t rows, int64
     a.c2 = (float)(1.4426950408889634 / (double)temperature);
     a.inv_t = (float)(1.0 / (double)temperature);
     a.t = temperature;
+    if (!std::isfinite(a.c2)) return fail(MUON_EINVAL, "temperature must be positive and finite");
     return MUON_OK;
 }
 
