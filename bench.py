@@ -348,7 +348,7 @@ def _sliced(wl, div):
 def _kernel_hash():
     import hashlib
     h = hashlib.sha256()
-    for f in ("gemm_tc.cu", "epilogue.cuh", "muon_internal.cuh"):
+    for f in ("gemm_tc.cu", "tc_ptx.cuh", "epilogue.cuh", "muon_internal.cuh"):
         with open(os.path.join(ROOT, "newton_schulz_frobenius_gb300", "csrc", f), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()[:16]
