@@ -628,7 +628,12 @@ glu_few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
 
 // dG = dH U act'(G) and dU = dH act(G), written at a pitch of whole 16-byte
 // pieces (zeros beyond ffn), eight columns per thread and step.  Bound by HBM:
-// three matrices read, two written.
+// three matrices read, two written.  3280 x 7504 (246 MB): 33 us, 7.4 TB/s with
+// the last writes still in L2; with the activation chosen per element and two
+// pieces per step it was 45 us, most of the difference instructions to fetch.
+// Rows that start anywhere (3282 x 7507): 50 us, from 55 with eight 2-byte loads
+// per piece; padded operands alone gained more (three of 1001 columns, 333 + 2 x
+// 2731 rows: 12.4 -> 9.1 us).
 struct GluGradArgs {
     const void* dh;
     const void* gate;
@@ -641,19 +646,57 @@ struct GluGradArgs {
     int vec;                    // the inputs' rows start on 16 bytes too
 };
 
-// Eight 16-bit values of a dense row, columns c .. c + 7 (zeros from `cols` on).
-__device__ __forceinline__ uint4 load8(const void* p, int64_t row, int c, int cols, bool vec) {
-    const uint16_t* r = static_cast<const uint16_t*>(p) + row * cols + c;
-    if (vec) return *reinterpret_cast<const uint4*>(r);
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const uint32_t lo = c + 2 * k < cols ? r[2 * k] : 0u, hi = c + 2 * k + 1 < cols ? r[2 * k + 1] : 0u;
-        w[k] = lo | (hi << 16);
+// Columns c .. c + 7 of a row of a dense matrix of `n` 16-bit elements whose
+// rows start anywhere (zeros from `cols` on), read as the two aligned 16-byte
+// vectors that hold them and shifted into place.  Vectors that would reach
+// outside the matrix, at its two ends, are left to by_elements().  Loads and
+// shifts are apart so that a thread's loads leave together.
+struct Shifted {
+    const uint16_t* r;
+    int off;                    // elements past the first vector's start
+    uint4 q0, q1;
+    __device__ __forceinline__ bool at(const void* p, int64_t n, int64_t e) {
+        const uint16_t* base = static_cast<const uint16_t*>(p);
+        r = base + e;
+        off = (int)(reinterpret_cast<uintptr_t>(r) & 15) / 2;
+        return e >= off && e - off + 16 <= n;
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    __device__ __forceinline__ void load() {
+        q0 = *reinterpret_cast<const uint4*>(r - off);
+        q1 = *(reinterpret_cast<const uint4*>(r - off) + 1);
+    }
+    __device__ __forceinline__ uint4 get(int left) const {
+        uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+        const bool by4 = off & 4, by2 = off & 2;
+#pragma unroll
+        for (int k = 0; k < 6; ++k) w[k] = by4 ? w[k + 2] : w[k];
+#pragma unroll
+        for (int k = 0; k < 5; ++k) w[k] = by2 ? w[k + 1] : w[k];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            w[k] = __funnelshift_r(w[k], w[k + 1], (off & 1) * 16);
+            w[k] = 2 * k + 1 < left ? w[k] : 2 * k < left ? w[k] & 0xFFFFu : 0u;
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ uint4 by_elements(int left) const {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t l = 2 * k < left ? r[2 * k] : 0u, h = 2 * k + 1 < left ? r[2 * k + 1] : 0u;
+            w[k] = l | (h << 16);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// i / pieces for i < n, in 32 bits where they do (a 64-bit division costs more
+// than the piece).
+__device__ __forceinline__ int64_t row_of(int64_t i, int64_t n, int pieces) {
+    return n <= INT32_MAX ? (int64_t)((uint32_t)i / (uint32_t)pieces) : i / pieces;
 }
 
+template <int ACT>
 __device__ __forceinline__ void glu_grad_piece(const GluGradArgs& a, int64_t i, const uint4& qd, const uint4& qg,
                                                const uint4& qu) {
     const bool f16 = a.dtype == MUON_F16;
@@ -664,7 +707,7 @@ __device__ __forceinline__ void glu_grad_piece(const GluGradArgs& a, int64_t i, 
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         float s;
-        const float act = activate<true>(g[k], a.act, &s);
+        const float act = activate<true>(g[k], ACT, &s);
         g[k] = d[k] * u[k] * s;
         u[k] = d[k] * act;
     }
@@ -672,26 +715,53 @@ __device__ __forceinline__ void glu_grad_piece(const GluGradArgs& a, int64_t i, 
     static_cast<uint4*>(a.du)[i] = pack8_h(u, f16);
 }
 
+// One copy of the arithmetic per loop: the eight activations are most of the
+// kernel's instructions, and a launch of a few microseconds is spent fetching them.
+template <int ACT>
 __device__ __forceinline__ void glu_grad(const GluGradArgs& a) {
     const int64_t n = a.rows * a.pieces, step = (int64_t)gridDim.x * 256;
     int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (a.vec) {                            // aligned rows are one dense run of pieces
+    if (i >= n) return;
+    if (a.vec) {                            // aligned rows are one dense run of pieces, loaded a piece ahead
         const uint4 *d = static_cast<const uint4*>(a.dh), *g = static_cast<const uint4*>(a.gate),
                     *u = static_cast<const uint4*>(a.up);
-        for (; i + step < n; i += 2 * step) {
-            const uint4 d0 = __ldcs(d + i), g0 = __ldcs(g + i), u0 = __ldcs(u + i);
-            const uint4 d1 = __ldcs(d + i + step), g1 = __ldcs(g + i + step), u1 = __ldcs(u + i + step);
-            glu_grad_piece(a, i, d0, g0, u0);
-            glu_grad_piece(a, i + step, d1, g1, u1);
+        uint4 qd = __ldcs(d + i), qg = __ldcs(g + i), qu = __ldcs(u + i);
+#pragma unroll 1
+        while (true) {
+            const int64_t at = i;
+            const uint4 cd = qd, cg = qg, cu = qu;
+            i += step;
+            if (i < n) {
+                qd = __ldcs(d + i);
+                qg = __ldcs(g + i);
+                qu = __ldcs(u + i);
+            }
+            glu_grad_piece<ACT>(a, at, cd, cg, cu);
+            if (i >= n) return;
         }
-        if (i < n) glu_grad_piece(a, i, d[i], g[i], u[i]);
-        return;
     }
+    const int64_t all = a.rows * a.ffn;
+#pragma unroll 1
     for (; i < n; i += step) {
-        const int64_t row = i / a.pieces;
-        const int col = (int)(i - row * a.pieces) * 8;
-        glu_grad_piece(a, i, load8(a.dh, row, col, a.ffn, false), load8(a.gate, row, col, a.ffn, false),
-                       load8(a.up, row, col, a.ffn, false));
+        const int64_t row = row_of(i, n, a.pieces);
+        const int c = (int)(i - row * a.pieces) * 8, left = a.ffn - c;
+        const int64_t e = row * a.ffn + c;
+        Shifted d, g, u;
+        const bool id = d.at(a.dh, all, e), ig = g.at(a.gate, all, e), iu = u.at(a.up, all, e);
+        uint4 qd, qg, qu;
+        if (id && ig && iu) {
+            d.load();
+            g.load();
+            u.load();
+            qd = d.get(left);
+            qg = g.get(left);
+            qu = u.get(left);
+        } else {
+            qd = d.by_elements(left);
+            qg = g.by_elements(left);
+            qu = u.by_elements(left);
+        }
+        glu_grad_piece<ACT>(a, i, qd, qg, qu);
     }
 }
 
@@ -704,19 +774,25 @@ struct PadArgs {
 };
 // What a call needs before its products, in one launch: operands blockIdx.y <
 // pads.n padded, and (backward) blockIdx.y == pads.n dG and dU.
+template <int ACT>
 __global__ void __launch_bounds__(256) glu_prepare_kernel(const __grid_constant__ PadArgs a,
                                                           const __grid_constant__ GluGradArgs g) {
     pdl_wait();
     pdl_trigger();
     const int o = blockIdx.y, pieces = (a.cols + 7) / 8;
     if (o == a.n) {
-        glu_grad(g);
+        glu_grad<ACT>(g);
         return;
     }
-    // a warp per row: no division per piece
-    for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < a.rows[o]; row += (int64_t)gridDim.x * 8)
-        for (int i = threadIdx.x & 31; i < pieces; i += 32)
-            static_cast<uint4*>(a.dst[o])[row * pieces + i] = load8(a.src[o], row, i * 8, a.cols, false);
+    const int64_t n = a.rows[o] * pieces, all = a.rows[o] * a.cols;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = row_of(i, n, pieces);
+        const int c = (int)(i - row * pieces) * 8, left = a.cols - c;
+        Shifted v;
+        const bool in = v.at(a.src[o], all, row * a.cols + c);
+        if (in) v.load();
+        static_cast<uint4*>(a.dst[o])[i] = in ? v.get(left) : v.by_elements(left);
+    }
 }
 
 // dX from its partial sums, added in the order of the parts.
@@ -748,6 +824,7 @@ __global__ void __launch_bounds__(256) part_sum_kernel(const __grid_constant__ P
 constexpr int64_t MAX_SIDE = 1 << 20;
 constexpr int64_t MAX_TOKENS = 1 << 24;
 constexpr int SPLIT_BLOCKS = 8;     // k-blocks a part of dX keeps at least
+constexpr int SUM_COST = 12;        // the sum of dX's parts, in k-blocks' time
 
 struct Operand {
     const void* p;
@@ -779,7 +856,7 @@ int prepare(Operand* const* ops, char* at, const GluGradArgs* g, int sms, cudaSt
         p.cols = (int)o.cols;               // the three share it
         ++p.n;
         o.ld = pad8(o.cols);
-        blocks = std::max(blocks, (o.rows + 7) / 8);
+        blocks = std::max(blocks, (o.rows * (pad8(o.cols) / 8) + 255) / 256);
         o.p = at;
         at += b;
     }
@@ -790,7 +867,10 @@ int prepare(Operand* const* ops, char* at, const GluGradArgs* g, int sms, cudaSt
     const unsigned parts = (unsigned)p.n + (g ? 1u : 0u);
     if (!parts) return MUON_OK;
     note_launch_begin(g ? KC_GLU : KC_OTHER, s);
-    cudaError_t e = launch_pdl(glu_prepare_kernel, dim3((unsigned)std::min<int64_t>(blocks, (int64_t)sms * 8), parts), dim3(256),
+    auto kern = ga.act == ACT_GELU        ? glu_prepare_kernel<ACT_GELU>
+                : ga.act == ACT_GELU_TANH ? glu_prepare_kernel<ACT_GELU_TANH>
+                                          : glu_prepare_kernel<ACT_SILU>;
+    cudaError_t e = launch_pdl(kern, dim3((unsigned)std::min<int64_t>(blocks, (int64_t)sms * 8), parts), dim3(256),
                                0, s, p, ga);
     note_launch_end(g ? KC_GLU : KC_OTHER, 0.0, s);
     if (e != cudaSuccess) return cuda_fail(e, "operand preparation launch");
@@ -826,6 +906,42 @@ GluTiles tiles(int64_t rows, int64_t cols, int64_t tile_cols, int64_t k, int seg
     return t;
 }
 
+// A tile's time in k-blocks: one of few costs what its 256 x 256 results take to
+// leave, about 8 k-blocks' time.
+int tile_cost(const GluTiles& t, int splits) { return std::max(8, t.segs * t.seg_blocks / splits); }
+
+// Tiles of family b that the clusters with one fewer of family a take first.
+int extra_of(int na, int nb, int P, int ca, int cb) {
+    const int r = na % P;
+    return r ? std::min(nb / (P - r), (ca + cb / 2) / cb) : 0;
+}
+
+// Parts of dX's contraction.  dX has few tiles and a long contraction (2 ffn)
+// when the tokens are few: the number of parts, of SPLIT_BLOCKS k-blocks at
+// least, with which the last cluster of tile_of()'s schedule ends first, the
+// partial sums' own launch counted as SUM_COST (333 tokens, 1001 x 2731:
+// 8 parts instead of the 9 that fit, products 27.2 -> 23.1 us; one token, 1235 x
+// 4575: 31.0 -> 26.0).
+int dx_splits(const GluTiles& a, const GluTiles& b, int nb, int P) {
+    const int blocks = a.segs * a.seg_blocks, most = std::max(1, std::min(P / a.count, blocks / SPLIT_BLOCKS));
+    const int cb = tile_cost(b, 1);
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int s = 1; s <= most; ++s) {
+        const int na = a.count * s, ca = tile_cost(a, s), r = na % P, light = r ? P - r : 0;
+        const int extra = extra_of(na, nb, P, ca, cb), rest = nb - light * extra;
+        const int64_t full = (na + P - 1) / P;      // tiles of a where no cluster has one fewer, or of those that have more
+        const int64_t heavy = full * ca + (int64_t)((rest - light + P - 1) / P) * cb;
+        const int64_t few = light ? (full - 1) * ca + (int64_t)(extra + (rest + P - 1) / P) * cb : 0;
+        const int64_t end = std::max(heavy, few) + (s > 1 ? SUM_COST : 0);
+        if (end < least) {
+            least = end;
+            best = s;
+        }
+    }
+    return best;
+}
+
 template <bool FWD>
 cudaError_t launch_glu(GluMaps& maps, GluArgs& g, cudaStream_t s) {
     auto kern = glu_kernel<FWD>;
@@ -853,13 +969,7 @@ cudaError_t launch_glu(GluMaps& maps, GluArgs& g, cudaStream_t s) {
     });
     if (err != cudaSuccess) return err;
     const int P = (int)std::min<int64_t>(most, (int64_t)g.a.count + g.nb);
-    const int r = g.a.count % P;
-    g.extra = 0;
-    if (r && g.nb) {
-        // a tile of few k-blocks costs what its 256 x 256 results take to leave, about 8 k-blocks' time
-        const int ka = g.a.segs * g.a.seg_blocks / g.a.splits, kb = std::max(8, g.b.segs * g.b.seg_blocks);
-        g.extra = std::min(g.nb / (P - r), (ka + kb / 2) / kb);
-    }
+    g.extra = extra_of(g.a.count, g.nb, P, tile_cost(g.a, g.a.splits), tile_cost(g.b, 1));
     cfg.gridDim = dim3((unsigned)(2 * P));
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, maps, g);
@@ -989,14 +1099,10 @@ extern "C" int muon_glu_backward(const void* x, const void* w_gate, const void* 
     g.status = dc.status;
     g.a = tiles(tokens, hidden, 2 * GM, ffn, 2);
     g.b = tiles(ffn, hidden, 2 * GM, tokens, 1);
-    // dX has few tiles and a long contraction (2 ffn) when the tokens are few:
-    // its k-blocks are then cut into parts, enough of them for the pairs of the
-    // device, at least SPLIT_BLOCKS each
-    const int pairs = dc.sms / 2, blocks = g.a.segs * g.a.seg_blocks;
-    g.a.splits = std::max(1, std::min(pairs / g.a.count, blocks / SPLIT_BLOCKS));
+    g.nb = dw_gate ? 2 * g.b.count : 0;
+    g.a.splits = dx_splits(g.a, g.b, g.nb, dc.sms / 2);
     g.a.count *= g.a.splits;
     if (!dx) g.a.count = 0;
-    g.nb = dw_gate ? 2 * g.b.count : 0;
     g.ldp = (hidden + 31) / 32 * 32;
     const size_t part = dx && g.a.splits > 1 ? align_up((size_t)g.a.splits * tokens * g.ldp * 4, 256) : 0;
     Workspace* w = nullptr;
