@@ -631,9 +631,9 @@ glu_few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
 // three matrices read, two written.  3280 x 7504 (246 MB): 33 us, 7.4 TB/s with
 // the last writes still in L2; with the activation chosen per element and two
 // pieces per step it was 45 us, most of the difference instructions to fetch.
-// Rows that start anywhere (3282 x 7507): 50 us, from 55 with eight 2-byte loads
-// per piece; padded operands alone gained more (three of 1001 columns, 333 + 2 x
-// 2731 rows: 12.4 -> 9.1 us).
+// Rows that start anywhere, 3282 x 7507 beside the padding of three operands of
+// 287 columns: 59 us, from 65 with eight 2-byte loads per piece; the padding of
+// 333 + 2 x 2731 rows of 1001 columns alone 12.4 -> 9.1.
 struct GluGradArgs {
     const void* dh;
     const void* gate;
