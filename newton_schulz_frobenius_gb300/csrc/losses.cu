@@ -387,6 +387,47 @@ __device__ __forceinline__ float3 merge_lanes(float top, float s, float si, floa
 // whether it leads its vector.
 __host__ __device__ constexpr int listing_bytes(int per, int k) { return (per + 15) / 16 * 16 + (k + 127) / 128 * 16; }
 
+// A warp's run of 16-byte vectors of 16-bit values, lane l's at g + 16 l bytes,
+// where g lies o bytes after a 16-byte boundary (o even, not 0) and lanes from
+// nact on have none.  The vector before a lane's own comes from its neighbour, so
+// all but the run's ends leave as aligned 16-byte stores; lane 0 writes the run's
+// first 16 - o bytes, the lane after the last (lane 0 after 31) its last o, in
+// powers of two.  0.6 GB of bf16 logits at 50001 with a gradient of another pitch,
+// policy loss: 777 us stored by elements, 331 so (245 where the rows agree).
+__device__ __forceinline__ void store_run(uint8_t* g, const uint4& q, int nact, int o) {
+    const int lane = threadIdx.x & 31, src = (lane + 31) & 31;
+    uint32_t w[8] = {__shfl_sync(0xffffffffu, q.x, src), __shfl_sync(0xffffffffu, q.y, src),
+                     __shfl_sync(0xffffffffu, q.z, src), __shfl_sync(0xffffffffu, q.w, src), q.x, q.y, q.z, q.w};
+    const int from = 16 - o;
+    const bool by8 = from & 8, by4 = from & 4;
+#pragma unroll
+    for (int k = 0; k < 6; ++k) w[k] = by8 ? w[k + 2] : w[k];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w[k] = by4 ? w[k + 1] : w[k];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], (from & 2) * 8);
+    uint8_t* at = g - o;
+    if (lane > 0 && lane < nact) *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (nact > 0 && (lane == 0 || lane == nact)) {
+        if (lane == 0) {                        // bytes o .. 15
+            const int p4 = (o + 3) & ~3, p8 = (p4 + 7) & ~7;
+            if (o & 2)
+                *reinterpret_cast<uint16_t*>(at + o) =
+                    (uint16_t)((o & 8 ? (o & 4 ? w[3] : w[2]) : (o & 4 ? w[1] : w[0])) >> 16);
+            if (p4 & 4) *reinterpret_cast<uint32_t*>(at + p4) = p4 & 8 ? w[3] : w[1];
+            if (p8 == 8) *reinterpret_cast<uint2*>(at + 8) = make_uint2(w[2], w[3]);
+        }
+        if (lane == (nact & 31)) {              // bytes 0 .. o - 1 of what follows the run
+            uint8_t* end = lane == 0 ? at + 512 : at;
+            if (o & 8) *reinterpret_cast<uint2*>(end) = make_uint2(w[0], w[1]);
+            if (o & 4) *reinterpret_cast<uint32_t*>(end + (o & 8)) = o & 8 ? w[2] : w[0];
+            if (o & 2)
+                *reinterpret_cast<uint16_t*>(end + (o & 12)) =
+                    (uint16_t)(o & 8 ? (o & 4 ? w[3] : w[2]) : (o & 4 ? w[1] : w[0]));
+        }
+    }
+}
+
 struct PartArgs {
     int csize;              // CTAs per row
     int per;                // vectors of a row per CTA, at most SLOTS NT
@@ -794,35 +835,46 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
         const uint64_t out2 = pair2(fac.z, fac.z);
         const uint64_t ref2 = pair2(-m, -m);
         T* gp = g + part0 + t * E;
+        const int off = a.same_align ? 0 : (int)(reinterpret_cast<uintptr_t>(gp) & 15);
+        // (`run`: rows whose gradient lies elsewhere between 16-byte boundaries, in a loop of their own:
+        // the aligned one with both in it took 4-10 % longer)
+        auto slot = [&](int u, bool run) {
+            const int i = t + u * NT;
+            if (GRAD && row >= 0) {
+                uint64_t v[E / 2];
+                float f[E];
+                unpack_pairs<T>(ring[i], v);
+                exp_vec<E>(v, ref2, c22);
 #pragma unroll
-        for (int qd = 0; qd < QUARTERS && (GRAD || row < 0); ++qd) {
-            const int end = min(slots, (qd + 1) * quarter);
-#pragma unroll 1
-            for (int u = qd * quarter; u < end; ++u) {
-                const int i = t + u * NT;
-                if (GRAD && row >= 0) {
-                    uint64_t v[E / 2];
-                    float f[E];
-                    unpack_pairs<T>(ring[i], v);
-                    exp_vec<E>(v, ref2, c22);
-#pragma unroll
-                    for (int j = 0; j < E / 2; ++j) v[j] = mul2(v[j], out2);
-                    split_pairs<E>(v, f);
-                    const uint4 packed = Vec<T>::pack(f);
-                    if (a.same_align) {
-                        // evict-first in distillation alone, where it measured 565-629 -> 536-579 us for 1.2 GB
-                        // of 16-bit logits; no difference in the policy loss
-                        if (SET) {
-                            if (i < count) __stcs(reinterpret_cast<uint4*>(gp + u * (NT * E)), packed);
-                        } else {
-                            if (i < count) *reinterpret_cast<uint4*>(gp + u * (NT * E)) = packed;
-                        }
+                for (int j = 0; j < E / 2; ++j) v[j] = mul2(v[j], out2);
+                split_pairs<E>(v, f);
+                const uint4 packed = Vec<T>::pack(f);
+                if (run) {
+                    if (sizeof(T) == 2) {
+                        store_run(reinterpret_cast<uint8_t*>(gp + u * (NT * E)), packed, min(32, count - (i - lane)), off);
                     } else if (i < count) {
 #pragma unroll
                         for (int j = 0; j < E; ++j) Vec<T>::st(gp + u * (NT * E) + j, f[j]);
                     }
+                } else if (SET) {
+                    // evict-first in distillation alone, where it measured 565-629 -> 536-579 us for 1.2 GB
+                    // of 16-bit logits; no difference in the policy loss
+                    if (i < count) __stcs(reinterpret_cast<uint4*>(gp + u * (NT * E)), packed);
+                } else {
+                    if (i < count) *reinterpret_cast<uint4*>(gp + u * (NT * E)) = packed;
                 }
-                issue(u);
+            }
+            issue(u);
+        };
+#pragma unroll
+        for (int qd = 0; qd < QUARTERS && (GRAD || row < 0); ++qd) {
+            const int end = min(slots, (qd + 1) * quarter);
+            if (GRAD && off != 0) {
+#pragma unroll 1
+                for (int u = qd * quarter; u < end; ++u) slot(u, true);
+            } else {
+#pragma unroll 1
+                for (int u = qd * quarter; u < end; ++u) slot(u, false);
             }
             cp_async_commit();
         }
@@ -831,7 +883,8 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
             if (at >= 0) Vec<T>::st(g + at, ex2((odd - m) * c2) * fac.z);
         }
         if (MODE == LM_POLICY && row >= 0) {
-            // the token's own entry over what its thread stored
+            // the token's own entry over what its warp stored
+            __syncwarp();
             const int at = tok - part0;
             const bool vec = at >= 0 && at < count * E;
             if (vec ? t == at / E % NT : rank == 0 && t == odd_thread(head, tok)) Vec<T>::st(g + tok, fac.y);
@@ -930,7 +983,7 @@ __global__ void __launch_bounds__(32 * TW) teacher_kernel(const __grid_constant_
 // all logits, a CTA per GC vectors of a row.  Rows are taken last first: the
 // statistics' launch read them in order, so the last ones are still in L2.
 constexpr int GC = 2048, GU = 4;        // vectors per CTA, in flight per thread
-template <typename T>
+template <typename T, bool SAME>        // the gradient's rows on the logits' 16-byte phase
 __global__ void __launch_bounds__(256, 4) row_grad_kernel(const __grid_constant__ RowLossArgs a, int chunks) {
     constexpr int E = Vec<T>::E;
     const int V = a.vocab, t = threadIdx.x;
@@ -950,8 +1003,8 @@ __global__ void __launch_bounds__(256, 4) row_grad_kernel(const __grid_constant_
         const int tok = on ? (int)ld_index(a.tokens, row, a.tok64) : -1;
         const float f = -st.coef * st.inv_s;
         const uint64_t f2 = pair2(f, f), ref2 = pair2(-st.mx, -st.mx);
-        const bool vec = !on || a.same_align;
-        for (int i0 = chunk * GC + t; i0 < end; i0 += GU * 256) {
+        const int off = SAME || !on ? 0 : (int)(reinterpret_cast<uintptr_t>(g + head) & 15);
+        for (int i0 = chunk * GC + t; (SAME ? i0 : i0 - (t & 31)) < end; i0 += GU * 256) {   // (whole warps, for store_run)
             uint4 q[GU];
 #pragma unroll
             for (int u = 0; u < GU; ++u)
@@ -959,7 +1012,8 @@ __global__ void __launch_bounds__(256, 4) row_grad_kernel(const __grid_constant_
 #pragma unroll
             for (int u = 0; u < GU; ++u) {
                 const int v0 = head + (i0 + u * 256) * E;
-                if (i0 + u * 256 < end) {
+                const bool mine = i0 + u * 256 < end;
+                if (SAME ? mine : i0 + u * 256 - (t & 31) < end) {
                     float r[E];
                     if (on) {
                         uint64_t v[E / 2];
@@ -977,9 +1031,11 @@ __global__ void __launch_bounds__(256, 4) row_grad_kernel(const __grid_constant_
 #pragma unroll
                         for (int j = 0; j < E; ++j) r[j] = 0.f;
                     }
-                    if (vec) {
-                        *reinterpret_cast<uint4*>(g + v0) = Vec<T>::pack(r);
-                    } else {
+                    if (off == 0) {
+                        if (mine) *reinterpret_cast<uint4*>(g + v0) = Vec<T>::pack(r);
+                    } else if (sizeof(T) == 2) {
+                        store_run(reinterpret_cast<uint8_t*>(g + v0), Vec<T>::pack(r), min(32, end - (i0 + u * 256 - (t & 31))), off);
+                    } else if (mine) {
 #pragma unroll
                         for (int j = 0; j < E; ++j) Vec<T>::st(g + v0 + j, r[j]);
                     }
@@ -1185,7 +1241,7 @@ cudaError_t launch_rows(const RowLossArgs& a, int mode, const DevCtx& dc, cudaSt
 template <typename T>
 cudaError_t launch_grad(const RowLossArgs& a, cudaStream_t s) {
     const int chunks = std::max(1, (a.vocab / Vec<T>::E + GC - 1) / GC);
-    return launch_pdl(row_grad_kernel<T>, dim3((unsigned)std::min<int64_t>(a.rows * chunks, 1 << 30)), dim3(256), 0, s, a,
+    return launch_pdl(a.same_align ? row_grad_kernel<T, true> : row_grad_kernel<T, false>, dim3((unsigned)std::min<int64_t>(a.rows * chunks, 1 << 30)), dim3(256), 0, s, a,
                       chunks);
 }
 

@@ -517,3 +517,39 @@ def test_refusals_on_the_device(mg):
     with pytest.raises(mg.MuonError):
         mg.muon_distill_loss(x, torch.zeros(4, 1025, dtype=torch.int32, device="cuda"),
                              torch.zeros(4, 1025, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("vocab", [5, 50, 1003, 4099, 50257, 131077])
+def test_gradient_rows_on_another_alignment_than_the_logits(mg, dtype, vocab):
+    """The gradient's rows start elsewhere between 16-byte boundaries than the
+    logits': the same bits, and nothing beside them is written."""
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[dtype]
+    rows = 9
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    x = torch.randn(rows, vocab, device="cuda", generator=g).to(dt)
+    tok = torch.randint(0, vocab, (rows,), device="cuda", generator=g)
+    tok[1], tok[2] = 0, vocab - 1
+    adv = torch.randn(rows, device="cuda", generator=g)
+    w = torch.ones(rows, device="cuda")
+    w[4] = 0.0
+    k = min(vocab, 7)
+    idx = torch.stack([torch.randperm(vocab, device="cuda", generator=g)[:k] for _ in range(rows)])
+    tv = torch.randn(rows, k, device="cuda", generator=g)
+    lse = torch.logsumexp(tv, 1) + 0.2
+    b = torch.tensor([0, 2, 5, 6, 8], dtype=torch.int32, device="cuda")
+    calls = [lambda o: mg.muon_policy_loss(x, tok, adv, weights=w, grad=o),
+             lambda o: mg.muon_distill_loss(x, idx, tv, weights=w, grad=o),
+             lambda o: mg.muon_distill_loss(x, idx, tv, teacher_lse=lse, weights=w, grad=o),
+             lambda o: mg.muon_preference_loss(x, tok, b, grad=o)]
+    for call in calls:
+        want = torch.empty_like(x)
+        call(want)
+        for pitch in (vocab + 16, vocab + 9):
+            for off in range(8):
+                buf = torch.full((rows, pitch), 7.0, device="cuda", dtype=dt)
+                got = buf[:, off:off + vocab]
+                call(got)
+                assert torch.equal(got, want), (pitch, off)
+                got.fill_(7.0)
+                assert bool((buf == 7.0).all()), (pitch, off)
