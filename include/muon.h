@@ -347,8 +347,8 @@ int muon_pack(void* const* mats, const int64_t* ms, const int64_t* ns, const int
  * Shared by the three calls:
  *   logits     rows x vocab logits on the device, row pitch ld >= vocab elements
  *              (dtype MUON_F32, MUON_BF16 or MUON_F16; any alignment of the
- *              element; rows whose pitch and base differ from `grad`'s by
- *              multiples of 16 bytes take vector stores).  vocab in [1, 2^19].
+ *              element; fastest where the rows' addresses differ from those of
+ *              `grad`'s by multiples of 16 bytes).  vocab in [1, 2^19].
  *   grad       receives d(sum of loss)/d(logits), same type, row pitch ld_grad;
  *              may be the logits themselves (ld_grad == ld), else the two must
  *              not overlap.  Columns beyond vocab are neither read nor written.
@@ -379,6 +379,7 @@ typedef enum { MUON_I32 = 32, MUON_I64 = 64 } muon_index;
  *                     indices: KL += p_r (log p_r - log q_r).  The term is left
  *                     out where q_r is 0 in fp32.
  *   loss[r] = weight T^2 KL  (rows entries, fp32).
+ * Keeps 16 bytes per entry and 8 per row in the workspace.
  */
 int muon_distill_loss(const void* logits, int64_t ld, int64_t rows, int64_t vocab, int dtype,
                       const void* teacher_idx, int idx_dtype, const void* teacher_logits,
@@ -412,7 +413,8 @@ int muon_policy_loss(const void* logits, int64_t ld, int64_t rows, int64_t vocab
  *       sequence without labels), seq_logp[2 pairs] receives it
  *   h = beta ((s_c - ref_c) - (s_r - ref_r)) - margin   (ref_logp[2 pairs], NULL: 0)
  *   loss[i] = weight (-(1 - label_smoothing) log sigmoid(h) - label_smoothing log sigmoid(-h))
- * Sequence sums are fp64.  Keeps 16 bytes per row in the workspace.
+ * Sequence sums are fp64.  A pair of weight 0 gives loss and gradient 0; its
+ * rows are read.  Keeps 16 bytes per row in the workspace.
  */
 int muon_preference_loss(const void* logits, int64_t ld, int64_t rows, int64_t vocab, int dtype,
                          const void* tokens, int token_dtype, const void* seq_bounds, int bounds_dtype,
