@@ -148,12 +148,18 @@ def _dtype_code(t) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}: float32, bfloat16 or float16")
 
 
+_raw_stream = None      # (handle of a device's current stream, current device), once torch has CUDA up
+
+
 def _stream_ptr(stream) -> int:
+    global _raw_stream
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream[0](_raw_stream[1]())     # the handle without a Stream object around it
         import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None and torch.cuda.is_initialized():
-            return raw(torch.cuda.current_device())     # the handle without a Stream object around it
+        raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        if raw is not None and dev is not None and torch.cuda.is_initialized():
+            _raw_stream = (raw, dev)
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -551,18 +557,21 @@ def _vector(t, n, name, dtype=None):
 
 
 def _loss_outputs(logits, grad, stream, *sizes):
-    """The gradient (a new tensor unless one was given) and fp32 vectors of the given sizes."""
+    """The gradient (a new tensor unless one was given), its pointer and pitch, and fp32 vectors of the given sizes."""
     import torch
     if stream is not None:
         with _on_stream(stream):
             return _loss_outputs(logits, grad, None, *sizes)
-    dev = logits.device
-    out = [torch.empty(n, dtype=torch.float32, device=dev) for n in sizes]
+    dev, f32, empty = logits.device, torch.float32, torch.empty
     if grad is None:
-        grad = torch.empty_like(logits, memory_format=torch.contiguous_format)
+        shape = logits.shape
+        grad = empty(shape, dtype=logits.dtype, device=dev)
+        gp, ldg = grad.data_ptr(), shape[1] or 1
     elif grad.shape != logits.shape or grad.dtype is not logits.dtype:
         raise ValueError("grad must have the logits' shape and dtype")
-    return (grad, *out)
+    else:
+        gp, ldg = _rows_of(grad, "grad")
+    return (grad, gp, ldg, *[empty(n, dtype=f32, device=dev) for n in sizes])
 
 
 def muon_distill_loss(logits, teacher_idx, teacher_logits, teacher_lse=None, weights=None, temperature: float = 1.0,
@@ -583,8 +592,7 @@ def muon_distill_loss(logits, teacher_idx, teacher_logits, teacher_lse=None, wei
             _index_code(teacher_idx, "teacher_idx"), _vector(teacher_logits, rows * k, "teacher_logits"),
             _dtype_code(teacher_logits), k, _vector(teacher_lse, rows, "teacher_lse", f32),
             _vector(weights, rows, "weights", f32), temperature)
-    grad, loss = _loss_outputs(logits, grad, stream, rows)
-    gp, ldg = _rows_of(grad, "grad")
+    grad, gp, ldg, loss = _loss_outputs(logits, grad, stream, rows)
     st = lib().muon_distill_loss(*args, loss.data_ptr(), gp, ldg, _stream_ptr(stream))
     if st:
         _check(st, "muon_distill_loss")
@@ -605,8 +613,7 @@ def muon_policy_loss(logits, tokens, advantages, old_logp=None, ref_logp=None, w
             _vector(advantages, rows, "advantages", f32), _vector(old_logp, rows, "old_logp", f32),
             _vector(ref_logp, rows, "ref_logp", f32), _vector(weights, rows, "weights", f32), temperature, clip_low,
             clip_high, kl_coef)
-    grad, loss, logp = _loss_outputs(logits, grad, stream, rows, rows)
-    gp, ldg = _rows_of(grad, "grad")
+    grad, gp, ldg, loss, logp = _loss_outputs(logits, grad, stream, rows, rows)
     st = lib().muon_policy_loss(*args, loss.data_ptr(), logp.data_ptr(), gp, ldg, _stream_ptr(stream))
     if st:
         _check(st, "muon_policy_loss")
@@ -632,8 +639,7 @@ def muon_preference_loss(logits, tokens, seq_bounds, ref_logp=None, weights=None
             _vector(seq_bounds, nb, "seq_bounds"), _index_code(seq_bounds, "seq_bounds"), pairs,
             _vector(ref_logp, 2 * pairs, "ref_logp", f32), _vector(weights, pairs, "weights", f32), beta, margin,
             label_smoothing, 1 if average else 0)
-    grad, loss, seq = _loss_outputs(logits, grad, stream, pairs, 2 * pairs)
-    gp, ldg = _rows_of(grad, "grad")
+    grad, gp, ldg, loss, seq = _loss_outputs(logits, grad, stream, pairs, 2 * pairs)
     st = lib().muon_preference_loss(*args, loss.data_ptr(), seq.data_ptr(), gp, ldg, _stream_ptr(stream))
     if st:
         _check(st, "muon_preference_loss")
@@ -650,20 +656,24 @@ ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
 def _glu_args(x, w_gate, w_up, act):
     dt = x.dtype
-    for t, nm in ((x, "x"), (w_gate, "w_gate"), (w_up, "w_up")):
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{nm} must be a contiguous CUDA tensor")
-        if t.dim() != 2:
-            raise ValueError(f"{nm} must be 2-D")
-        if t.dtype is not dt:
-            raise TypeError(f"{nm}: dtype differs from x")
+    if not (x.is_cuda and w_gate.is_cuda and w_up.is_cuda and x.is_contiguous() and w_gate.is_contiguous()
+            and w_up.is_contiguous() and x.dim() == 2 and w_gate.dim() == 2 and w_up.dim() == 2
+            and w_gate.dtype is dt and w_up.dtype is dt):
+        for t, nm in ((x, "x"), (w_gate, "w_gate"), (w_up, "w_up")):
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{nm} must be a contiguous CUDA tensor")
+            if t.dim() != 2:
+                raise ValueError(f"{nm} must be 2-D")
+            if t.dtype is not dt:
+                raise TypeError(f"{nm}: dtype differs from x")
     tokens, hidden = x.shape
-    ffn = w_gate.shape[0]
-    if w_gate.shape[1] != hidden or w_up.shape != w_gate.shape:
+    shape = w_gate.shape
+    if shape[1] != hidden or w_up.shape != shape:
         raise ValueError("x is tokens x hidden, w_gate and w_up ffn x hidden")
-    if act not in ACTIVATIONS:
+    code = ACTIVATIONS.get(act)
+    if code is None:
         raise ValueError(f"act {act!r}: one of {sorted(ACTIVATIONS)}")
-    return tokens, hidden, ffn, _dtype_code(x), ACTIVATIONS[act]
+    return tokens, hidden, shape[0], _dtype_code(x), code
 
 
 def _new(stream, *like):
