@@ -84,43 +84,12 @@ struct Cfg {
 // one per CTA of a cluster (rank selects the row block); tiles_m then counts
 // row-block pairs, and in sym 2 pair p holds tn = 0 .. p.
 struct TileSched {
-    int tiles_m, tiles_n, per_batch, total, sym, pair, mc;
+    int tiles_m, tiles_n, per_batch, total, sym, pair;
 
-    // Units before pair row p of a symmetric multicast schedule: row i holds
-    // floor(i / 2) + 1 units of two tiles (tn = 2j and 2j + 1, up to i).
-    __host__ __device__ static int mc_sym_units(int p) { return p + (p / 2) * ((p - 1) / 2); }
-
-    // rank: the CTA's rank in its cluster.  valid (multicast schedules only):
-    // false when this pair's tile of the unit lies outside the matrix (odd
-    // tile counts); the pair then repeats its partner's tile and stores nothing.
-    __device__ __forceinline__ void decode(int t, int& b, int& tm, int& tn, int rank = 0, bool* valid = nullptr) const {
+    // rank: the CTA's rank in its cluster.
+    __device__ __forceinline__ void decode(int t, int& b, int& tm, int& tn, int rank = 0) const {
         b = t / per_batch;
         const int l = t - b * per_batch;
-        if (mc) {
-            // a unit is two pair tiles sharing pair row p (the same A rows):
-            // pair c = rank >> 1 takes column tile 2j + c
-            const int c = rank >> 1;
-            int p, j, lim;
-            if (sym) {
-                p = (int)(2.0f * (sqrtf((float)l + 1.0f) - 1.0f));
-                if (p < 0) p = 0;
-                while (p > 0 && mc_sym_units(p) > l) --p;
-                while (mc_sym_units(p + 1) <= l) ++p;
-                j = l - mc_sym_units(p);
-                lim = p;                       // tn <= p
-            } else {
-                p = l % tiles_m;
-                j = l / tiles_m;
-                lim = tiles_n - 1;
-            }
-            tn = 2 * j + c;
-            const bool ok = tn <= lim;
-            if (!ok) tn = 2 * j;
-            if (valid) *valid = ok;
-            tm = 2 * p + (rank & 1);
-            return;
-        }
-        if (valid) *valid = true;
         if (pair) {
             int p;
             if (sym) {
@@ -224,7 +193,7 @@ __device__ __forceinline__ void epi_store_tma(const GemmArgs& a, const CUtensorM
 // tiles keep two accumulators (a chunk accumulates while the previous one is
 // added); a 2-SM pair's 128 x 256 half-tile leaves room for one accumulator
 // beside the running sum, so its products wait for each chunk's addition.
-template <int BN, bool B_KMAJOR, bool TF32, bool PAIR, bool MC, bool CH = false>
+template <int BN, bool B_KMAJOR, bool TF32, bool PAIR, bool CH = false>
 __global__ void __launch_bounds__(NTHREADS, 1)
 gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmC, const __grid_constant__ GemmArgs args, const TileSched sched) {
@@ -234,11 +203,10 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     constexpr int NBUF = (CH && PAIR) ? 1 : 2;         // TMEM accumulators that alternate
     constexpr int SUM_COL = NBUF * BN;                 // chunked: first column of the running sum
     static_assert(!TF32 || B_KMAJOR, "TF32 products read both operands K-major");
-    static_assert(!CH || (TF32 && !MC && (PAIR ? BN == 256 : BN == 128)),
+    static_assert(!CH || (TF32 && (PAIR ? BN == 256 : BN == 128)),
                   "chunked accumulation: TF32, unpaired 128-wide or paired 256-wide tiles");
     static_assert(!CH || SUM_COL + BN <= TCOLS, "running sum inside the TMEM allocation");
     static_assert(!PAIR || BN == 256, "paired products use 128 x 256 tiles per CTA");
-    static_assert(!MC || PAIR, "multicast clusters are made of 2-SM pairs");
     constexpr int MM = PAIR ? 2 * BM : BM;      // rows of one product instruction
     const uint32_t IDESC = TF32 ? idesc_tf32(MM, BN) : idesc_f16kind(MM, BN, !B_KMAJOR, args.dtype == MUON_F16);
     constexpr int KE = TF32 ? 32 : 64;    // elements per 128-byte k-block
@@ -265,21 +233,14 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     // of B; the odd CTA relays "stage full" to the even CTA, which issues the
     // M = 256 products and commits to both; both epilogues report to the even
     // CTA's accumulator barrier.
-    // Multicast launches (MC): a cluster of two pairs takes two tiles that
-    // share their A rows (pair row p, column tiles 2j and 2j + 1).  CTA
-    // (pair c, half h) loads rows c * 64 .. + 64 of its 128 A rows and
-    // multicasts them to itself and to CTA (1 - c, h), so each A row leaves L2
-    // once per cluster; a stage is refilled only after both pairs' products
-    // have released it (the empty barriers count both pairs' commits).
     const int rank = PAIR ? (int)cluster_ctarank() : 0;
-    const int lead = rank & ~1;             // the even CTA of this CTA's pair
     const int unit0 = PAIR ? (int)cluster_idx() : (int)blockIdx.x;
     const int ustep = PAIR ? (int)cluster_count() : (int)gridDim.x;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(full0 + 8 * s, (PAIR && (rank & 1) == 0) ? 2 : 1);   // own copies (+ the peer's relay)
-            mbar_init(empty0 + 8 * s, MC ? 2 : 1);                        // one commit per pair
+            mbar_init(full0 + 8 * s, (PAIR && rank == 0) ? 2 : 1);   // own copies (+ the peer's relay)
+            mbar_init(empty0 + 8 * s, 1);
         }
         mbar_init(accf0, 1);
         mbar_init(accf0 + 8, 1);
@@ -342,17 +303,10 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     }
                     const uint32_t fb = full0 + 8 * stage;
                     mbar_expect_tx(fb, C::STAGE_BYTES);
-                    if (MC) {
-                        // half of the A rows, to this CTA and its counterpart in the other pair
-                        const int c = rank >> 1, h = rank & 1;
-                        tma_load_3d_mc(smem_u32(sA + stage * C::A_BYTES + c * (C::A_BYTES / 2)), &tmA, fb, kb * KE,
-                                       tm * BM + c * (BM / 2), b, (uint16_t)((1u << h) | (1u << (2 + h))));
-                    } else {
-                        tma_load_3d(smem_u32(sA + stage * C::A_BYTES), &tmA, fb, kb * KE, tm * BM, b);
-                    }
+                    tma_load_3d(smem_u32(sA + stage * C::A_BYTES), &tmA, fb, kb * KE, tm * BM, b);
                     if (PAIR) {
-                        // this CTA's half of B: rows (K-major) or columns (MN-major) (rank & 1) * BN / 2 ..
-                        const int hb = (rank & 1) * (BN / 2);
+                        // this CTA's half of B: rows (K-major) or columns (MN-major) rank * BN / 2 ..
+                        const int hb = rank * (BN / 2);
                         if (B_KMAJOR) {
                             tma_load_3d(smem_u32(sB + stage * C::B_BYTES), &tmB, fb, kb * KE, tn * BN + hb, b);
                         } else {
@@ -386,7 +340,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 if (issued[s] >= 0) wait_drain(full0 + 8 * s, (uint32_t)issued[s]);
         }
         __syncwarp();
-    } else if (warp == 1 && PAIR && (rank & 1) == 1) {
+    } else if (warp == 1 && PAIR && rank == 1) {
         // ---------------- relay (odd CTA of a pair) ----------------
         // every completed stage of this CTA is reported to the even CTA's full
         // barrier; this CTA refills it only after the even CTA's commit
@@ -400,7 +354,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         ok = false;
                         break;
                     }
-                    mbar_arrive_remote_relaxed(full0 + 8 * stage, (uint32_t)lead);
+                    mbar_arrive_remote_relaxed(full0 + 8 * stage, 0);
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
@@ -450,8 +404,8 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                             else tc_mma_bf16(d, ad, bd, IDESC, accum);
                         }
                     }
-                    // release the stage in both CTAs of the pair (MC: of both pairs)
-                    if (PAIR) tc_commit2(empty0 + 8 * stage, (uint16_t)(MC ? 0xF : (0x3u << lead)));
+                    // release the stage in both CTAs of the pair
+                    if (PAIR) tc_commit2(empty0 + 8 * stage, (uint16_t)0x3);
                     else tc_commit(empty0 + 8 * stage);
                     if (++stage == S) {
                         stage = 0;
@@ -459,7 +413,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     }
                 }
                 if (!ok) break;
-                if (PAIR) tc_commit2(accf0 + 8 * acc, (uint16_t)(0x3u << lead));
+                if (PAIR) tc_commit2(accf0 + 8 * acc, (uint16_t)0x3);
                 else tc_commit(accf0 + 8 * acc);
                 acc = (acc + 1) % NBUF;
                 if (acc == 0) aphase ^= 1u;
@@ -467,7 +421,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             }
             if (!ok) {
                 // wait (bounded) for the products this thread issued
-                if (PAIR) tc_commit2(drain_bar, (uint16_t)(0x1u << lead));
+                if (PAIR) tc_commit2(drain_bar, (uint16_t)0x1);
                 else tc_commit(drain_bar);
                 wait_drain(drain_bar, 0);
             }
@@ -485,10 +439,8 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         uint32_t aphase = 0;
         for (int t = unit0; t < sched.total; t += ustep) {
             int b, tm, tn;
-            bool vtile = true;
-            sched.decode(t, b, tm, tn, rank, &vtile);
-            const bool valid = MC ? vtile : true;  // MC: a repeated tile is computed, not stored
-            if (valid && args.epi == EPI_UPDATE) {
+            sched.decode(t, b, tm, tn, rank);
+            if (args.epi == EPI_UPDATE) {
                 // the update reads the caller's W: start pulling this tile's
                 // part into L2 while the products are still accumulating
                 const MatEntry e = args.mats[b];
@@ -531,7 +483,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        if (PAIR && (rank & 1)) mbar_arrive_remote(acce0 + 8 * acc, (uint32_t)lead);
+                        if (PAIR && rank == 1) mbar_arrive_remote(acce0 + 8 * acc, 0);
                         else mbar_arrive(acce0 + 8 * acc);
                     }
                     acc = (acc + 1) % NBUF;
@@ -546,8 +498,8 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             if (args.epi == EPI_UPDATE || args.epi == EPI_OUT) ent = args.mats[b];
             const int row0 = tm * BM + q * 32;
             const int warp_row_max = row0 + 31;
-            const int ch_beg = half * (HALF_COLS / 32), ch_end = valid ? (half + 1) * (HALF_COLS / 32) : ch_beg;
-            const bool loads = valid && (args.epi == EPI_POLY || args.epi == EPI_UPDATE);
+            const int ch_beg = half * (HALF_COLS / 32), ch_end = (half + 1) * (HALF_COLS / 32);
+            const bool loads = args.epi == EPI_POLY || args.epi == EPI_UPDATE;
             float gcur[32], gnxt[32];
             if (loads) epi_load_chunk<32>(args, ent, b, row0 + lane, tn * BN + ch_beg * 32, gcur);
             // every lane observes the barrier itself; the warp proceeds only together
@@ -587,7 +539,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (PAIR && (rank & 1)) mbar_arrive_remote(acce0 + 8 * acc, (uint32_t)lead);
+                if (PAIR && rank == 1) mbar_arrive_remote(acce0 + 8 * acc, 0);
                 else mbar_arrive(acce0 + 8 * acc);
             }
             acc = (acc + 1) % NBUF;
@@ -653,11 +605,11 @@ bool tma_store_enabled() {
     return !(e && e[0] == '0');
 }
 
-template <int BN, bool B_KMAJOR, bool TF32, bool PAIR, bool MC, bool CH = false>
+template <int BN, bool B_KMAJOR, bool TF32, bool PAIR, bool CH = false>
 cudaError_t launch_impl(const GemmArgs& a, int num_sms, cudaStream_t s) {
     using C = Cfg<BN, PAIR, B_KMAJOR>;
-    auto kern = gemm_tc_kernel<BN, B_KMAJOR, TF32, PAIR, MC, CH>;
-    constexpr int CL = MC ? 4 : 2;           // CTAs per cluster of a paired launch
+    auto kern = gemm_tc_kernel<BN, B_KMAJOR, TF32, PAIR, CH>;
+    constexpr int CL = 2;                    // CTAs per cluster of a paired launch
     static std::once_flag attr_once;
     static cudaError_t attr_err = cudaSuccess;
     static int max_clusters = 0;
@@ -684,9 +636,8 @@ cudaError_t launch_impl(const GemmArgs& a, int num_sms, cudaStream_t s) {
 
     CUtensorMap mA, mB;
     constexpr uint32_t KE = TF32 ? 32 : 64;   // elements per 128-byte k-block
-    // multicast launches load A in halves of BM / 2 rows
     if (!make_map(&mA, a.A, a.dtype, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.batch, (uint64_t)a.lda,
-                  (uint64_t)a.strideA, KE, MC ? BM / 2 : BM))
+                  (uint64_t)a.strideA, KE, BM))
         return cudaErrorInvalidValue;
     // a paired K-major B tile arrives as two halves of BN / 2 rows
     bool okB = B_KMAJOR ? make_map(&mB, a.B, a.dtype, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.batch,
@@ -713,12 +664,10 @@ cudaError_t launch_impl(const GemmArgs& a, int num_sms, cudaStream_t s) {
     sc.tiles_n = (a.N + BN - 1) / BN;
     sc.sym = a.symmetric ? (BN == 256 ? 2 : 1) : 0;
     sc.pair = PAIR ? 1 : 0;
-    sc.mc = MC ? 1 : 0;
     if (PAIR) {
         const int pm = (sc.tiles_m + 1) / 2;
         sc.tiles_m = pm;
-        if (MC) sc.per_batch = sc.sym ? TileSched::mc_sym_units(pm) : pm * ((sc.tiles_n + 1) / 2);
-        else sc.per_batch = sc.sym ? pm * (pm + 1) / 2 : pm * sc.tiles_n;
+        sc.per_batch = sc.sym ? pm * (pm + 1) / 2 : pm * sc.tiles_n;
     } else if (sc.sym == 2) {
         sc.per_batch = 0;
         for (int tm = 0; tm < sc.tiles_m; ++tm) sc.per_batch += tm / 2 + 1;
@@ -769,30 +718,25 @@ cudaError_t launch_gemm_tc(const GemmArgs& a, int num_sms, cudaStream_t s) {
     // loads its own operand tiles)
     const int bn = a.symmetric ? (a.tile_n == 256 ? 256 : 128) : (a.tile_n == 128 ? 128 : 256);
     const bool pair = (bn == 256) && a.pair != 0;
-    const bool mc = pair && a.mc != 0;
     if (tf32) {
         // chunked accumulation: paired 256-wide tiles when asked for, else unpaired 128-wide
         if (a.kchunk > 0)
-            return (bn == 256 && pair) ? tc::launch_impl<256, true, true, true, false, true>(a, num_sms, s)
-                                       : tc::launch_impl<128, true, true, false, false, true>(a, num_sms, s);
-        if (bn == 128) return tc::launch_impl<128, true, true, false, false>(a, num_sms, s);
-        if (!pair) return tc::launch_impl<256, true, true, false, false>(a, num_sms, s);
-        return mc ? tc::launch_impl<256, true, true, true, true>(a, num_sms, s)
-                  : tc::launch_impl<256, true, true, true, false>(a, num_sms, s);
+            return (bn == 256 && pair) ? tc::launch_impl<256, true, true, true, true>(a, num_sms, s)
+                                       : tc::launch_impl<128, true, true, false, true>(a, num_sms, s);
+        if (bn == 128) return tc::launch_impl<128, true, true, false>(a, num_sms, s);
+        return pair ? tc::launch_impl<256, true, true, true>(a, num_sms, s)
+                    : tc::launch_impl<256, true, true, false>(a, num_sms, s);
     }
     if (bn == 128) {
-        return a.b_kmajor ? tc::launch_impl<128, true, false, false, false>(a, num_sms, s)
-                          : tc::launch_impl<128, false, false, false, false>(a, num_sms, s);
+        return a.b_kmajor ? tc::launch_impl<128, true, false, false>(a, num_sms, s)
+                          : tc::launch_impl<128, false, false, false>(a, num_sms, s);
     }
     if (pair) {
-        if (mc)
-            return a.b_kmajor ? tc::launch_impl<256, true, false, true, true>(a, num_sms, s)
-                              : tc::launch_impl<256, false, false, true, true>(a, num_sms, s);
-        return a.b_kmajor ? tc::launch_impl<256, true, false, true, false>(a, num_sms, s)
-                          : tc::launch_impl<256, false, false, true, false>(a, num_sms, s);
+        return a.b_kmajor ? tc::launch_impl<256, true, false, true>(a, num_sms, s)
+                          : tc::launch_impl<256, false, false, true>(a, num_sms, s);
     }
-    return a.b_kmajor ? tc::launch_impl<256, true, false, false, false>(a, num_sms, s)
-                      : tc::launch_impl<256, false, false, false, false>(a, num_sms, s);
+    return a.b_kmajor ? tc::launch_impl<256, true, false, false>(a, num_sms, s)
+                      : tc::launch_impl<256, false, false, false>(a, num_sms, s);
 }
 
 }  // namespace muon

@@ -1,0 +1,23 @@
+"""What the CUDA sources must not hold, read as text."""
+from __future__ import annotations
+
+import glob
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "newton_schulz_frobenius_gb300", "csrc")
+
+
+def _sources():
+    return sorted(p for e in ("cu", "cuh", "h") for p in glob.glob(os.path.join(CSRC, "*." + e)))
+
+
+def test_no_multicast_load():
+    """No bulk copy of the library delivers to several CTAs of a cluster: the
+    library also runs in jobs on several GPUs.  (tcgen05.commit's multicast
+    arrive is a signal, not a load.)"""
+    for path in _sources():
+        text = re.sub(r'"\s*\n\s*"', "", open(path).read())     # adjacent string literals joined
+        for ins in re.findall(r"cp\.async\.bulk[^;\"]*", text):
+            assert "multicast" not in ins, (path, ins)
+        assert "MUON_MC" not in text, path
