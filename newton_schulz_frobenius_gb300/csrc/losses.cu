@@ -211,7 +211,7 @@ __device__ __forceinline__ void policy_row(const RowLossArgs& a, const PolicyRow
     const float rc = fminf(fmaxf(r, a.lo), a.hi);
     const float u = r * p.adv, uc = rc * p.adv;
     loss = -fminf(u, uc);
-    dl = (u <= uc || u != u) ? -u : 0.f;
+    dl = u <= uc ? -u : 0.f;
     if (a.kl != 0.f) {
         const float x = p.ref - lp;
         // exp(x) - x - 1 cancels for small x: expm1 keeps it
@@ -219,6 +219,9 @@ __device__ __forceinline__ void policy_row(const RowLossArgs& a, const PolicyRow
         loss += a.kl * (em - x);
         dl -= a.kl * em;
     }
+    // min and max drop a NaN: a row without a distribution, or a NaN among its
+    // values, has no loss either
+    if (lp != lp || u != u) loss = dl = lp + u;
 }
 
 __device__ __forceinline__ float ex2(float x) {
