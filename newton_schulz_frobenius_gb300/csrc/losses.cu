@@ -209,7 +209,8 @@ struct PolicyRow {
 __device__ __forceinline__ void policy_row(const RowLossArgs& a, const PolicyRow& p, float lp, float& loss, float& dl) {
     const float r = a.old_logp ? expf(lp - p.old) : 1.0f;
     const float rc = fminf(fmaxf(r, a.lo), a.hi);
-    const float u = r * p.adv, uc = rc * p.adv;
+    // an advantage of 0 takes the term out, also where the ratio has left fp32's range
+    const float u = p.adv == 0.f && r == r ? 0.f : r * p.adv, uc = rc * p.adv;
     loss = -fminf(u, uc);
     dl = u <= uc ? -u : 0.f;
     if (a.kl != 0.f) {

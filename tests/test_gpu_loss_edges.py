@@ -51,3 +51,14 @@ def test_policy_rows_without_a_value_have_no_loss(mg, dtype, vocab, with_old, kl
     one = dict(kw, old_logp=old[5:] if with_old else None, ref_logp=cu([-2.0]) if kl else None)
     alone = mg.muon_policy_loss(x[5:], cu([11], torch.int64), adv[5:], **one)
     assert torch.equal(alone[0], loss[5:]) and torch.equal(alone[2], g[5:])
+
+
+def test_policy_ratio_beyond_the_range(mg):
+    """exp(logp - old) over the largest fp32 number: with no advantage the row has loss and gradient 0, with a
+    positive one the clipped loss and gradient 0."""
+    x = logits(3, 500, "f32", 2)
+    x[:, 7] = 30.0                              # logp near 0
+    adv = cu([0.0, 1.5, 0.0])
+    old = cu([-100.0, -100.0, -INF])
+    loss, logp, g = mg.muon_policy_loss(x, cu([7, 7, 7], torch.int64), adv, old, clip_high=0.25)
+    assert loss.tolist() == [0.0, -1.875, 0.0] and not g.any()
