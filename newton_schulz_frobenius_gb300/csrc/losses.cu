@@ -790,7 +790,9 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
                     if (dp.y != 0.f) dm = dp.x + dp.y * (dp.z - m);
                     dm = warp_sum(dm);
                     const float ps = warp_sum(dp.y);
-                    if (writes) a.loss[row] = w * a.t * a.t * (kl + (ps != 0.f ? teacher.y - dm * a.inv_t + ps * log_s : 0.f));
+                    if (ps != 0.f) kl += teacher.y - dm * a.inv_t + ps * log_s;
+                    // a row without a distribution has no loss, with nothing listed either
+                    if (writes) a.loss[row] = all > 0.f ? w * a.t * a.t * kl : NAN;
                     const float scale = w * a.t;
                     if (lane == 0)
                         factors = make_float4(m, scale * (mass + rest) * inv_s, scale * (mass + rest - share) * inv_s, scale);

@@ -62,3 +62,22 @@ def test_policy_ratio_beyond_the_range(mg):
     old = cu([-100.0, -100.0, -INF])
     loss, logp, g = mg.muon_policy_loss(x, cu([7, 7, 7], torch.int64), adv, old, clip_high=0.25)
     assert loss.tolist() == [0.0, -1.875, 0.0] and not g.any()
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype,vocab", [("f32", 40), ("bf16", 5003), ("f16", 70001)])
+def test_distill_rows_without_a_distribution_have_no_loss(mg, dtype, vocab, tail):
+    """No finite logit or a NaN logit, with entries listed and with padding alone: loss and gradient are NaN."""
+    x = logits(6, vocab, dtype, 3)
+    x[1] = x[2] = -INF
+    x[3, vocab - 1] = x[4, vocab - 1] = NAN
+    idx = cu([[1, 9, -1]] * 6, torch.int64)
+    idx[2] = idx[4] = idx[5] = -1
+    t = cu([[1.0, 2.0, 3.0]] * 6)
+    lse = cu([3.0] * 6) if tail else None
+    loss, g = mg.muon_distill_loss(x, idx, t, teacher_lse=lse)
+    for r in range(6):
+        nan = 1 <= r <= 4
+        assert bool(torch.isnan(loss[r])) == nan, r
+        assert bool(torch.isnan(g[r]).all() if nan else torch.isfinite(g[r]).all()), r
+    assert loss[5] == 0 if not tail else abs(loss[5].item()) < 1e-6
