@@ -1117,14 +1117,16 @@ __global__ void __launch_bounds__(PT) pair_kernel(const __grid_constant__ PairAr
     if (a.average)
         for (int i = 0; i < 2; ++i) val[i] = cnt[i] > 0 ? val[i] / cnt[i] : 0.0;
     const float h = (float)((double)a.beta * (val[0] - val[1] - ref) - (double)a.margin);
-    // -log sigmoid(h), and sigmoid(h), sigmoid(-h) without overflow
-    const float e = expf(-fabsf(h));
-    const float soft = fmaxf(-h, 0.f) + log1pf(e);
+    // -log sigmoid(h) and -log sigmoid(-h), each by itself (their difference h
+    // may be infinite, or all that is left of the smaller one), and sigmoid(h),
+    // sigmoid(-h) without overflow
+    const float e = expf(-fabsf(h)), near = log1pf(e);
     const float big = 1.0f / (1.0f + e), small = e * big;
     const float sp = h >= 0.f ? big : small, sn = h >= 0.f ? small : big;
-    float loss = (1.0f - a.smoothing) * soft, dh = -(1.0f - a.smoothing) * sn;
+    float loss = 0.f, dh = -(1.0f - a.smoothing) * sn;
+    if (a.smoothing != 1.f) loss = (1.0f - a.smoothing) * (fmaxf(-h, 0.f) + near);
     if (a.smoothing != 0.f) {
-        loss += a.smoothing * (soft + h);
+        loss += a.smoothing * (fmaxf(h, 0.f) + near);
         dh += a.smoothing * sp;
     }
     if (h != h) loss = dh = h;

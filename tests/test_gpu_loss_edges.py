@@ -81,3 +81,39 @@ def test_distill_rows_without_a_distribution_have_no_loss(mg, dtype, vocab, tail
         assert bool(torch.isnan(loss[r])) == nan, r
         assert bool(torch.isnan(g[r]).all() if nan else torch.isfinite(g[r]).all()), r
     assert loss[5] == 0 if not tail else abs(loss[5].item()) < 1e-6
+
+
+@pytest.mark.parametrize("smoothing", [0.0, 0.25, 1.0])
+@pytest.mark.parametrize("side", [0, 1])
+def test_preference_with_a_banned_label(mg, side, smoothing):
+    """A label of probability 0 on one side: h is -inf or inf, each sigmoid's logarithm 0 or infinite, and the
+    gradient, whose sigmoids are 0 and 1, finite.  Smoothing's own term follows the same rule."""
+    x = logits(4, 60, "f32", 4)
+    tok = np.array([3, 5, 7, 9])
+    x[2 * side, tok[2 * side]] = -INF
+    bounds = [0, 2, 4]
+    loss, seq, g = mg.muon_preference_loss(x, cu(tok, torch.int64), cu(bounds, torch.int64), beta=0.5,
+                                           label_smoothing=smoothing)
+    weight = smoothing if side else 1 - smoothing       # of the term that is infinite
+    assert loss[0].item() == (INF if weight else 0.0)
+    assert seq[side].item() == -INF and torch.isfinite(seq[1 - side])
+    # dL/dh is weight or -weight; the rows' softmax is finite, and 0 at the banned label
+    X = x.double().cpu().numpy()
+    q = np.exp(X - X.max(1, keepdims=True))
+    q /= q.sum(1, keepdims=True)
+    one = np.zeros_like(q)
+    one[np.arange(4), tok] = 1
+    dh = weight if side else -weight
+    want = 0.5 * dh * np.array([1, 1, -1, -1.0])[:, None] * (one - q)
+    assert np.abs(g.double().cpu().numpy() - want).max() <= 2.0 ** -21 * 32      # 32: the spread of the logits
+
+
+def test_preference_smoothed_loss_far_from_the_margin(mg):
+    """-log sigmoid(-h) at h near -30 is e^h: within e^h times the error of h (a few roundings of 32)."""
+    x = logits(2, 60, "f32", 5)
+    tok, bounds = np.array([3, 5]), np.array([0, 1, 2])
+    loss, _, _ = mg.muon_preference_loss(x, cu(tok, torch.int64), cu(bounds, torch.int64), margin=30.0, beta=0.25,
+                                         label_smoothing=1.0)
+    want, _, _ = lo.preference(x.double().cpu().numpy(), tok, bounds, margin=30.0, beta=0.25, smoothing=1.0)
+    assert 0 < want[0] < 1e-11
+    assert abs(loss[0].item() / want[0] - 1) <= 4 * 2.0 ** -24 * 32 + 2.0 ** -20
