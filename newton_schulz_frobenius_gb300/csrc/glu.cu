@@ -28,6 +28,8 @@
 #include "epilogue.cuh"
 #include "tc_ptx.cuh"
 
+#include <cfloat>
+
 namespace muon {
 
 namespace {
@@ -51,8 +53,8 @@ constexpr int GROUP = 16;
 
 enum Act : int { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
 
-// act(g), and act'(g) where asked for.  Written so that large |g| give 0, 1 or
-// g, never an infinity times zero.
+// act(g), and act'(g) where asked for.  Written so that large finite |g| give 0,
+// 1 or g, never an infinity times zero.
 template <bool GRAD>
 __device__ __forceinline__ float activate(float g, int act, float* grad) {
     if (act == ACT_GELU) {
@@ -706,6 +708,9 @@ __device__ __forceinline__ void glu_grad_piece(const GluGradArgs& a, int64_t i, 
     unpack8_h(qu, u, f16);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
+        // a gate that its rounding took out of fp16's range: the limits of act and
+        // act', as at the largest finite number (NaN stays)
+        if (fabsf(g[k]) > FLT_MAX) g[k] = copysignf(FLT_MAX, g[k]);
         float s;
         const float act = activate<true>(g[k], ACT, &s);
         g[k] = d[k] * u[k] * s;
