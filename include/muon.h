@@ -439,6 +439,11 @@ int muon_preference_loss(const void* logits, int64_t ld, int64_t rows, int64_t v
  * The backward pass keeps dg and du in the workspace (4 bytes per token and ffn
  * column); rows that do not start on 16 bytes (a size that is not a multiple of
  * 8, a pointer off it) are copied there padded first.
+ * Accuracy: the tensor core's fp32 accumulators truncate; a sum of n terms of
+ * one sign comes out short by 6.4e-9 n of its value.  Contractions of the
+ * backward pass beyond 65536 terms (tokens, 2 ffn) are therefore summed in parts,
+ * with 4 more workspace bytes per result and part; the forward pass keeps one
+ * accumulator (hidden beyond 65536: short by more than fp16's half ulp).
  */
 typedef enum { MUON_ACT_SILU = 0, MUON_ACT_GELU = 1 /* exact */, MUON_ACT_GELU_TANH = 2 } muon_act;
 int muon_glu_forward(const void* x, const void* w_gate, const void* w_up, void* h, void* gate, void* up,

@@ -89,7 +89,7 @@ struct GluTiles {
     int tiles_m, tiles_n;       // pairs of row blocks, column tiles
     int seg_blocks, segs;       // k-blocks of one segment (one A and B map each), segments
     int count;                  // units of one output: tiles, times splits
-    int splits;                 // parts the k-blocks are cut into (family a only)
+    int splits;                 // parts the k-blocks are cut into
 };
 
 struct GluArgs {
@@ -102,6 +102,7 @@ struct GluArgs {
     int extra;                  // tiles of b a cluster with one tile of a less takes first
     GluOut out[3];              // H, G, U or dX, dWg, dWu
     float* part;                // dX in splits > 1 parts: [splits][rows][ldp] partial sums
+    float* part_w;              // dWg and dWu likewise: [2][splits][rows][ldp]
     int64_t ldp;
     int* status;
 };
@@ -394,9 +395,11 @@ glu_kernel(const __grid_constant__ GluMaps maps, const __grid_constant__ GluArgs
                     if (c0 >= f.cols || r0 >= f.rows) break;
                     float v[32];
                     tmem_ld32(lanes + (uint32_t)(ch * 32), v);
-                    if (t.family == 0 && f.splits > 1) {
+                    if (f.splits > 1) {
+                        const int64_t plane = t.family ? (int64_t)(t.which - 1) * f.splits + t.split : t.split;
                         if (r0 + lane < f.rows)     // ldp is a multiple of 32
-                            store_row_run<32>(g.part, ((int64_t)t.split * f.rows + r0 + lane) * g.ldp + c0, v, MUON_F32);
+                            store_row_run<32>(t.family ? g.part_w : g.part, (plane * f.rows + r0 + lane) * g.ldp + c0, v,
+                                              MUON_F32);
                         continue;
                     }
                     store_chunk(g, &maps.out[t.which], g.out[t.which], f.rows, f.cols, r0, c0, v, stage, groups);
@@ -800,7 +803,7 @@ __global__ void __launch_bounds__(256) glu_prepare_kernel(const __grid_constant_
     }
 }
 
-// dX from its partial sums, added in the order of the parts.
+// A result from its partial sums, added in the order of the parts.
 struct PartSumArgs {
     const float* part;
     void* out;
@@ -830,6 +833,12 @@ constexpr int64_t MAX_SIDE = 1 << 20;
 constexpr int64_t MAX_TOKENS = 1 << 24;
 constexpr int SPLIT_BLOCKS = 8;     // k-blocks a part of dX keeps at least
 constexpr int SUM_COST = 12;        // the sum of dX's parts, in k-blocks' time
+// The accumulators truncate: a product of same-signed terms comes out short by
+// 6.4e-9 per term (measured: 2.7e-5 at 2^12 terms, 4.2e-4 at 2^16, 6.7e-3 at
+// 2^20), which passes fp16's half ulp beyond 2^16.  The backward pass cuts longer
+// contractions (tokens, 2 ffn) into parts of at most MAX_BLOCKS k-blocks, whose
+// fp32 sums are added in round-to-nearest.
+constexpr int MAX_BLOCKS = 1024;
 
 struct Operand {
     const void* p;
@@ -921,6 +930,9 @@ int extra_of(int na, int nb, int P, int ca, int cb) {
     return r ? std::min(nb / (P - r), (ca + cb / 2) / cb) : 0;
 }
 
+// Parts that keep an accumulator's rounding below the results'.
+int least_splits(const GluTiles& t) { return (t.segs * t.seg_blocks + MAX_BLOCKS - 1) / MAX_BLOCKS; }
+
 // Parts of dX's contraction.  dX has few tiles and a long contraction (2 ffn)
 // when the tokens are few: the number of parts, of SPLIT_BLOCKS k-blocks at
 // least, with which the last cluster of tile_of()'s schedule ends first, the
@@ -928,11 +940,12 @@ int extra_of(int na, int nb, int P, int ca, int cb) {
 // 8 parts instead of the 9 that fit, products 27.2 -> 23.1 us; one token, 1235 x
 // 4575: 31.0 -> 26.0).
 int dx_splits(const GluTiles& a, const GluTiles& b, int nb, int P) {
-    const int blocks = a.segs * a.seg_blocks, most = std::max(1, std::min(P / a.count, blocks / SPLIT_BLOCKS));
-    const int cb = tile_cost(b, 1);
-    int best = 1;
+    const int blocks = a.segs * a.seg_blocks, from = least_splits(a);
+    const int most = std::max(from, std::min(P / a.count, blocks / SPLIT_BLOCKS));
+    const int cb = tile_cost(b, b.splits);
+    int best = from;
     int64_t least = INT64_MAX;
-    for (int s = 1; s <= most; ++s) {
+    for (int s = from; s <= most; ++s) {
         const int na = a.count * s, ca = tile_cost(a, s), r = na % P, light = r ? P - r : 0;
         const int extra = extra_of(na, nb, P, ca, cb), rest = nb - light * extra;
         const int64_t full = (na + P - 1) / P;      // tiles of a where no cluster has one fewer, or of those that have more
@@ -974,7 +987,7 @@ cudaError_t launch_glu(GluMaps& maps, GluArgs& g, cudaStream_t s) {
     });
     if (err != cudaSuccess) return err;
     const int P = (int)std::min<int64_t>(most, (int64_t)g.a.count + g.nb);
-    g.extra = extra_of(g.a.count, g.nb, P, tile_cost(g.a, g.a.splits), tile_cost(g.b, 1));
+    g.extra = extra_of(g.a.count, g.nb, P, tile_cost(g.a, g.a.splits), tile_cost(g.b, g.b.splits));
     cfg.gridDim = dim3((unsigned)(2 * P));
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, maps, g);
@@ -1104,15 +1117,23 @@ extern "C" int muon_glu_backward(const void* x, const void* w_gate, const void* 
     g.status = dc.status;
     g.a = tiles(tokens, hidden, 2 * GM, ffn, 2);
     g.b = tiles(ffn, hidden, 2 * GM, tokens, 1);
+    g.b.splits = least_splits(g.b);
+    // (their results alone, 128 KB a tile, are more than the device holds)
+    if ((int64_t)g.a.count * least_splits(g.a) + (int64_t)2 * g.b.count * g.b.splits > 1 << 30)
+        return fail(MUON_ENOMEM, "products of more than 2^30 tiles");
+    g.b.count *= g.b.splits;
     g.nb = dw_gate ? 2 * g.b.count : 0;
     g.a.splits = dx_splits(g.a, g.b, g.nb, dc.sms / 2);
     g.a.count *= g.a.splits;
     if (!dx) g.a.count = 0;
     g.ldp = (hidden + 31) / 32 * 32;
     const size_t part = dx && g.a.splits > 1 ? align_up((size_t)g.a.splits * tokens * g.ldp * 4, 256) : 0;
+    const size_t plane_w = (size_t)g.b.splits * ffn * g.ldp;
+    const size_t part_w = dw_gate && g.b.splits > 1 ? align_up(2 * plane_w * 4, 256) : 0, parts = part + part_w;
     Workspace* w = nullptr;
-    if ((r = ws_get(dc.device, s, 2 * half + part + padded_bytes(X) + padded_bytes(G) + padded_bytes(U), &w))) return r;
+    if ((r = ws_get(dc.device, s, 2 * half + parts + padded_bytes(X) + padded_bytes(G) + padded_bytes(U), &w))) return r;
     g.part = reinterpret_cast<float*>(w->base + 2 * half);
+    g.part_w = reinterpret_cast<float*>(w->base + 2 * half + part);
     GluGradArgs ga;
     ga.dh = dh; ga.gate = gate; ga.up = up;
     ga.dg = w->base; ga.du = w->base + half;
@@ -1120,7 +1141,7 @@ extern "C" int muon_glu_backward(const void* x, const void* w_gate, const void* 
     ga.dtype = dtype; ga.act = act;
     ga.vec = tma_ok(dh, ffn) && tma_ok(gate, ffn) && tma_ok(up, ffn);
     Operand* const ops[3] = {&X, &G, &U};
-    if ((r = prepare(ops, w->base + 2 * half + part, &ga, dc.sms, s))) return r;
+    if ((r = prepare(ops, w->base + 2 * half + parts, &ga, dc.sms, s))) return r;
     const Operand DG{ga.dg, tokens, ffn, ldw}, DU{ga.du, tokens, ffn, ldw};
     GluMaps maps;
     std::memset(&maps, 0, sizeof maps);
@@ -1138,12 +1159,16 @@ extern "C" int muon_glu_backward(const void* x, const void* w_gate, const void* 
     cudaError_t e = launch_glu<false>(maps, g, s);
     note_launch_end(KC_GLU, (dx ? 4.0 : 0.0) * tokens * (double)hidden * ffn + (dw_gate ? 4.0 : 0.0) * tokens * (double)hidden * ffn, s);
     if (e != cudaSuccess) return cuda_fail(e, "glu backward launch");
-    if (part) {
-        PartSumArgs p{g.part, dx, tokens, g.ldp, (int)hidden, g.a.splits, dtype};
+    const PartSumArgs sums[3] = {{g.part, dx, tokens, g.ldp, (int)hidden, g.a.splits, dtype},
+                                 {g.part_w, dw_gate, ffn, g.ldp, (int)hidden, g.b.splits, dtype},
+                                 {g.part_w + plane_w, dw_up, ffn, g.ldp, (int)hidden, g.b.splits, dtype}};
+    for (int i = 0; i < 3; ++i) {
+        if (!(i ? part_w : part)) continue;
         note_launch_begin(KC_GLU, s);
         e = launch_pdl(part_sum_kernel,
-                       dim3((unsigned)std::min<int64_t>(tokens, 65535), (unsigned)std::min<int64_t>((hidden + 255) / 256, 64)),
-                       dim3(256), 0, s, p);
+                       dim3((unsigned)std::min<int64_t>(sums[i].rows, 65535),
+                            (unsigned)std::min<int64_t>((hidden + 255) / 256, 64)),
+                       dim3(256), 0, s, sums[i]);
         note_launch_end(KC_GLU, 0.0, s);
         if (e != cudaSuccess) return cuda_fail(e, "glu partial sum launch");
     }

@@ -56,3 +56,45 @@ def test_a_gate_beyond_the_range_from_the_forward_pass(mg):
     assert (gate[0] == -INF).all() and not h[0].any()
     dx, dwg, dwu = mg.muon_glu_backward(x, wg, wu, gate, up, torch.ones_like(h))
     assert not dx[0].any() and all(torch.isfinite(t).all() for t in (dx, dwg, dwu))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("tokens,hidden,ffn", [(65600, 72, 40), (300001, 264, 136), (1 << 18, 33, 300)])
+def test_weight_gradients_over_many_tokens(mg, dtype, tokens, hidden, ffn):
+    """Sums of one sign, the worst case of an accumulator that truncates: 65536 terms of it at most, 2^-23 of the
+    sum per 16 terms, then one rounding.  gate = 32 and powers of two keep dg and du exact: silu(32) = 32 and
+    silu'(32) = 1 in fp32.  Columns of several sizes spread the results over a power of two, so that the mean of the
+    errors shows what truncation takes from all of them: the roundings leave it 2^-12 (five deviations of bf16's,
+    2^-8 / sqrt(3 n), over the smallest n of 2880 entries)."""
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+
+    def positive(cols):
+        size = torch.rand((1, cols), generator=g, device="cuda") * 0.5 + 0.5
+        return (size * (torch.rand((tokens, cols), generator=g, device="cuda") * 0.5 + 0.5)).to(DT[dtype])
+
+    x, dh = positive(hidden), positive(ffn) * 2.0 ** -13
+    gate, up = torch.full_like(dh, 32.0), torch.full_like(dh, 16.0)
+    w = torch.zeros(ffn, hidden, dtype=x.dtype, device="cuda")
+    dx, dwg, dwu = mg.muon_glu_backward(x, w, w, gate, up, dh)
+    assert not dx.any()
+    ref = sum(dh[k:k + 32768].double().T @ x[k:k + 32768].double() for k in range(0, tokens, 32768))
+    short = 4096 * 2.0 ** -23
+    for got, want in ((dwg, 16 * ref), (dwu, 32 * ref)):
+        err = got.double() / want - 1
+        assert err.abs().max().item() <= short + {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}[dtype] + 2.0 ** -20
+        assert abs(err.mean().item()) <= short + 2.0 ** -12
+
+
+def test_input_gradient_over_a_wide_block(mg):
+    """2 ffn beyond 65536 terms: dX in parts, ragged and crossing from dG Wg to dU Wu.  Per part of at most 1024
+    k-blocks 2^-11 of the magnitudes' sum at worst; over random signs the running sum is far below it."""
+    tokens, hidden, ffn = 300, 200, 40001
+    x, dh = rand((tokens, hidden), "f16", 1), rand((tokens, ffn), "f16", 2)
+    wg, wu = rand((ffn, hidden), "f16", 3, 0.01), rand((ffn, hidden), "f16", 4, 0.01)
+    gate, up = torch.full_like(dh, 32.0), torch.full_like(dh, 0.5)
+    dx, dwg, dwu = mg.muon_glu_backward(x, wg, wu, gate, up, dh)
+    want = (dh.double() * 0.5) @ wg.double() + (dh.double() * 32) @ wu.double()
+    size = (dh.double().abs() * 0.5) @ wg.double().abs() + (dh.double().abs() * 32) @ wu.double().abs()
+    assert ((dx.double() - want).abs() <= 2.0 ** -11 * want.abs() + 2.0 ** -11 * size).all()
+    for got, ref in ((dwg, (dh.double() * 0.5).T @ x.double()), (dwu, (dh.double() * 32).T @ x.double())):
+        assert ((got.double() - ref).abs() <= 2.0 ** -11 * ref.abs() + 2.0 ** -14 * ref.abs().max()).all()
