@@ -32,7 +32,10 @@
  *     host allocation (tables sized by the arguments) returns MUON_ENOMEM.
  *   - The library keeps a workspace per (device, stream) that only grows; the
  *     first call of a new shape set may allocate and therefore must not be made
- *     while the stream is being captured into a CUDA graph.
+ *     while the stream is being captured into a CUDA graph.  A captured call
+ *     holds the workspace of its time: that block stays with the process when a
+ *     larger call on the stream takes a new one, and the graph's replays must
+ *     be ordered against that stream's other work.
  *   - Host threads may call the library concurrently on different streams.
  *     Calls on one stream from several host threads must be serialised by the
  *     caller (a growing workspace is freed once the stream drains, while

@@ -68,6 +68,7 @@ constexpr int STAGE_SLOTS = 4;
 struct Workspace {
     char* base = nullptr;
     size_t bytes = 0;
+    bool held = false;          // a captured graph holds base's address
     int* pcnt = nullptr;        // prep kernel's per-matrix arrival counters (zero between launches)
     int pcnt_cap = 0;
     MatEntry* h_stage[STAGE_SLOTS] = {nullptr, nullptr, nullptr, nullptr};

@@ -95,11 +95,25 @@ int get_dev(DevCtx& out) {
 
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
 
+// Whether the stream is recording a graph, whose launches will hold the
+// addresses that they are given.
+static bool capturing(cudaStream_t s) {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &st) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return st == cudaStreamCaptureStatusActive;
+}
+
 int ws_get(int dev, cudaStream_t s, size_t need, Workspace** out) {
+    const bool cap = capturing(s);
     std::lock_guard<std::mutex> lk(g_mu);
     Workspace& w = g_ws[{dev, s}];
     if (w.bytes < need) {
-        if (w.base) {
+        // a block that a graph may hold is never freed: nothing tells when its last replay is over
+        const bool keep = cap || w.held;
+        if (w.base && !keep) {
             cudaError_t e = cudaStreamSynchronize(s);
             if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize(workspace grow)");
             cudaFree(w.base);
@@ -107,14 +121,19 @@ int ws_get(int dev, cudaStream_t s, size_t need, Workspace** out) {
             w.bytes = 0;
         }
         size_t want = align_up(need + need / 4, 1 << 20);
-        cudaError_t e = dev_alloc(reinterpret_cast<void**>(&w.base), want);
+        void* p = nullptr;
+        cudaError_t e = dev_alloc(&p, want);
         if (e != cudaSuccess) {
             cudaGetLastError();
             return fail(MUON_ENOMEM, "workspace allocation of %zu bytes failed: %s", want, cudaGetErrorString(e));
         }
+        if (w.base) logf(2, "workspace of %zu bytes kept for a captured graph on device %d", w.bytes, dev);
+        w.base = static_cast<char*>(p);
         w.bytes = want;
+        w.held = false;
         logf(2, "workspace grown to %zu bytes on device %d", want, dev);
     }
+    w.held = w.held || cap;
     *out = &w;
     return MUON_OK;
 }
