@@ -21,3 +21,8 @@ def test_no_multicast_load():
         for ins in re.findall(r"cp\.async\.bulk[^;\"]*", text):
             assert "multicast" not in ins, (path, ins)
         assert "MUON_MC" not in text, path
+
+
+def test_every_source_counts_for_a_rebuild():
+    from newton_schulz_frobenius_gb300 import _build
+    assert {os.path.basename(p) for p in os.listdir(CSRC)} <= {os.path.basename(p) for p in _build._deps()}
