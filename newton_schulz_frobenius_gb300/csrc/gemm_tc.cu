@@ -610,12 +610,13 @@ cudaError_t launch_impl(const GemmArgs& a, int num_sms, cudaStream_t s) {
     using C = Cfg<BN, PAIR, B_KMAJOR>;
     auto kern = gemm_tc_kernel<BN, B_KMAJOR, TF32, PAIR, CH>;
     constexpr int CL = 2;                    // CTAs per cluster of a paired launch
-    static std::once_flag attr_once;
-    static cudaError_t attr_err = cudaSuccess;
-    static int max_clusters = 0;
-    std::call_once(attr_once, [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
-        if (attr_err == cudaSuccess && PAIR) {
+    static OncePer<int, int> fits;           // by device; paired launches: clusters resident at once
+    int device = 0, max_clusters = 0;
+    cudaError_t attr_err = cudaGetDevice(&device);
+    if (attr_err != cudaSuccess) return attr_err;
+    attr_err = fits.get(device, &max_clusters, [&](int& n) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+        if (e == cudaSuccess && PAIR) {
             // how many clusters of this kernel fit on the device at once
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(CL * (num_sms / CL));
@@ -628,9 +629,10 @@ cudaError_t launch_impl(const GemmArgs& a, int num_sms, cudaStream_t s) {
             at[0].val.clusterDim.z = 1;
             cfg.attrs = at;
             cfg.numAttrs = 1;
-            attr_err = cudaOccupancyMaxActiveClusters(&max_clusters, kern, &cfg);
-            if (attr_err == cudaSuccess && max_clusters < 1) attr_err = cudaErrorInvalidConfiguration;
+            e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+            if (e == cudaSuccess && n < 1) e = cudaErrorInvalidConfiguration;
         }
+        return e;
     });
     if (attr_err != cudaSuccess) return attr_err;
 

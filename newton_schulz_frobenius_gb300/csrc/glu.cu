@@ -961,11 +961,10 @@ int dx_splits(const GluTiles& a, const GluTiles& b, int nb, int P) {
 }
 
 template <bool FWD>
-cudaError_t launch_glu(GluMaps& maps, GluArgs& g, cudaStream_t s) {
+cudaError_t launch_glu(GluMaps& maps, GluArgs& g, int device, cudaStream_t s) {
     auto kern = glu_kernel<FWD>;
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    static int most = 0;
+    static OncePer<int, int> fits;          // by device: pairs resident at once
+    int most = 0;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(GT);
     cfg.dynamicSmemBytes = GLU_SMEM;
@@ -978,12 +977,12 @@ cudaError_t launch_glu(GluMaps& maps, GluArgs& g, cudaStream_t s) {
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    std::call_once(once, [&] {
-        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GLU_SMEM);
-        if (err != cudaSuccess) return;
+    const cudaError_t err = fits.get(device, &most, [&](int& n) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GLU_SMEM);
+        if (e != cudaSuccess) return e;
         cfg.gridDim = dim3(2);
-        err = cudaOccupancyMaxActiveClusters(&most, kern, &cfg);
-        if (err == cudaSuccess && most < 1) err = cudaErrorInvalidConfiguration;
+        e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+        return e == cudaSuccess && n < 1 ? cudaErrorInvalidConfiguration : e;
     });
     if (err != cudaSuccess) return err;
     const int P = (int)std::min<int64_t>(most, (int64_t)g.a.count + g.nb);
@@ -993,11 +992,12 @@ cudaError_t launch_glu(GluMaps& maps, GluArgs& g, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, kern, maps, g);
 }
 
-int launch_few(const Operand& X, const Operand& W, const Operand& U, FewArgs& g, int sms, cudaStream_t s) {
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    std::call_once(once, [] {
-        err = cudaFuncSetAttribute(glu_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+int launch_few(const Operand& X, const Operand& W, const Operand& U, FewArgs& g, const DevCtx& dc, cudaStream_t s) {
+    static OncePer<int, int> attr;          // by device
+    const int sms = dc.sms;
+    int set = 0;
+    const cudaError_t err = attr.get(dc.device, &set, [](int&) {
+        return cudaFuncSetAttribute(glu_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
     });
     if (err != cudaSuccess) return cuda_fail(err, "cudaFuncSetAttribute");
     g.n = (g.tokens + 15) / 16 * 16;
@@ -1065,7 +1065,7 @@ extern "C" int muon_glu_forward(const void* x, const void* w_gate, const void* w
         f.tokens = (int)tokens; f.ffn = (int)ffn; f.kblocks = (int)((hidden + FEW_SUB * GK - 1) / (FEW_SUB * GK));
         f.out[0] = GluOut{h, ffn}; f.out[1] = GluOut{gate, ffn}; f.out[2] = GluOut{up, ffn};
         f.status = dc.status;
-        return launch_few(X, G, U, f, dc.sms, s);
+        return launch_few(X, G, U, f, dc, s);
     }
     GluArgs g;
     GluMaps maps;
@@ -1082,7 +1082,7 @@ extern "C" int muon_glu_forward(const void* x, const void* w_gate, const void* w
     for (int i = 0; ok && g.tma_out && i < (g.save ? 3 : 1); ++i) ok = map_out(&maps.out[i], g.out[i], dtype, tokens, ffn);
     if (!ok) return fail(MUON_ECUDA, "tensor map creation failed");
     note_launch_begin(KC_GLU, s);
-    cudaError_t e = launch_glu<true>(maps, g, s);
+    cudaError_t e = launch_glu<true>(maps, g, dc.device, s);
     note_launch_end(KC_GLU, 4.0 * (double)tokens * hidden * ffn, s);
     if (e != cudaSuccess) return cuda_fail(e, "glu forward launch");
     return MUON_OK;
@@ -1156,7 +1156,7 @@ extern "C" int muon_glu_backward(const void* x, const void* w_gate, const void* 
         ok = map_out(&maps.out[1], g.out[1], dtype, ffn, hidden) && map_out(&maps.out[2], g.out[2], dtype, ffn, hidden);
     if (!ok) return fail(MUON_ECUDA, "tensor map creation failed");
     note_launch_begin(KC_GLU, s);
-    cudaError_t e = launch_glu<false>(maps, g, s);
+    cudaError_t e = launch_glu<false>(maps, g, dc.device, s);
     note_launch_end(KC_GLU, (dx ? 4.0 : 0.0) * tokens * (double)hidden * ffn + (dw_gate ? 4.0 : 0.0) * tokens * (double)hidden * ffn, s);
     if (e != cudaSuccess) return cuda_fail(e, "glu backward launch");
     const PartSumArgs sums[3] = {{g.part, dx, tokens, g.ldp, (int)hidden, g.a.splits, dtype},

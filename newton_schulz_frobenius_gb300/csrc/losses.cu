@@ -1161,20 +1161,20 @@ size_t row_smem(int per, int k) {
 constexpr size_t PART_SMEM = 85000, MAX_SMEM = 220000;
 
 template <typename T, int MODE, int NT>
-cudaError_t launch_part(const RowLossArgs& a, int64_t nv, int csize, int* status, cudaStream_t s) {
+cudaError_t launch_part(const RowLossArgs& a, int64_t nv, int csize, const DevCtx& dc, cudaStream_t s) {
     auto kern = row_loss_kernel<T, MODE, NT>;
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    std::call_once(once, [&] {
-        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   (int)MAX_SMEM);
-        if (err == cudaSuccess) err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    static OncePer<int, int> attrs;                         // by device
+    int set = 0;
+    cudaError_t err = attrs.get(dc.device, &set, [&](int&) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MAX_SMEM);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        return e;
     });
     if (err != cudaSuccess) return err;
     PartArgs pa;
     pa.csize = csize;
     pa.per = (int)((nv + csize - 1) / csize);
-    pa.status = status;
+    pa.status = dc.status;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)csize);
     cfg.blockDim = dim3(NT + TEACHER<MODE>);
@@ -1186,21 +1186,22 @@ cudaError_t launch_part(const RowLossArgs& a, int64_t nv, int csize, int* status
     at[1].id = cudaLaunchAttributeClusterDimension;
     at[1].val.clusterDim.x = (unsigned)csize;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    // clusters resident at once, by cluster size and slots
-    static std::atomic<int> fits[MAX_CLUSTER + 1][64];
-    std::atomic<int>& fit = fits[csize][(pa.per + NT - 1) / NT];
-    int n = fit.load();
-    if (n == 0) {
+    // clusters resident at once, by device, cluster size and slots
+    static OncePer<std::tuple<int, int, int>, int> fits;
+    int n = 0;
+    err = fits.get({dc.device, csize, (pa.per + NT - 1) / NT}, &n, [&](int& v) {
         cfg.attrs = at + 1;
         cfg.numAttrs = 1;
         cudaLaunchConfig_t most = cfg;
         most.dynamicSmemBytes = row_smem<T, MODE, NT>((pa.per + NT - 1) / NT * NT, MODE == LM_DISTILL ? 256 : 0);
-        cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kern, &most);
-        if (e != cudaSuccess) return e;
-        if (n < 1) return cudaErrorInvalidConfiguration;
-        fit.store(n);
-        muon::logf(2, "row loss mode %d: %d threads, %d CTAs per row, %d vectors each, %zu bytes, %d clusters", MODE, NT, csize, pa.per, most.dynamicSmemBytes, n);
-    }
+        cudaError_t e = cudaOccupancyMaxActiveClusters(&v, kern, &most);
+        if (e == cudaSuccess && v < 1) e = cudaErrorInvalidConfiguration;
+        if (e == cudaSuccess)
+            muon::logf(2, "row loss mode %d: %d threads, %d CTAs per row, %d vectors each, %zu bytes, %d clusters", MODE,
+                       NT, csize, pa.per, most.dynamicSmemBytes, v);
+        return e;
+    });
+    if (err != cudaSuccess) return err;
     cfg.gridDim = dim3((unsigned)(csize * std::min<int64_t>(a.rows, n)));
     // A launch whose clusters walk several rows each waits for the one before it
     // to end: placed beside its last CTAs, clusters may leave holes that one of
@@ -1228,7 +1229,7 @@ template <typename T, int MODE>
 cudaError_t launch_mode(const RowLossArgs& a, const DevCtx& dc, cudaStream_t s) {
     constexpr int NT = 256 - TEACHER<MODE>, SMALL = 128 - TEACHER<MODE>;
     const int64_t nv = std::max(1, a.vocab / Vec<T>::E);       // whole vectors of a row at most
-    if (nv <= SLOTS * SMALL) return launch_part<T, MODE, SMALL>(a, nv, 1, dc.status, s);
+    if (nv <= SLOTS * SMALL) return launch_part<T, MODE, SMALL>(a, nv, 1, dc, s);
     auto smem = [&](int c) { return row_smem<T, MODE, NT>((int)((nv + c - 1) / c), a.k); };
     int c = 1;
     if (MODE == LM_DISTILL)
@@ -1236,7 +1237,7 @@ cudaError_t launch_mode(const RowLossArgs& a, const DevCtx& dc, cudaStream_t s) 
     else
         c = (int)std::min<int64_t>(MAX_CLUSTER, (nv + SLOTS * NT - 1) / (SLOTS * NT));
     while (c <= 4 && a.rows * c < dc.sms && nv > (int64_t)c * 4 * NT) c *= 2;
-    return launch_part<T, MODE, NT>(a, nv, c, dc.status, s);
+    return launch_part<T, MODE, NT>(a, nv, c, dc, s);
 }
 
 template <typename T>

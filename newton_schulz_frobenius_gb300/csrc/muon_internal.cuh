@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <map>
+#include <mutex>
 #include <utility>
 
 #include "../../include/muon.h"
@@ -250,6 +252,31 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
+
+// What is found or set up once for each key and kept: a kernel's attributes and
+// how many of its clusters fit hold on the device that was current, so the key
+// names that device.  A failure is the caller's and is not kept.
+template <typename K, typename V>
+class OncePer {
+public:
+    template <typename Make>        // cudaError_t make(V&)
+    cudaError_t get(const K& key, V* out, Make make) {
+        std::lock_guard<std::mutex> lk(mu_);
+        auto it = of_.find(key);
+        if (it == of_.end()) {
+            V v{};
+            const cudaError_t e = make(v);
+            if (e != cudaSuccess) return e;
+            it = of_.emplace(key, v).first;
+        }
+        *out = it->second;
+        return cudaSuccess;
+    }
+
+private:
+    std::mutex mu_;
+    std::map<K, V> of_;
+};
 
 // Kernel-class bookkeeping for launch counting and optional event timing.
 enum KernelClass : int {

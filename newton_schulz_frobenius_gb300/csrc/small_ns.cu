@@ -832,9 +832,15 @@ bool small_ns_fits(int m, int n, int nseg, const int* segs) {
 }
 
 cudaError_t launch_small_ns(const SmallArgs& a, int num_sms, cudaStream_t s) {
-    static cudaError_t attr = cudaFuncSetAttribute(small::small_ns_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   small::SMEM_BYTES);
-    if (attr != cudaSuccess) return attr;
+    static OncePer<int, int> attr;           // by device
+    int device = 0, set = 0;
+    cudaError_t err = cudaGetDevice(&device);
+    if (err == cudaSuccess)
+        err = attr.get(device, &set, [](int&) {
+            return cudaFuncSetAttribute(small::small_ns_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        small::SMEM_BYTES);
+        });
+    if (err != cudaSuccess) return err;
     if (a.nb < 1 || a.nb > SMALL_MAX_BUCKETS || a.param_dtype != MUON_BF16) return cudaErrorInvalidValue;
     for (int i = 0; i < a.nb; ++i) {
         const SmallBucket& bk = a.bk[i];

@@ -45,6 +45,16 @@ def forward(tokens, hidden=256, ffn=512, stream=0):
 def backward(tokens, hidden=256, ffn=512, stream=0):
     st = L.muon_glu_backward(P, P, P, P, P, P, P, P, P, tokens, hidden, ffn, 1, 0, stream)
     assert st == 0, mg.last_error_message()
+
+def product(tile_n, symmetric=0, size=512):
+    st = L.muon_debug_gemm(P, P, P, size, size, size, 1, 1, 1, symmetric, 0, 1.0, 0.0, 0.0, 0.0, tile_n, None)
+    assert st == 0, mg.last_error_message()
+
+def step(rows, cols):
+    one = (ctypes.c_void_p * 1)(P)
+    i64 = ctypes.c_int64 * 1
+    st = L.muon_step(one, one, one, i64(rows), i64(cols), 1, 1, 1, 0.02, 0.95, 0.1, 1, None)
+    assert st == 0, mg.last_error_message()
 """
 
 

@@ -10,15 +10,17 @@
 #include <stdarg.h>
 #include <stdint.h>
 #include <stdio.h>
+#include <stdlib.h>
 #include <string.h>
 
-static int device, capture;
+static int device, capture, failing = -1;
 static uintptr_t next_block = 0x100000000u;
 static char text[1 << 20];
 static size_t used;
 
 void fake_set_device(int d) { device = d; }
 void fake_set_capturing(int on) { capture = on; }
+void fake_set_failing(int d) { failing = d; } /* a device whose kernels' attributes cannot be set */
 void fake_clear(void) { used = 0; text[0] = 0; }
 const char* fake_log(void) { return text; }
 
@@ -88,6 +90,7 @@ cudaError_t CUDARTAPI cudaStreamIsCapturing(cudaStream_t s, enum cudaStreamCaptu
 }
 cudaError_t CUDARTAPI cudaFuncSetAttribute(const void* f, enum cudaFuncAttribute a, int v) {
     const int i = slot(f);
+    if (device == failing) return cudaErrorDevicesUnavailable;
     if (a == cudaFuncAttributeMaxDynamicSharedMemorySize) funcs[i].smem = v;
     if (a == cudaFuncAttributeNonPortableClusterSizeAllowed) funcs[i].wide = v;
     note("attribute %d %p %d %d\n", device, f, (int)a, v);
@@ -108,6 +111,25 @@ cudaError_t CUDARTAPI cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const voi
     const cudaError_t e = check(c, f);
     note("launch %d %p %zu %u %u %d\n", device, f, c->dynamicSmemBytes, cluster_of(c), c->gridDim.x, (int)e);
     return e;
+}
+cudaError_t CUDARTAPI cudaMallocHost(void** p, size_t n) {
+    *p = calloc(1, n);
+    return cudaSuccess;
+}
+cudaError_t CUDARTAPI cudaFreeHost(void* p) { free(p); return cudaSuccess; }
+cudaError_t CUDARTAPI cudaMemcpyAsync(void* d, const void* s, size_t n, enum cudaMemcpyKind k, cudaStream_t st) {
+    (void)d; (void)s; (void)n; (void)k; (void)st;
+    return cudaSuccess;
+}
+cudaError_t CUDARTAPI cudaEventCreate(cudaEvent_t* e) { *e = (cudaEvent_t)1; return cudaSuccess; }
+cudaError_t CUDARTAPI cudaEventCreateWithFlags(cudaEvent_t* e, unsigned f) { (void)f; *e = (cudaEvent_t)1; return cudaSuccess; }
+cudaError_t CUDARTAPI cudaEventDestroy(cudaEvent_t e) { (void)e; return cudaSuccess; }
+cudaError_t CUDARTAPI cudaEventRecord(cudaEvent_t e, cudaStream_t s) { (void)e; (void)s; return cudaSuccess; }
+cudaError_t CUDARTAPI cudaEventSynchronize(cudaEvent_t e) { (void)e; return cudaSuccess; }
+cudaError_t CUDARTAPI cudaEventElapsedTime(float* ms, cudaEvent_t a, cudaEvent_t b) {
+    (void)a; (void)b;
+    *ms = 1.0f;
+    return cudaSuccess;
 }
 static int encode_tiled(void) { return 0; }
 cudaError_t CUDARTAPI cudaGetDriverEntryPointByVersion(const char* name, void** fn, unsigned int version,

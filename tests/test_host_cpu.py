@@ -52,3 +52,58 @@ distill()                                       # the block it has still serves
 out = dict(status=st, nomem=mg.MUON_ENOMEM, mallocs=len(log("malloc")) - n, frees=len(log("free")))
 """)
     assert out["status"] == out["nomem"] and out["mallocs"] == 0 and out["frees"] == 0
+
+
+CALLS = """
+calls = dict(
+    policy=lambda: policy(rows=200, vocab=70001, dtype=1),          # clusters, above 48 KB
+    statistics=lambda: preference(rows=200, vocab=70001, dtype=1),
+    distill=lambda: distill(rows=200, vocab=70001, dtype=1, k=64),
+    wide=lambda: policy(rows=200, vocab=1 << 19),                   # 16 CTAs per row
+    few=lambda: forward(5), forward=lambda: forward(500), backward=lambda: backward(500),
+    product=lambda: product(128), paired=lambda: product(256),
+    small=lambda: step(128, 128),
+)
+"""
+
+
+def test_every_device_gets_its_kernels_set_up(tmp_path):
+    """Limits of shared memory and cluster size, and how many clusters fit, are per device: a second device of the
+    process serves the same calls as the first."""
+    out = run(tmp_path, CALLS + """
+out = {}
+for name, call in calls.items():
+    out[name] = []
+    for d in (0, 1, 0):
+        fake.fake_set_device(d)
+        fake.fake_clear()
+        try:
+            call()
+            bad = [l for l in log("launch") if l[5] != "0" or l[0] != str(d)]
+            out[name].append([len(log("launch")) > 0, bad, len(log("attribute"))])
+        except AssertionError as e:
+            out[name].append(str(e))
+""")
+    for name, (first, second, again) in out.items():
+        assert first == [True, [], first[2]] and first[2] > 0, (name, first)
+        assert second == first, (name, second)
+        assert again == [True, [], 0], (name, again)          # set up once
+
+
+def test_a_failing_device_leaves_the_others_alone(tmp_path):
+    """An error of one device's set-up is neither kept for it nor passed on."""
+    out = run(tmp_path, CALLS + """
+out = {}
+for name, call in calls.items():
+    out[name] = []
+    for failing, d in ((0, 0), (0, 1), (-1, 0)):
+        fake.fake_set_failing(failing)
+        fake.fake_set_device(d)
+        try:
+            call()
+            out[name].append("ok")
+        except AssertionError:
+            out[name].append("error")
+""")
+    for name, got in out.items():
+        assert got == ["error", "ok", "ok"], (name, got)
