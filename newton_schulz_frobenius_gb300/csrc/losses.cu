@@ -1186,14 +1186,16 @@ cudaError_t launch_part(const RowLossArgs& a, int64_t nv, int csize, const DevCt
     at[1].id = cudaLaunchAttributeClusterDimension;
     at[1].val.clusterDim.x = (unsigned)csize;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    // clusters resident at once, by device, cluster size and slots
+    // clusters resident at once with what a CTA keeps (a teacher's entries
+    // included), by device, cluster size and kilobytes
     static OncePer<std::tuple<int, int, int>, int> fits;
+    const int kb = (int)((cfg.dynamicSmemBytes + 1023) / 1024);
     int n = 0;
-    err = fits.get({dc.device, csize, (pa.per + NT - 1) / NT}, &n, [&](int& v) {
+    err = fits.get({dc.device, csize, kb}, &n, [&](int& v) {
         cfg.attrs = at + 1;
         cfg.numAttrs = 1;
         cudaLaunchConfig_t most = cfg;
-        most.dynamicSmemBytes = row_smem<T, MODE, NT>((pa.per + NT - 1) / NT * NT, MODE == LM_DISTILL ? 256 : 0);
+        most.dynamicSmemBytes = std::min((size_t)kb * 1024, MAX_SMEM);
         cudaError_t e = cudaOccupancyMaxActiveClusters(&v, kern, &most);
         if (e == cudaSuccess && v < 1) e = cudaErrorInvalidConfiguration;
         if (e == cudaSuccess)

@@ -107,3 +107,27 @@ for name, call in calls.items():
 """)
     for name, got in out.items():
         assert got == ["error", "ok", "ok"], (name, got)
+
+
+def test_distillation_plans_with_its_own_shared_memory(tmp_path):
+    """How many clusters fit is asked for what a launch takes, to the kilobyte, whatever the teacher's entries: the
+    grid is the rows' clusters or all that fit, no fewer and no more."""
+    out = run(tmp_path, """
+out = []
+for vocab, dtype in ((57344, 1), (131072, 0), (1 << 19, 0), (5000, 2)):
+    for k in (1, 64, 256, 512, 1024):
+        fake.fake_clear()
+        distill(rows=9000, vocab=vocab, dtype=dtype, k=k)
+        dev, fn, smem, cluster, grid, code = log("launch")[-1]
+        asked = [l for l in log("occupancy") if l[1] == fn]
+        out.append((vocab, k, int(smem), int(cluster), int(grid), int(code), [int(v) for v in asked[-1][2:]] if asked else None))
+""")
+    known = {}
+    for vocab, k, smem, cluster, grid, code, asked in out:
+        assert code == 0
+        key = (vocab, cluster, (smem + 1023) // 1024)
+        if asked:
+            known[key] = asked
+        size, width, fits = known[key]
+        assert width == cluster and smem <= size < smem + 1024, (vocab, k, smem, known[key])
+        assert grid == cluster * min(9000, fits)
