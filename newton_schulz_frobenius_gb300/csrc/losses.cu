@@ -132,74 +132,6 @@ struct Vec<__half> {
     static __device__ __forceinline__ uint4 pack(const float (&v)[8]) { return pack8_h(v, true); }
 };
 
-// A row is walked in 16-byte vectors aligned in memory: vector i holds the
-// elements E i - shift .. E i - shift + E - 1, where shift is how many elements
-// the row starts after a 16-byte boundary (odd vocabularies, sliced heads).
-// Elements outside [0, V) are never touched; they read as -inf.
-template <typename T>
-__device__ __forceinline__ int row_shift(const T* row) {
-    return (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
-}
-
-template <typename T>
-__device__ __forceinline__ uint4 load_vec(const T* row, int v0, int vocab) {
-    constexpr int E = Vec<T>::E;
-    if (v0 >= 0 && v0 + E <= vocab) return *reinterpret_cast<const uint4*>(row + v0);
-    float x[E];
-#pragma unroll
-    for (int j = 0; j < E; ++j) x[j] = (v0 + j >= 0 && v0 + j < vocab) ? Vec<T>::ld(row + v0 + j) : -INFINITY;
-    return Vec<T>::pack(x);
-}
-
-template <typename T>
-__device__ __forceinline__ void store_vec(T* row, int v0, int vocab, const float (&x)[Vec<T>::E], bool aligned) {
-    constexpr int E = Vec<T>::E;
-    if (aligned && v0 >= 0 && v0 + E <= vocab) {
-        *reinterpret_cast<uint4*>(row + v0) = Vec<T>::pack(x);
-    } else {
-#pragma unroll
-        for (int j = 0; j < E; ++j)
-            if (v0 + j >= 0 && v0 + j < vocab) Vec<T>::st(row + v0 + j, x[j]);
-    }
-}
-
-template <int NW>
-__device__ __forceinline__ float block_sum(float v, float* red) {
-    __syncthreads();            // red may still be read from the previous reduction
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < NW; ++i) s += red[i];
-    return s;
-}
-
-template <int NW>
-__device__ __forceinline__ float block_max(float v, float* red) {
-    __syncthreads();
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float s = red[0];
-#pragma unroll
-    for (int i = 1; i < NW; ++i) s = fmaxf(s, red[i]);
-    return s;
-}
-
-template <typename T, int NT>
-__device__ __forceinline__ void zero_row(T* row, int vocab) {
-    constexpr int E = Vec<T>::E;
-    const int shift = row_shift(row);
-    const int nv = (vocab + shift + E - 1) / E;
-    float z[E];
-#pragma unroll
-    for (int j = 0; j < E; ++j) z[j] = 0.f;
-    for (int i = threadIdx.x; i < nv; i += NT) store_vec<T>(row, i * E - shift, vocab, z, true);
-}
-
 // What the policy loss needs of one row besides its logits.
 struct PolicyRow {
     float w, adv, old, ref;

@@ -26,3 +26,14 @@ def test_no_multicast_load():
 def test_every_source_counts_for_a_rebuild():
     from newton_schulz_frobenius_gb300 import _build
     assert {os.path.basename(p) for p in os.listdir(CSRC)} <= {os.path.basename(p) for p in _build._deps()}
+
+
+def test_no_helper_without_a_caller():
+    """Every function that the operators' files define is called somewhere."""
+    everything = "".join(open(p).read() for p in _sources())
+    for name in ("losses.cu", "glu.cu"):
+        text = open(os.path.join(CSRC, name)).read()
+        defined = set(re.findall(r"__forceinline__ [\w:<>&* ]*?(\w+)\(", text))
+        assert len(defined) > 5
+        unused = {n for n in defined if len(re.findall(rf"\b{n}\b", everything)) < 2}
+        assert not unused, (name, sorted(unused))
