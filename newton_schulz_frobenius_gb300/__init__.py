@@ -505,6 +505,19 @@ def muon_adamw_step(params, grads, exp_avgs, exp_avg_sqs, lr: float, beta1: floa
 # ---------------------------------------------------------------------------
 # losses over the vocabulary, with their gradients
 # ---------------------------------------------------------------------------
+#
+# These calls and the feed-forward block's stand outside autograd: their results
+# carry no graph, whatever their inputs require, and the caller passes the
+# gradients on (logits.backward(grad)).  A tensor that the caller gives to be
+# written counts as changed in place.
+
+
+def _written(t) -> None:
+    """Moves the version of a tensor that a call has written, so that a backward pass that saved its old values says so."""
+    import torch
+    if not t.is_inference():
+        torch.autograd.graph.increment_version(t)
+
 
 def _on_stream(stream):
     """Context in which new tensors belong to `stream` (None: the current one)."""
@@ -571,6 +584,7 @@ def _loss_outputs(logits, grad, stream, *sizes):
         raise ValueError("grad must have the logits' shape and dtype")
     else:
         gp, ldg = _rows_of(grad, "grad")
+        _written(grad)
     return (grad, gp, ldg, *[empty(n, dtype=f32, device=dev) for n in sizes])
 
 
@@ -717,6 +731,9 @@ def muon_glu_backward(x, w_gate, w_up, gate, up, dh, act: str = "silu", need_dx:
                 raise ValueError(f"{nm} must be ffn x hidden of x's dtype")
     want = ([((tokens, hidden), x)] if need_dx else []) + [((ffn, hidden), x)] * ((dw_gate is None) + (dw_up is None))
     new = _new(stream, *want)
+    for t in (dw_gate, dw_up):
+        if t is not None:
+            _written(t)
     dx = new.pop(0) if need_dx else None
     dw_gate = new.pop(0) if dw_gate is None else dw_gate
     dw_up = new.pop(0) if dw_up is None else dw_up
