@@ -354,7 +354,9 @@ int muon_pack(void* const* mats, const int64_t* ms, const int64_t* ns, const int
  *              `grad`'s by multiples of 16 bytes).  vocab in [1, 2^19].
  *   grad       receives d(sum of loss)/d(logits), same type, row pitch ld_grad;
  *              may be the logits themselves (ld_grad == ld), else the two must
- *              not overlap.  Columns beyond vocab are neither read nor written.
+ *              not overlap, from their first element to their last (rows of
+ *              one between rows of the other are refused).  Columns beyond vocab
+ *              are neither read nor written.
  *   weights    NULL or one fp32 weight per row (per pair in the preference
  *              loss), a factor of loss and gradient: 1/N of a mean, a loss
  *              scale, 0 for rows outside the loss.  A row of weight 0 is not
@@ -363,8 +365,8 @@ int muon_pack(void* const* mats, const int64_t* ms, const int64_t* ns, const int
  *   index dtypes MUON_I32 or MUON_I64.
  * Arithmetic is fp32, the gradient rounded once; results do not depend on
  * scheduling.  Logits of -inf are banned entries (probability 0, gradient 0); a
- * row without a finite logit has no distribution and gives NaN.  rows == 0
- * is valid.  Masked rows' outputs are written (zeros).
+ * row without a finite logit, or with a NaN among its logits or values, gives a
+ * NaN loss and gradient.  rows == 0 is valid.  Masked rows' outputs are written (zeros).
  */
 typedef enum { MUON_I32 = 32, MUON_I64 = 64 } muon_index;
 
@@ -382,6 +384,8 @@ typedef enum { MUON_I32 = 32, MUON_I64 = 64 } muon_index;
  *                     indices: KL += p_r (log p_r - log q_r).  The term is left
  *                     out where q_r is 0 in fp32.
  *   loss[r] = weight T^2 KL  (rows entries, fp32).
+ * Made for lists of up to about 100 entries; the time grows with k, and with its
+ * square where a row repeats an index or k nears 1024.
  * Keeps 16 bytes per entry and 8 per row in the workspace.
  */
 int muon_distill_loss(const void* logits, int64_t ld, int64_t rows, int64_t vocab, int dtype,
@@ -397,8 +401,9 @@ int muon_distill_loss(const void* logits, int64_t ld, int64_t rows, int64_t voca
  *   loss[r] = weight (-min(ratio A, clip(ratio, 1 - clip_low, 1 + clip_high) A)
  *             + kl_coef (exp(ref_logp[r] - l) - (ref_logp[r] - l) - 1))
  * with A = advantages[r]; a ratio beyond the clip on the side its advantage
- * favours has no gradient.  ref_logp may be NULL when kl_coef is 0; clip_low
- * in [0, 1], clip_high >= 0.  logp[r] receives l (0 for rows outside the loss).
+ * favours has no gradient; an advantage of 0 takes the ratio's term out.
+ * ref_logp may be NULL when kl_coef is 0; clip_low in [0, 1], clip_high >= 0.
+ * logp[r] receives l (0 for rows outside the loss).
  */
 int muon_policy_loss(const void* logits, int64_t ld, int64_t rows, int64_t vocab, int dtype,
                      const void* tokens, int token_dtype, const float* advantages, const float* old_logp,

@@ -264,9 +264,10 @@ __device__ __forceinline__ void st_async_f4(uint32_t local, uint32_t bar, uint32
 // for 9155 rows.
 //
 // Bound: the policy loss by HBM for fp32 (131072 logits: 5.9 TB/s of logits and
-// gradients, 0.87 of the copy rate), by instruction issue for 16-bit types (5.2
-// TB/s, 0.77: twice the logits per byte; issue slots 65-70 % busy, the rest are
-// waits between the walks).  The statistics alone read at 4.3-5.5 TB/s.
+// gradients, 0.87 of the copy rate), for 16-bit types by the walks' instructions
+// and the waits between them (5.2 TB/s, 0.77: twice the logits per byte; issue
+// slots 61 % busy, DRAM 63 %, the largest stall the barriers).  The statistics
+// alone read at 4.3-5.5 TB/s.
 // Other forms measured for 65536 bf16 logits, 1.2 GB: one CTA per row with the
 // second walk reading L2 again 498 us (and 603 at 131072, where the rows in
 // flight no longer fit L2), the exponentials kept in registers over a cluster
@@ -374,12 +375,15 @@ struct PartArgs {
 // walks stay free of them: the first walk leaves out whole vectors that hold one
 // (their other logits are summed by that warp), and the second stores all
 // logits alike, the listed ones' gradients following once it is through.
-// Listings are kept for three rows: the one walked, the one listed next, and the
-// one before, which other warps may still be walking.  The warp's loads run a row
-// ahead (cp.async), since its chain of steps is what the walks would wait for.
-// Measured for 64 entries, 1.2 GB of logits at 65536: bf16 568 us (3.9-4.2 TB/s,
-// the walkers' two or three CTAs per SM and their issue slots bound it), fp32 467
-// (5.1 TB/s).  Listed logits handled inside the walks took 1.0-1.1 ms (branches
+// Listings are kept for three rows in turn.  (A row's own is read before the
+// first barrier of its pass alone, and the next one's written between the two
+// barriers, so fewer would do.)  The warp's loads run a row ahead (cp.async),
+// since its chain of steps is what the walks would wait for.
+// Measured for 64 entries, 1.2 GB of logits at 65536: bf16 568 us (3.9-4.2 TB/s:
+// two or three CTAs per SM are too few warps, 24 % active, to cover the waits;
+// issue slots and DRAM 54 % busy each), fp32 467 (5.1 TB/s).  More entries cost:
+// 4096 rows of 131072 bf16 logits 474 us with 64, 0.88 ms with 256, 5.9 ms with
+// 1024 (with the rest's class 0.49, 1.16 and 8.7).  Listed logits handled inside the walks took 1.0-1.1 ms (branches
 // that a fifth of a warp's vectors take, and partial sectors).
 constexpr int TEACHERS = 3;
 template <int MODE>
@@ -839,8 +843,8 @@ row_loss_kernel(const __grid_constant__ RowLossArgs a, const __grid_constant__ P
 
 // The teacher's side of every row, a warp per row: its softmax over the listed
 // entries (or against its own log-sum-exp), and repeated indices brought
-// together (looked for only where two entries of a row share a bit of a 32768-bit
-// map).  The student's logits at the entries are left to the row's own CTAs,
+// together (looked for, in k^2 steps, only where two entries of a row share a bit
+// of a 32768-bit map: 6 % of rows without a repeat at k = 64, all at 1024).  The student's logits at the entries are left to the row's own CTAs,
 // which read them while they read the row: gathered here, from all over the
 // logits at once, they took 0.4 ms for 9155 x 64.
 constexpr int TW = 4;                       // warps of a CTA
