@@ -9,8 +9,8 @@
 // Products run on 2-SM tcgen05 pairs (M = 256, N = 256, fp32 accumulation in
 // TMEM, two accumulators so that a tile's epilogue runs under the next tile's
 // products), fed by TMA through a ring of six 32 KB stages per CTA.  Bound: the
-// tensor pipe under the power cap.  Forward 8192 x 4096 x 14336 bf16 1.53-1.69
-// PFLOP/s by box and load (0.90-0.99 of the sustained cuBLAS rate), the backward
+// tensor pipe under the power cap.  Forward 8192 x 4096 x 14336 bf16 1.50-1.69
+// PFLOP/s by box and load (0.88-0.99 of the sustained cuBLAS rate), the backward
 // products of 4096 x 2048 x 8192 1.57.
 //
 // Forward: a pair's tile is 256 tokens x 128 ffn columns of BOTH projections.
@@ -51,7 +51,7 @@ constexpr int GLU_SMEM = STAGES * STAGE_BYTES + NEPI * 2 * OUT_BYTES + NBARS * 8
 static_assert(GLU_SMEM <= 232448, "shared memory per CTA");
 // Row pairs of tiles that share their B tiles in L2: forward 8192 x 4096 x 14336
 // 1144 us, with groups of 4, 8 and 32 1172, 1152 and 1201 (one box, at the fast
-// end of 1144-1264).
+// end of 1144-1280).
 constexpr int GROUP = 16;
 
 enum Act : int { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
