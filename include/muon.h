@@ -460,6 +460,62 @@ int muon_glu_backward(const void* x, const void* w_gate, const void* w_up, const
                       const void* dh, void* dx, void* dw_gate, void* dw_up, int64_t tokens, int64_t hidden,
                       int64_t ffn, int dtype, int act, void* stream);
 
+/*
+ * Rows of a block that is split over experts.  A slot is one choice of one token:
+ * slot t k + j is token t's j-th expert.  Sorted rows hold the slots in the order
+ * of their experts, equal experts in slot order; expert e's rows are
+ * [bounds[e], bounds[e + 1]), and slots without an expert (an index outside
+ * [0, num_experts): dropped choices, padding) come behind bounds[num_experts].
+ *   sort              experts: `slots` indices (MUON_I32 or MUON_I64).  Receives
+ *                     row_of[slot], its inverse slot_of[row], and num_experts + 1 bounds.
+ *   dispatch          xs[row_of[t k + j]] = x[t]; rows behind the last expert: 0
+ *   combine           y[t] = residual[t] + sum_j weights[t k + j] ys[row_of[t k + j]],
+ *                     rows behind the last expert left out (and not read); weights NULL: 1,
+ *                     which makes it the gradient of dispatch; residual may be NULL
+ *   combine_backward  dys[row_of[t k + j]] = weights[t k + j] dy[t] and
+ *                     dweights[t k + j] = <dy[t], ys[row_of[t k + j]]>; both 0 for rows
+ *                     behind the last expert (ys not read there).  The residual's
+ *                     gradient is dy.
+ * x, residual and dy are tokens x hidden with a row pitch; xs, ys, dys (tokens k
+ * rows) and y are contiguous; one type, MUON_F32, MUON_BF16 or MUON_F16, any
+ * alignment of the element (fastest where rows start on 16 bytes).  Weights and
+ * dweights are fp32.  Sums are fp32 in the order of the choices, rounded once.
+ * row_of and bounds are read on the device: as muon_expert_sort wrote them, or
+ * any rows; those outside [0, tokens k) are left out.  A row named twice by row_of
+ * is written twice.  tokens k in [0, 2^24], k and num_experts in [1, 1024], hidden
+ * in [1, 2^20].  Outputs must not overlap anything else of the call.  No workspace.
+ */
+int muon_expert_sort(const void* experts, int index_dtype, int64_t slots, int64_t num_experts, int* row_of,
+                     int* slot_of, int* bounds, void* stream);
+int muon_expert_dispatch(const void* x, int64_t ldx, int64_t tokens, int64_t k, int64_t hidden, int dtype,
+                         const int* row_of, const int* bounds, int64_t num_experts, void* xs, void* stream);
+int muon_expert_combine(const void* ys, int64_t tokens, int64_t k, int64_t hidden, int dtype, const int* row_of,
+                        const int* bounds, int64_t num_experts, const float* weights, const void* residual,
+                        int64_t ld_residual, void* y, void* stream);
+int muon_expert_combine_backward(const void* dy, int64_t ld_dy, const void* ys, int64_t tokens, int64_t k,
+                                 int64_t hidden, int dtype, const int* row_of, const int* bounds,
+                                 int64_t num_experts, const float* weights, void* dys, float* dweights,
+                                 void* stream);
+
+/*
+ * Dropout: y[i] = residual[i] + (kept(i) ? x[i] / (1 - p) : 0) over n contiguous
+ * elements (MUON_F32, MUON_BF16 or MUON_F16), residual NULL: 0.  The mask depends
+ * on i, seed and offset alone and is never stored: the gradient of x is the same
+ * call on dy without the residual, whose gradient is dy.
+ *   mask   Philox4x32-10, key = seed, counter = (i / 8, offset), 64 bits each; of the
+ *          128 bits element i takes the 16 bits number i % 8 (from word 0's low
+ *          half upwards) and stays if they are at least c = round(65536 p).
+ *          1 - p in the formula is 1 - c / 65536, so the mean is kept exactly.
+ *   seed, offset  by value, or read from the device in state (two int64: seed, offset)
+ *          if that is not NULL, so that replays of a captured call can draw anew.
+ *          Calls that shall differ (steps, layers) differ in one of them.
+ * p in [0, 1], p = 1 drops everything.  A dropped element gives 0 even where x is
+ * infinite or NaN.  fp32 arithmetic, rounded once.  y may be x or residual; else
+ * the three must not overlap.  n in [0, 2^40].  No workspace.
+ */
+int muon_dropout(const void* x, const void* residual, void* y, int64_t n, int dtype, double p, int64_t seed,
+                 int64_t offset, const int64_t* state, void* stream);
+
 /* ---- diagnostics (not part of the method) ---------------------------------- */
 
 /* Total kernels this library has launched in this process. */

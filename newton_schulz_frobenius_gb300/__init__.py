@@ -48,6 +48,8 @@ EXPORTS = (
     "muon_pack_plan", "muon_pack",
     "muon_distill_loss", "muon_policy_loss", "muon_preference_loss",
     "muon_glu_forward", "muon_glu_backward",
+    "muon_expert_sort", "muon_expert_dispatch", "muon_expert_combine", "muon_expert_combine_backward",
+    "muon_dropout",
 )
 
 _lib = None
@@ -111,6 +113,11 @@ def lib() -> ctypes.CDLL:
                                        vp, vp, vp, i64, vp]),
         "muon_glu_forward": (i32, [vp] * 6 + [i64, i64, i64, i32, i32, vp]),
         "muon_glu_backward": (i32, [vp] * 9 + [i64, i64, i64, i32, i32, vp]),
+        "muon_expert_sort": (i32, [vp, i32, i64, i64, vp, vp, vp, vp]),
+        "muon_expert_dispatch": (i32, [vp, i64, i64, i64, i64, i32, vp, vp, i64, vp, vp]),
+        "muon_expert_combine": (i32, [vp, i64, i64, i64, i32, vp, vp, i64, vp, vp, i64, vp, vp]),
+        "muon_expert_combine_backward": (i32, [vp, i64, vp, i64, i64, i64, i32, vp, vp, i64, vp, vp, vp, vp]),
+        "muon_dropout": (i32, [vp, vp, vp, i64, i32, ctypes.c_double, i64, i64, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -743,3 +750,153 @@ def muon_glu_backward(x, w_gate, w_up, gate, up, dh, act: str = "silu", need_dx:
     if st:
         _check(st, "muon_glu_backward")
     return dx, dw_gate, dw_up
+
+
+# ---------------------------------------------------------------------------
+# a block split over experts: tokens to sorted rows and back
+# ---------------------------------------------------------------------------
+
+
+def _one_device(first, *others):
+    """Every tensor given is on the current device (the one whose stream the call takes)."""
+    import torch
+    dev = first.device
+    if dev.type != "cuda" or any(t is not None and t.device != dev for t in others):
+        raise ValueError("tensors must be on one CUDA device")
+    if dev.index is not None and dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _route(row_of, bounds):
+    """(tokens, k, experts, pointers) of what muon_expert_sort returned."""
+    import torch
+    if row_of.dim() != 2:
+        raise ValueError("row_of must be tokens x k")
+    tokens, k = row_of.shape
+    experts = bounds.numel() - 1
+    if bounds.dim() != 1 or experts < 1:
+        raise ValueError("bounds needs experts + 1 entries")
+    i32 = torch.int32
+    return tokens, k, experts, _vector(row_of, tokens * k, "row_of", i32), _vector(bounds, experts + 1, "bounds", i32)
+
+
+def muon_expert_sort(experts, num_experts: int, stream=None):
+    """Sorts the slots of experts (tokens x k, or one per token; int32 or int64)
+    by expert.  Returns (row_of, slot_of, bounds), int32: the sorted row of each
+    slot (experts' shape, 2-D), the slot of each row, and num_experts + 1 row
+    offsets.  Slots whose index is outside [0, num_experts) come last."""
+    import torch
+    _one_device(experts)
+    if experts.dim() not in (1, 2):
+        raise ValueError("experts must be tokens x k")
+    shape = experts.shape if experts.dim() == 2 else (experts.shape[0], 1)
+    n = experts.numel()
+    ptr, code = _vector(experts, n, "experts"), _index_code(experts, "experts")
+    num = int(num_experts)
+    with _on_stream(stream):
+        row_of = torch.empty(shape, dtype=torch.int32, device=experts.device)
+        slot_of, bounds = (torch.empty(m, dtype=torch.int32, device=experts.device) for m in (n, min(max(num, 0), 1024) + 1))
+    st = lib().muon_expert_sort(ptr, code, n, num, row_of.data_ptr(), slot_of.data_ptr(), bounds.data_ptr(),
+                                _stream_ptr(stream))
+    if st:
+        _check(st, "muon_expert_sort")
+    return row_of, slot_of, bounds
+
+
+def muon_expert_dispatch(x, row_of, bounds, stream=None):
+    """Copies each token's row of x to its k sorted rows: (tokens k) x hidden.
+    Rows behind the last expert are zero.  Its gradient is
+    muon_expert_combine(dxs, row_of, bounds)."""
+    _one_device(x, row_of, bounds)
+    xp, ld = _rows_of(x, "x")
+    tokens, k, experts, rp, bp = _route(row_of, bounds)
+    if x.shape[0] != tokens:
+        raise ValueError("x and row_of differ in tokens")
+    xs, = _new(stream, ((tokens * k, x.shape[1]), x))
+    st = lib().muon_expert_dispatch(xp, ld, tokens, k, x.shape[1], _dtype_code(x), rp, bp, experts, xs.data_ptr(),
+                                    _stream_ptr(stream))
+    if st:
+        _check(st, "muon_expert_dispatch")
+    return xs
+
+
+def _sorted_rows(t, name, rows):
+    _cuda_contig(t, name)
+    if t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError(f"{name} must be (tokens k) x columns")
+    return t.data_ptr()
+
+
+def muon_expert_combine(ys, row_of, bounds, weights=None, residual=None, stream=None):
+    """Sums each token's sorted rows of ys, weighted (weights: tokens x k, fp32;
+    None: 1), onto residual (tokens x hidden, contiguous rows; None: 0)."""
+    import torch
+    _one_device(ys, row_of, bounds, weights, residual)
+    tokens, k, experts, rp, bp = _route(row_of, bounds)
+    yp, hidden = _sorted_rows(ys, "ys", tokens * k), ys.shape[1]
+    wp = _vector(weights, tokens * k, "weights", torch.float32)
+    ap, lda = None, hidden
+    if residual is not None:
+        if residual.shape != (tokens, hidden) or residual.dtype is not ys.dtype:
+            raise ValueError("residual must be tokens x hidden of ys' type")
+        ap, lda = _rows_of(residual, "residual")
+    y, = _new(stream, ((tokens, hidden), ys))
+    st = lib().muon_expert_combine(yp, tokens, k, hidden, _dtype_code(ys), rp, bp, experts, wp, ap, lda, y.data_ptr(),
+                                   _stream_ptr(stream))
+    if st:
+        _check(st, "muon_expert_combine")
+    return y
+
+
+def muon_expert_combine_backward(dy, ys, row_of, bounds, weights, stream=None):
+    """Gradients (dys, dweights) of muon_expert_combine with weights; the
+    residual's is dy itself."""
+    import torch
+    _one_device(dy, ys, row_of, bounds, weights)
+    tokens, k, experts, rp, bp = _route(row_of, bounds)
+    yp, hidden = _sorted_rows(ys, "ys", tokens * k), ys.shape[1]
+    if dy.shape != (tokens, hidden) or dy.dtype is not ys.dtype:
+        raise ValueError("dy must be tokens x hidden of ys' type")
+    dp, ldd = _rows_of(dy, "dy")
+    if weights is None:
+        raise ValueError("weights are required")
+    wp = _vector(weights, tokens * k, "weights", torch.float32)
+    dys, dw = _new(stream, (ys.shape, ys), ((tokens, k), weights))
+    st = lib().muon_expert_combine_backward(dp, ldd, yp, tokens, k, hidden, _dtype_code(ys), rp, bp, experts, wp,
+                                            dys.data_ptr(), dw.data_ptr(), _stream_ptr(stream))
+    if st:
+        _check(st, "muon_expert_combine_backward")
+    return dys, dw
+
+
+# ---------------------------------------------------------------------------
+# dropout
+# ---------------------------------------------------------------------------
+
+
+def muon_dropout(x, p: float, seed: int = 0, offset: int = 0, state=None, residual=None, out=None, stream=None):
+    """residual + dropout(x) with probability p (in steps of 2^-16), residual
+    None: 0.  The mask follows from (seed, offset) and the element's index and is
+    not stored: the gradient of x is muon_dropout(dy, p, ...) with the same two.
+    state: an int64 CUDA tensor (seed, offset), read when the kernel runs, in
+    their place.  out: a tensor to write to, x and residual included."""
+    import torch
+    _one_device(x, state, residual, out)
+    _cuda_contig(x, "x")
+    for t, nm in ((residual, "residual"), (out, "out")):
+        if t is not None:
+            _cuda_contig(t, nm)
+            if t.shape != x.shape or t.dtype is not x.dtype:
+                raise ValueError(f"{nm} must have x's shape and dtype")
+    sp = _vector(state, 2, "state", torch.int64)
+    if out is None:
+        out, = _new(stream, (x.shape, x))
+    else:
+        _written(out)
+    # 64 bits each, taken as they are
+    seed, offset = (((int(v) & 0xFFFFFFFFFFFFFFFF) ^ (1 << 63)) - (1 << 63) for v in (seed, offset))
+    st = lib().muon_dropout(x.data_ptr(), None if residual is None else residual.data_ptr(), out.data_ptr(), x.numel(),
+                            _dtype_code(x), float(p), seed, offset, sp, _stream_ptr(stream))
+    if st:
+        _check(st, "muon_dropout")
+    return out

@@ -1,0 +1,226 @@
+"""Sorting slots by expert, tokens to sorted rows and back, on the GPU against the fp64 oracle.
+
+Bars.  The sort and dispatch are exact.  combine sums k products and a residual
+in fp32: at most (k + 2) 2^-24 of the magnitudes' sum; one rounding to the type,
+half an ulp of the value.  dys is one fp32 product, rounded.  dweights is an
+fp32 sum of hidden products, at most hidden / 32 + 32 of them one after the
+other in a lane and five more joins: that many times 2^-24 of the magnitudes' sum.
+"""
+import numpy as np
+import pytest
+
+from oracle import expert_oracle as eo
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+TINY = {"f32": 1e-44, "bf16": 1e-37, "f16": 2.0 ** -25}
+E24 = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def mg():
+    import __graft_entry__
+    __graft_entry__.build()
+    import newton_schulz_frobenius_gb300 as pkg
+    return pkg
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def rand(rows, cols, dtype, seed, off=0, pitch=None):
+    """A matrix whose first element is `off` elements into its storage, with rows `pitch` apart."""
+    pitch = pitch or cols
+    buf = torch.full((rows * pitch + off + 8,), float("nan"), dtype=DT[dtype], device="cuda")
+    v = buf[off:off + rows * pitch].view(rows, pitch)[:, :cols]
+    v.copy_(torch.randn(rows, cols, generator=gen(seed), device="cuda"))
+    return v
+
+
+def choices(tokens, k, experts, seed=0, dropped=0.0, dtype=torch.int32):
+    e = torch.randint(0, experts, (tokens, k), generator=gen(seed), device="cuda")
+    lost = torch.rand((tokens, k), generator=gen(seed + 1), device="cuda") < dropped
+    return torch.where(lost, torch.full_like(e, -1), e).to(dtype)
+
+
+def close(got, want, err, dtype, what):
+    bound = HALF[dtype] * 1.001 * np.abs(want) + TINY[dtype] + err
+    d = np.abs(f64(got) - want)
+    assert not (~(d <= bound)).any(), (what, int((~(d <= bound)).sum()), np.nanmax(d - bound), want.shape)
+
+
+def check_sort(mg, e, n):
+    got = mg.muon_expert_sort(e, n)
+    want = eo.sort(e.cpu().numpy().reshape(e.shape[0], -1), n)
+    for a, b in zip(got, want):
+        assert a.dtype == torch.int32 and np.array_equal(a.cpu().numpy(), b)
+    return got
+
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+@pytest.mark.parametrize("tokens,k,experts", [(1, 1, 1), (1, 8, 64), (3, 2, 5), (31, 1, 7), (33, 3, 1024), (500, 6, 160),
+                                              (1024, 1, 3), (4097, 1, 1000), (3001, 7, 257), (8193, 4, 64)])
+def test_sort(mg, tokens, k, experts, dtype):
+    check_sort(mg, choices(tokens, k, experts, dropped=0.1, dtype=dtype), experts)
+    check_sort(mg, choices(tokens, k, experts, seed=5, dtype=dtype), experts)
+
+
+def test_sort_many_slots(mg):
+    """More than one walk of 32 slots per warp in a full cluster; the largest table."""
+    e = choices(300007, 2, 1024, dropped=0.01)
+    row_of, slot_of, bounds = mg.muon_expert_sort(e, 1024)
+    flat = e.reshape(-1).long()
+    flat = torch.where(flat < 0, torch.full_like(flat, 1024), flat)
+    want = torch.argsort(flat, stable=True)
+    assert torch.equal(slot_of.long(), want)
+    assert torch.equal(row_of.reshape(-1)[want].long(), torch.arange(flat.numel(), device="cuda"))
+    assert torch.equal(bounds.long(), torch.searchsorted(flat[want].contiguous(), torch.arange(1025, device="cuda")))
+
+
+def test_sort_extremes(mg):
+    check_sort(mg, torch.full((700, 3), 4, dtype=torch.int32, device="cuda"), 9)        # one expert takes all
+    check_sort(mg, torch.full((700, 3), -1, dtype=torch.int32, device="cuda"), 9)       # nobody takes any
+    check_sort(mg, torch.full((700, 3), 9, dtype=torch.int64, device="cuda"), 9)        # one too high
+    far = torch.tensor([[1 << 32, -(1 << 40), 2, (1 << 32) + 1]], device="cuda")        # not what their low words say
+    check_sort(mg, far, 9)
+    check_sort(mg, choices(50, 1, 4).reshape(-1), 4)                                    # one choice per token, 1-D
+    row_of, slot_of, bounds = mg.muon_expert_sort(torch.empty((0, 2), dtype=torch.int32, device="cuda"), 5)
+    assert row_of.shape == (0, 2) and slot_of.numel() == 0 and bounds.tolist() == [0] * 6
+
+
+SHAPES = [(1, 1, 1, 1), (1, 8, 64, 4096), (2, 3, 4, 7), (5, 2, 8, 33), (16, 2, 8, 1024), (37, 6, 160, 1001),
+          (130, 8, 64, 520), (257, 1, 3, 2050), (64, 40, 64, 24), (300, 4, 16, 4099)]
+
+
+def check_rows(mg, tokens, k, experts, hidden, dtype, dropped=0.15, off=0, pitch=None, out_off=0):
+    row_of, slot_of, bounds = mg.muon_expert_sort(choices(tokens, k, experts, seed=tokens, dropped=dropped), experts)
+    ro, live = row_of.cpu().numpy().astype(np.int64), int(bounds[-1])
+    x = rand(tokens, hidden, dtype, 1, off, pitch)
+    xs = mg.muon_expert_dispatch(x, row_of, bounds)
+    assert np.array_equal(f64(xs), eo.dispatch(f64(x), ro, live))
+    ys = rand(tokens * k, hidden, dtype, 2, out_off)
+    ys[live:] = float("nan")                    # rows of dropped slots are not read
+    w = torch.randn(tokens, k, generator=gen(3), device="cuda")
+    res, dy = rand(tokens, hidden, dtype, 4, off, pitch), rand(tokens, hidden, dtype, 5, off, pitch)
+    Y, W, R, D = f64(ys), f64(w), f64(res), f64(dy)
+    Y[live:] = 0.0
+    for weights, residual in ((w, None), (w, res), (None, None), (None, res)):
+        y = mg.muon_expert_combine(ys, row_of, bounds, weights=weights, residual=residual)
+        ww, rr = (None if weights is None else W), (None if residual is None else R)
+        size = eo.combine(np.abs(Y), ro, live, None if ww is None else np.abs(ww), None if rr is None else np.abs(rr))
+        close(y, eo.combine(Y, ro, live, ww, rr), (k + 2) * E24 * size, dtype, "y")
+    dys, dw = mg.muon_expert_combine_backward(dy, ys, row_of, bounds, w)
+    want, want_w = eo.combine_backward(D, Y, ro, live, W)
+    close(dys, want, E24 * np.abs(want), dtype, "dys")
+    _, size = eo.combine_backward(np.abs(D), np.abs(Y), ro, live, np.abs(W))
+    assert (np.abs(f64(dw) - want_w) <= (hidden / 32 + 40) * E24 * size).all()
+    assert dw.dtype == torch.float32 and not dw[row_of >= live].any()
+    return xs, dys, dw
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_rows(mg, shape, dtype):
+    check_rows(mg, *shape, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_strides_and_alignment(mg, dtype):
+    check_rows(mg, 40, 4, 8, 256, dtype, pitch=264)             # rows of a wider matrix
+    check_rows(mg, 40, 4, 8, 255, dtype, pitch=391)
+    check_rows(mg, 40, 4, 8, 256, dtype, off=1)
+    check_rows(mg, 40, 4, 8, 256, dtype, off=3, out_off=5)
+    check_rows(mg, 40, 4, 8, 251, dtype, off=7, out_off=2)
+
+
+def test_all_or_none_dropped(mg):
+    check_rows(mg, 33, 4, 8, 200, "bf16", dropped=0.0)
+    xs, dys, dw = check_rows(mg, 33, 4, 8, 200, "bf16", dropped=1.1)
+    assert not xs.any() and not dys.any() and not dw.any()
+
+
+def test_the_same_expert_twice(mg):
+    """A token that names an expert twice has two rows there; both count."""
+    e = torch.tensor([[1, 1], [0, 1]], dtype=torch.int32, device="cuda")
+    row_of, slot_of, bounds = mg.muon_expert_sort(e, 2)
+    assert row_of.tolist() == [[1, 2], [0, 3]]
+    ys = torch.arange(4.0, device="cuda")[:, None].expand(4, 8).contiguous()
+    y = mg.muon_expert_combine(ys, row_of, bounds, weights=torch.tensor([[0.5, 2.0], [1.0, 3.0]], device="cuda"))
+    assert y[:, 0].tolist() == [4.5, 9.0]
+
+
+def test_rows_outside_are_left_out(mg):
+    """row_of and bounds that no sort wrote: rows outside the matrix are left out, ends outside it stop at its own."""
+    x = rand(4, 24, "f32", 1)
+    row_of = torch.tensor([[0, 1], [2, -7], [1 << 30, 3], [4, 8]], dtype=torch.int32, device="cuda")
+    for end, live in ((1000, 8), (5, 5), (-4, 0)):
+        bounds = torch.tensor([0, end], dtype=torch.int32, device="cuda")
+        ys = rand(8, 24, "f32", 2)
+        part = torch.zeros(4, 2, 24, dtype=torch.float64, device="cuda")
+        for t in range(4):
+            for j in range(2):
+                r = int(row_of[t, j])
+                if 0 <= r < live:
+                    part[t, j] = ys[r].double()
+        y = mg.muon_expert_combine(ys, row_of, bounds)
+        assert torch.allclose(y.double(), part.sum(1), rtol=1e-6, atol=1e-6)
+        xs = mg.muon_expert_dispatch(x, row_of, bounds)
+        for t, j in ((0, 0), (0, 1), (1, 0), (2, 1), (3, 0)):
+            r = int(row_of[t, j])
+            assert torch.equal(xs[r], x[t] if r < live else torch.zeros_like(x[t]))
+        w = torch.full((4, 2), 2.0, device="cuda")
+        dys, dw = mg.muon_expert_combine_backward(x, ys, row_of, bounds, w)
+        want = (x.double()[:, None] * part).sum(2)
+        assert torch.allclose(dw.double(), want, rtol=1e-5, atol=1e-5)
+
+
+def test_large_offsets(mg):
+    """Element offsets beyond 2^31: the last rows are where they should be."""
+    tokens, k, hidden = 40000, 4, 16384
+    row_of, slot_of, bounds = mg.muon_expert_sort(choices(tokens, k, 3), 3)
+    x = torch.randint(-100, 100, (tokens, hidden), generator=gen(9), device="cuda", dtype=torch.int16).to(torch.bfloat16)
+    xs = mg.muon_expert_dispatch(x, row_of, bounds)
+    assert xs.numel() > 1 << 31
+    assert torch.equal(xs[-5:], x[slot_of[-5:].long() // k])
+    y = mg.muon_expert_combine(xs, row_of, bounds)
+    assert torch.equal(y, (x * k))              # integers: exact sums
+    del y
+    w = torch.full((tokens, k), 0.5, device="cuda")
+    dys, dw = mg.muon_expert_combine_backward(x, xs, row_of, bounds, w)
+    assert torch.equal(dys[-5:], xs[-5:] * 0.5)
+    want = (x.double() ** 2).sum(1)
+    assert ((dw.double() - want[:, None]).abs() <= (hidden / 32 + 40) * E24 * want[:, None]).all()
+
+
+def test_binding_refusals(mg):
+    row_of, slot_of, bounds = mg.muon_expert_sort(choices(4, 2, 3), 3)
+    x, ys, w = rand(4, 16, "bf16", 1), rand(8, 16, "bf16", 2), torch.ones(4, 2, device="cuda")
+    for call in (lambda: mg.muon_expert_dispatch(x[:3], row_of, bounds),
+                 lambda: mg.muon_expert_dispatch(x.t(), row_of, bounds),
+                 lambda: mg.muon_expert_dispatch(x, row_of.t(), bounds),
+                 lambda: mg.muon_expert_dispatch(x, row_of, bounds[:1]),
+                 lambda: mg.muon_expert_combine(ys[:7], row_of, bounds),
+                 lambda: mg.muon_expert_combine(ys, row_of, bounds, weights=w[:3]),
+                 lambda: mg.muon_expert_combine(ys, row_of, bounds, residual=x.float()),
+                 lambda: mg.muon_expert_combine_backward(x, ys, row_of, bounds, None),
+                 lambda: mg.muon_expert_combine_backward(x.float(), ys, row_of, bounds, w),
+                 lambda: mg.muon_expert_combine(ys, row_of, bounds.cpu())):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: mg.muon_expert_dispatch(x, row_of.long(), bounds),
+                 lambda: mg.muon_expert_dispatch(x.double(), row_of, bounds),
+                 lambda: mg.muon_expert_combine(ys, row_of, bounds, weights=w.half()),
+                 lambda: mg.muon_expert_sort(w, 3)):
+        with pytest.raises(TypeError):
+            call()
+    for n in (0, 1025, 1 << 40):
+        with pytest.raises(mg.MuonError):
+            mg.muon_expert_sort(choices(4, 2, 3), n)
