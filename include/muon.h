@@ -498,6 +498,49 @@ int muon_expert_combine_backward(const void* dy, int64_t ld_dy, const void* ys, 
                                  void* stream);
 
 /*
+ * Products of a block that is split over experts: muon_glu_* and one linear layer
+ * for each expert's rows of a sorted matrix (muon_expert_dispatch), the forms a
+ * block's two ends take.  rows x columns matrices and experts' matrices are
+ * row-major and contiguous, of one type, MUON_BF16 or MUON_F16 (MUON_EDTYPE for
+ * fp32); bounds are num_experts + 1 non-decreasing row offsets on the device, as
+ * muon_expert_sort writes them (bounds[0] counts as 0, the others are clamped to
+ * [0, rows]); e below is the expert of a row.
+ *   glu_forward      gate = x w_gate[e]^T, up = x w_up[e]^T, h = act(gate) up as
+ *                    muon_glu_forward; x rows x hidden, weights num_experts x ffn x hidden
+ *   glu_backward     as muon_glu_backward; dw_gate, dw_up num_experts x ffn x hidden
+ *   linear_forward   y = x w[e]^T; x rows x in, w num_experts x out x in
+ *   linear_backward  dx = dy w[e], dw[e] = dy_e^T x_e over the expert's rows
+ * Results of rows behind the last expert, and gradients of experts without rows,
+ * are zero; no result depends on what rows of another expert, or rows behind the
+ * last one, hold.  dx, or the weights' gradients, may be NULL.
+ * rows in [0, 2^24], num_experts in [1, 1024], sides in [1, 2^20].  Outputs must
+ * not overlap anything else of the call.  Contractions beyond 65536 terms are summed
+ * in parts (as in muon_glu_backward), the forward passes' too.
+ *   scratch  device memory of the caller that the call may write until it has run
+ *            (256-byte aligned); *scratch_bytes holds its size.  A call that needs
+ *            more writes what it needs there, launches nothing and returns
+ *            MUON_ENOMEM, so a first call with NULL and 0 asks.  Forward passes
+ *            over sides that are multiples of 8 and pointers on 16 bytes need
+ *            none; other rows are copied there padded, the weights' too; the
+ *            gated backward pass keeps dg and du there (4 bytes per row and ffn
+ *            column).  Calls that can run at once, captured graphs among them,
+ *            must not share it.
+ */
+int muon_expert_glu_forward(const void* x, const void* w_gate, const void* w_up, const int* bounds, void* h,
+                            void* gate, void* up, int64_t rows, int64_t num_experts, int64_t hidden, int64_t ffn,
+                            int dtype, int act, void* scratch, int64_t* scratch_bytes, void* stream);
+int muon_expert_glu_backward(const void* x, const void* w_gate, const void* w_up, const void* gate, const void* up,
+                             const void* dh, const int* bounds, void* dx, void* dw_gate, void* dw_up, int64_t rows,
+                             int64_t num_experts, int64_t hidden, int64_t ffn, int dtype, int act, void* scratch,
+                             int64_t* scratch_bytes, void* stream);
+int muon_expert_linear_forward(const void* x, const void* w, const int* bounds, void* y, int64_t rows,
+                               int64_t num_experts, int64_t in, int64_t out, int dtype, void* scratch,
+                               int64_t* scratch_bytes, void* stream);
+int muon_expert_linear_backward(const void* x, const void* w, const void* dy, const int* bounds, void* dx, void* dw,
+                                int64_t rows, int64_t num_experts, int64_t in, int64_t out, int dtype,
+                                void* scratch, int64_t* scratch_bytes, void* stream);
+
+/*
  * Dropout: y[i] = residual[i] + (kept(i) ? x[i] / (1 - p) : 0) over n contiguous
  * elements (MUON_F32, MUON_BF16 or MUON_F16), residual NULL: 0.  The mask depends
  * on i, seed and offset alone and is never stored: the gradient of x is the same

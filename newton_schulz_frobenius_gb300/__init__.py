@@ -49,6 +49,7 @@ EXPORTS = (
     "muon_distill_loss", "muon_policy_loss", "muon_preference_loss",
     "muon_glu_forward", "muon_glu_backward",
     "muon_expert_sort", "muon_expert_dispatch", "muon_expert_combine", "muon_expert_combine_backward",
+    "muon_expert_glu_forward", "muon_expert_glu_backward", "muon_expert_linear_forward", "muon_expert_linear_backward",
     "muon_dropout",
 )
 
@@ -117,6 +118,10 @@ def lib() -> ctypes.CDLL:
         "muon_expert_dispatch": (i32, [vp, i64, i64, i64, i64, i32, vp, vp, i64, vp, vp]),
         "muon_expert_combine": (i32, [vp, i64, i64, i64, i32, vp, vp, i64, vp, vp, i64, vp, vp]),
         "muon_expert_combine_backward": (i32, [vp, i64, vp, i64, i64, i64, i32, vp, vp, i64, vp, vp, vp, vp]),
+        "muon_expert_glu_forward": (i32, [vp] * 7 + [i64, i64, i64, i64, i32, i32, vp, i64p, vp]),
+        "muon_expert_glu_backward": (i32, [vp] * 10 + [i64, i64, i64, i64, i32, i32, vp, i64p, vp]),
+        "muon_expert_linear_forward": (i32, [vp] * 4 + [i64, i64, i64, i64, i32, vp, i64p, vp]),
+        "muon_expert_linear_backward": (i32, [vp] * 6 + [i64, i64, i64, i64, i32, vp, i64p, vp]),
         "muon_dropout": (i32, [vp, vp, vp, i64, i32, ctypes.c_double, i64, i64, vp, vp]),
     }
     for name, (res, args) in sig.items():
@@ -867,6 +872,117 @@ def muon_expert_combine_backward(dy, ys, row_of, bounds, weights, stream=None):
     if st:
         _check(st, "muon_expert_combine_backward")
     return dys, dw
+
+
+def _with_scratch(name, device, stream, *args):
+    """Calls an entry point that takes scratch, with as much as it asks for."""
+    import torch
+    fn, need, s = getattr(lib(), name), ctypes.c_int64(0), _stream_ptr(stream)
+    st = fn(*args, None, ctypes.byref(need), s)
+    if st == MUON_ENOMEM and need.value:
+        with _on_stream(stream):        # the caching allocator hands it on in the stream's order
+            scratch = torch.empty(need.value, dtype=torch.uint8, device=device)
+        st = fn(*args, scratch.data_ptr(), ctypes.byref(need), s)
+    if st:
+        _check(st, name)
+
+
+def _matrix(t, shape, dtype, name):
+    _cuda_contig(t, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {' x '.join(map(str, shape))}, got {' x '.join(map(str, t.shape))}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: {dtype} required, got {t.dtype}")
+    return t.data_ptr()
+
+
+def _expert_args(x, weights, bounds):
+    """(rows, experts, columns of a row, rows of an expert's matrix, type code, bounds) of an experts' product."""
+    import torch
+    w = weights[0]
+    if x.dim() != 2 or w.dim() != 3:
+        raise ValueError("x must be rows x columns, the weights experts x rows x columns")
+    (rows, cols), (experts, out) = x.shape, w.shape[:2]
+    _matrix(x, (rows, cols), x.dtype, "x")
+    for t in weights:
+        _matrix(t, (experts, out, cols), x.dtype, "weights")
+    bp = _vector(bounds, experts + 1, "bounds", torch.int32)
+    return rows, experts, cols, out, _dtype_code(x), bp
+
+
+def _act_code(act):
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError(f"act {act!r}: one of {sorted(ACTIVATIONS)}")
+    return code
+
+
+def muon_expert_glu_forward(x, w_gate, w_up, bounds, act: str = "silu", save: bool = True, stream=None):
+    """muon_glu_forward of every expert over its rows of x (sorted rows x hidden;
+    weights experts x ffn x hidden; bounds from muon_expert_sort).  Returns
+    (h, gate, up), or h alone with save=False; rows behind the last expert are zero."""
+    _one_device(x, w_gate, w_up, bounds)
+    rows, experts, hidden, ffn, dt, bp = _expert_args(x, (w_gate, w_up), bounds)
+    code = _act_code(act)
+    out = _new(stream, *[((rows, ffn), x)] * (3 if save else 1))
+    ptrs = [t.data_ptr() for t in out] if save else (out[0].data_ptr(), None, None)
+    _with_scratch("muon_expert_glu_forward", x.device, stream, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), bp,
+                  *ptrs, rows, experts, hidden, ffn, dt, code)
+    return tuple(out) if save else out[0]
+
+
+def muon_expert_glu_backward(x, w_gate, w_up, gate, up, dh, bounds, act: str = "silu", need_dx: bool = True,
+                             dw_gate=None, dw_up=None, stream=None):
+    """Gradients (dx, dw_gate, dw_up) of muon_expert_glu_forward.  dw_gate and
+    dw_up may be tensors to write into (whose matrices a MuonGroup reads);
+    need_dx=False leaves dx out (None)."""
+    _one_device(x, w_gate, w_up, gate, up, dh, bounds, dw_gate, dw_up)
+    rows, experts, hidden, ffn, dt, bp = _expert_args(x, (w_gate, w_up), bounds)
+    code = _act_code(act)
+    kept = [_matrix(t, (rows, ffn), x.dtype, nm) for t, nm in ((gate, "gate"), (up, "up"), (dh, "dh"))]
+    for t, nm in ((dw_gate, "dw_gate"), (dw_up, "dw_up")):
+        if t is not None:
+            _matrix(t, w_gate.shape, x.dtype, nm)
+    dx, = _new(stream, (x.shape, x)) if need_dx else (None,)
+    dw_gate, dw_up = _to_write(stream, w_gate, dw_gate, dw_up)
+    _with_scratch("muon_expert_glu_backward", x.device, stream, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+                  *kept, bp, dx.data_ptr() if need_dx else None, dw_gate.data_ptr(), dw_up.data_ptr(), rows, experts,
+                  hidden, ffn, dt, code)
+    return dx, dw_gate, dw_up
+
+
+def _to_write(stream, like, *given):
+    """The tensors given to be written, marked so, and new ones like `like` for those that are None."""
+    for t in given:
+        if t is not None:
+            _written(t)
+    new = iter(_new(stream, *[(like.shape, like)] * sum(t is None for t in given)))
+    return [next(new) if t is None else t for t in given]
+
+
+def muon_expert_linear_forward(x, w, bounds, stream=None):
+    """x w[e]^T for every expert's rows of x (sorted rows x in; w experts x out x in)."""
+    _one_device(x, w, bounds)
+    rows, experts, cols, out, dt, bp = _expert_args(x, (w,), bounds)
+    y, = _new(stream, ((rows, out), x))
+    _with_scratch("muon_expert_linear_forward", x.device, stream, x.data_ptr(), w.data_ptr(), bp, y.data_ptr(), rows,
+                  experts, cols, out, dt)
+    return y
+
+
+def muon_expert_linear_backward(x, w, dy, bounds, need_dx: bool = True, dw=None, stream=None):
+    """Gradients (dx, dw) of muon_expert_linear_forward; dw may be a tensor to
+    write into, need_dx=False leaves dx out (None)."""
+    _one_device(x, w, dy, bounds, dw)
+    rows, experts, cols, out, dt, bp = _expert_args(x, (w,), bounds)
+    dp = _matrix(dy, (rows, out), x.dtype, "dy")
+    if dw is not None:
+        _matrix(dw, w.shape, x.dtype, "dw")
+    dx, = _new(stream, (x.shape, x)) if need_dx else (None,)
+    dw, = _to_write(stream, w, dw)
+    _with_scratch("muon_expert_linear_backward", x.device, stream, x.data_ptr(), w.data_ptr(), dp, bp,
+                  dx.data_ptr() if need_dx else None, dw.data_ptr(), rows, experts, cols, out, dt)
+    return dx, dw
 
 
 # ---------------------------------------------------------------------------

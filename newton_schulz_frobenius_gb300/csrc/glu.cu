@@ -26,9 +26,8 @@
 // runs all three products: dX as one contraction over 2 ffn (first dG Wg, then
 // dU Wu, in one accumulator), dWg and dWu with both operands read MN-major, so
 // nothing is transposed in memory.
-#include "host.h"
 #include "epilogue.cuh"
-#include "tc_ptx.cuh"
+#include "glu_parts.cuh"
 
 #include <cfloat>
 
@@ -53,38 +52,6 @@ static_assert(GLU_SMEM <= 232448, "shared memory per CTA");
 // 1144 us, with groups of 4, 8 and 32 1172, 1152 and 1201 (one box, at the fast
 // end of 1144-1280).
 constexpr int GROUP = 16;
-
-enum Act : int { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
-
-// act(g), and act'(g) where asked for.  Written so that large finite |g| give 0,
-// 1 or g, never an infinity times zero.
-template <bool GRAD>
-__device__ __forceinline__ float activate(float g, int act, float* grad) {
-    if (act == ACT_GELU) {
-        const float cdf = 0.5f * erfcf(-0.70710678118654752f * g);
-        if (GRAD) *grad = fmaf(g * expf(-0.5f * g * g), 0.3989422804014327f, cdf);
-        return g * cdf;
-    }
-    if (act == ACT_GELU_TANH) {
-        // (1 + tanh u) / 2 = sigmoid(2 u)
-        const float k2 = 1.5957691216057308f;
-        const float s = 1.0f / (1.0f + __expf(-k2 * g * fmaf(0.044715f * g, g, 1.0f)));
-        if (GRAD) {
-            const float c = fminf(fmaxf(g, -30.f), 30.f);
-            *grad = fmaf(c * s * (1.0f - s), k2 * fmaf(0.134145f * c, c, 1.0f), s);
-        }
-        return g * s;
-    }
-    const float s = 1.0f / (1.0f + __expf(-g));
-    if (GRAD) *grad = s * fmaf(g, 1.0f - s, 1.0f);
-    return g * s;
-}
-
-// One output matrix: rows x cols, row-major with pitch ld.
-struct GluOut {
-    void* p;
-    int64_t ld;
-};
 
 // One family of tiles: rows x cols outputs over kblocks k-blocks.
 struct GluTiles {
@@ -634,26 +601,6 @@ glu_few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
     }
 }
 
-// dG = dH U act'(G) and dU = dH act(G), written at a pitch of whole 16-byte
-// pieces (zeros beyond ffn), eight columns per thread and step.  Bound by HBM:
-// three matrices read, two written.  3280 x 7504 (246 MB): 33 us, 7.4 TB/s with
-// the last writes still in L2; with the activation chosen per element and two
-// pieces per step it was 45 us, most of the difference instructions to fetch.
-// Rows that start anywhere, 3282 x 7507 beside the padding of three operands of
-// 287 columns: 59 us, from 65 with eight 2-byte loads per piece; the padding of
-// 333 + 2 x 2731 rows of 1001 columns alone 12.4 -> 9.1.
-struct GluGradArgs {
-    const void* dh;
-    const void* gate;
-    const void* up;
-    void* dg;
-    void* du;
-    int64_t rows;
-    int ffn, pieces;            // columns, 16-byte pieces of a workspace row
-    int dtype, act;
-    int vec;                    // the inputs' rows start on 16 bytes too
-};
-
 // Columns c .. c + 7 of a row of a dense matrix of `n` 16-bit elements whose
 // rows start anywhere (zeros from `cols` on), read as the two aligned 16-byte
 // vectors that hold them and shifted into place.  Vectors that would reach
@@ -704,6 +651,13 @@ __device__ __forceinline__ int64_t row_of(int64_t i, int64_t n, int pieces) {
     return n <= INT32_MAX ? (int64_t)((uint32_t)i / (uint32_t)pieces) : i / pieces;
 }
 
+// dG and dU (GluGradArgs), eight columns per thread and step.  Bound by HBM:
+// three matrices read, two written.  3280 x 7504 (246 MB): 33 us, 7.4 TB/s with
+// the last writes still in L2; with the activation chosen per element and two
+// pieces per step it was 45 us, most of the difference instructions to fetch.
+// Rows that start anywhere, 3282 x 7507 beside the padding of three operands of
+// 287 columns: 59 us, from 65 with eight 2-byte loads per piece; the padding of
+// 333 + 2 x 2731 rows of 1001 columns alone 12.4 -> 9.1.
 template <int ACT>
 __device__ __forceinline__ void glu_grad_piece(const GluGradArgs& a, int64_t i, const uint4& qd, const uint4& qg,
                                                const uint4& qu) {
@@ -781,7 +735,7 @@ struct PadArgs {
     const void* src[3];
     void* dst[3];
     int64_t rows[3];
-    int cols, n;
+    int cols[3], n;
 };
 // What a call needs before its products, in one launch: operands blockIdx.y <
 // pads.n padded, and (backward) blockIdx.y == pads.n dG and dU.
@@ -790,17 +744,18 @@ __global__ void __launch_bounds__(256) glu_prepare_kernel(const __grid_constant_
                                                           const __grid_constant__ GluGradArgs g) {
     pdl_wait();
     pdl_trigger();
-    const int o = blockIdx.y, pieces = (a.cols + 7) / 8;
+    const int o = blockIdx.y;
     if (o == a.n) {
         glu_grad<ACT>(g);
         return;
     }
-    const int64_t n = a.rows[o] * pieces, all = a.rows[o] * a.cols;
+    const int cols = a.cols[o], pieces = (cols + 7) / 8;
+    const int64_t n = a.rows[o] * pieces, all = a.rows[o] * cols;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int64_t row = row_of(i, n, pieces);
-        const int c = (int)(i - row * pieces) * 8, left = a.cols - c;
+        const int c = (int)(i - row * pieces) * 8, left = cols - c;
         Shifted v;
-        const bool in = v.at(a.src[o], all, row * a.cols + c);
+        const bool in = v.at(a.src[o], all, row * cols + c);
         if (in) v.load();
         static_cast<uint4*>(a.dst[o])[i] = in ? v.get(left) : v.by_elements(left);
     }
@@ -843,34 +798,22 @@ constexpr int SUM_COST = 12;        // the sum of dX's parts, in k-blocks' time
 // fp32 sums are added in round-to-nearest.
 constexpr int MAX_BLOCKS = 1024;
 
-struct Operand {
-    const void* p;
-    int64_t rows, cols, ld;
-};
+}  // namespace
 
-bool tma_ok(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0; }
-
-// A caller's matrix as the copy engine can read it: itself, or (rows that do not
-// start on 16 bytes) a padded copy at `at` in the workspace.
-size_t padded_bytes(const Operand& o) {
-    return tma_ok(o.p, o.ld) ? 0 : align_up((size_t)o.rows * pad8(o.cols) * 2, 256);
-}
-// Points the operands that need it at padded copies and makes these, with dG and
-// dU where `g` is given, in one launch.
-int prepare(Operand* const* ops, char* at, const GluGradArgs* g, int sms, cudaStream_t s) {
+int glu_prepare(Operand* const* ops, int nops, char* at, const GluGradArgs* g, int sms, cudaStream_t s) {
     PadArgs p;
     GluGradArgs ga;
     std::memset(&p, 0, sizeof p);
     std::memset(&ga, 0, sizeof ga);
     int64_t blocks = 1;
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < nops; ++i) {
         Operand& o = *ops[i];
         const size_t b = padded_bytes(o);
         if (!b) continue;
         p.src[p.n] = o.p;
         p.dst[p.n] = at;
         p.rows[p.n] = o.rows;
-        p.cols = (int)o.cols;               // the three share it
+        p.cols[p.n] = (int)o.cols;
         ++p.n;
         o.ld = pad8(o.cols);
         blocks = std::max(blocks, (o.rows * (pad8(o.cols) / 8) + 255) / 256);
@@ -894,21 +837,7 @@ int prepare(Operand* const* ops, char* at, const GluGradArgs* g, int sms, cudaSt
     return MUON_OK;
 }
 
-bool map_in(CUtensorMap* m, const Operand& o, int dtype, uint32_t box_cols, uint32_t box_rows) {
-    return make_map(m, o.p, dtype, (uint64_t)o.cols, (uint64_t)o.rows, 1, (uint64_t)o.ld, 0, box_cols, box_rows);
-}
-
-// 32 x 32 chunks in 64-byte swizzled rows.
-bool map_out(CUtensorMap* m, const GluOut& o, int dtype, int64_t rows, int64_t cols) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 1};
-    cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2, (cuuint64_t)o.ld * 2 * (cuuint64_t)rows};
-    cuuint32_t box[3] = {32, 32, 1}, elem[3] = {1, 1, 1};
-    return fn(m, dtype == MUON_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, o.p, dims,
-              strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
+namespace {
 
 GluTiles tiles(int64_t rows, int64_t cols, int64_t tile_cols, int64_t k, int segs) {
     GluTiles t;
@@ -1059,7 +988,7 @@ extern "C" int muon_glu_forward(const void* x, const void* w_gate, const void* w
         Workspace* w = nullptr;
         if ((r = ws_get(dc.device, s, need, &w))) return r;
         Operand* const ops[3] = {&X, &G, &U};
-        if ((r = prepare(ops, w->base, nullptr, dc.sms, s))) return r;
+        if ((r = glu_prepare(ops, 3, w->base, nullptr, dc.sms, s))) return r;
     }
     if (tokens <= FEW_TOKENS) {
         FewArgs f;
@@ -1144,7 +1073,7 @@ extern "C" int muon_glu_backward(const void* x, const void* w_gate, const void* 
     ga.dtype = dtype; ga.act = act;
     ga.vec = tma_ok(dh, ffn) && tma_ok(gate, ffn) && tma_ok(up, ffn);
     Operand* const ops[3] = {&X, &G, &U};
-    if ((r = prepare(ops, w->base + 2 * half + parts, &ga, dc.sms, s))) return r;
+    if ((r = glu_prepare(ops, 3, w->base + 2 * half + parts, &ga, dc.sms, s))) return r;
     const Operand DG{ga.dg, tokens, ffn, ldw}, DU{ga.du, tokens, ffn, ldw};
     GluMaps maps;
     std::memset(&maps, 0, sizeof maps);

@@ -8,6 +8,8 @@ from __future__ import annotations
 
 import numpy as np
 
+from oracle import glu_oracle as go
+
 
 def sort(experts, n):
     """(row_of, slot_of, bounds) slot by slot; indices outside [0, n) last."""
@@ -85,3 +87,42 @@ def dropout(x, p, seed, offset, residual=None):
     if cut < 65536:
         y[keep] = x[keep] / (1.0 - cut / 65536.0)
     return y if residual is None else y + residual
+
+
+def segments(bounds, rows):
+    """[first, last) rows of each expert, as the library reads bounds."""
+    out = []
+    for e in range(len(bounds) - 1):
+        first = min(max(0 if e == 0 else int(bounds[e]), 0), rows)
+        out.append((first, min(max(int(bounds[e + 1]), first), rows)))
+    return out
+
+
+def glu_forward(x, wg, wu, bounds, kind):
+    rows, ffn = x.shape[0], wg.shape[1]
+    out = [np.zeros((rows, ffn)) for _ in range(3)]
+    for e, (a, b) in enumerate(segments(bounds, rows)):
+        for o, v in zip(out, go.forward(x[a:b], wg[e], wu[e], kind)):
+            o[a:b] = v
+    return out
+
+
+def glu_backward(x, wg, wu, gate, up, dh, bounds, kind):
+    dx, dwg, dwu = np.zeros(x.shape), np.zeros(wg.shape), np.zeros(wu.shape)
+    for e, (a, b) in enumerate(segments(bounds, x.shape[0])):
+        dx[a:b], dwg[e], dwu[e] = go.backward(x[a:b], wg[e], wu[e], gate[a:b], up[a:b], dh[a:b], kind)
+    return dx, dwg, dwu
+
+
+def linear_forward(x, w, bounds):
+    y = np.zeros((x.shape[0], w.shape[1]))
+    for e, (a, b) in enumerate(segments(bounds, x.shape[0])):
+        y[a:b] = x[a:b] @ w[e].T
+    return y
+
+
+def linear_backward(x, w, dy, bounds):
+    dx, dw = np.zeros(x.shape), np.zeros(w.shape)
+    for e, (a, b) in enumerate(segments(bounds, x.shape[0])):
+        dx[a:b], dw[e] = dy[a:b] @ w[e], dy[a:b].T @ x[a:b]
+    return dx, dw

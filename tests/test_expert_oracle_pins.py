@@ -56,3 +56,40 @@ def test_round_trip_and_gradients():
             num = (f(up, w) - f(dn, w) if pos == 0 else f(x, up) - f(x, dn)) / (2 * h)
             assert abs(num - grad[i]) < 1e-6 * (1 + abs(num))
     assert (experts.reshape(-1)[slot_of[live:]] == -1).all()
+
+
+def test_product_gradients():
+    """The experts' block and layer: gradients by central differences of a sum over the forward formulas."""
+    rng = np.random.default_rng(1)
+    R, E, D, F = 7, 3, 4, 5
+    bounds = [0, 2, 2, 6]
+    x, dh, dy = rng.normal(size=(R, D)), rng.normal(size=(R, F)), rng.normal(size=(R, D))
+    wg, wu, wd = rng.normal(size=(E, F, D)), rng.normal(size=(E, F, D)), rng.normal(size=(E, D, F))
+    h, gate, up = eo.glu_forward(x, wg, wu, bounds, "silu")
+    assert not h[6].any() and h[:2].any()
+    grads = eo.glu_backward(x, wg, wu, gate, up, dh, bounds, "silu")
+    lin = eo.linear_backward(dh, wd, dy, bounds)
+    assert not grads[1][1].any() and not lin[1][1].any()
+
+    def differences(f, args, k):
+        out = np.zeros(args[k].shape)
+        for i in np.ndindex(out.shape):
+            up_, dn = [a.copy() for a in args], [a.copy() for a in args]
+            up_[k][i] += 1e-6
+            dn[k][i] -= 1e-6
+            out[i] = (f(*up_) - f(*dn)) / 2e-6
+        return out
+
+    def block(x, wg, wu):
+        return float((dh * eo.glu_forward(x, wg, wu, bounds, "silu")[0]).sum())
+
+    def layer(v, w):
+        return float((dy * eo.linear_forward(v, w, bounds)).sum())
+    for k, g in enumerate(grads):
+        assert np.allclose(differences(block, [x, wg, wu], k), g, rtol=1e-5, atol=1e-6)
+    for k, g in enumerate(lin):
+        assert np.allclose(differences(layer, [dh, wd], k), g, rtol=1e-5, atol=1e-6)
+
+
+def test_segments():
+    assert eo.segments([7, 3, 1, 9, -2], 6) == [(0, 3), (3, 3), (1, 6), (6, 6)]
