@@ -24,7 +24,7 @@ struct DropArgs {
     int64_t n;
     const int64_t* state;       // device {seed, offset}, or null: the two below
     uint64_t seed, offset;
-    uint32_t cut;               // p 65536
+    uint32_t cut;               // p 65536, in the upper half of a word
     float scale;
     int dtype;
 };
@@ -46,45 +46,86 @@ __device__ __forceinline__ uint4 philox(uint64_t b, uint64_t seed, uint64_t offs
     return make_uint4(c0, c1, c2, c3);
 }
 
-// A dropped element is 0 whatever it was (infinities and NaN too).
-__device__ __forceinline__ void drop8(const DropArgs& a, const uint4& bits, const float (&x)[8], const float (&add)[8],
-                                      float (&y)[8]) {
-    const uint32_t w[4] = {bits.x, bits.y, bits.z, bits.w};
+// Eight elements from their 16-byte pieces (one, of fp32 two) and back.
+template <int DTYPE>
+__device__ __forceinline__ void load8(const void* p, int64_t b, float (&v)[8]) {
+    const uint4* q = static_cast<const uint4*>(p);
+    if constexpr (DTYPE == MUON_F32) {
+        const uint4 lo = q[2 * b], hi = q[2 * b + 1];
+        const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const uint32_t r = k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xFFFFu;
-        y[k] = r >= a.cut ? fmaf(x[k], a.scale, add[k]) : add[k];
+        for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(w[k]);
+    } else {
+        unpack8_h(q[b], v, DTYPE == MUON_F16);
     }
 }
 
-template <bool VEC>
+template <int DTYPE>
+__device__ __forceinline__ void store8(void* p, int64_t b, const float (&v)[8]) {
+    uint4* q = static_cast<uint4*>(p);
+    if constexpr (DTYPE == MUON_F32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            q[2 * b + h] = make_uint4(__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
+                                      __float_as_uint(v[4 * h + 3]));
+    } else {
+        q[b] = pack8_h(v, DTYPE == MUON_F16);
+    }
+}
+
+// A dropped element is 0 whatever it was (infinities and NaN too).  A word holds
+// two numbers; compared with cut << 16 the upper one needs no shift.
+template <bool ADD>
+__device__ __forceinline__ void drop8(const DropArgs& a, const uint4& bits, float (&x)[8], const float (&add)[8]) {
+    const uint32_t w[4] = {bits.x, bits.y, bits.z, bits.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t r = k & 1 ? w[k / 2] : w[k / 2] << 16;
+        x[k] = r >= a.cut ? (ADD ? fmaf(x[k], a.scale, add[k]) : x[k] * a.scale) : (ADD ? add[k] : 0.f);
+    }
+}
+
+template <int DTYPE, bool VEC, bool ADD>
 __global__ void __launch_bounds__(DT) dropout_kernel(const __grid_constant__ DropArgs a) {
     pdl_wait();
     pdl_trigger();
     const uint64_t seed = a.state ? (uint64_t)a.state[0] : a.seed, offset = a.state ? (uint64_t)a.state[1] : a.offset;
-    const int64_t blocks = (a.n + 7) / 8, step = (int64_t)gridDim.x * DT;
-    for (int64_t b = (int64_t)blockIdx.x * DT + threadIdx.x; b < blocks; b += step) {
-        float x[8], add[8], y[8];
+    const int64_t blocks = (a.n + 7) / 8, whole = VEC ? a.n / 8 : 0, step = (int64_t)gridDim.x * DT;
+    int64_t b = (int64_t)blockIdx.x * DT + threadIdx.x;
+    float x[8], add[8];
+    for (; b < whole; b += step) {
+        load8<DTYPE>(a.x, b, x);
+        if (ADD) load8<DTYPE>(a.add, b, add);
+        drop8<ADD>(a, philox((uint64_t)b, seed, offset), x, add);
+        store8<DTYPE>(a.y, b, x);
+    }
+    // elements that are no whole aligned piece
+#pragma unroll 1
+    for (; b < blocks; b += step) {
         const int n = (int)min((int64_t)8, a.n - 8 * b);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) add[k] = x[k] = 0.f;
-        if (VEC && n == 8) {
-            load_row_run<8>(a.x, 8 * b, x, a.dtype);
-            if (a.add) load_row_run<8>(a.add, 8 * b, add, a.dtype);
-        } else {
-            for (int k = 0; k < 8; ++k) {
-                if (k < n) x[k] = ld_elem(a.x, 8 * b + k, a.dtype);
-                if (k < n && a.add) add[k] = ld_elem(a.add, 8 * b + k, a.dtype);
-            }
+        for (int k = 0; k < 8; ++k) {
+            x[k] = k < n ? ld_elem(a.x, 8 * b + k, DTYPE) : 0.f;
+            add[k] = ADD && k < n ? ld_elem(a.add, 8 * b + k, DTYPE) : 0.f;
         }
-        drop8(a, philox((uint64_t)b, seed, offset), x, add, y);
-        if (VEC && n == 8) {
-            store_row_run<8>(a.y, 8 * b, y, a.dtype);
-        } else {
-            for (int k = 0; k < 8; ++k)
-                if (k < n) st_elem(a.y, 8 * b + k, y[k], a.dtype);
-        }
+        drop8<ADD>(a, philox((uint64_t)b, seed, offset), x, add);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < n) st_elem(a.y, 8 * b + k, x[k], DTYPE);
     }
+}
+
+template <int DTYPE>
+auto dropout_form(bool vec, bool add) {
+    return vec ? (add ? dropout_kernel<DTYPE, true, true> : dropout_kernel<DTYPE, true, false>)
+               : (add ? dropout_kernel<DTYPE, false, true> : dropout_kernel<DTYPE, false, false>);
+}
+
+// p = 1: the residual, or zeros.
+int drop_all(const void* residual, void* y, size_t bytes, cudaStream_t s) {
+    if (!residual) MUON_CUDA(cudaMemsetAsync(y, 0, bytes, s));
+    else if (residual != y) MUON_CUDA(cudaMemcpyAsync(y, residual, bytes, cudaMemcpyDeviceToDevice, s));
+    return MUON_OK;
 }
 
 }  // namespace
@@ -111,12 +152,17 @@ extern "C" int muon_dropout(const void* x, const void* residual, void* y, int64_
     a.x = x; a.add = residual; a.y = y; a.n = n; a.dtype = dtype;
     a.state = state;
     a.seed = (uint64_t)seed; a.offset = (uint64_t)offset;
-    a.cut = (uint32_t)std::floor(p * 65536.0 + 0.5);
-    a.scale = a.cut < 65536u ? (float)(65536.0 / (65536.0 - a.cut)) : 0.f;
+    const double cut = std::floor(p * 65536.0 + 0.5);
+    if (cut >= 65536.0) return drop_all(residual, y, (size_t)n * esize(dtype), s);
+    a.cut = (uint32_t)cut << 16;
+    a.scale = (float)(65536.0 / (65536.0 - cut));
     const bool vec = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(residual) | reinterpret_cast<uintptr_t>(y)) & 15) == 0;
     const int64_t ctas = ((n + 7) / 8 + DT - 1) / DT;
+    auto kern = dtype == MUON_F32    ? dropout_form<MUON_F32>(vec, residual != nullptr)
+                : dtype == MUON_BF16 ? dropout_form<MUON_BF16>(vec, residual != nullptr)
+                                     : dropout_form<MUON_F16>(vec, residual != nullptr);
     note_launch_begin(KC_OTHER, s);
-    const cudaError_t e = launch_pdl(vec ? dropout_kernel<true> : dropout_kernel<false>,
+    const cudaError_t e = launch_pdl(kern,
                                      dim3((unsigned)std::min<int64_t>(ctas, (int64_t)dc.sms * 8)), dim3(DT), 0, s, a);
     note_launch_end(KC_OTHER, 0.0, s);
     return e == cudaSuccess ? MUON_OK : cuda_fail(e, "dropout launch");

@@ -7,16 +7,28 @@
 //                 dX = dG Wg_e + dU Wu_e, dWg_e = dG^T X, dWu_e = dU^T X
 //   linear        Y = X W_e^T;  dX = dY W_e, dW_e = dY^T X
 //
-// One persistent launch of 2-SM tcgen05 pairs covers all experts: M = 256,
-// N = 256, fp32 accumulation in TMEM, two accumulators so that a tile's epilogue
-// runs under the next tile's products, fed by TMA through a ring of six 32 KB
-// stages per CTA.  A tile never spans two experts; where one ends inside a tile
-//   - rows of the next expert are multiplied along and not stored (their results
-//     are rows of their own, so whatever they hold stays theirs),
-//   - in dW, where rows are the contraction, the last k-block's rows of the next
-//     expert are zeroed in shared memory before the tensor core reads them.
-// Every warp finds its tiles from the bounds, so no host copy of them is needed
-// and a captured call follows new ones.
+// One persistent launch of 2-SM tcgen05 pairs covers all experts (M = 256, N up to
+// 256, fp32 accumulation in TMEM, two accumulators so that a tile's epilogue runs
+// under the next tile's products), fed by TMA through a ring of six 32 KB stages
+// per CTA.  Every warp finds its tiles from the bounds, so no host copy of them is
+// needed and a captured call follows new ones.
+//
+// Results over sorted rows (family a: forward, dX) are computed transposed: 256
+// rows of the weights are the M side and an expert's rows the N side, whose extent
+// follows the expert in steps of 32.  An expert's rows are cut into
+// ceil(rows / 256) tiles of nearly equal extent, so that ragged or small experts
+// cost little more than their rows.  The epilogue turns 32 x 32 chunks
+// around through the neighbour lane.  In the gated forward pass each CTA's M side
+// is 64 rows of Wg and the same 64 of Wu: gate and value of a result are in two
+// warps, which exchange half of their rows through shared memory.  (Sixteen rows of
+// each in turn would put them in one warp, but eight copies of 2 KB per stage and
+// CTA hold the copy engine up: 16384 rows, 8 x 4096 x 14336 3468 us.)
+//
+// Where an expert ends inside a tile, rows of the next one are multiplied along
+// and not stored (their results are columns of their own, whatever they hold).
+// In the weights' gradients (family b) the rows are the contraction: a warp of its
+// own zeroes the next expert's rows in the last k-block, in shared memory,
+// before the tensor core reads them.
 #include "epilogue.cuh"
 #include "glu_parts.cuh"
 
@@ -26,23 +38,52 @@ namespace {
 
 using namespace tc;
 
-constexpr int GM = 128;                     // rows of a CTA's half-tile
+constexpr int GM = 128;                     // rows of a CTA's half of the M side
 constexpr int GK = 64;                      // k-block: 128 bytes
 constexpr int NEPI = 8;
-constexpr int GT = 64 + 32 * NEPI;
-constexpr int STAGES = 6;
-constexpr int OP_BYTES = GM * GK * 2;       // one operand tile of a stage (A, or this CTA's half of B)
-constexpr int STAGE_BYTES = 2 * OP_BYTES;
-constexpr int OUT_BYTES = 32 * 32 * 2;      // one output chunk of a warp: 32 x 32, 64-byte swizzled rows
-constexpr int NBARS = 2 * STAGES + 6;
-constexpr int EXP_SMEM = STAGES * STAGE_BYTES + NEPI * 2 * OUT_BYTES + NBARS * 8 + 16 + 1024;
+constexpr int GT = 64 + 32 * NEPI + 32;     // producer, issuer, epilogue, tails
+constexpr int SUB = 2;                      // k-blocks of a stage
+constexpr int STAGES = 6 / SUB;
+constexpr int OP_BYTES = GM * GK * 2;       // one operand's k-block of a stage (A, or this CTA's half of B)
+constexpr int OUT_BYTES = 32 * 32 * 2;      // output chunk of a warp: 32 x 32, 64-byte swizzled rows
+constexpr int NBARS = 3 * STAGES + 5;
+constexpr int EXP_SMEM = STAGES * SUB * 2 * OP_BYTES + NEPI * 2 * OUT_BYTES + NBARS * 8 + 16 + 1024;
 static_assert(EXP_SMEM <= 232448, "shared memory per CTA");
-constexpr int GROUP = 16;                   // row pairs of tiles that share their B tiles in L2
+constexpr int GROUP = 16;                   // row tiles that share their weights' tiles in L2
+constexpr int ROW_TILE = 256;
 // The accumulators truncate: a sum of n terms of one sign comes out short by
 // 6.4e-9 n of its value, so contractions are cut into parts of at most MAX_BLOCKS
 // k-blocks (65536 terms), whose fp32 sums are added in round-to-nearest.
 constexpr int MAX_BLOCKS = 1024;
 constexpr size_t PART_BYTES = (size_t)GM * 256 * 4;     // a CTA's running sums
+
+// wait_bounded(), which reads the clock as soon as a wait does not succeed at once:
+// some hundred nanoseconds that a stage of a full ring then comes late (linear
+// forward 16384 x 14336 x 4096 in eight ragged experts: 1217 -> 1120 us with one
+// k-block per stage).  Here the clock starts after the waits of a normal pass.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return wait_bounded(bar, parity, abort_flag, status);
+}
+
+// The address of a barrier of CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t bar_of(uint32_t bar, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(bar), "r"(rank));
+    return r;
+}
+
+// A tile load to this CTA's shared memory that reports to a barrier (bar_of) of
+// either CTA of the pair.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
 
 enum Mode : int { FWD_GLU = 0, FWD_LINEAR = 1, BACKWARD = 2 };
 
@@ -53,7 +94,7 @@ struct ExpArgs {
     int rows, experts;
     const int* bounds;
     // family a: results over the sorted rows (forward, dX)
-    int a_on, cols_a, tiles_n;  // columns of the result, column tiles
+    int a_on, cols_a, tiles_w;  // columns of the result, tiles of them
     int seg_blocks, segs;       // k-blocks of one segment (one A and B map each), segments
     // family b: the weights' gradients
     int nb;                     // results per expert: 0, 1 or 2
@@ -64,24 +105,25 @@ struct ExpArgs {
 };
 
 struct ExpMaps {
-    CUtensorMap a[2], b[2];     // family a: operands by segment (gated forward: b = Wg, Wu)
+    CUtensorMap a[2];           // family a: weights by segment (gated forward: Wg, Wu)
+    CUtensorMap b[2][4];        // rows by segment, boxes of 16, 32, 64, 128 rows
     CUtensorMap a2[2], b2;      // family b: dG, dU (dY) read MN-major; X
     CUtensorMap out[3];
 };
 
 // [first, last) rows of expert e, within the matrix whatever the bounds hold.
-// Expert `experts` has the rows behind the last one's, whose results are zero.
 __device__ __forceinline__ void expert_rows(const ExpArgs& g, int e, int& first, int& last) {
     const int lo = e == 0 ? 0 : g.bounds[e];
     first = min(max(lo, 0), g.rows);
-    last = e == g.experts ? g.rows : min(max(g.bounds[e + 1], first), g.rows);
+    last = min(max(g.bounds[e + 1], first), g.rows);
 }
 
 struct Tile {
     int family, which;          // 0: a, 1: b; output index
     int e;
     int first, last;            // the expert's rows
-    int tm, tn;
+    int r0, n;                  // family a: the tile's first row, and its extent in steps of 32
+    int tm, tn;                 // family a: tn = weights' tile; b: row and column tile
     int blocks;                 // k-blocks of its contraction (0: the result is zero)
 };
 
@@ -91,28 +133,40 @@ struct Tile {
 // cluster ends within a tile of the others.
 struct Walk {
     int c, P, j;
-    int na, nb, mine, light, extra;
+    int nb, mine, light, extra;
     int e, base, first, last, here;         // family a: current expert, id of its first tile, its rows and tiles
+    int end;                                // of the experts' rows; "expert" g.experts has those behind, results zero
 
     __device__ __forceinline__ void tiles_of(const ExpArgs& g) {
-        expert_rows(g, e, first, last);
-        here = (last - first + 2 * GM - 1) / (2 * GM) * g.tiles_n;
+        if (e < g.experts) {
+            expert_rows(g, e, first, last);
+        } else {
+            first = end;
+            last = g.rows;
+        }
+        here = (last - first + ROW_TILE - 1) / ROW_TILE * g.tiles_w;
     }
     // Called by whole warps.
     __device__ __forceinline__ void init(const ExpArgs& g, int cluster, int clusters) {
         c = cluster;
         P = clusters;
         j = 0;
-        na = 0;
+        int na = 0;
         const int lane = threadIdx.x & 31;
+        end = 0;
         if (g.a_on) {
-            for (int k = lane; k <= g.experts; k += 32) {
+            for (int k = lane; k < g.experts; k += 32) {
                 int lo, hi;
                 expert_rows(g, k, lo, hi);
-                na += (hi - lo + 2 * GM - 1) / (2 * GM) * g.tiles_n;
+                na += (hi - lo + ROW_TILE - 1) / ROW_TILE * g.tiles_w;
+                end = max(end, hi);
             }
 #pragma unroll
-            for (int d = 16; d; d >>= 1) na += __shfl_xor_sync(0xffffffffu, na, d);
+            for (int d = 16; d; d >>= 1) {
+                na += __shfl_xor_sync(0xffffffffu, na, d);
+                end = max(end, __shfl_xor_sync(0xffffffffu, end, d));
+            }
+            na += (g.rows - end + ROW_TILE - 1) / ROW_TILE * g.tiles_w;
         }
         nb = g.experts * g.nb * g.tiles_mb * g.tiles_nb;
         const int r = na % P;
@@ -146,7 +200,11 @@ struct Walk {
             t.first = first;
             t.last = last;
             t.blocks = e == g.experts ? 0 : g.segs * g.seg_blocks;
-            place(l, here / g.tiles_n, g.tiles_n, t);
+            const int tiles = here / g.tiles_w;
+            place(l, tiles, g.tiles_w, t);
+            const int per = ((last - first + tiles - 1) / tiles + 31) & ~31;
+            t.r0 = first + t.tm * per;
+            t.n = min(per, (last - t.r0 + 31) & ~31);
             return true;
         }
         const int k = j - mine;
@@ -172,54 +230,204 @@ struct Walk {
         t.tm = from + l % size;
         t.tn = l / size;
     }
+    // Rows of the next expert in the tile's last k-block?
+    static __device__ __forceinline__ bool ragged(const Tile& t) { return t.family && (t.last - t.first) % GK != 0; }
 };
 
-// One warp's 32 x 32 chunk (rows r0 + lane of `rows`, columns c0 .. of `cols`) of
-// matrix z of an output of z_rows rows each.
-__device__ __forceinline__ void store_chunk(const ExpArgs& g, const CUtensorMap* map, const GluOut& o, int rows, int cols,
-                                            int r0, int c0, int z, int z_rows, const float (&v)[32], uint8_t* stage,
-                                            int& groups) {
-    const int lane = threadIdx.x & 31;
-    // a tile store ends with the matrix: an expert's last rows leave row by row
-    const bool tile = g.tma_out && (r0 + 32 <= rows || rows == z_rows);
-    if (groups >= 2 || !tile) {             // the store that last used this buffer has read it
-        if (lane == 0) {
+// Where a chunk of results goes: 32 rows from r0 of `rows`, 32 columns from c0 of
+// `cols`, of matrix z (z_rows rows each).
+struct Place {
+    int rows, cols, r0, c0, z, z_rows;
+};
+
+// Whether a chunk leaves as a tile: a tile store ends with the matrix, an
+// expert's last rows leave row by row.
+__device__ __forceinline__ bool as_tile(const ExpArgs& g, const Place& p) {
+    return g.tma_out && (p.r0 + 32 <= p.rows || p.rows == p.z_rows);
+}
+
+// The warp's next output buffer, once the store that last used it has read it.
+__device__ __forceinline__ uint8_t* out_buffer(uint8_t* stage, int groups, bool tile) {
+    if (groups >= 2 || !tile) {
+        if ((threadIdx.x & 31) == 0) {
             if (tile) bulk_wait_read1();
             else bulk_wait_read0();
         }
         __syncwarp();
     }
-    uint8_t* buf = stage + (groups & 1) * OUT_BYTES;
-    // 64-byte swizzle: 16-byte piece k of row r at k ^ ((r / 2) % 4)
+    return stage + (groups & 1) * OUT_BYTES;
+}
+
+// Offset of 16-byte piece k of row r in a chunk: 64-byte swizzle, piece k at k ^ ((r / 2) % 4).
+__device__ __forceinline__ int piece_at(int r, int k) { return r * 64 + ((k ^ ((r >> 1) & 3)) << 4); }
+
+// A chunk that does not leave as a tile: rows up to p.rows.
+__device__ __forceinline__ void store_rows(const ExpArgs& g, const GluOut& o, const Place& p, const uint8_t* buf) {
+    const int lane = threadIdx.x & 31, n = min(32, p.rows - p.r0);
+    uint16_t* out = static_cast<uint16_t*>(o.p) + ((int64_t)p.z * p.z_rows + p.r0) * o.ld + p.c0;
+    if (g.tma_out) {                        // rows start on 16 bytes: eight of them per step
+        const int k = lane & 3;
+        for (int i = lane >> 2; i < n; i += 8)
+            if (p.c0 + 8 * k < p.cols)
+                *reinterpret_cast<uint4*>(out + (int64_t)i * o.ld + 8 * k) =
+                    *reinterpret_cast<const uint4*>(buf + piece_at(i, k));
+    } else if (p.c0 + lane < p.cols) {      // a row's 32 columns per store
+#pragma unroll 8
+        for (int i = 0; i < n; ++i)
+            out[(int64_t)i * o.ld + lane] =
+                *reinterpret_cast<const uint16_t*>(buf + piece_at(i, lane >> 3) + (lane & 7) * 2);
+    }
+}
+
+// One warp's 32 x 32 chunk, a row per lane.
+__device__ __forceinline__ void store_chunk(const ExpArgs& g, const CUtensorMap* map, const GluOut& o, const Place& p,
+                                            const float (&v)[32], uint8_t* stage, int& groups) {
+    const int lane = threadIdx.x & 31;
+    const bool tile = as_tile(g, p);
+    uint8_t* buf = out_buffer(stage, groups, tile);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<uint4*>(buf + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) =
-            pack8_h(v + 8 * k, g.dtype == MUON_F16);
+        *reinterpret_cast<uint4*>(buf + piece_at(lane, k)) = pack8_h(v + 8 * k, g.dtype == MUON_F16);
+    if (tile) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
     if (tile) {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
         if (lane == 0) {
-            tma_store_3d(map, smem_u32(buf), c0, r0, z);
+            tma_store_3d(map, smem_u32(buf), p.c0, p.r0, p.z);
             bulk_commit();
         }
         ++groups;
         return;
     }
+    store_rows(g, o, p, buf);
     __syncwarp();
-    const int n = min(32, rows - r0);
-    uint16_t* p = static_cast<uint16_t*>(o.p) + ((int64_t)z * z_rows + r0) * o.ld + c0;
-    if (g.tma_out) {                        // rows start on 16 bytes: eight of them per step
-        const int k = lane & 3;
-        for (int i = lane >> 2; i < n; i += 8)
-            if (c0 + 8 * k < cols)
-                *reinterpret_cast<uint4*>(p + (int64_t)i * o.ld + 8 * k) =
-                    *reinterpret_cast<const uint4*>(buf + i * 64 + ((k ^ ((i >> 1) & 3)) << 4));
-    } else if (c0 + lane < cols) {          // a row's 32 columns per store
-#pragma unroll 8
-        for (int i = 0; i < n; ++i)
-            p[(int64_t)i * o.ld + lane] = *reinterpret_cast<const uint16_t*>(
-                buf + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + (lane & 7) * 2);
+}
+
+__device__ __forceinline__ uint32_t pack2_h(float lo, float hi, bool f16) {
+    if (f16) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
     }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// One warp's 32 x 32 chunk, a column per lane: neighbours exchange one value of
+// each pair of rows and write two columns of one of them.
+__device__ __forceinline__ void store_turned(const ExpArgs& g, const CUtensorMap* map, const GluOut& o, const Place& p,
+                                             const float (&v)[32], uint8_t* stage, int& groups) {
+    const int lane = threadIdx.x & 31;
+    const bool tile = as_tile(g, p), odd = lane & 1, f16 = g.dtype == MUON_F16;
+    uint8_t* buf = out_buffer(stage, groups, tile);
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? v[k] : v[k + 1], 1);
+        *reinterpret_cast<uint32_t*>(buf + (k + odd) * 64 + (((lane >> 3) ^ ((k >> 1) & 3)) << 4) + ((lane >> 1) & 3) * 4) =
+            odd ? pack2_h(got, v[k + 1], f16) : pack2_h(v[k], got, f16);
+    }
+    if (tile) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (tile) {
+        if (lane == 0) {
+            tma_store_3d(map, smem_u32(buf), p.c0, p.r0, p.z);
+            bulk_commit();
+        }
+        ++groups;
+        return;
+    }
+    store_rows(g, o, p, buf);
+    __syncwarp();
+}
+
+// The two warps that hold G and U of the same columns.
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+// Whether both of them say so.
+__device__ __forceinline__ bool pair_all(int id, bool v) {
+    int all;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                 "barrier.cta.red.and.pred q, %2, 64, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+                 : "=r"(all) : "r"((uint32_t)v), "r"(id) : "memory");
+    return all != 0;
+}
+
+// One copy of the loop per activation: chosen per element, the code of the other two
+// stands between the elements of the one, and an epilogue of 32 chunks spends
+// its time fetching it (64 experts, 512 rows each, 2048 x 1024: 383 us per call).
+template <int ACT>
+__device__ __forceinline__ void times_act(const float (&gate)[16], float (&v)[32]) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        if (ACT == ACT_GELU) {
+            v[k] *= activate<false>(gate[k], ACT, nullptr);
+            continue;
+        }
+        // g sigmoid(z), as activate() has it but for the quotient: two ulp instead of half
+        // of one, far below the results' rounding, for a third of the instructions
+        const float x = gate[k];
+        const float z = ACT == ACT_SILU ? x : 1.5957691216057308f * x * fmaf(0.044715f * x, x, 1.0f);
+        v[k] *= __fdividef(x, 1.0f + __expf(-z));
+    }
+}
+
+// A pair's 32 x 32 chunk of the gated block, a column per lane, G in one warp and U
+// in the other.  Each stores its own matrix where it is kept; then they exchange half
+// of their rows through their second buffers and write the results of 16 rows each.
+__device__ __forceinline__ void store_gated(const ExpArgs& g, const CUtensorMap* maps, const Place& p, bool is_up, int id,
+                                            float (&v)[32], uint8_t* stage, uint8_t* others, int& groups) {
+    const int lane = threadIdx.x & 31;
+    const bool odd = lane & 1, f16 = g.dtype == MUON_F16;
+    if (g.save) {
+        int own = 0;                        // (the first buffer, whatever was stored before)
+        const int w = is_up ? 2 : 1;
+        if (groups > 0) {
+            if (lane == 0) bulk_wait_read0();
+            __syncwarp();
+        }
+        store_turned(g, &maps[w], g.out[w], p, v, stage, own);
+        groups += own;
+    } else if (groups > 0) {
+        if (lane == 0) bulk_wait_read0();
+        __syncwarp();
+    }
+    // rows 0 .. 15 are the G warp's, rows 16 .. 31 the U warp's
+    float* send = reinterpret_cast<float*>(stage + OUT_BYTES);
+    const float* got = reinterpret_cast<const float*>(others + OUT_BYTES);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) send[k * 32 + lane] = is_up ? v[k] : v[16 + k];
+    pair_sync(id);
+    float gate[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const float o = got[k * 32 + lane];
+        gate[k] = is_up ? o : v[k];
+        v[k] = is_up ? v[16 + k] : o;
+    }
+    pair_sync(id);                          // the other has read this warp's
+    if (g.act == ACT_GELU) times_act<ACT_GELU>(gate, v);
+    else if (g.act == ACT_GELU_TANH) times_act<ACT_GELU_TANH>(gate, v);
+    else times_act<ACT_SILU>(gate, v);
+    Place mine = p;
+    mine.r0 += is_up ? 16 : 0;
+    if (mine.r0 >= p.rows) return;
+    const bool tile = g.tma_out && (mine.r0 + 16 <= p.rows || p.rows == p.z_rows);
+    uint8_t* buf = stage + OUT_BYTES;
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) {
+        const float other = __shfl_xor_sync(0xffffffffu, odd ? v[k] : v[k + 1], 1);
+        *reinterpret_cast<uint32_t*>(buf + (k + odd) * 64 + (((lane >> 3) ^ ((k >> 1) & 3)) << 4) + ((lane >> 1) & 3) * 4) =
+            odd ? pack2_h(other, v[k + 1], f16) : pack2_h(v[k], other, f16);
+    }
+    if (tile) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (tile) {
+        if (lane == 0) {
+            tma_store_3d(&maps[0], smem_u32(buf), p.c0, mine.r0, 0);
+            bulk_commit();
+        }
+        ++groups;
+        return;
+    }
+    mine.rows = min(p.rows, mine.r0 + 16);
+    store_rows(g, g.out[0], mine, buf);
     __syncwarp();
 }
 
@@ -229,27 +437,27 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
-    uint8_t* sB = smem + STAGES * OP_BYTES;
-    uint8_t* sOut = sB + STAGES * OP_BYTES;
+    uint8_t* sB = smem + STAGES * SUB * OP_BYTES;
+    uint8_t* sOut = sB + STAGES * SUB * OP_BYTES;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + NEPI * 2 * OUT_BYTES);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, accf0 = empty0 + 8 * STAGES;
-    const uint32_t acce0 = accf0 + 16, drain_bar = acce0 + 16, tail_bar = drain_bar + 8;
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, raw0 = empty0 + 8 * STAGES;
+    const uint32_t accf0 = raw0 + 8 * STAGES, acce0 = accf0 + 16, drain_bar = acce0 + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank();
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(full0 + 8 * s, rank == 0 ? 2 : 1);    // own copies (even CTA: and the odd one's relay)
+            mbar_init(full0 + 8 * s, 2);                    // the even CTA's: both CTAs' copies
             mbar_init(empty0 + 8 * s, 1);
+            mbar_init(raw0 + 8 * s, 1);                     // copies whose last rows are yet to be zeroed
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(accf0 + 8 * i, 1);
             mbar_init(acce0 + 8 * i, 2 * NEPI);
         }
         mbar_init(drain_bar, 1);
-        mbar_init(tail_bar, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -270,140 +478,118 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
     Tile t;
     if (warp == 0) {
         // ---------------- TMA producer ----------------
-        uint32_t flight = 0, phases = 0;            // per stage: a copy was issued, and its phase
-        int stage = 0;
-        uint32_t phase = 0, tail_phase = 0;
-        bool ok = true, tail_flight = false;
-        while (ok && w.next(g, t)) {
-            const int m0 = t.tm * 2 * GM + rank * GM;
-            for (int kb = 0; kb < t.blocks; ++kb) {
-                const uint32_t fb = full0 + 8 * stage;
-                const uint32_t a = smem_u32(sA + stage * OP_BYTES), b = smem_u32(sB + stage * OP_BYTES);
-                // rows of this k-block that are the expert's, where rows are the contraction
-                const int left = t.family ? t.last - t.first - kb * GK : GK;
-                if (lane == 0) {
-                    ok = wait_bounded(empty0 + 8 * stage, phase ^ 1u, abort_flag, g.status);
-                    if (ok) {
-                        const uint32_t bar = left < GK ? tail_bar : fb;
-                        mbar_expect_tx(bar, STAGE_BYTES);
-                        if (MODE == FWD_GLU) {
-                            tma_load_3d(a, &maps.a[0], bar, kb * GK, t.first + m0, 0);
-                            tma_load_3d(b, &maps.b[rank], bar, kb * GK, t.tn * GM, t.e);    // 128 rows of Wg or of Wu
-                        } else if (MODE == FWD_LINEAR) {
-                            tma_load_3d(a, &maps.a[0], bar, kb * GK, t.first + m0, 0);
-                            tma_load_3d(b, &maps.b[0], bar, kb * GK, t.tn * 2 * GM + rank * GM, t.e);
-                        } else {
-                            const int n0 = t.tn * 2 * GM + rank * GM;
-                            if (t.family == 0) {
-                                const int seg = kb >= g.seg_blocks ? 1 : 0, k0 = (kb - seg * g.seg_blocks) * GK;
-                                tma_load_3d(a, &maps.a[seg], bar, k0, t.first + m0, 0);
-                                tma_load_3d(b, &maps.b[seg], bar, n0, k0, t.e);
-                                tma_load_3d(b + OP_BYTES / 2, &maps.b[seg], bar, n0 + 64, k0, t.e);
-                            } else {
-                                const int k0 = t.first + kb * GK;
-                                tma_load_3d(a, &maps.a2[t.which], bar, m0, k0, 0);
-                                tma_load_3d(a + OP_BYTES / 2, &maps.a2[t.which], bar, m0 + 64, k0, 0);
-                                tma_load_3d(b, &maps.b2, bar, n0, k0, 0);
-                                tma_load_3d(b + OP_BYTES / 2, &maps.b2, bar, n0 + 64, k0, 0);
-                            }
-                        }
-                        if (left < GK) {
-                            tail_flight = true;
-                            flight &= ~(1u << stage);
-                        } else {
-                            flight |= 1u << stage;
-                            phases = (phases & ~(1u << stage)) | (phase << stage);
-                        }
-                    }
-                }
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-                if (!ok) break;
-                if (left < GK) {
-                    // the last rows belong to the next expert: zeroed in both operands (an
-                    // infinity there must not meet a zero here), then the stage is full
-                    const bool got = wait_bounded(tail_bar, tail_phase, abort_flag, g.status);
-                    ok = __all_sync(0xffffffffu, got);
-                    if (!ok) break;
-                    tail_flight = false;
-                    tail_phase ^= 1u;
-                    const int pieces = (GK - left) * 8;     // 16 bytes each, the rows of a half tile are 128 bytes
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        uint8_t* half = (h < 2 ? sA : sB) + stage * OP_BYTES + (h & 1) * (OP_BYTES / 2);
-                        for (int i = lane; i < pieces; i += 32)
-                            *reinterpret_cast<uint4*>(half + left * 128 + i * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(fb);
-                }
-                if (++stage == STAGES) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-        }
-        // this CTA's copies still in flight (after an abort nobody consumes them)
         if (lane == 0) {
-            for (int s = 0; s < STAGES; ++s)
-                if ((flight >> s) & 1) wait_drain(full0 + 8 * s, (phases >> s) & 1);
-            if (tail_flight) wait_drain(tail_bar, tail_phase);
-        }
-        __syncwarp();
-    } else if (warp == 1 && rank == 1) {
-        // ---------------- relay: the odd CTA's filled stages to the even CTA ----------------
-        if (lane == 0) {
+            uint32_t flight = 0, phases = 0;            // per stage: copies on `full` were issued, and their phase
+            uint32_t raw_flight = 0, raw_phases = 0;    // on `raw`, and its phase for the next ones
+            const uint32_t full_pair = bar_of(full0, 0), raw_own = bar_of(raw0, rank);
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
             while (ok && w.next(g, t)) {
-                for (int kb = 0; kb < t.blocks; ++kb) {
-                    if (!wait_bounded(full0 + 8 * stage, phase, abort_flag, g.status)) {
+                const bool ragged = Walk::ragged(t);
+                // family a: boxes of 16 << box rows hold this CTA's half of the tile's
+                const int hn = t.n / 2, box = hn <= 16 ? 0 : hn <= 32 ? 1 : hn <= 64 ? 2 : 3;
+                const uint32_t bytes = OP_BYTES + (t.family ? OP_BYTES : (16 << box) * GK * 2);
+                for (int k1 = 0; k1 < t.blocks; k1 += SUB) {
+                    if (!wait_for(empty0 + 8 * stage, phase ^ 1u, abort_flag, g.status)) {
                         ok = false;
                         break;
                     }
-                    // (a stage whose rows were zeroed here: those writes go along)
-                    if (t.family && t.last - t.first - kb * GK < GK) mbar_arrive_remote(full0 + 8 * stage, 0);
+                    const int n = min(SUB, t.blocks - k1);
+                    const bool tail = ragged && k1 + SUB >= t.blocks;
+                    // both CTAs' copies report to the even CTA, those of a tail each to its own
+                    const uint32_t bar = (tail ? raw_own : full_pair) + 8 * stage;
+                    if (tail) mbar_expect_tx(raw0 + 8 * stage, bytes * n);
+                    else if (rank == 0) mbar_expect_tx(full0 + 8 * stage, 2 * bytes * n);
                     else mbar_arrive_remote_relaxed(full0 + 8 * stage, 0);
+#pragma unroll
+                    for (int i = 0; i < SUB; ++i) {
+                        if (i >= n) break;
+                        const int kb = k1 + i;
+                        const uint32_t a = smem_u32(sA + (stage * SUB + i) * OP_BYTES), b = smem_u32(sB + (stage * SUB + i) * OP_BYTES);
+                        if (MODE == BACKWARD && t.family) {
+                            const int k0 = t.first + kb * GK, m0 = t.tm * 2 * GM + rank * GM, n0 = t.tn * 2 * GM + rank * GM;
+                            tma_load_pair(a, &maps.a2[t.which], bar, m0, k0, 0);
+                            tma_load_pair(a + OP_BYTES / 2, &maps.a2[t.which], bar, m0 + 64, k0, 0);
+                            tma_load_pair(b, &maps.b2, bar, n0, k0, 0);
+                            tma_load_pair(b + OP_BYTES / 2, &maps.b2, bar, n0 + 64, k0, 0);
+                            continue;
+                        }
+                        const int seg = MODE == BACKWARD && kb >= g.seg_blocks ? 1 : 0, k0 = (kb - seg * g.seg_blocks) * GK;
+                        if (MODE == FWD_GLU) {
+                            const int f = t.tn * GM + rank * (GM / 2);
+                            tma_load_pair(a, &maps.a[0], bar, k0, f, t.e);
+                            tma_load_pair(a + OP_BYTES / 2, &maps.a[1], bar, k0, f, t.e);
+                        } else if (MODE == FWD_LINEAR) {
+                            tma_load_pair(a, &maps.a[0], bar, k0, t.tn * 2 * GM + rank * GM, t.e);
+                        } else {
+                            const int m0 = t.tn * 2 * GM + rank * GM;
+                            tma_load_pair(a, &maps.a[seg], bar, m0, k0, t.e);
+                            tma_load_pair(a + OP_BYTES / 2, &maps.a[seg], bar, m0 + 64, k0, t.e);
+                        }
+                        tma_load_pair(b, &maps.b[seg][box], bar, k0, t.r0 + rank * hn, 0);
+                    }
+                    if (tail) {
+                        raw_flight |= 1u << stage;
+                        raw_phases ^= 1u << stage;
+                        flight &= ~(1u << stage);
+                    } else {
+                        flight |= 1u << stage;
+                        phases = (phases & ~(1u << stage)) | (phase << stage);
+                    }
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
+            // copies still in flight (after an abort nobody consumes them): the even CTA
+            // sees those of both; the odd one, which may have issued some that the
+            // even one does not know of, waits out the limit on a barrier that nothing completes
+            for (int s = 0; s < STAGES; ++s) {
+                if (rank == 0 && ((flight >> s) & 1)) wait_drain(full0 + 8 * s, (phases >> s) & 1);
+                if ((raw_flight >> s) & 1) wait_drain(raw0 + 8 * s, ((raw_phases >> s) & 1) ^ 1u);
+            }
+            if (rank == 1 && !ok) wait_drain(full0, 0);
         }
         __syncwarp();
+    } else if (warp == 1 && rank == 1) {
+        // (the even CTA issues the pair's products)
     } else if (warp == 1) {
         // ---------------- MMA issuer (even CTA) ----------------
         if (lane == 0) {
             int stage = 0, acc = 0;
             uint32_t phase = 0, aphase = 0;
             bool ok = true;
-            constexpr bool FWD = MODE != BACKWARD;
+            constexpr bool A_MN = MODE == BACKWARD;     // the weights (dX) or rows (dW) as stored are MN-major there
             while (ok && w.next(g, t)) {
-                const bool fam_b = !FWD && t.family;
+                const bool b_mn = MODE == BACKWARD && t.family;
                 const uint32_t idesc =
-                    idesc_f16kind(2 * GM, 256, !FWD, g.dtype == MUON_F16) | (fam_b ? (1u << 15) : 0u);
+                    idesc_f16kind(2 * GM, t.family ? 256 : t.n, b_mn, g.dtype == MUON_F16) | (A_MN ? (1u << 15) : 0u);
                 for (int from = 0; ok && from < t.blocks; from += MAX_BLOCKS) {
                     const int upto = min(from + MAX_BLOCKS, t.blocks);
-                    if (!wait_bounded(acce0 + 8 * acc, aphase ^ 1u, abort_flag, g.status)) {
+                    if (!wait_for(acce0 + 8 * acc, aphase ^ 1u, abort_flag, g.status)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t d = tmem + (uint32_t)(acc * 256);
-                    for (int kb = from; kb < upto; ++kb) {
-                        if (!wait_bounded(full0 + 8 * stage, phase, abort_flag, g.status)) {
+                    for (int k1 = from; k1 < upto; k1 += SUB) {
+                        if (!wait_for(full0 + 8 * stage, phase, abort_flag, g.status)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t a = smem_u32(sA + stage * OP_BYTES), b = smem_u32(sB + stage * OP_BYTES);
 #pragma unroll
-                        for (int kk = 0; kk < GK / 16; ++kk) {
-                            const uint64_t ad = fam_b ? sdesc(a + kk * 2048, GK * 128, 1024) : sdesc(a + kk * 32, 16, 1024);
-                            const uint64_t bd = FWD ? sdesc(b + kk * 32, 16, 1024) : sdesc(b + kk * 2048, GK * 128, 1024);
-                            tc_mma2_bf16(d, ad, bd, idesc, (kb > from || kk > 0) ? 1u : 0u);
+                        for (int i = 0; i < SUB; ++i) {
+                            if (k1 + i >= upto) break;
+                            const uint32_t a = smem_u32(sA + (stage * SUB + i) * OP_BYTES), b = smem_u32(sB + (stage * SUB + i) * OP_BYTES);
+#pragma unroll
+                            for (int kk = 0; kk < GK / 16; ++kk) {
+                                const uint64_t ad = A_MN ? sdesc(a + kk * 2048, GK * 128, 1024) : sdesc(a + kk * 32, 16, 1024);
+                                const uint64_t bd = b_mn ? sdesc(b + kk * 2048, GK * 128, 1024) : sdesc(b + kk * 32, 16, 1024);
+                                tc_mma2_bf16(d, ad, bd, idesc, (k1 + i > from || kk > 0) ? 1u : 0u);
+                            }
                         }
                         tc_commit2(empty0 + 8 * stage, (uint16_t)0x3);
                         if (++stage == STAGES) {
@@ -423,53 +609,97 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
             }
         }
         __syncwarp();
+    } else if (warp == 2 + NEPI) {
+        // ---------------- tails: the next expert's rows of a last k-block ----------------
+        if (MODE == BACKWARD && g.nb) {
+            int stage = 0;                  // of the tile's first k-blocks
+            uint32_t phases = 0;
+            while (w.next(g, t)) {
+                const int steps = (t.blocks + SUB - 1) / SUB;
+                const int s = (stage + steps + STAGES - 1) % STAGES;        // of its last one
+                stage = (stage + steps) % STAGES;
+                if (!Walk::ragged(t)) continue;
+                // zeroed in both operands: an infinity there must not meet a zero
+                const bool got = wait_for(raw0 + 8 * s, (phases >> s) & 1, abort_flag, g.status);
+                if (!__all_sync(0xffffffffu, got)) break;
+                phases ^= 1u << s;
+                const int left = (t.last - t.first) % GK, pieces = (GK - left) * 8;     // rows of a half tile are 128 bytes
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint8_t* half = (h < 2 ? sA : sB) + (s * SUB + (t.blocks - 1) % SUB) * OP_BYTES + (h & 1) * (OP_BYTES / 2) + left * 128;
+                    for (int i = lane; i < pieces; i += 32) *reinterpret_cast<uint4*>(half + i * 16) = make_uint4(0, 0, 0, 0);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(full0 + 8 * s, 0);
+            }
+        }
+        __syncwarp();
     } else {
         // ---------------- epilogue (warps 2..9) ----------------
         const int q = warp & 3, half = (warp - 2) / 4;
         uint8_t* stage = sOut + (warp - 2) * 2 * OUT_BYTES;
+        // gated forward: quarters 0, 1 hold G and quarters 2, 3 U of the same columns
+        const int pair = 1 + half * 2 + (q & 1);
+        uint8_t* others = sOut + (((warp - 2) & ~3) + ((warp - 2 + 2) & 3)) * 2 * OUT_BYTES;
         int groups = 0, acc = 0;
         uint32_t aphase = 0;
         bool ok = true;
         while (ok && w.next(g, t)) {
-            // rows and columns of the result, and the matrix of its output
-            const int rows = t.family ? g.rows_b : t.last, cols = t.family ? g.cols_b : g.cols_a;
-            const int z = t.family ? t.e : 0, z_rows = t.family ? g.rows_b : g.rows;
-            const int r0 = (t.family ? 0 : t.first) + t.tm * 2 * GM + rank * GM + q * 32;
-            const int o = t.family ? 1 + t.which : 0;
-            constexpr int W = MODE == FWD_GLU ? 2 : 4;      // chunks of a warp
-            const int n0 = t.tn * (MODE == FWD_GLU ? GM : 2 * GM);
+            Place p;
+            int o = 0, chunks;              // output, 32-column chunks of the accumulator
+            if (MODE == BACKWARD && t.family) {
+                p = Place{g.rows_b, g.cols_b, t.tm * 2 * GM + rank * GM + q * 32, t.tn * 2 * GM, t.e, g.rows_b};
+                o = 1 + t.which;
+                chunks = min(8, (p.cols - p.c0 + 31) / 32);
+                if (p.r0 >= p.rows) chunks = 0;
+            } else {
+                const int c0 = MODE == FWD_GLU ? t.tn * GM + rank * (GM / 2) + (q & 1) * 32 : t.tn * 2 * GM + rank * GM + q * 32;
+                p = Place{t.last, g.cols_a, t.r0, c0, 0, g.rows};
+                chunks = c0 < p.cols ? t.n / 32 : 0;
+            }
+            // chunk ch: rows 32 ch.. (family a) or columns 32 ch.. (family b)
+            auto chunk = [&](int ch, float(&v)[32]) {
+                Place c = p;
+                if (MODE == BACKWARD && t.family) {
+                    c.c0 += 32 * ch;
+                    store_chunk(g, &maps.out[o], g.out[o], c, v, stage, groups);
+                } else {
+                    c.r0 += 32 * ch;
+                    if (MODE == FWD_GLU) store_gated(g, maps.out, c, q >= 2, pair, v, stage, others, groups);
+                    else store_turned(g, &maps.out[0], g.out[0], c, v, stage, groups);
+                }
+            };
             if (t.blocks == 0) {
                 // nothing to sum (an expert without rows, rows behind the last expert)
                 float v[32];
+#pragma unroll 1
+                for (int ch = half; ch < chunks; ch += 2) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = 0.f;
-                for (int ch = W * half; ch < W * half + W; ++ch) {
-                    const int c0 = n0 + ch * 32;
-                    if (c0 >= cols || r0 >= rows) break;
-                    store_chunk(g, &maps.out[o], g.out[o], rows, cols, r0, c0, z, z_rows, v, stage, groups);
-                    if (MODE == FWD_GLU && g.save) {
-                        store_chunk(g, &maps.out[1], g.out[1], rows, cols, r0, c0, z, z_rows, v, stage, groups);
-                        store_chunk(g, &maps.out[2], g.out[2], rows, cols, r0, c0, z, z_rows, v, stage, groups);
-                    }
+                    for (int k = 0; k < 32; ++k) v[k] = 0.f;
+                    chunk(ch, v);
                 }
                 continue;
             }
             for (int from = 0; from < t.blocks; from += MAX_BLOCKS) {
-                const bool got = wait_bounded(accf0 + 8 * acc, aphase, abort_flag, g.status);
-                ok = __all_sync(0xffffffffu, got);
+                const bool got = wait_for(accf0 + 8 * acc, aphase, abort_flag, g.status);
+                // a pair goes on together, whichever of its warps saw the wait give up
+                ok = MODE == FWD_GLU ? pair_all(pair, got) : __all_sync(0xffffffffu, got);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
                 const bool more = from + MAX_BLOCKS < t.blocks;
-                // this thread's running sums: its row of the CTA's, 256 columns
+                // this thread's running sums: its lane of the accumulator, 256 columns
                 float* part = g.part + ((size_t)blockIdx.x * GM + q * 32 + lane) * 256;
-                // columns at `at` of the accumulator, with the parts before
-                auto sums = [&](int at, float(&v)[32]) {
-                    tmem_ld32(lanes + (uint32_t)at, v);
+#pragma unroll 1
+                for (int ch = half; ch < chunks; ch += 2) {
+                    float v[32];
+                    tmem_ld32(lanes + (uint32_t)(ch * 32), v);
+                    float* at = part + ch * 32;
                     if (from) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 4) {
-                            const float4 f = *reinterpret_cast<const float4*>(part + at + k);
+                            const float4 f = *reinterpret_cast<const float4*>(at + k);
                             v[k] += f.x;
                             v[k + 1] += f.y;
                             v[k + 2] += f.z;
@@ -479,30 +709,10 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
                     if (more) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
-                            *reinterpret_cast<float4*>(part + at + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-                    }
-                };
-#pragma unroll 1
-                for (int ch = W * half; ch < W * half + W; ++ch) {
-                    const int c0 = n0 + ch * 32;
-                    if (c0 >= cols || r0 >= rows) break;
-                    float v[32];
-                    if (MODE == FWD_GLU) {
-                        float uv[32];
-                        sums(ch * 32, v);
-                        sums(GM + ch * 32, uv);
-                        if (more) continue;
-                        if (g.save) {
-                            store_chunk(g, &maps.out[1], g.out[1], rows, cols, r0, c0, z, z_rows, v, stage, groups);
-                            store_chunk(g, &maps.out[2], g.out[2], rows, cols, r0, c0, z, z_rows, uv, stage, groups);
-                        }
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = uv[k] * activate<false>(v[k], g.act, nullptr);
+                            *reinterpret_cast<float4*>(at + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
                     } else {
-                        sums(ch * 32, v);
-                        if (more) continue;
+                        chunk(ch, v);
                     }
-                    store_chunk(g, &maps.out[o], g.out[o], rows, cols, r0, c0, z, z_rows, v, stage, groups);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -541,7 +751,7 @@ int blocks_of(int64_t k) { return (int)((k + GK - 1) / GK); }
 int set_tiles(ExpArgs& g, int64_t cols_a, int tile_cols, int64_t k, int segs, int nb, int64_t rows_b, int64_t cols_b,
               int64_t* most) {
     g.cols_a = (int)cols_a;
-    g.tiles_n = (int)((cols_a + tile_cols - 1) / tile_cols);
+    g.tiles_w = (int)((cols_a + tile_cols - 1) / tile_cols);
     g.seg_blocks = blocks_of(k);
     g.segs = segs;
     g.nb = nb;
@@ -549,7 +759,7 @@ int set_tiles(ExpArgs& g, int64_t cols_a, int tile_cols, int64_t k, int segs, in
     g.cols_b = (int)cols_b;
     g.tiles_mb = (int)((rows_b + 2 * GM - 1) / (2 * GM));
     g.tiles_nb = (int)((cols_b + 2 * GM - 1) / (2 * GM));
-    *most = (g.a_on ? ((int64_t)g.rows / (2 * GM) + g.experts + 1) * g.tiles_n : 0) +
+    *most = (g.a_on ? ((int64_t)g.rows / ROW_TILE + g.experts + 1) * g.tiles_w : 0) +
             (int64_t)g.experts * nb * g.tiles_mb * g.tiles_nb;
     // (their results alone, 128 KB a tile, are more than the device holds)
     return *most > 1 << 30 ? fail(MUON_ENOMEM, "products of more than 2^30 tiles") : MUON_OK;
@@ -558,6 +768,13 @@ int set_tiles(ExpArgs& g, int64_t cols_a, int tile_cols, int64_t k, int segs, in
 // Whether a contraction of this launch can take more than one part.
 bool in_parts(const ExpArgs& g) {
     return (g.a_on && g.segs * g.seg_blocks > MAX_BLOCKS) || (g.nb && blocks_of(g.rows) > MAX_BLOCKS);
+}
+
+// Rows as family a's N side.
+bool map_rows(CUtensorMap (&m)[4], const Operand& o, int dtype) {
+    for (int i = 0; i < 4; ++i)
+        if (!map_in(&m[i], o, dtype, GK, 16u << i)) return false;
+    return true;
 }
 
 template <int MODE>
@@ -696,9 +913,9 @@ extern "C" int muon_expert_glu_forward(const void* x, const void* w_gate, const 
     std::memset(&maps, 0, sizeof maps);
     g.out[0] = GluOut{h, ffn}; g.out[1] = GluOut{gate, ffn}; g.out[2] = GluOut{up, ffn};
     g.tma_out = tma_ok(h, ffn) && tma_ok(gate, ffn) && tma_ok(up, ffn);
-    bool ok = map_in(&maps.a[0], X, dtype, GK, GM) && map_in(&maps.b[0], G, dtype, GK, GM, num_experts) &&
-              map_in(&maps.b[1], U, dtype, GK, GM, num_experts);
-    for (int i = 0; ok && g.tma_out && i < (g.save ? 3 : 1); ++i) ok = map_out(&maps.out[i], g.out[i], dtype, rows, ffn);
+    bool ok = map_in(&maps.a[0], G, dtype, GK, GM / 2, num_experts) && map_in(&maps.a[1], U, dtype, GK, GM / 2, num_experts) &&
+              map_rows(maps.b[0], X, dtype);
+    for (int i = 0; ok && g.tma_out && i < (g.save ? 3 : 1); ++i) ok = map_out(&maps.out[i], g.out[i], dtype, rows, ffn, 1, i ? 32 : 16);
     if (!ok) return fail(MUON_ECUDA, "tensor map creation failed");
     return launch_expert<FWD_GLU>(maps, g, most, 4.0 * (double)rows * hidden * ffn, dc, s);
 } MUON_CATCH_ALL
@@ -748,8 +965,8 @@ extern "C" int muon_expert_glu_backward(const void* x, const void* w_gate, const
     std::memset(&maps, 0, sizeof maps);
     g.out[0] = GluOut{dx, hidden}; g.out[1] = GluOut{dw_gate, hidden}; g.out[2] = GluOut{dw_up, hidden};
     g.tma_out = tma_ok(dx, hidden) && tma_ok(dw_gate, hidden) && tma_ok(dw_up, hidden);
-    bool ok = map_in(&maps.a[0], DG, dtype, GK, GM) && map_in(&maps.a[1], DU, dtype, GK, GM) &&
-              map_in(&maps.b[0], G, dtype, 64, GK, num_experts) && map_in(&maps.b[1], U, dtype, 64, GK, num_experts) &&
+    bool ok = map_in(&maps.a[0], G, dtype, 64, GK, num_experts) && map_in(&maps.a[1], U, dtype, 64, GK, num_experts) &&
+              map_rows(maps.b[0], DG, dtype) && map_rows(maps.b[1], DU, dtype) &&
               map_in(&maps.a2[0], DG, dtype, 64, GK) && map_in(&maps.a2[1], DU, dtype, 64, GK) &&
               map_in(&maps.b2, X, dtype, 64, GK);
     if (ok && g.tma_out && dx) ok = map_out(&maps.out[0], g.out[0], dtype, rows, hidden);
@@ -787,7 +1004,7 @@ extern "C" int muon_expert_linear_forward(const void* x, const void* w, const in
     std::memset(&maps, 0, sizeof maps);
     g.out[0] = GluOut{y, out};
     g.tma_out = tma_ok(y, out);
-    bool ok = map_in(&maps.a[0], X, dtype, GK, GM) && map_in(&maps.b[0], W, dtype, GK, GM, num_experts);
+    bool ok = map_in(&maps.a[0], W, dtype, GK, GM, num_experts) && map_rows(maps.b[0], X, dtype);
     if (ok && g.tma_out) ok = map_out(&maps.out[0], g.out[0], dtype, rows, out);
     if (!ok) return fail(MUON_ECUDA, "tensor map creation failed");
     return launch_expert<FWD_LINEAR>(maps, g, most, 2.0 * (double)rows * in * out, dc, s);
@@ -821,7 +1038,7 @@ extern "C" int muon_expert_linear_backward(const void* x, const void* w, const v
     std::memset(&maps, 0, sizeof maps);
     g.out[0] = GluOut{dx, in}; g.out[1] = GluOut{dw, in};
     g.tma_out = tma_ok(dx, in) && tma_ok(dw, in);
-    bool ok = map_in(&maps.a[0], D, dtype, GK, GM) && map_in(&maps.b[0], W, dtype, 64, GK, num_experts) &&
+    bool ok = map_in(&maps.a[0], W, dtype, 64, GK, num_experts) && map_rows(maps.b[0], D, dtype) &&
               map_in(&maps.a2[0], D, dtype, 64, GK) && map_in(&maps.b2, X, dtype, 64, GK);
     if (ok && g.tma_out && dx) ok = map_out(&maps.out[0], g.out[0], dtype, rows, in);
     if (ok && g.tma_out && dw) ok = map_out(&maps.out[1], g.out[1], dtype, out, in, num_experts);

@@ -34,7 +34,8 @@ constexpr int64_t MAX_HIDDEN = 1 << 20;
 // experts find each other by a match, so nothing depends on scheduling.
 constexpr int SORT_T = 1024;
 constexpr int SORT_WARPS = SORT_T / 32;
-constexpr int SORT_CLUSTER = 8;
+constexpr int SORT_CLUSTER = 16;
+constexpr int SORT_AHEAD = 8;       // loads of a warp in flight
 
 struct SortArgs {
     const void* experts;
@@ -53,9 +54,9 @@ __device__ __forceinline__ uint32_t ld_cluster(const uint32_t* p, uint32_t rank)
     return v;
 }
 
-// Expert of a slot: experts_n for none, -1 beyond the last slot.
-__device__ __forceinline__ int expert_of(const SortArgs& a, int64_t i) {
-    if (i >= a.slots) return -1;
+// Expert of a slot: experts_n for none, -1 beyond the run's last slot.
+__device__ __forceinline__ int expert_of(const SortArgs& a, int64_t i, int64_t last) {
+    if (i >= last) return -1;
     if (a.index64) {
         const int64_t e = static_cast<const int64_t*>(a.experts)[i];
         return e >= 0 && e < a.experts_n ? (int)e : a.experts_n;
@@ -78,23 +79,30 @@ __global__ void __launch_bounds__(SORT_T, 1) expert_sort_kernel(const __grid_con
     pdl_trigger();
 
     const int64_t first = ((int64_t)rank * SORT_WARPS + warp) * a.per_warp;
+    const int64_t last = min(first + a.per_warp, (int64_t)a.slots);
     uint32_t* mine = table + warp * bins;
-    for (int r = 0; r < a.per_warp && first + r < a.slots; r += 32) {
-        const int e = expert_of(a, first + r + lane);
-        const uint32_t same = __match_any_sync(0xffffffffu, e);
-        if (e >= 0 && lane == __ffs((int)same) - 1) mine[e] += (uint32_t)__popc(same);
-        __syncwarp();
+    int e[SORT_AHEAD];
+    for (int64_t i = first; i < last; i += 32 * SORT_AHEAD) {
+#pragma unroll
+        for (int r = 0; r < SORT_AHEAD; ++r) e[r] = expert_of(a, i + 32 * r + lane, last);
+#pragma unroll
+        for (int r = 0; r < SORT_AHEAD; ++r) {
+            const uint32_t same = __match_any_sync(0xffffffffu, e[r]);
+            if (e[r] >= 0 && lane == __ffs((int)same) - 1) mine[e[r]] += (uint32_t)__popc(same);
+            __syncwarp();
+        }
     }
     __syncthreads();
     // per expert: the warps' counts become the places before each warp's first
-    for (int e = threadIdx.x; e < bins; e += SORT_T) {
+    for (int b = threadIdx.x; b < bins; b += SORT_T) {
         uint32_t n = 0;
+#pragma unroll 8
         for (int w = 0; w < SORT_WARPS; ++w) {
-            const uint32_t c = table[w * bins + e];
-            table[w * bins + e] = n;
+            const uint32_t c = table[w * bins + b];
+            table[w * bins + b] = n;
             n += c;
         }
-        total[e] = n;
+        total[b] = n;
     }
     tc::cluster_sync();
     // all CTAs' counts of expert threadIdx.x, and those of the CTAs before this one
@@ -136,19 +144,24 @@ __global__ void __launch_bounds__(SORT_T, 1) expert_sort_kernel(const __grid_con
         if (rank == 0) a.bounds[0] = 0;
     }
     __syncthreads();
-    for (int r = 0; r < a.per_warp && first + r < a.slots; r += 32) {
-        const int64_t i = first + r + lane;
-        const int e = expert_of(a, i);
-        const uint32_t same = __match_any_sync(0xffffffffu, e);
-        const uint32_t at = e >= 0 ? mine[e] : 0;
-        __syncwarp();
-        if (e >= 0) {
-            if (lane == __ffs((int)same) - 1) mine[e] = at + (uint32_t)__popc(same);
-            const int row = (int)(total[e] + at + (uint32_t)__popc(same & ((1u << lane) - 1)));
-            a.row_of[i] = row;
-            a.slot_of[row] = (int)i;
+    for (int64_t i = first; i < last; i += 32 * SORT_AHEAD) {
+        if (a.per_warp > 32 * SORT_AHEAD) {     // else the first walk's are still here
+#pragma unroll
+            for (int r = 0; r < SORT_AHEAD; ++r) e[r] = expert_of(a, i + 32 * r + lane, last);
         }
-        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < SORT_AHEAD; ++r) {
+            const uint32_t same = __match_any_sync(0xffffffffu, e[r]);
+            const uint32_t at = e[r] >= 0 ? mine[e[r]] : 0;
+            __syncwarp();
+            if (e[r] >= 0) {
+                if (lane == __ffs((int)same) - 1) mine[e[r]] = at + (uint32_t)__popc(same);
+                const int row = (int)(total[e[r]] + at + (uint32_t)__popc(same & ((1u << lane) - 1)));
+                a.row_of[i + 32 * r + lane] = row;
+                a.slot_of[row] = (int)(i + 32 * r + lane);
+            }
+            __syncwarp();
+        }
     }
 }
 
@@ -427,7 +440,9 @@ extern "C" int muon_expert_sort(const void* experts, int index_dtype, int64_t sl
     int set = 0;
     const size_t most = (size_t)(SORT_WARPS + 1) * (MAX_EXPERTS + 1) * 4;
     cudaError_t e = attr.get(dc.device, &set, [&](int&) {
-        return cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+        cudaError_t r = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+        if (r == cudaSuccess) r = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        return r;
     });
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
     cudaLaunchConfig_t cfg = {};

@@ -77,13 +77,14 @@ inline bool map_in(CUtensorMap* m, const Operand& o, int dtype, uint32_t box_col
                         (uint64_t)(o.rows * o.ld), box_cols, box_rows);
 }
 
-// 32 x 32 chunks in 64-byte swizzled rows.
-inline bool map_out(CUtensorMap* m, const GluOut& o, int dtype, int64_t rows, int64_t cols, int64_t batch = 1) {
+// Chunks of 32 columns (64-byte swizzled) and 32 or 16 rows.
+inline bool map_out(CUtensorMap* m, const GluOut& o, int dtype, int64_t rows, int64_t cols, int64_t batch = 1,
+                    uint32_t box_rows = 32) {
     auto fn = tc::encode_fn();
     if (!fn) return false;
     cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
     cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2, (cuuint64_t)o.ld * 2 * (cuuint64_t)rows};
-    cuuint32_t box[3] = {32, 32, 1}, elem[3] = {1, 1, 1};
+    cuuint32_t box[3] = {32, box_rows, 1}, elem[3] = {1, 1, 1};
     return fn(m, dtype == MUON_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, o.p, dims,
               strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
