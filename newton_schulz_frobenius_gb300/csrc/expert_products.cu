@@ -15,7 +15,7 @@
 //
 // Results over sorted rows (family a: forward, dX) are computed transposed: 256
 // rows of the weights are the M side and an expert's rows the N side, whose extent
-// follows the expert in steps of 32.  An expert's rows are cut into
+// follows the expert (32, or in steps of 64).  An expert's rows are cut into
 // ceil(rows / 256) tiles of nearly equal extent, so that ragged or small experts
 // cost little more than their rows.  The epilogue turns 32 x 32 chunks
 // around through the neighbour lane.  In the gated forward pass each CTA's M side
@@ -26,9 +26,12 @@
 //
 // Where an expert ends inside a tile, rows of the next one are multiplied along
 // and not stored (their results are columns of their own, whatever they hold).
-// In the weights' gradients (family b) the rows are the contraction: a warp of its
-// own zeroes the next expert's rows in the last k-block, in shared memory,
-// before the tensor core reads them.
+// In the weights' gradients (family b) the rows are the contraction, so there an
+// expert's last k-block must not hold rows of the next one: a launch before
+// copies these blocks, zeros behind their rows, and the products read the copies.
+// (Zeroed in shared memory instead, between the copy's arrival and the products, a
+// tile waited about 1 us for its last stage: dW of 64 ragged experts of 512 rows on
+// average, 2048 x 1024, 146 us against 114 of even ones.)
 #include "epilogue.cuh"
 #include "glu_parts.cuh"
 
@@ -41,12 +44,12 @@ using namespace tc;
 constexpr int GM = 128;                     // rows of a CTA's half of the M side
 constexpr int GK = 64;                      // k-block: 128 bytes
 constexpr int NEPI = 8;
-constexpr int GT = 64 + 32 * NEPI + 32;     // producer, issuer, epilogue, tails
+constexpr int GT = 64 + 32 * NEPI;          // producer, issuer, epilogue
 constexpr int SUB = 2;                      // k-blocks of a stage
 constexpr int STAGES = 6 / SUB;
 constexpr int OP_BYTES = GM * GK * 2;       // one operand's k-block of a stage (A, or this CTA's half of B)
 constexpr int OUT_BYTES = 32 * 32 * 2;      // output chunk of a warp: 32 x 32, 64-byte swizzled rows
-constexpr int NBARS = 3 * STAGES + 5;
+constexpr int NBARS = 2 * STAGES + 5;
 constexpr int EXP_SMEM = STAGES * SUB * 2 * OP_BYTES + NEPI * 2 * OUT_BYTES + NBARS * 8 + 16 + 1024;
 static_assert(EXP_SMEM <= 232448, "shared memory per CTA");
 constexpr int GROUP = 16;                   // row tiles that share their weights' tiles in L2
@@ -85,12 +88,33 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
         : "memory");
 }
 
+__device__ __forceinline__ void arrive_relaxed(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// 128 columns from c of 64 rows from r of matrix z, as two blocks of 64 columns:
+// one copy from a map by blocks of columns, or two.
+__device__ __forceinline__ void load_columns(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c, int r, int z,
+                                             bool whole) {
+    if (whole) {
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+            " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(r), "r"(c / 64), "r"(z)
+            : "memory");
+    } else {
+        tma_load_pair(dst, map, bar, c, r, z);
+        tma_load_pair(dst + OP_BYTES / 2, map, bar, c + 64, r, z);
+    }
+}
+
 enum Mode : int { FWD_GLU = 0, FWD_LINEAR = 1, BACKWARD = 2 };
 
 struct ExpArgs {
     int dtype, act;
     int save;                   // gated forward: G and U leave too
     int tma_out;                // outputs leave through tile stores
+    int whole_a, whole_a2, whole_b2;        // MN-major operands' maps are by blocks of 64 columns
     int rows, experts;
     const int* bounds;
     // family a: results over the sorted rows (forward, dX)
@@ -104,10 +128,16 @@ struct ExpArgs {
     int* status;
 };
 
+// Extents of family a's tiles: 32, or multiples of 64 rows, half of them per CTA in
+// one box, so that each copy brings the tile's rows alone.
+constexpr int BOXES = 5;
+__host__ __device__ constexpr int box_rows(int i) { return i == 0 ? 16 : 32 * i; }
+
 struct ExpMaps {
     CUtensorMap a[2];           // family a: weights by segment (gated forward: Wg, Wu)
-    CUtensorMap b[2][4];        // rows by segment, boxes of 16, 32, 64, 128 rows
+    CUtensorMap b[2][BOXES];    // rows by segment, in boxes of box_rows()
     CUtensorMap a2[2], b2;      // family b: dG, dU (dY) read MN-major; X
+    CUtensorMap a2_tail[2], b2_tail;        // the experts' last k-blocks of them
     CUtensorMap out[3];
 };
 
@@ -122,7 +152,7 @@ struct Tile {
     int family, which;          // 0: a, 1: b; output index
     int e;
     int first, last;            // the expert's rows
-    int r0, n;                  // family a: the tile's first row, and its extent in steps of 32
+    int r0, n;                  // family a: the tile's first row, and its extent
     int tm, tn;                 // family a: tn = weights' tile; b: row and column tile
     int blocks;                 // k-blocks of its contraction (0: the result is zero)
 };
@@ -202,9 +232,9 @@ struct Walk {
             t.blocks = e == g.experts ? 0 : g.segs * g.seg_blocks;
             const int tiles = here / g.tiles_w;
             place(l, tiles, g.tiles_w, t);
-            const int per = ((last - first + tiles - 1) / tiles + 31) & ~31;
+            const int per = extent((last - first + tiles - 1) / tiles);
             t.r0 = first + t.tm * per;
-            t.n = min(per, (last - t.r0 + 31) & ~31);
+            t.n = min(per, extent(last - t.r0));
             return true;
         }
         const int k = j - mine;
@@ -224,14 +254,13 @@ struct Walk {
         place(id - t.which * tiles, g.tiles_mb, g.tiles_nb, t);
         return true;
     }
+    static __device__ __forceinline__ int extent(int rows) { return rows <= 32 ? 32 : (rows + 63) & ~63; }
     __device__ __forceinline__ void place(int l, int tiles_m, int tiles_n, Tile& t) {
         const int per = GROUP * tiles_n, grp = l / per, from = grp * GROUP, size = min(GROUP, tiles_m - from);
         l -= grp * per;
         t.tm = from + l % size;
         t.tn = l / size;
     }
-    // Rows of the next expert in the tile's last k-block?
-    static __device__ __forceinline__ bool ragged(const Tile& t) { return t.family && (t.last - t.first) % GK != 0; }
 };
 
 // Where a chunk of results goes: 32 rows from r0 of `rows`, 32 columns from c0 of
@@ -442,8 +471,8 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
     uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + NEPI * 2 * OUT_BYTES);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, raw0 = empty0 + 8 * STAGES;
-    const uint32_t accf0 = raw0 + 8 * STAGES, acce0 = accf0 + 16, drain_bar = acce0 + 16;
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, accf0 = empty0 + 8 * STAGES;
+    const uint32_t acce0 = accf0 + 16, drain_bar = acce0 + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank();
 
@@ -451,7 +480,6 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full0 + 8 * s, 2);                    // the even CTA's: both CTAs' copies
             mbar_init(empty0 + 8 * s, 1);
-            mbar_init(raw0 + 8 * s, 1);                     // copies whose last rows are yet to be zeroed
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(accf0 + 8 * i, 1);
@@ -479,77 +507,90 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
     if (warp == 0) {
         // ---------------- TMA producer ----------------
         if (lane == 0) {
-            uint32_t flight = 0, phases = 0;            // per stage: copies on `full` were issued, and their phase
-            uint32_t raw_flight = 0, raw_phases = 0;    // on `raw`, and its phase for the next ones
-            const uint32_t full_pair = bar_of(full0, 0), raw_own = bar_of(raw0, rank);
+            uint32_t flight = 0, phases = 0;            // per stage: copies were issued, and their phase
+            const uint32_t full_pair = bar_of(full0, 0), a0 = smem_u32(sA), b0 = smem_u32(sB);
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
+            // waits for a stage to be free and says how many bytes the pair's copies bring
+            auto open = [&](uint32_t bytes) {
+                ok = wait_for(empty0 + 8 * stage, phase ^ 1u, abort_flag, g.status);
+                if (!ok) return;
+                if (rank == 0) mbar_expect_tx(full0 + 8 * stage, 2 * bytes);
+                else arrive_relaxed(full_pair + 8 * stage);
+                flight |= 1u << stage;
+                phases = (phases & ~(1u << stage)) | (phase << stage);
+            };
+            auto close = [&] {
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            };
             while (ok && w.next(g, t)) {
-                const bool ragged = Walk::ragged(t);
-                // family a: boxes of 16 << box rows hold this CTA's half of the tile's
-                const int hn = t.n / 2, box = hn <= 16 ? 0 : hn <= 32 ? 1 : hn <= 64 ? 2 : 3;
-                const uint32_t bytes = OP_BYTES + (t.family ? OP_BYTES : (16 << box) * GK * 2);
-                for (int k1 = 0; k1 < t.blocks; k1 += SUB) {
-                    if (!wait_for(empty0 + 8 * stage, phase ^ 1u, abort_flag, g.status)) {
-                        ok = false;
-                        break;
+                if (MODE == BACKWARD && t.family) {
+                    const bool ragged = (t.last - t.first) % GK != 0;
+                    const int m0 = t.tm * 2 * GM + rank * GM, n0 = t.tn * 2 * GM + rank * GM;
+                    const CUtensorMap *ma = &maps.a2[t.which], *mb = &maps.b2;
+                    int k0 = t.first;
+                    for (int left = t.blocks; left > 0; left -= SUB) {
+                        open((uint32_t)(min(left, SUB) * 2 * OP_BYTES));
+                        if (!ok) break;
+                        const uint32_t bar = full_pair + 8 * stage, at = (uint32_t)(stage * SUB * OP_BYTES);
+#pragma unroll
+                        for (int i = 0; i < SUB; ++i) {
+                            if (i >= left) break;
+                            if (ragged && left - i == 1) {
+                                // a last k-block of fewer rows stands padded with zeros in the scratch
+                                ma = &maps.a2_tail[t.which];
+                                mb = &maps.b2_tail;
+                                k0 = t.e * GK;
+                            }
+                            load_columns(a0 + at + i * OP_BYTES, ma, bar, m0, k0, 0, g.whole_a2);
+                            load_columns(b0 + at + i * OP_BYTES, mb, bar, n0, k0, 0, g.whole_b2);
+                            k0 += GK;
+                        }
+                        close();
                     }
-                    const int n = min(SUB, t.blocks - k1);
-                    const bool tail = ragged && k1 + SUB >= t.blocks;
-                    // both CTAs' copies report to the even CTA, those of a tail each to its own
-                    const uint32_t bar = (tail ? raw_own : full_pair) + 8 * stage;
-                    if (tail) mbar_expect_tx(raw0 + 8 * stage, bytes * n);
-                    else if (rank == 0) mbar_expect_tx(full0 + 8 * stage, 2 * bytes * n);
-                    else mbar_arrive_remote_relaxed(full0 + 8 * stage, 0);
+                    continue;
+                }
+                const int hn = t.n / 2, r0 = t.r0 + rank * hn;      // this CTA's rows of the tile
+                const int c0 = MODE == FWD_GLU ? t.tn * GM + rank * (GM / 2) : t.tn * 2 * GM + rank * GM;
+                const uint32_t bytes = OP_BYTES + hn * GK * 2;
+                const CUtensorMap *ma = &maps.a[0], *mb = &maps.b[0][hn / 32];
+                int k0 = 0;
+                for (int left = t.blocks; left > 0; left -= SUB) {
+                    open(min(left, SUB) * bytes);
+                    if (!ok) break;
+                    const uint32_t bar = full_pair + 8 * stage, at = (uint32_t)(stage * SUB * OP_BYTES);
 #pragma unroll
                     for (int i = 0; i < SUB; ++i) {
-                        if (i >= n) break;
-                        const int kb = k1 + i;
-                        const uint32_t a = smem_u32(sA + (stage * SUB + i) * OP_BYTES), b = smem_u32(sB + (stage * SUB + i) * OP_BYTES);
-                        if (MODE == BACKWARD && t.family) {
-                            const int k0 = t.first + kb * GK, m0 = t.tm * 2 * GM + rank * GM, n0 = t.tn * 2 * GM + rank * GM;
-                            tma_load_pair(a, &maps.a2[t.which], bar, m0, k0, 0);
-                            tma_load_pair(a + OP_BYTES / 2, &maps.a2[t.which], bar, m0 + 64, k0, 0);
-                            tma_load_pair(b, &maps.b2, bar, n0, k0, 0);
-                            tma_load_pair(b + OP_BYTES / 2, &maps.b2, bar, n0 + 64, k0, 0);
-                            continue;
-                        }
-                        const int seg = MODE == BACKWARD && kb >= g.seg_blocks ? 1 : 0, k0 = (kb - seg * g.seg_blocks) * GK;
+                        if (i >= left) break;
+                        const uint32_t a = a0 + at + i * OP_BYTES, b = b0 + at + i * OP_BYTES;
                         if (MODE == FWD_GLU) {
-                            const int f = t.tn * GM + rank * (GM / 2);
-                            tma_load_pair(a, &maps.a[0], bar, k0, f, t.e);
-                            tma_load_pair(a + OP_BYTES / 2, &maps.a[1], bar, k0, f, t.e);
+                            tma_load_pair(a, &maps.a[0], bar, k0, c0, t.e);
+                            tma_load_pair(a + OP_BYTES / 2, &maps.a[1], bar, k0, c0, t.e);
                         } else if (MODE == FWD_LINEAR) {
-                            tma_load_pair(a, &maps.a[0], bar, k0, t.tn * 2 * GM + rank * GM, t.e);
+                            tma_load_pair(a, &maps.a[0], bar, k0, c0, t.e);
                         } else {
-                            const int m0 = t.tn * 2 * GM + rank * GM;
-                            tma_load_pair(a, &maps.a[seg], bar, m0, k0, t.e);
-                            tma_load_pair(a + OP_BYTES / 2, &maps.a[seg], bar, m0 + 64, k0, t.e);
+                            load_columns(a, ma, bar, c0, k0, t.e, g.whole_a);
                         }
-                        tma_load_pair(b, &maps.b[seg][box], bar, k0, t.r0 + rank * hn, 0);
+                        tma_load_pair(b, mb, bar, k0, r0, 0);
+                        k0 += GK;
+                        if (MODE == BACKWARD && k0 >= g.seg_blocks * GK) {      // from dG Wg to dU Wu
+                            k0 = 0;
+                            ma = &maps.a[1];
+                            mb = &maps.b[1][hn / 32];
+                        }
                     }
-                    if (tail) {
-                        raw_flight |= 1u << stage;
-                        raw_phases ^= 1u << stage;
-                        flight &= ~(1u << stage);
-                    } else {
-                        flight |= 1u << stage;
-                        phases = (phases & ~(1u << stage)) | (phase << stage);
-                    }
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    close();
                 }
             }
             // copies still in flight (after an abort nobody consumes them): the even CTA
             // sees those of both; the odd one, which may have issued some that the
             // even one does not know of, waits out the limit on a barrier that nothing completes
-            for (int s = 0; s < STAGES; ++s) {
+            for (int s = 0; s < STAGES; ++s)
                 if (rank == 0 && ((flight >> s) & 1)) wait_drain(full0 + 8 * s, (phases >> s) & 1);
-                if ((raw_flight >> s) & 1) wait_drain(raw0 + 8 * s, ((raw_phases >> s) & 1) ^ 1u);
-            }
             if (rank == 1 && !ok) wait_drain(full0, 0);
         }
         __syncwarp();
@@ -562,10 +603,13 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
             uint32_t phase = 0, aphase = 0;
             bool ok = true;
             constexpr bool A_MN = MODE == BACKWARD;     // the weights (dX) or rows (dW) as stored are MN-major there
+            const uint64_t ad0 = A_MN ? sdesc(smem_u32(sA), GK * 128, 1024) : sdesc(smem_u32(sA), 16, 1024);
             while (ok && w.next(g, t)) {
                 const bool b_mn = MODE == BACKWARD && t.family;
                 const uint32_t idesc =
                     idesc_f16kind(2 * GM, t.family ? 256 : t.n, b_mn, g.dtype == MUON_F16) | (A_MN ? (1u << 15) : 0u);
+                const uint64_t bd0 = b_mn ? sdesc(smem_u32(sB), GK * 128, 1024) : sdesc(smem_u32(sB), 16, 1024);
+                const int b_step = b_mn ? 2048 / 16 : 2;
                 for (int from = 0; ok && from < t.blocks; from += MAX_BLOCKS) {
                     const int upto = min(from + MAX_BLOCKS, t.blocks);
                     if (!wait_for(acce0 + 8 * acc, aphase ^ 1u, abort_flag, g.status)) {
@@ -583,13 +627,12 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
 #pragma unroll
                         for (int i = 0; i < SUB; ++i) {
                             if (k1 + i >= upto) break;
-                            const uint32_t a = smem_u32(sA + (stage * SUB + i) * OP_BYTES), b = smem_u32(sB + (stage * SUB + i) * OP_BYTES);
+                            // (addresses count in 16 bytes in a descriptor's lowest bits)
+                            const uint64_t at = (uint64_t)((stage * SUB + i) * (OP_BYTES / 16));
 #pragma unroll
-                            for (int kk = 0; kk < GK / 16; ++kk) {
-                                const uint64_t ad = A_MN ? sdesc(a + kk * 2048, GK * 128, 1024) : sdesc(a + kk * 32, 16, 1024);
-                                const uint64_t bd = b_mn ? sdesc(b + kk * 2048, GK * 128, 1024) : sdesc(b + kk * 32, 16, 1024);
-                                tc_mma2_bf16(d, ad, bd, idesc, (k1 + i > from || kk > 0) ? 1u : 0u);
-                            }
+                            for (int kk = 0; kk < GK / 16; ++kk)
+                                tc_mma2_bf16(d, ad0 + at + kk * (A_MN ? 2048 / 16 : 2), bd0 + at + kk * b_step, idesc,
+                                             (k1 + i > from || kk > 0) ? 1u : 0u);
                         }
                         tc_commit2(empty0 + 8 * stage, (uint16_t)0x3);
                         if (++stage == STAGES) {
@@ -606,32 +649,6 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
             if (!ok) {
                 tc_commit2(drain_bar, (uint16_t)0x1);
                 wait_drain(drain_bar, 0);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 2 + NEPI) {
-        // ---------------- tails: the next expert's rows of a last k-block ----------------
-        if (MODE == BACKWARD && g.nb) {
-            int stage = 0;                  // of the tile's first k-blocks
-            uint32_t phases = 0;
-            while (w.next(g, t)) {
-                const int steps = (t.blocks + SUB - 1) / SUB;
-                const int s = (stage + steps + STAGES - 1) % STAGES;        // of its last one
-                stage = (stage + steps) % STAGES;
-                if (!Walk::ragged(t)) continue;
-                // zeroed in both operands: an infinity there must not meet a zero
-                const bool got = wait_for(raw0 + 8 * s, (phases >> s) & 1, abort_flag, g.status);
-                if (!__all_sync(0xffffffffu, got)) break;
-                phases ^= 1u << s;
-                const int left = (t.last - t.first) % GK, pieces = (GK - left) * 8;     // rows of a half tile are 128 bytes
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint8_t* half = (h < 2 ? sA : sB) + (s * SUB + (t.blocks - 1) % SUB) * OP_BYTES + (h & 1) * (OP_BYTES / 2) + left * 128;
-                    for (int i = lane; i < pieces; i += 32) *reinterpret_cast<uint4*>(half + i * 16) = make_uint4(0, 0, 0, 0);
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(full0 + 8 * s, 0);
             }
         }
         __syncwarp();
@@ -736,6 +753,32 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
     }
 }
 
+// The experts' last k-blocks of up to three matrices (rows on 16 bytes, pitch ld):
+// block e of dst holds the rows of expert e's last, partial k-block, zeros behind
+// them; experts without one are left out (nothing reads theirs).
+struct TailArgs {
+    const void* src[3];
+    void* dst[3];
+    int64_t ld[3];              // of both
+    int rows;
+    const int* bounds;
+};
+
+__global__ void __launch_bounds__(256) tails_kernel(const __grid_constant__ TailArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const int m = blockIdx.z, e = blockIdx.x;
+    const int first = e == 0 ? 0 : min(max(a.bounds[e], 0), a.rows), last = min(max(a.bounds[e + 1], first), a.rows);
+    const int left = (last - first) % GK;
+    if (left == 0) return;
+    const int pieces = (int)(a.ld[m] / 8);
+    const uint4* src = static_cast<const uint4*>(a.src[m]) + (int64_t)(last - left) * pieces;
+    uint4* dst = static_cast<uint4*>(a.dst[m]) + (int64_t)e * GK * pieces;
+    const int n = GK * pieces, live = left * pieces;
+    for (int i = blockIdx.y * 256 + threadIdx.x; i < n; i += gridDim.y * 256)
+        dst[i] = i < live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+}
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
@@ -770,10 +813,57 @@ bool in_parts(const ExpArgs& g) {
     return (g.a_on && g.segs * g.seg_blocks > MAX_BLOCKS) || (g.nb && blocks_of(g.rows) > MAX_BLOCKS);
 }
 
+// A matrix read MN-major: by blocks of 64 columns, where its columns are whole ones
+// (128 of them are one copy then: half the instructions of the producer, whose time
+// per stage the ring feels), else as it is.
+bool map_columns(CUtensorMap* m, const Operand& o, int dtype, int* whole, int64_t batch = 1) {
+    *whole = o.cols % 64 == 0;
+    if (!*whole) return map_in(m, o, dtype, 64, GK, batch);
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[4] = {64, (cuuint64_t)o.rows, (cuuint64_t)(o.cols / 64), (cuuint64_t)batch};
+    cuuint64_t strides[3] = {(cuuint64_t)o.ld * 2, 128, (cuuint64_t)(o.rows * o.ld) * 2};
+    cuuint32_t box[4] = {64, GK, 2, 1}, elem[4] = {1, 1, 1, 1};
+    return fn(m, dtype == MUON_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+              const_cast<void*>(o.p), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Bytes of the experts' last k-blocks of a matrix of pitch ld.
+size_t tail_bytes(const ExpArgs& g, int64_t ld) { return g.nb ? align_up((size_t)g.experts * GK * ld * 2, 256) : 0; }
+
+// Copies them for the matrices of family b to `at`, one after the other, and maps
+// both: which of ops is family b's B operand, the others are its A operands.
+int set_family_b(ExpMaps& maps, ExpArgs& g, const Operand* const* ops, int n, char* at, int sms, cudaStream_t s) {
+    TailArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.rows = g.rows;
+    a.bounds = g.bounds;
+    int64_t widest = 1;
+    for (int i = 0; i < n; ++i) {
+        const Operand& o = *ops[i];
+        CUtensorMap* whole = i < n - 1 ? &maps.a2[i] : &maps.b2;
+        CUtensorMap* tail = i < n - 1 ? &maps.a2_tail[i] : &maps.b2_tail;
+        const Operand t{at, (int64_t)g.experts * GK, o.cols, o.ld};
+        int* by_blocks = i < n - 1 ? &g.whole_a2 : &g.whole_b2;         // (the A operands have one shape)
+        if (!map_columns(whole, o, g.dtype, by_blocks) || !map_columns(tail, t, g.dtype, by_blocks))
+            return fail(MUON_ECUDA, "tensor map creation failed");
+        a.src[i] = o.p; a.dst[i] = at; a.ld[i] = o.ld;
+        widest = std::max(widest, o.ld);
+        at += tail_bytes(g, o.ld);
+    }
+    // a few pieces per thread, fewer CTAs per expert where experts fill the device
+    const int64_t y = std::max<int64_t>(1, std::min<int64_t>((widest * GK / 8 + 511) / 512, (int64_t)sms * 16 / (g.experts * n)));
+    note_launch_begin(KC_OTHER, s);
+    const cudaError_t e = launch_pdl(tails_kernel, dim3((unsigned)g.experts, (unsigned)y, (unsigned)n), dim3(256), 0, s, a);
+    note_launch_end(KC_OTHER, 0.0, s);
+    return e == cudaSuccess ? MUON_OK : cuda_fail(e, "expert tails launch");
+}
+
 // Rows as family a's N side.
-bool map_rows(CUtensorMap (&m)[4], const Operand& o, int dtype) {
-    for (int i = 0; i < 4; ++i)
-        if (!map_in(&m[i], o, dtype, GK, 16u << i)) return false;
+bool map_rows(CUtensorMap (&m)[BOXES], const Operand& o, int dtype) {
+    for (int i = 0; i < BOXES; ++i)
+        if (!map_in(&m[i], o, dtype, GK, (uint32_t)box_rows(i))) return false;
     return true;
 }
 
@@ -947,8 +1037,9 @@ extern "C" int muon_expert_glu_backward(const void* x, const void* w_gate, const
     const size_t half = align_up((size_t)rows * ldw * 2, 256);
     size_t part = 0;
     if ((r = part_bytes<BACKWARD>(g, most, dc, &part))) return r;
-    if ((r = scratch_check(scratch, scratch_bytes, part + 2 * half + padded_bytes(X) + padded_bytes(G) + padded_bytes(U))))
-        return r;
+    const size_t pads = padded_bytes(X) + padded_bytes(G) + padded_bytes(U);
+    const size_t tails = 2 * tail_bytes(g, ldw) + tail_bytes(g, pad8(hidden));
+    if ((r = scratch_check(scratch, scratch_bytes, part + 2 * half + pads + tails))) return r;
     char* at = static_cast<char*>(scratch);
     g.part = reinterpret_cast<float*>(at);
     GluGradArgs ga;
@@ -965,15 +1056,15 @@ extern "C" int muon_expert_glu_backward(const void* x, const void* w_gate, const
     std::memset(&maps, 0, sizeof maps);
     g.out[0] = GluOut{dx, hidden}; g.out[1] = GluOut{dw_gate, hidden}; g.out[2] = GluOut{dw_up, hidden};
     g.tma_out = tma_ok(dx, hidden) && tma_ok(dw_gate, hidden) && tma_ok(dw_up, hidden);
-    bool ok = map_in(&maps.a[0], G, dtype, 64, GK, num_experts) && map_in(&maps.a[1], U, dtype, 64, GK, num_experts) &&
-              map_rows(maps.b[0], DG, dtype) && map_rows(maps.b[1], DU, dtype) &&
-              map_in(&maps.a2[0], DG, dtype, 64, GK) && map_in(&maps.a2[1], DU, dtype, 64, GK) &&
-              map_in(&maps.b2, X, dtype, 64, GK);
+    bool ok = map_columns(&maps.a[0], G, dtype, &g.whole_a, num_experts) && map_columns(&maps.a[1], U, dtype, &g.whole_a, num_experts) &&
+              map_rows(maps.b[0], DG, dtype) && map_rows(maps.b[1], DU, dtype);
     if (ok && g.tma_out && dx) ok = map_out(&maps.out[0], g.out[0], dtype, rows, hidden);
     if (ok && g.tma_out && dw_gate)
         ok = map_out(&maps.out[1], g.out[1], dtype, ffn, hidden, num_experts) &&
              map_out(&maps.out[2], g.out[2], dtype, ffn, hidden, num_experts);
     if (!ok) return fail(MUON_ECUDA, "tensor map creation failed");
+    const Operand* const contracted[3] = {&DG, &DU, &X};
+    if (dw_gate && (r = set_family_b(maps, g, contracted, 3, at + part + 2 * half + pads, dc.sms, s))) return r;
     return launch_expert<BACKWARD>(maps, g, most, ((dx ? 4.0 : 0.0) + (dw_gate ? 4.0 : 0.0)) * (double)rows * hidden * ffn, dc, s);
 } MUON_CATCH_ALL
 
@@ -1029,7 +1120,8 @@ extern "C" int muon_expert_linear_backward(const void* x, const void* w, const v
     size_t part = 0;
     if ((r = part_bytes<BACKWARD>(g, most, dc, &part))) return r;
     const size_t pads = padded_bytes(X) + padded_bytes(W) + padded_bytes(D);
-    if ((r = scratch_check(scratch, scratch_bytes, part + pads))) return r;
+    const size_t tails = tail_bytes(g, pad8(out)) + tail_bytes(g, pad8(in));
+    if ((r = scratch_check(scratch, scratch_bytes, part + pads + tails))) return r;
     g.part = static_cast<float*>(scratch);
     Operand* const ops[3] = {&X, &W, &D};
     if (pads && (r = glu_prepare(ops, 3, static_cast<char*>(scratch) + part, nullptr, dc.sms, s))) return r;
@@ -1038,10 +1130,11 @@ extern "C" int muon_expert_linear_backward(const void* x, const void* w, const v
     std::memset(&maps, 0, sizeof maps);
     g.out[0] = GluOut{dx, in}; g.out[1] = GluOut{dw, in};
     g.tma_out = tma_ok(dx, in) && tma_ok(dw, in);
-    bool ok = map_in(&maps.a[0], W, dtype, 64, GK, num_experts) && map_rows(maps.b[0], D, dtype) &&
-              map_in(&maps.a2[0], D, dtype, 64, GK) && map_in(&maps.b2, X, dtype, 64, GK);
+    bool ok = map_columns(&maps.a[0], W, dtype, &g.whole_a, num_experts) && map_rows(maps.b[0], D, dtype);
     if (ok && g.tma_out && dx) ok = map_out(&maps.out[0], g.out[0], dtype, rows, in);
     if (ok && g.tma_out && dw) ok = map_out(&maps.out[1], g.out[1], dtype, out, in, num_experts);
     if (!ok) return fail(MUON_ECUDA, "tensor map creation failed");
+    const Operand* const contracted[2] = {&D, &X};
+    if (dw && (r = set_family_b(maps, g, contracted, 2, static_cast<char*>(scratch) + part + pads, dc.sms, s))) return r;
     return launch_expert<BACKWARD>(maps, g, most, ((dx ? 2.0 : 0.0) + (dw ? 2.0 : 0.0)) * (double)rows * in * out, dc, s);
 } MUON_CATCH_ALL
