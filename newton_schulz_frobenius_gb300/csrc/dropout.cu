@@ -29,21 +29,27 @@ struct DropArgs {
     int dtype;
 };
 
-// Eight 16-bit numbers of block b, two to a word, the even element in the low half.
-__device__ __forceinline__ uint4 philox(uint64_t b, uint64_t seed, uint64_t offset) {
-    uint32_t c0 = (uint32_t)b, c1 = (uint32_t)(b >> 32), c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
+// Eight 16-bit numbers of each of two blocks, two to a word, the even element in
+// the low half.
+__device__ __forceinline__ void philox2(uint64_t b0, uint64_t b1, uint64_t seed, uint64_t offset, uint4& r0, uint4& r1) {
+    uint32_t c[2][4] = {{(uint32_t)b0, (uint32_t)(b0 >> 32), (uint32_t)offset, (uint32_t)(offset >> 32)},
+                        {(uint32_t)b1, (uint32_t)(b1 >> 32), (uint32_t)offset, (uint32_t)(offset >> 32)}};
     uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
 #pragma unroll
     for (int i = 0; i < 10; ++i) {
-        const uint64_t p = (uint64_t)0xD2511F53u * c0, q = (uint64_t)0xCD9E8D57u * c2;
-        c0 = (uint32_t)(q >> 32) ^ c1 ^ k0;
-        c2 = (uint32_t)(p >> 32) ^ c3 ^ k1;
-        c1 = (uint32_t)q;
-        c3 = (uint32_t)p;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint64_t p = (uint64_t)0xD2511F53u * c[j][0], q = (uint64_t)0xCD9E8D57u * c[j][2];
+            c[j][0] = (uint32_t)(q >> 32) ^ c[j][1] ^ k0;
+            c[j][2] = (uint32_t)(p >> 32) ^ c[j][3] ^ k1;
+            c[j][1] = (uint32_t)q;
+            c[j][3] = (uint32_t)p;
+        }
         k0 += 0x9E3779B9u;
         k1 += 0xBB67AE85u;
     }
-    return make_uint4(c0, c1, c2, c3);
+    r0 = make_uint4(c[0][0], c[0][1], c[0][2], c[0][3]);
+    r1 = make_uint4(c[1][0], c[1][1], c[1][2], c[1][3]);
 }
 
 // Eight elements from their 16-byte pieces (one, of fp32 two) and back.
@@ -90,25 +96,40 @@ __global__ void __launch_bounds__(DT) dropout_kernel(const __grid_constant__ Dro
     pdl_wait();
     pdl_trigger();
     const uint64_t seed = a.state ? (uint64_t)a.state[0] : a.seed, offset = a.state ? (uint64_t)a.state[1] : a.offset;
-    const int64_t blocks = (a.n + 7) / 8, whole = VEC ? a.n / 8 : 0, step = (int64_t)gridDim.x * DT;
-    int64_t b = (int64_t)blockIdx.x * DT + threadIdx.x;
+    const int64_t blocks = (a.n + 7) / 8, whole = VEC ? a.n / 8 : 0;
+    // two blocks per thread, 256 apart: their loads leave together, and the key's
+    // ten steps are taken once
+    int64_t b = (int64_t)blockIdx.x * 2 * DT + threadIdx.x;
+    const int64_t end = min(blocks, ((int64_t)blockIdx.x + 1) * 2 * DT);
     float x[8], add[8];
-    for (; b < whole; b += step) {
+    if (b + DT < whole) {
+        float x2[8], add2[8];
         load8<DTYPE>(a.x, b, x);
-        if (ADD) load8<DTYPE>(a.add, b, add);
-        drop8<ADD>(a, philox((uint64_t)b, seed, offset), x, add);
+        load8<DTYPE>(a.x, b + DT, x2);
+        if (ADD) {
+            load8<DTYPE>(a.add, b, add);
+            load8<DTYPE>(a.add, b + DT, add2);
+        }
+        uint4 r, r2;
+        philox2((uint64_t)b, (uint64_t)b + DT, seed, offset, r, r2);
+        drop8<ADD>(a, r, x, add);
+        drop8<ADD>(a, r2, x2, add2);
         store8<DTYPE>(a.y, b, x);
+        store8<DTYPE>(a.y, b + DT, x2);
+        return;
     }
-    // elements that are no whole aligned piece
+    // the last blocks, and elements that are no aligned pieces
 #pragma unroll 1
-    for (; b < blocks; b += step) {
+    for (; b < end; b += DT) {
         const int n = (int)min((int64_t)8, a.n - 8 * b);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             x[k] = k < n ? ld_elem(a.x, 8 * b + k, DTYPE) : 0.f;
             add[k] = ADD && k < n ? ld_elem(a.add, 8 * b + k, DTYPE) : 0.f;
         }
-        drop8<ADD>(a, philox((uint64_t)b, seed, offset), x, add);
+        uint4 bits, unused;
+        philox2((uint64_t)b, (uint64_t)b, seed, offset, bits, unused);
+        drop8<ADD>(a, bits, x, add);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             if (k < n) st_elem(a.y, 8 * b + k, x[k], DTYPE);
@@ -157,13 +178,13 @@ extern "C" int muon_dropout(const void* x, const void* residual, void* y, int64_
     a.cut = (uint32_t)cut << 16;
     a.scale = (float)(65536.0 / (65536.0 - cut));
     const bool vec = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(residual) | reinterpret_cast<uintptr_t>(y)) & 15) == 0;
-    const int64_t ctas = ((n + 7) / 8 + DT - 1) / DT;
+    const int64_t ctas = ((n + 7) / 8 + 2 * DT - 1) / (2 * DT);
     auto kern = dtype == MUON_F32    ? dropout_form<MUON_F32>(vec, residual != nullptr)
                 : dtype == MUON_BF16 ? dropout_form<MUON_BF16>(vec, residual != nullptr)
                                      : dropout_form<MUON_F16>(vec, residual != nullptr);
     note_launch_begin(KC_OTHER, s);
     const cudaError_t e = launch_pdl(kern,
-                                     dim3((unsigned)std::min<int64_t>(ctas, (int64_t)dc.sms * 8)), dim3(DT), 0, s, a);
+                                     dim3((unsigned)ctas), dim3(DT), 0, s, a);
     note_launch_end(KC_OTHER, 0.0, s);
     return e == cudaSuccess ? MUON_OK : cuda_fail(e, "dropout launch");
 } MUON_CATCH_ALL

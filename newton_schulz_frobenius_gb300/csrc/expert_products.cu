@@ -708,10 +708,20 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
                 const bool more = from + MAX_BLOCKS < t.blocks;
                 // this thread's running sums: its lane of the accumulator, 256 columns
                 float* part = g.part + ((size_t)blockIdx.x * GM + q * 32 + lane) * 256;
+                auto release = [&] {        // the accumulator has been read
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (rank == 1) mbar_arrive_remote(acce0 + 8 * acc, 0);
+                        else mbar_arrive(acce0 + 8 * acc);
+                    }
+                };
+                if (half >= chunks) release();
 #pragma unroll 1
                 for (int ch = half; ch < chunks; ch += 2) {
                     float v[32];
                     tmem_ld32(lanes + (uint32_t)(ch * 32), v);
+                    if (ch + 2 >= chunks) release();
                     float* at = part + ch * 32;
                     if (from) {
 #pragma unroll
@@ -730,12 +740,6 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
                     } else {
                         chunk(ch, v);
                     }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (rank == 1) mbar_arrive_remote(acce0 + 8 * acc, 0);
-                    else mbar_arrive(acce0 + 8 * acc);
                 }
                 acc ^= 1;
                 if (acc == 0) aphase ^= 1u;

@@ -31,7 +31,9 @@ constexpr int64_t MAX_HIDDEN = 1 << 20;
 // columns are summed over the CTA's warps and, through distributed shared
 // memory, over the cluster's CTAs before it, experts are summed in order, and a
 // second walk over the same slots hands out the places.  Within 32 slots equal
-// experts find each other by a match, so nothing depends on scheduling.
+// experts find each other by votes, so nothing depends on scheduling.  Bound by
+// latency: 4.8 us for 16384 slots and 64 experts, 8.0 for 65536, 12.6 for 131072
+// (back to back in a graph), beyond that by the sixteen SMs' scattered stores.
 constexpr int SORT_T = 1024;
 constexpr int SORT_WARPS = SORT_T / 32;
 constexpr int SORT_CLUSTER = 16;
@@ -50,8 +52,22 @@ struct SortArgs {
 __device__ __forceinline__ uint32_t ld_cluster(const uint32_t* p, uint32_t rank) {
     uint32_t a, v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
+}
+
+// Lanes with the same expert, by a vote on each of its bits (the instruction that
+// matches values takes its time for each different one: 65536 slots to 64 experts
+// 10.8 us with it).
+__device__ __forceinline__ uint32_t same_expert(int e, int bits) {
+    uint32_t same = 0xffffffffu;
+#pragma unroll 4
+    for (int b = 0; b < bits; ++b) {
+        const bool set = (e >> b) & 1;
+        const uint32_t m = __ballot_sync(0xffffffffu, set);
+        same &= set ? m : ~m;
+    }
+    return same;
 }
 
 // Expert of a slot: experts_n for none, -1 beyond the run's last slot.
@@ -81,14 +97,22 @@ __global__ void __launch_bounds__(SORT_T, 1) expert_sort_kernel(const __grid_con
     const int64_t first = ((int64_t)rank * SORT_WARPS + warp) * a.per_warp;
     const int64_t last = min(first + a.per_warp, (int64_t)a.slots);
     uint32_t* mine = table + warp * bins;
+    const int bits = 33 - __clz(E);         // of 0 .. E, and one that -1 alone has set
     int e[SORT_AHEAD];
-    for (int64_t i = first; i < last; i += 32 * SORT_AHEAD) {
+    uint32_t same[SORT_AHEAD];
+    auto read = [&](int64_t i) {
 #pragma unroll
         for (int r = 0; r < SORT_AHEAD; ++r) e[r] = expert_of(a, i + 32 * r + lane, last);
 #pragma unroll
+        for (int r = 0; r < SORT_AHEAD; ++r)
+            if (i + 32 * r < last) same[r] = same_expert(e[r], bits);
+    };
+    for (int64_t i = first; i < last; i += 32 * SORT_AHEAD) {
+        read(i);
+#pragma unroll
         for (int r = 0; r < SORT_AHEAD; ++r) {
-            const uint32_t same = __match_any_sync(0xffffffffu, e[r]);
-            if (e[r] >= 0 && lane == __ffs((int)same) - 1) mine[e[r]] += (uint32_t)__popc(same);
+            if (i + 32 * r >= last) break;
+            if (e[r] >= 0 && lane == __ffs((int)same[r]) - 1) mine[e[r]] += (uint32_t)__popc(same[r]);
             __syncwarp();
         }
     }
@@ -106,16 +130,19 @@ __global__ void __launch_bounds__(SORT_T, 1) expert_sort_kernel(const __grid_con
     }
     tc::cluster_sync();
     // all CTAs' counts of expert threadIdx.x, and those of the CTAs before this one
-    uint32_t all = 0, before = 0, rest = 0;
-    if ((int)threadIdx.x < E) {
-        for (int c = 0; c < C; ++c) {
-            const uint32_t n = ld_cluster(total + threadIdx.x, (uint32_t)c);
-            if (c < rank) before += n;
-            all += n;
+    uint32_t all = 0, before = 0, rest = 0, none = 0;
+    auto counts = [&](int bin, uint32_t& upto_here, uint32_t& of_all) {
+        uint32_t n[SORT_CLUSTER];           // all on their way before the first is used
+#pragma unroll
+        for (int c = 0; c < SORT_CLUSTER; ++c) n[c] = c < C ? ld_cluster(total + bin, (uint32_t)c) : 0;
+#pragma unroll
+        for (int c = 0; c < SORT_CLUSTER; ++c) {
+            if (c < rank) upto_here += n[c];
+            of_all += n[c];
         }
-    }
-    if (threadIdx.x == 0)
-        for (int c = 0; c < rank; ++c) rest += ld_cluster(total + E, (uint32_t)c);
+    };
+    if ((int)threadIdx.x < E) counts(threadIdx.x, before, all);
+    if (threadIdx.x == SORT_T - 1) counts(E, rest, none);
     __syncwarp();
     tc::cluster_sync();                 // the others have read this CTA's counts
     uint32_t upto = all;                // inclusive sum over experts
@@ -139,24 +166,19 @@ __global__ void __launch_bounds__(SORT_T, 1) expert_sort_kernel(const __grid_con
         total[threadIdx.x] = upto - all + before;
         if (rank == 0) a.bounds[threadIdx.x + 1] = (int)upto;
     }
-    if (threadIdx.x == 0) {
-        total[E] = sums[SORT_WARPS - 1] + rest;
-        if (rank == 0) a.bounds[0] = 0;
-    }
+    if (threadIdx.x == SORT_T - 1) total[E] = sums[SORT_WARPS - 1] + rest;
+    if (threadIdx.x == 0 && rank == 0) a.bounds[0] = 0;
     __syncthreads();
     for (int64_t i = first; i < last; i += 32 * SORT_AHEAD) {
-        if (a.per_warp > 32 * SORT_AHEAD) {     // else the first walk's are still here
-#pragma unroll
-            for (int r = 0; r < SORT_AHEAD; ++r) e[r] = expert_of(a, i + 32 * r + lane, last);
-        }
+        if (a.per_warp > 32 * SORT_AHEAD) read(i);      // else the first walk's are still here
 #pragma unroll
         for (int r = 0; r < SORT_AHEAD; ++r) {
-            const uint32_t same = __match_any_sync(0xffffffffu, e[r]);
+            if (i + 32 * r >= last) break;
             const uint32_t at = e[r] >= 0 ? mine[e[r]] : 0;
             __syncwarp();
             if (e[r] >= 0) {
-                if (lane == __ffs((int)same) - 1) mine[e[r]] = at + (uint32_t)__popc(same);
-                const int row = (int)(total[e[r]] + at + (uint32_t)__popc(same & ((1u << lane) - 1)));
+                if (lane == __ffs((int)same[r]) - 1) mine[e[r]] = at + (uint32_t)__popc(same[r]);
+                const int row = (int)(total[e[r]] + at + (uint32_t)__popc(same[r] & ((1u << lane) - 1)));
                 a.row_of[i + 32 * r + lane] = row;
                 a.slot_of[row] = (int)(i + 32 * r + lane);
             }
@@ -181,11 +203,13 @@ struct RowArgs {
     int64_t tokens;
     int k, hidden, experts_n;
     int dtype;
-    int pieces;                 // 16-byte pieces of a row
-    int group;                  // backward: warps that share a row
+    int slots;                  // of a row: 16-byte pieces, or 4-byte words that it can touch
+    int span;                   // dispatch, combine: slots of a warp
+    int group;                  // backward: warps that share a token's rows, a power of two
 };
 
 constexpr int RT = 256;
+constexpr int J = 4;                // slots of a token that a warp of the backward pass works at once
 
 // Rows of live slots: those before the last expert's end.
 __device__ __forceinline__ int live_rows(const RowArgs& a) {
@@ -193,37 +217,115 @@ __device__ __forceinline__ int live_rows(const RowArgs& a) {
     return (int)min((int64_t)max(a.bounds[a.experts_n], 0), rows);
 }
 
-// Piece c (16 bytes) of a row that starts at element e.
-template <int ES, bool VEC>
-__device__ __forceinline__ uint4 load_piece(const void* p, int64_t e, int c, int hidden) {
-    constexpr int V = 16 / ES;
-    if (VEC) return reinterpret_cast<const uint4*>(static_cast<const char*>(p) + e * ES)[c];
-    uint32_t w[4] = {0, 0, 0, 0};
-    const int n = min(V, hidden - c * V);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        if (i >= n) break;
-        if (ES == 4) w[i % 4] = static_cast<const uint32_t*>(p)[e + c * V + i];
-        else w[i / 2] |= (uint32_t)static_cast<const uint16_t*>(p)[e + c * V + i] << (16 * (i & 1));
+// Rows that start on 16 bytes are read and written as pieces of 16 bytes, others as
+// the aligned 4-byte words that their elements fall into, 32 neighbours per warp
+// and access: as few wavefronts, four times the instructions, but none to shift
+// 16 bytes into place (16384 tokens, 4 rows of 1001 bf16 each: combine 86 us with
+// aligned 16-byte loads shifted through the neighbour lane).
+//
+// Word i of a row of 16-bit elements holds columns 2 i - p and 2 i - p + 1, where p is
+// 1 if the row starts in the middle of a word; first and last words may hold columns
+// of other rows.
+template <int ES>
+struct Words {
+    static constexpr int E = 4 / ES, U = 4;     // elements of a word, words of a lane at once (32 apart)
+    uint32_t* p;                // the word that holds the row's first element
+    int odd, count;             // words that hold columns of the row
+    bool half;                  // the last one holds a column of another row too
+    bool whole;                 // every word is in the matrix and may be read
+    __device__ __forceinline__ Words(const void* base, int64_t n, int64_t e, int hidden) {
+        char* at = static_cast<char*>(const_cast<void*>(base)) + e * ES;
+        odd = ES == 2 ? (int)(reinterpret_cast<uintptr_t>(at) & 2) / 2 : 0;
+        p = reinterpret_cast<uint32_t*>(at - odd * ES);
+        count = (hidden + odd + E - 1) / E;
+        half = ES == 2 && ((hidden + odd) & 1);
+        whole = (e > 0 || !odd) && (e + hidden < n || !half);
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    __device__ __forceinline__ bool has(int i) const { return (uint32_t)i < (uint32_t)count; }
+    // At one of the matrix' two ends: a word, from its elements in the matrix.
+    __device__ __forceinline__ uint32_t load_end(int i) const {
+        if (!has(i)) return 0;
+        const uint16_t* at = reinterpret_cast<const uint16_t*>(p + i);
+        const uint32_t lo = i == 0 && odd ? 0 : at[0], hi = i == count - 1 && half ? 0 : at[1];
+        return lo | hi << 16;
+    }
+    // The words with the columns that words i, i + 32 .. of a row of parity `as` hold.
+    __device__ __forceinline__ void load(uint32_t (&q)[U], int i, int as) const {
+        if (ES == 4 || (whole && odd == as)) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) q[u] = has(i + 32 * u) ? p[i + 32 * u] : 0;
+            return;
+        }
+        const int k = odd == as ? i : odd ? i : i - 1;      // then the first of two words each
+        if (whole) {
+            uint32_t next[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                q[u] = has(k + 32 * u) ? p[k + 32 * u] : 0;
+                next[u] = has(k + 32 * u + 1) ? p[k + 32 * u + 1] : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) q[u] = __funnelshift_r(q[u], next[u], 16);
+            return;
+        }
+#pragma unroll 1
+        for (int u = 0; u < U; ++u) {
+            const uint32_t a = load_end(k + 32 * u), b = load_end(k + 32 * u + 1);
+            const uint32_t v = odd == as ? a : __funnelshift_r(a, b, 16);
+            if (u == 0) q[0] = v;
+            else if (u == 1) q[1] = v;
+            else if (u == 2) q[2] = v;
+            else q[3] = v;
+        }
+    }
+    __device__ __forceinline__ void store(int i, const uint32_t (&v)[U]) const {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = i + 32 * u;
+            if (!has(k)) continue;
+            if (ES == 2 && k == 0 && odd) reinterpret_cast<uint16_t*>(p)[1] = (uint16_t)(v[u] >> 16);
+            else if (ES == 2 && k == count - 1 && half) *reinterpret_cast<uint16_t*>(p + k) = (uint16_t)v[u];
+            else __stcs(p + k, v[u]);
+        }
+    }
+};
+
+template <int ES>
+__device__ __forceinline__ void word_floats(uint32_t q, float (&v)[4 / ES], bool f16) {
+    if constexpr (ES == 4) {
+        v[0] = __uint_as_float(q);
+    } else {
+        const float2 f = f16 ? __half22float2(*reinterpret_cast<const __half2*>(&q))
+                             : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&q));
+        v[0] = f.x;
+        v[1] = f.y;
+    }
 }
 
-template <int ES, bool VEC>
-__device__ __forceinline__ void store_piece(void* p, int64_t e, int c, int hidden, const uint4& q) {
-    constexpr int V = 16 / ES;
-    if (VEC) {
-        reinterpret_cast<uint4*>(static_cast<char*>(p) + e * ES)[c] = q;
-        return;
+template <int ES>
+__device__ __forceinline__ uint32_t word_of(const float (&v)[4 / ES], bool f16) {
+    if constexpr (ES == 4) {
+        return __float_as_uint(v[0]);
+    } else if (f16) {
+        const __half2 h = __floats2half2_rn(v[0], v[1]);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[0], v[1]);
+        return *reinterpret_cast<const uint32_t*>(&h);
     }
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    const int n = min(V, hidden - c * V);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        if (i >= n) break;
-        if (ES == 4) static_cast<uint32_t*>(p)[e + c * V + i] = w[i % 4];
-        else static_cast<uint16_t*>(p)[e + c * V + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
-    }
+}
+
+__device__ __forceinline__ uint4 no_piece() { return make_uint4(0, 0, 0, 0); }
+
+// Piece c of a row on 16 bytes that starts at element e.
+template <int ES>
+__device__ __forceinline__ const uint4* piece(const void* p, int64_t e, int c) {
+    return reinterpret_cast<const uint4*>(static_cast<const char*>(p) + e * ES) + c;
+}
+template <int ES>
+__device__ __forceinline__ void put_piece(void* p, int64_t e, int c, const uint4& q) {
+    // (rows leave the caches to what is read again)
+    __stcs(reinterpret_cast<uint4*>(static_cast<char*>(p) + e * ES) + c, q);
 }
 
 template <int ES>
@@ -244,7 +346,15 @@ __device__ __forceinline__ uint4 from_floats(const float (&v)[16 / ES], bool f16
     else return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
 }
 
-// A warp takes one token and a run of its pieces, reads them once and writes
+// Indices (and weights) of 32 choices of a token from j0 on, a lane each, so that
+// nothing waits for one at a time.
+__device__ __forceinline__ int rows_of(const RowArgs& a, int64_t t, int j0, int64_t rows) {
+    const int j = j0 + (threadIdx.x & 31);
+    const int r = j < a.k ? a.row_of[t * a.k + j] : -1;
+    return r < rows ? r : -1;
+}
+
+// A warp takes one token and some runs of its slots, reads them once and writes
 // them to the token's k rows.
 template <int ES, bool VEC>
 __global__ void __launch_bounds__(RT) dispatch_kernel(const __grid_constant__ RowArgs a) {
@@ -252,120 +362,216 @@ __global__ void __launch_bounds__(RT) dispatch_kernel(const __grid_constant__ Ro
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, live = live_rows(a);
-    const int runs = (a.pieces + 32 * U - 1) / (32 * U);
-    const int64_t rows = a.tokens * a.k, items = a.tokens * runs;
-    for (int64_t i = (int64_t)blockIdx.x * (RT / 32) + (threadIdx.x >> 5); i < items; i += (int64_t)gridDim.x * (RT / 32)) {
-        const int64_t t = i / runs;
-        const int c0 = (int)(i - t * runs) * 32 * U + lane;
-        uint4 q[U];
+    const int64_t t = (int64_t)blockIdx.x * (RT / 32) + (threadIdx.x >> 5), rows = a.tokens * a.k;
+    if (t >= a.tokens) return;
+    const int begin = blockIdx.y * a.span, end = min(a.slots, begin + a.span);
+    for (int j0 = 0; j0 < a.k; j0 += 32) {
+        const int some = min(32, a.k - j0), mine = rows_of(a, t, j0, rows);
+        for (int c = begin + lane; c - lane < end; c += 32 * U) {
+            if constexpr (VEC) {
+                uint4 q[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (c0 + 32 * u < a.pieces) q[u] = load_piece<ES, VEC>(a.x, t * a.ldx, c0 + 32 * u, a.hidden);
-        for (int j = 0; j < a.k; ++j) {
-            const int64_t r = a.row_of[t * a.k + j];
-            if (r < 0 || r >= rows) continue;
+                for (int u = 0; u < U; ++u)
+                    if (c + 32 * u < a.slots) q[u] = *piece<ES>(a.x, t * a.ldx, c + 32 * u);
+#pragma unroll 4
+                for (int j = 0; j < some; ++j) {
+                    const int64_t r = __shfl_sync(0xffffffffu, mine, j);
+                    if (r < 0) continue;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (c0 + 32 * u < a.pieces)
-                    store_piece<ES, VEC>(a.out, r * a.hidden, c0 + 32 * u, a.hidden,
-                                         r < live ? q[u] : make_uint4(0, 0, 0, 0));
+                    for (int u = 0; u < U; ++u)
+                        if (c + 32 * u < a.slots) put_piece<ES>(a.out, r * a.hidden, c + 32 * u, r < live ? q[u] : no_piece());
+                }
+            } else {
+                const Words<ES> in(a.x, (a.tokens - 1) * a.ldx + a.hidden, t * a.ldx, a.hidden);
+                uint32_t q[2][U];           // for rows of either parity
+                const uint32_t zeros[U] = {0, 0, 0, 0};
+                in.load(q[0], c, 0);
+                if (ES == 2) in.load(q[1], c, 1);
+#pragma unroll 2
+                for (int j = 0; j < some; ++j) {
+                    const int64_t r = __shfl_sync(0xffffffffu, mine, j);
+                    if (r < 0) continue;
+                    const Words<ES> out(a.out, rows * a.hidden, r * a.hidden, a.hidden);
+                    if (r >= live) out.store(c, zeros);
+                    else if (ES == 2 && out.odd) out.store(c, q[1]);
+                    else out.store(c, q[0]);
+                }
+            }
         }
     }
 }
 
-// A warp takes one token and a run of its pieces and sums the token's k rows
-// there in fp32, in the order of the choices; one rounding.
+// A warp takes one token and some runs of its slots and sums the token's k rows
+// there in fp32, in the order of the choices; one rounding.  Bound by latency, so
+// by warps: 8192 tokens, 8 rows of 2048 bf16 each: 60 us at eight CTAs per SM, 69
+// at six, 71 at three with twice the loads in flight per warp.
 template <int ES, bool VEC>
-__global__ void __launch_bounds__(RT) combine_kernel(const __grid_constant__ RowArgs a) {
-    constexpr int V = 16 / ES;
+__global__ void __launch_bounds__(RT, VEC ? 8 : 5) combine_kernel(const __grid_constant__ RowArgs a) {
+    constexpr int V = VEC ? 16 / ES : 4 / ES, U = VEC ? 1 : 4;      // elements of a slot, slots of a lane
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, live = live_rows(a);
     const bool f16 = a.dtype == MUON_F16;
-    const int runs = (a.pieces + 31) / 32;
-    const int64_t items = a.tokens * runs;
-    for (int64_t i = (int64_t)blockIdx.x * (RT / 32) + (threadIdx.x >> 5); i < items; i += (int64_t)gridDim.x * (RT / 32)) {
-        const int64_t t = i / runs;
-        const int c = (int)(i - t * runs) * 32 + lane;
-        if (c >= a.pieces) continue;
-        float acc[V], v[V];
+    const int64_t t = (int64_t)blockIdx.x * (RT / 32) + (threadIdx.x >> 5), rows = a.tokens * a.k;
+    if (t >= a.tokens) return;
+    const Words<ES> out(a.out, a.tokens * a.hidden, t * a.hidden, a.hidden);
+    const int begin = blockIdx.y * a.span, end = min(a.slots, begin + a.span);
+    const int first = rows_of(a, t, 0, live);
+    const float first_weight = a.weights && lane < a.k ? a.weights[t * a.k + lane] : 1.f;
+    for (int c = begin + lane; c - lane < end; c += 32 * U) {
+        float acc[U][V], v[V];
 #pragma unroll
-        for (int n = 0; n < V; ++n) acc[n] = 0.f;
-        if (a.y) to_floats<ES>(load_piece<ES, VEC>(a.y, t * a.ldy, c, a.hidden), acc, f16);
-#pragma unroll 4
-        for (int j = 0; j < a.k; ++j) {
-            const int r = a.row_of[t * a.k + j];
-            if (r < 0 || r >= live) continue;
-            const float w = a.weights ? a.weights[t * a.k + j] : 1.f;
-            to_floats<ES>(load_piece<ES, VEC>(a.x, (int64_t)r * a.hidden, c, a.hidden), v, f16);
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int n = 0; n < V; ++n) acc[n] = fmaf(w, v[n], acc[n]);
+            for (int k = 0; k < V; ++k) acc[u][k] = 0.f;
+        if (a.y) {
+            if constexpr (VEC) {
+                if (c < a.slots) to_floats<ES>(*piece<ES>(a.y, t * a.ldy, c), acc[0], f16);
+            } else {
+                const Words<ES> add(a.y, (a.tokens - 1) * a.ldy + a.hidden, t * a.ldy, a.hidden);
+                uint32_t q[U];
+                add.load(q, c, out.odd);
+#pragma unroll
+                for (int u = 0; u < U; ++u) word_floats<ES>(q[u], acc[u], f16);
+            }
         }
-        store_piece<ES, VEC>(a.out, t * a.hidden, c, a.hidden, from_floats<ES>(acc, f16));
+        for (int j0 = 0; j0 < a.k; j0 += 32) {
+            int mine = first;
+            float weight = first_weight;
+            if (j0) {
+                mine = rows_of(a, t, j0, live);
+                weight = a.weights && j0 + lane < a.k ? a.weights[t * a.k + j0 + lane] : 1.f;
+            }
+            const int some = min(32, a.k - j0);
+#pragma unroll(VEC ? 4 : 2)
+            for (int j = 0; j < some; ++j) {
+                const int r = __shfl_sync(0xffffffffu, mine, j);
+                const float w = __shfl_sync(0xffffffffu, weight, j);
+                if (r < 0) continue;
+                if constexpr (VEC) {
+                    if (c >= a.slots) continue;
+                    to_floats<ES>(*piece<ES>(a.x, (int64_t)r * a.hidden, c), v, f16);
+#pragma unroll
+                    for (int k = 0; k < V; ++k) acc[0][k] = fmaf(w, v[k], acc[0][k]);
+                } else {
+                    const Words<ES> in(a.x, rows * a.hidden, (int64_t)r * a.hidden, a.hidden);
+                    uint32_t q[U];
+                    in.load(q, c, out.odd);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        word_floats<ES>(q[u], v, f16);
+#pragma unroll
+                        for (int k = 0; k < V; ++k) acc[u][k] = fmaf(w, v[k], acc[u][k]);
+                    }
+                }
+            }
+        }
+        if constexpr (VEC) {
+            if (c < a.slots) put_piece<ES>(a.out, t * a.hidden, c, from_floats<ES>(acc[0], f16));
+        } else {
+            uint32_t q[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) q[u] = word_of<ES>(acc[u], f16);
+            out.store(c, q);
+        }
     }
 }
 
-// `group` warps share a slot's row: they read it beside its token's dy (which
-// the slots of a token, neighbours in a CTA, take from L1), write w dy, and sum
-// the products in a fixed order.
+// `group` warps share J slots of a token: they read its dy once and the slots'
+// rows beside it, write w dy, and sum the products in a fixed order.
 template <int ES, bool VEC>
-__global__ void __launch_bounds__(RT) combine_backward_kernel(const __grid_constant__ RowArgs a) {
-    constexpr int V = 16 / ES, U = 2;
-    __shared__ float part[RT / 32];
+__global__ void __launch_bounds__(RT, 4) combine_backward_kernel(const __grid_constant__ RowArgs a) {
+    constexpr int V = VEC ? 16 / ES : 4 / ES, U = VEC ? 1 : 4;
+    __shared__ float part[RT / 32][J];
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, live = live_rows(a);
     const bool f16 = a.dtype == MUON_F16;
-    const int G = a.group, per = RT / 32 / G, place = warp % G;
-    const int64_t rows = a.tokens * a.k;
-    for (int64_t s0 = (int64_t)blockIdx.x * per; s0 < rows; s0 += (int64_t)gridDim.x * per) {
-        const int64_t s = s0 + warp / G;
-        float dot = 0.f;
-        const int64_t r = s < rows ? a.row_of[s] : -1;
-        if (r >= 0 && r < rows) {
-            const bool on = r < live;
-            const int64_t t = s / a.k;
-            const float w = on ? a.weights[s] : 0.f;
-            for (int c0 = place * 32 + lane; c0 < a.pieces; c0 += 32 * G * U) {
-                uint4 qd[U], qy[U];
+    const int G = a.group, place = warp & (G - 1);
+    const int64_t rows = a.tokens * a.k, n = rows * a.hidden;
+    const int64_t t = (int64_t)blockIdx.x * (RT / 32 / G) + warp / G, s = t * a.k + blockIdx.y * J;    // the first slot
+    const int some = t < a.tokens ? min(J, a.k - (int)blockIdx.y * J) : 0;
+    int r[J];
+    float w[J], dot[J];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int c = c0 + 32 * G * u;
-                    if (!on || c >= a.pieces) continue;
-                    qd[u] = load_piece<ES, VEC>(a.y, t * a.ldy, c, a.hidden);
-                    qy[u] = load_piece<ES, VEC>(a.x, r * a.hidden, c, a.hidden);
+    for (int j = 0; j < J; ++j) {
+        r[j] = j < some ? a.row_of[s + j] : -1;
+        if (r[j] >= rows) r[j] = -1;
+        w[j] = r[j] >= 0 && r[j] < live ? a.weights[s + j] : 0.f;
+        dot[j] = 0.f;
+    }
+    for (int c = place * 32 * U + lane; some > 0 && c - lane < a.slots; c += 32 * U * G) {
+        if constexpr (VEC) {
+            uint4 qd, qy[J];
+            if (c >= a.slots) break;
+            qd = *piece<ES>(a.y, t * a.ldy, c);
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                qy[j] = r[j] >= 0 && r[j] < live ? *piece<ES>(a.x, (int64_t)r[j] * a.hidden, c) : no_piece();
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (r[j] < 0) continue;
+                float d[V], y[V];
+                to_floats<ES>(qd, d, f16);
+                to_floats<ES>(qy[j], y, f16);
+                const bool on = r[j] < live;
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    if (on) dot[j] = fmaf(d[k], y[k], dot[j]);
+                    d[k] *= w[j];
                 }
+                put_piece<ES>(a.out, (int64_t)r[j] * a.hidden, c, on ? from_floats<ES>(d, f16) : no_piece());
+            }
+        } else {
+            const Words<ES> dy(a.y, (a.tokens - 1) * a.ldy + a.hidden, t * a.ldy, a.hidden);
+            uint32_t qd[2][U];              // for rows of either parity
+            dy.load(qd[0], c, 0);
+            if (ES == 2) dy.load(qd[1], c, 1);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (r[j] < 0) continue;
+                const bool on = r[j] < live;
+                const Words<ES> in(a.x, n, (int64_t)r[j] * a.hidden, a.hidden), out(a.out, n, (int64_t)r[j] * a.hidden, a.hidden);
+                uint32_t q[U];
+                if (on) in.load(q, c, out.odd);
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int c = c0 + 32 * G * u;
-                    if (c >= a.pieces) continue;
                     float d[V], y[V];
-#pragma unroll
-                    for (int n = 0; n < V; ++n) d[n] = 0.f;
-                    if (on) {
-                        to_floats<ES>(qd[u], d, f16);
-                        to_floats<ES>(qy[u], y, f16);
-#pragma unroll
-                        for (int n = 0; n < V; ++n) {
-                            dot = fmaf(d[n], y[n], dot);
-                            d[n] *= w;
-                        }
+                    if (!on) q[u] = 0;
+                    word_floats<ES>(ES == 2 && out.odd ? qd[1][u] : qd[0][u], d, f16);
+                    word_floats<ES>(q[u], y, f16);
+                    if (ES == 2) {          // columns of other rows in a first or last word, and behind it
+                        const int k = c + 32 * u;
+                        if (k >= out.count || (k == 0 && out.odd)) y[0] = d[0] = 0.f;
+                        if (k >= out.count || (k == out.count - 1 && out.half)) y[V - 1] = d[V - 1] = 0.f;
                     }
-                    store_piece<ES, VEC>(a.out, r * a.hidden, c, a.hidden, from_floats<ES>(d, f16));
+#pragma unroll
+                    for (int k = 0; k < V; ++k) {
+                        if (on) dot[j] = fmaf(d[k], y[k], dot[j]);
+                        d[k] *= w[j];
+                    }
+                    q[u] = on ? word_of<ES>(d, f16) : 0;
                 }
+                out.store(c, q);
             }
         }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-        if (G > 1) {
-            __syncthreads();
-            if (lane == 0) part[warp] = dot;
-            __syncthreads();
-            dot = 0.f;
-            for (int g = 0; g < G; ++g) dot += part[warp / G * G + g];
-        }
-        if (s < rows && place == 0 && lane == 0) a.dweights[s] = dot;
     }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+#pragma unroll
+        for (int d = 16; d; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
+    }
+    if (G > 1) {
+        __syncthreads();
+        if (lane < J) part[warp][lane] = lane == 0 ? dot[0] : lane == 1 ? dot[1] : lane == 2 ? dot[2] : dot[3];
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            dot[j] = 0.f;
+            for (int g = 0; g < G; ++g) dot[j] += part[warp / G * G + g][j];
+        }
+    }
+    if (place == 0 && lane < some) a.dweights[s + lane] = lane == 0 ? dot[0] : lane == 1 ? dot[1] : lane == 2 ? dot[2] : dot[3];
 }
 
 // ---------------------------------------------------------------------------
@@ -395,17 +601,30 @@ RowArgs row_args(int64_t tokens, int64_t k, int64_t hidden, int dtype, const int
     std::memset(&a, 0, sizeof a);
     a.tokens = tokens; a.k = (int)k; a.hidden = (int)hidden; a.dtype = dtype;
     a.row_of = row_of; a.bounds = bounds; a.experts_n = (int)experts_n;
-    a.pieces = (int)((hidden * (int64_t)esize(dtype) + 15) / 16);
     return a;
 }
 
+// Slots of a row: its pieces, or its words, one more where it may start inside one.
+int slots_of(const RowArgs& a, bool vec) {
+    const int es = (int)esize(a.dtype);
+    return vec ? (int)((int64_t)a.hidden * es / 16) : es == 4 ? a.hidden : a.hidden / 2 + 1;
+}
+
 template <typename K>
-int launch_rows(K kernel, const RowArgs& a, int64_t ctas, int sms, cudaStream_t s, const char* what) {
+int launch_rows(K kernel, const RowArgs& a, int64_t x, int64_t y, cudaStream_t s, const char* what) {
     note_launch_begin(KC_OTHER, s);
-    const cudaError_t e = launch_pdl(kernel, dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(ctas, (int64_t)sms * 8))),
-                                     dim3(RT), 0, s, a);
+    const cudaError_t e = launch_pdl(kernel, dim3((unsigned)x, (unsigned)y), dim3(RT), 0, s, a);
     note_launch_end(KC_OTHER, 0.0, s);
     return e == cudaSuccess ? MUON_OK : cuda_fail(e, what);
+}
+
+// A token's row in steps of a warp: one warp takes them all once the tokens fill the device.
+template <typename K>
+int launch_token_rows(K kernel, RowArgs& a, int step, int sms, cudaStream_t s, const char* what) {
+    const int steps = (a.slots + step - 1) / step;
+    const int each = (int)std::max<int64_t>(1, std::min<int64_t>(steps, a.tokens * steps / ((int64_t)sms * 64)));
+    a.span = each * step;
+    return launch_rows(kernel, a, (a.tokens + RT / 32 - 1) / (RT / 32), (steps + each - 1) / each, s, what);
 }
 
 }  // namespace
@@ -427,8 +646,8 @@ extern "C" int muon_expert_sort(const void* experts, int index_dtype, int64_t sl
     DevCtx dc;
     if ((r = get_dev(dc))) return r;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    int C = 1;                              // CTAs: four slots per thread until the cluster is full
-    while (C < SORT_CLUSTER && (int64_t)C * SORT_T * 4 < slots) C *= 2;
+    int C = 1;                              // CTAs: a slot per thread until the cluster is full
+    while (C < SORT_CLUSTER && (int64_t)C * SORT_T < slots) C *= 2;
     SortArgs a;
     a.experts = experts;
     a.index64 = index_dtype == MUON_I64;
@@ -480,10 +699,10 @@ extern "C" int muon_expert_dispatch(const void* x, int64_t ldx, int64_t tokens, 
     a.x = x; a.ldx = ldx; a.out = xs;
     const int es = (int)esize(dtype);
     const bool vec = aligned16(x) && aligned16(xs) && (ldx * es) % 16 == 0 && (hidden * es) % 16 == 0;
-    const int64_t ctas = (tokens * ((a.pieces + 127) / 128) + 7) / 8;
+    a.slots = slots_of(a, vec);
     auto kern = es == 2 ? (vec ? dispatch_kernel<2, true> : dispatch_kernel<2, false>)
                         : (vec ? dispatch_kernel<4, true> : dispatch_kernel<4, false>);
-    return launch_rows(kern, a, ctas, dc.sms, s, "expert dispatch launch");
+    return launch_token_rows(kern, a, 128, dc.sms, s, "expert dispatch launch");
 } MUON_CATCH_ALL
 
 extern "C" int muon_expert_combine(const void* ys, int64_t tokens, int64_t k, int64_t hidden, int dtype,
@@ -503,10 +722,10 @@ extern "C" int muon_expert_combine(const void* ys, int64_t tokens, int64_t k, in
     const int es = (int)esize(dtype);
     const bool vec = aligned16(ys) && aligned16(y) && aligned16(residual) && (hidden * es) % 16 == 0 &&
                      (!residual || (ld_residual * es) % 16 == 0);
-    const int64_t ctas = (tokens * ((a.pieces + 31) / 32) + 7) / 8;
+    a.slots = slots_of(a, vec);
     auto kern = es == 2 ? (vec ? combine_kernel<2, true> : combine_kernel<2, false>)
                         : (vec ? combine_kernel<4, true> : combine_kernel<4, false>);
-    return launch_rows(kern, a, ctas, dc.sms, s, "expert combine launch");
+    return launch_token_rows(kern, a, vec ? 32 : 128, dc.sms, s, "expert combine launch");
 } MUON_CATCH_ALL
 
 extern "C" int muon_expert_combine_backward(const void* dy, int64_t ld_dy, const void* ys, int64_t tokens, int64_t k,
@@ -527,11 +746,12 @@ extern "C" int muon_expert_combine_backward(const void* dy, int64_t ld_dy, const
     a.x = ys; a.y = dy; a.ldy = ld_dy; a.out = dys; a.weights = weights; a.dweights = dweights;
     const int es = (int)esize(dtype);
     const bool vec = aligned16(dy) && aligned16(ys) && aligned16(dys) && (hidden * es) % 16 == 0 && (ld_dy * es) % 16 == 0;
-    const int64_t slots = tokens * k;
-    a.group = 1;                            // more warps to a row while rows are too few to fill the device
-    while (a.group < RT / 32 && slots * a.group < (int64_t)dc.sms * 16 && a.group * 64 < a.pieces) a.group *= 2;
+    a.slots = slots_of(a, vec);
+    const int64_t items = tokens * ((k + 3) / 4);
+    a.group = 1;                            // more warps to a token while tokens are too few to fill the device
+    while (a.group < RT / 32 && items * a.group < (int64_t)dc.sms * 16 && a.group * (vec ? 32 : 128) < a.slots) a.group *= 2;
     const int per = RT / 32 / a.group;
     auto kern = es == 2 ? (vec ? combine_backward_kernel<2, true> : combine_backward_kernel<2, false>)
                         : (vec ? combine_backward_kernel<4, true> : combine_backward_kernel<4, false>);
-    return launch_rows(kern, a, (slots + per - 1) / per, dc.sms, s, "expert combine backward launch");
+    return launch_rows(kern, a, (tokens + per - 1) / per, (k + 3) / 4, s, "expert combine backward launch");
 } MUON_CATCH_ALL
