@@ -764,12 +764,19 @@ def muon_glu_backward(x, w_gate, w_up, gate, up, dh, act: str = "silu", need_dx:
 
 def _one_device(first, *others):
     """Every tensor given is on the current device (the one whose stream the call takes)."""
-    import torch
-    dev = first.device
-    if dev.type != "cuda" or any(t is not None and t.device != dev for t in others):
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors must be on one CUDA device")
+    if dev < 0:
         raise ValueError("tensors must be on one CUDA device")
-    if dev.index is not None and dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    if _raw_stream is None:
+        import torch
+        current = torch.cuda.current_device()
+    else:
+        current = _raw_stream[1]()
+    if dev != current:
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{current}")
 
 
 def _route(row_of, bounds):

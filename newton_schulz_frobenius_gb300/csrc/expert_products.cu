@@ -864,9 +864,9 @@ int set_family_b(ExpMaps& maps, ExpArgs& g, const Operand* const* ops, int n, ch
     return e == cudaSuccess ? MUON_OK : cuda_fail(e, "expert tails launch");
 }
 
-// Rows as family a's N side.
+// Rows as family a's N side, in the boxes that experts of no more than all rows take.
 bool map_rows(CUtensorMap (&m)[BOXES], const Operand& o, int dtype) {
-    for (int i = 0; i < BOXES; ++i)
+    for (int i = 0; i < BOXES && (i == 0 || 2 * box_rows(i - 1) < o.rows); ++i)
         if (!map_in(&m[i], o, dtype, GK, (uint32_t)box_rows(i))) return false;
     return true;
 }
