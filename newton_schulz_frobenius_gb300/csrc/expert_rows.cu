@@ -223,72 +223,75 @@ __device__ __forceinline__ int live_rows(const RowArgs& a) {
 // 16 bytes into place (16384 tokens, 4 rows of 1001 bf16 each: combine 86 us with
 // aligned 16-byte loads shifted through the neighbour lane).
 //
-// Word i of a row of 16-bit elements holds columns 2 i - p and 2 i - p + 1, where p is
-// 1 if the row starts in the middle of a word; first and last words may hold columns
-// of other rows.
+// Word i of a row of 16-bit elements holds columns 2 i - odd and 2 i - odd + 1, odd = 1 if
+// the row starts in the middle of a word.  Words whose columns are all the row's
+// go 128 at a time per warp, four to a lane, without a question about the ends;
+// a first or last column that shares its word with another row is an edge, worked
+// by itself (edges: instructions are what bounds short rows).
 template <int ES>
 struct Words {
     static constexpr int E = 4 / ES, U = 4;     // elements of a word, words of a lane at once (32 apart)
-    uint32_t* p;                // the word that holds the row's first element
-    int odd, count;             // words that hold columns of the row
-    bool half;                  // the last one holds a column of another row too
-    bool whole;                 // every word is in the matrix and may be read
-    __device__ __forceinline__ Words(const void* base, int64_t n, int64_t e, int hidden) {
-        char* at = static_cast<char*>(const_cast<void*>(base)) + e * ES;
-        odd = ES == 2 ? (int)(reinterpret_cast<uintptr_t>(at) & 2) / 2 : 0;
-        p = reinterpret_cast<uint32_t*>(at - odd * ES);
-        count = (hidden + odd + E - 1) / E;
-        half = ES == 2 && ((hidden + odd) & 1);
-        whole = (e > 0 || !odd) && (e + hidden < n || !half);
+    char* row;                  // the first element
+    int odd, end, hidden;       // whole words: [odd, end)
+    bool inside;                // words around its ends are in the matrix too
+    __device__ __forceinline__ Words(const void* base, int64_t n, int64_t e, int h) : hidden(h) {
+        row = static_cast<char*>(const_cast<void*>(base)) + e * ES;
+        odd = ES == 2 ? (int)(reinterpret_cast<uintptr_t>(row) & 2) / 2 : 0;
+        end = (h + odd) / E;
+        inside = (e > 0 || !odd) && (e + h < n || end * E == h + odd);
     }
-    __device__ __forceinline__ bool has(int i) const { return (uint32_t)i < (uint32_t)count; }
-    // At one of the matrix' two ends: a word, from its elements in the matrix.
-    __device__ __forceinline__ uint32_t load_end(int i) const {
-        if (!has(i)) return 0;
-        const uint16_t* at = reinterpret_cast<const uint16_t*>(p + i);
-        const uint32_t lo = i == 0 && odd ? 0 : at[0], hi = i == count - 1 && half ? 0 : at[1];
-        return lo | hi << 16;
-    }
-    // The words with the columns that words i, i + 32 .. of a row of parity `as` hold.
-    __device__ __forceinline__ void load(uint32_t (&q)[U], int i, int as) const {
-        if (ES == 4 || (whole && odd == as)) {
+    __device__ __forceinline__ uint32_t* words() const { return reinterpret_cast<uint32_t*>(row - odd * ES); }
+    // Which of words i, i + 32 .. are whole ones of a row of parity `as`, a bit each.
+    static __device__ __forceinline__ uint32_t whole(int i, int as, int hidden) {
+        uint32_t m = 0;
 #pragma unroll
-            for (int u = 0; u < U; ++u) q[u] = has(i + 32 * u) ? p[i + 32 * u] : 0;
-            return;
-        }
-        const int k = odd == as ? i : odd ? i : i - 1;      // then the first of two words each
-        if (whole) {
+        for (int u = 0; u < U; ++u)
+            if ((uint32_t)(i + 32 * u - as) < (uint32_t)((hidden + as) / E - as)) m |= 1u << u;
+        return m;
+    }
+    // The columns of words i, i + 32 .. of a row of parity `as`; 0 for those not in `m`.
+    __device__ __forceinline__ void load(uint32_t (&q)[U], int i, int as, uint32_t m) const {
+        if (ES == 4 || odd == as) {
+            const uint32_t* p = words() + i;
+#pragma unroll
+            for (int u = 0; u < U; ++u) q[u] = m >> u & 1 ? p[32 * u] : 0;
+        } else if (inside) {                    // each from two words
+            const uint32_t* p = words() + i - as;
             uint32_t next[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                q[u] = has(k + 32 * u) ? p[k + 32 * u] : 0;
-                next[u] = has(k + 32 * u + 1) ? p[k + 32 * u + 1] : 0;
+                q[u] = m >> u & 1 ? p[32 * u] : 0;
+                next[u] = m >> u & 1 ? p[32 * u + 1] : 0;
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) q[u] = __funnelshift_r(q[u], next[u], 16);
-            return;
-        }
-#pragma unroll 1
-        for (int u = 0; u < U; ++u) {
-            const uint32_t a = load_end(k + 32 * u), b = load_end(k + 32 * u + 1);
-            const uint32_t v = odd == as ? a : __funnelshift_r(a, b, 16);
-            if (u == 0) q[0] = v;
-            else if (u == 1) q[1] = v;
-            else if (u == 2) q[2] = v;
-            else q[3] = v;
-        }
-    }
-    __device__ __forceinline__ void store(int i, const uint32_t (&v)[U]) const {
+        } else {                                // at one of the matrix' two ends
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + 2 * i - as;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = i + 32 * u;
-            if (!has(k)) continue;
-            if (ES == 2 && k == 0 && odd) reinterpret_cast<uint16_t*>(p)[1] = (uint16_t)(v[u] >> 16);
-            else if (ES == 2 && k == count - 1 && half) *reinterpret_cast<uint16_t*>(p + k) = (uint16_t)v[u];
-            else __stcs(p + k, v[u]);
+            for (int u = 0; u < U; ++u) q[u] = m >> u & 1 ? p[64 * u] | (uint32_t)p[64 * u + 1] << 16 : 0;
         }
     }
+    __device__ __forceinline__ void store(int i, const uint32_t (&v)[U], uint32_t m) const {
+        uint32_t* p = words() + i;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (m >> u & 1) __stcs(p + 32 * u, v[u]);
+    }
+    // The edges' columns, lanes 0 and 1: -1 if this lane has none.
+    __device__ __forceinline__ int edge(int lane) const {
+        if (ES == 4) return -1;
+        if (lane == 0) return odd ? 0 : -1;
+        return lane == 1 && end * E != hidden + odd ? hidden - 1 : -1;
+    }
+    __device__ __forceinline__ uint16_t& at(int column) const { return reinterpret_cast<uint16_t*>(row)[column]; }
 };
+
+__device__ __forceinline__ float half_float(uint16_t q, bool f16) {
+    return f16 ? __half2float(__ushort_as_half(q)) : __bfloat162float(__ushort_as_bfloat16(q));
+}
+__device__ __forceinline__ uint16_t half_of(float v, bool f16) {
+    return f16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
 
 template <int ES>
 __device__ __forceinline__ void word_floats(uint32_t q, float (&v)[4 / ES], bool f16) {
@@ -383,18 +386,23 @@ __global__ void __launch_bounds__(RT) dispatch_kernel(const __grid_constant__ Ro
                 }
             } else {
                 const Words<ES> in(a.x, (a.tokens - 1) * a.ldx + a.hidden, t * a.ldx, a.hidden);
-                uint32_t q[2][U];           // for rows of either parity
+                // for rows of either parity
+                const uint32_t m[2] = {Words<ES>::whole(c, 0, a.hidden), ES == 2 ? Words<ES>::whole(c, 1, a.hidden) : 0};
+                uint32_t q[2][U];
                 const uint32_t zeros[U] = {0, 0, 0, 0};
-                in.load(q[0], c, 0);
-                if (ES == 2) in.load(q[1], c, 1);
+                in.load(q[0], c, 0, m[0]);
+                if (ES == 2) in.load(q[1], c, 1, m[1]);
 #pragma unroll 2
                 for (int j = 0; j < some; ++j) {
                     const int64_t r = __shfl_sync(0xffffffffu, mine, j);
                     if (r < 0) continue;
                     const Words<ES> out(a.out, rows * a.hidden, r * a.hidden, a.hidden);
-                    if (r >= live) out.store(c, zeros);
-                    else if (ES == 2 && out.odd) out.store(c, q[1]);
-                    else out.store(c, q[0]);
+                    const bool odd = ES == 2 && out.odd;
+                    if (r >= live) out.store(c, zeros, odd ? m[1] : m[0]);
+                    else if (odd) out.store(c, q[1], m[1]);
+                    else out.store(c, q[0], m[0]);
+                    const int edge = c == lane && begin == 0 ? out.edge(lane) : -1;
+                    if (edge >= 0) out.at(edge) = r < live ? in.at(edge) : (uint16_t)0;
                 }
             }
         }
@@ -406,7 +414,7 @@ __global__ void __launch_bounds__(RT) dispatch_kernel(const __grid_constant__ Ro
 // by warps: 8192 tokens, 8 rows of 2048 bf16 each: 60 us at eight CTAs per SM, 69
 // at six, 71 at three with twice the loads in flight per warp.
 template <int ES, bool VEC>
-__global__ void __launch_bounds__(RT, VEC ? 8 : 5) combine_kernel(const __grid_constant__ RowArgs a) {
+__global__ void __launch_bounds__(RT, VEC ? 8 : ES == 4 ? 7 : 5) combine_kernel(const __grid_constant__ RowArgs a) {
     constexpr int V = VEC ? 16 / ES : 4 / ES, U = VEC ? 1 : 4;      // elements of a slot, slots of a lane
     pdl_wait();
     pdl_trigger();
@@ -420,6 +428,7 @@ __global__ void __launch_bounds__(RT, VEC ? 8 : 5) combine_kernel(const __grid_c
     const float first_weight = a.weights && lane < a.k ? a.weights[t * a.k + lane] : 1.f;
     for (int c = begin + lane; c - lane < end; c += 32 * U) {
         float acc[U][V], v[V];
+        const uint32_t m = VEC ? 0 : Words<ES>::whole(c, out.odd, a.hidden);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -430,7 +439,7 @@ __global__ void __launch_bounds__(RT, VEC ? 8 : 5) combine_kernel(const __grid_c
             } else {
                 const Words<ES> add(a.y, (a.tokens - 1) * a.ldy + a.hidden, t * a.ldy, a.hidden);
                 uint32_t q[U];
-                add.load(q, c, out.odd);
+                add.load(q, c, out.odd, m);
 #pragma unroll
                 for (int u = 0; u < U; ++u) word_floats<ES>(q[u], acc[u], f16);
             }
@@ -456,7 +465,7 @@ __global__ void __launch_bounds__(RT, VEC ? 8 : 5) combine_kernel(const __grid_c
                 } else {
                     const Words<ES> in(a.x, rows * a.hidden, (int64_t)r * a.hidden, a.hidden);
                     uint32_t q[U];
-                    in.load(q, c, out.odd);
+                    in.load(q, c, out.odd, m);
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         word_floats<ES>(q[u], v, f16);
@@ -472,8 +481,20 @@ __global__ void __launch_bounds__(RT, VEC ? 8 : 5) combine_kernel(const __grid_c
             uint32_t q[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) q[u] = word_of<ES>(acc[u], f16);
-            out.store(c, q);
+            out.store(c, q, m);
         }
+    }
+    if constexpr (!VEC) {
+        const int edge = begin == 0 ? out.edge(lane) : -1;
+        if (edge < 0) return;
+        float sum = a.y ? half_float(static_cast<const uint16_t*>(a.y)[t * a.ldy + edge], f16) : 0.f;
+        for (int j = 0; j < a.k; ++j) {
+            const int r = a.row_of[t * a.k + j];
+            if (r < 0 || r >= live) continue;
+            sum = fmaf(a.weights ? a.weights[t * a.k + j] : 1.f,
+                       half_float(static_cast<const uint16_t*>(a.x)[(int64_t)r * a.hidden + edge], f16), sum);
+        }
+        out.at(edge) = half_of(sum, f16);
     }
 }
 
@@ -524,35 +545,43 @@ __global__ void __launch_bounds__(RT, 4) combine_backward_kernel(const __grid_co
             }
         } else {
             const Words<ES> dy(a.y, (a.tokens - 1) * a.ldy + a.hidden, t * a.ldy, a.hidden);
-            uint32_t qd[2][U];              // for rows of either parity
-            dy.load(qd[0], c, 0);
-            if (ES == 2) dy.load(qd[1], c, 1);
+            const bool ends = c == lane;    // (the first step works the edges)
+            // for rows of either parity
+            const uint32_t m[2] = {Words<ES>::whole(c, 0, a.hidden), ES == 2 ? Words<ES>::whole(c, 1, a.hidden) : 0};
+            uint32_t qd[2][U];
+            dy.load(qd[0], c, 0, m[0]);
+            if (ES == 2) dy.load(qd[1], c, 1, m[1]);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 if (r[j] < 0) continue;
                 const bool on = r[j] < live;
-                const Words<ES> in(a.x, n, (int64_t)r[j] * a.hidden, a.hidden), out(a.out, n, (int64_t)r[j] * a.hidden, a.hidden);
-                uint32_t q[U];
-                if (on) in.load(q, c, out.odd);
+                const int64_t e = (int64_t)r[j] * a.hidden;
+                const Words<ES> in(a.x, n, e, a.hidden), out(a.out, n, e, a.hidden);
+                const bool odd = ES == 2 && out.odd;
+                const uint32_t mine = odd ? m[1] : m[0];
+                uint32_t q[U] = {0, 0, 0, 0};
+                if (on) {
+                    in.load(q, c, out.odd, mine);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float d[V], y[V];
-                    if (!on) q[u] = 0;
-                    word_floats<ES>(ES == 2 && out.odd ? qd[1][u] : qd[0][u], d, f16);
-                    word_floats<ES>(q[u], y, f16);
-                    if (ES == 2) {          // columns of other rows in a first or last word, and behind it
-                        const int k = c + 32 * u;
-                        if (k >= out.count || (k == 0 && out.odd)) y[0] = d[0] = 0.f;
-                        if (k >= out.count || (k == out.count - 1 && out.half)) y[V - 1] = d[V - 1] = 0.f;
-                    }
+                    for (int u = 0; u < U; ++u) {
+                        float d[V], y[V];
+                        word_floats<ES>(odd ? qd[1][u] : qd[0][u], d, f16);
+                        word_floats<ES>(q[u], y, f16);
 #pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        if (on) dot[j] = fmaf(d[k], y[k], dot[j]);
-                        d[k] *= w[j];
+                        for (int k = 0; k < V; ++k) {
+                            dot[j] = fmaf(d[k], y[k], dot[j]);
+                            d[k] *= w[j];
+                        }
+                        q[u] = word_of<ES>(d, f16);
                     }
-                    q[u] = on ? word_of<ES>(d, f16) : 0;
                 }
-                out.store(c, q);
+                out.store(c, q, mine);
+                const int edge = ends ? out.edge(lane) : -1;
+                if (edge >= 0) {
+                    const float d = on ? half_float(dy.at(edge), f16) : 0.f;
+                    if (on) dot[j] = fmaf(d, half_float(in.at(edge), f16), dot[j]);
+                    out.at(edge) = on ? half_of(d * w[j], f16) : (uint16_t)0;
+                }
             }
         }
     }
