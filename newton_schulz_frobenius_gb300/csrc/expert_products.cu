@@ -31,7 +31,17 @@
 // copies these blocks, zeros behind their rows, and the products read the copies.
 // (Zeroed in shared memory instead, between the copy's arrival and the products, a
 // tile waited about 1 us for its last stage: dW of 64 ragged experts of 512 rows on
-// average, 2048 x 1024, 146 us against 114 of even ones.)
+// average, 2048 x 1024, 146 us against 114 of even ones; now 132 against 118.)
+//
+// What bounds it: with long contractions the rate at which L2 delivers operands, 64
+// bytes per cycle and SM, which a 256 x 256 tile takes in full, and the power cap: 8
+// experts of 4096 x 14336, 16384 rows, even: gated forward 1.97-2.1 ms (1.83-1.95
+// PFLOP/s), linear forward 1.06 (1.81), linear backward 2.25 (1.71); uneven experts,
+// whose last tiles are smaller, 2.25-2.4, 1.1 and 2.35.  With short ones (64 experts of
+// 512 rows, 2048 x 1024) a tile's epilogue beside its 8 to 32 k-blocks, 55-65 % of the
+// product's floor; with few rows HBM (16 rows through 8 experts of 2048 x 8192: 75 us,
+// 6.4 TB/s).  An epilogue of sixteen warps (of 96 registers) and plain instead of tile
+// stores were built and were slower.
 #include "epilogue.cuh"
 #include "glu_parts.cuh"
 
@@ -45,7 +55,11 @@ constexpr int GM = 128;                     // rows of a CTA's half of the M sid
 constexpr int GK = 64;                      // k-block: 128 bytes
 constexpr int NEPI = 8;
 constexpr int GT = 64 + 32 * NEPI;          // producer, issuer, epilogue
-constexpr int SUB = 2;                      // k-blocks of a stage
+// k-blocks of a stage.  A stage costs its waits and its copies' issue whatever it
+// holds: gated forward 16384 rows, 8 x 4096 x 14336: two 1972 us, one 2097 (short
+// contractions, as of 64 experts of 512 rows, gain 1 % with one); three 2360, too
+// coarse a ring.
+constexpr int SUB = 2;
 constexpr int STAGES = 6 / SUB;
 constexpr int OP_BYTES = GM * GK * 2;       // one operand's k-block of a stage (A, or this CTA's half of B)
 constexpr int OUT_BYTES = 32 * 32 * 2;      // output chunk of a warp: 32 x 32, 64-byte swizzled rows
@@ -110,6 +124,21 @@ __device__ __forceinline__ void load_columns(uint32_t dst, const CUtensorMap* ma
 
 enum Mode : int { FWD_GLU = 0, FWD_LINEAR = 1, BACKWARD = 2 };
 
+// Division of numbers below 2^31 by a number known beforehand: the product with
+// 2^32 / d, rounded up, is at most one too high.
+struct Div {
+    uint32_t d, m;
+    __host__ __device__ __forceinline__ void set(int by) {
+        d = (uint32_t)(by < 1 ? 1 : by);
+        m = 0xffffffffu / d + 1;                // (0 for 1)
+    }
+    __device__ __forceinline__ int of(int n) const {
+        uint32_t q = d == 1 ? (uint32_t)n : __umulhi((uint32_t)n, m);
+        if (q * d > (uint32_t)n) --q;
+        return (int)q;
+    }
+};
+
 struct ExpArgs {
     int dtype, act;
     int save;                   // gated forward: G and U leave too
@@ -123,6 +152,7 @@ struct ExpArgs {
     // family b: the weights' gradients
     int nb;                     // results per expert: 0, 1 or 2
     int rows_b, cols_b, tiles_mb, tiles_nb;
+    Div group_a, group_b, rest_b, matrix_b;     // tiles of a group of either family, rows of b's last group, tiles of a result of b
     GluOut out[3];              // H, G, U; Y; or dX, dW, dWu
     float* part;                // running sums of contractions in several parts
     int* status;
@@ -161,10 +191,18 @@ struct Tile {
 // left with one fewer then take `extra` of family b's, and the rest of family b
 // goes round-robin starting with those: with a's tiles the longer ones, every
 // cluster ends within a tile of the others.
+//
+// Every warp walks them, so a step between tiles is on everybody's way: nothing is
+// divided but by numbers known before, of an expert's once per expert (128 rows through
+// 8 experts of 4096 x 14336, whose gradients' tiles are a k-block each: backward 844 ->
+// 812 us).
+template <bool B>                           // with a family b
 struct Walk {
     int c, P, j;
     int nb, mine, light, extra;
-    int e, base, first, last, here;         // family a: current expert, id of its first tile, its rows and tiles
+    // family a: current expert, id of its first tile, its rows and tiles, tiles along its rows, their extent
+    int e, base, first, last, here, along, per, ready;
+    Div rest;                               // rows of tiles of its last group
     int end;                                // of the experts' rows; "expert" g.experts has those behind, results zero
 
     __device__ __forceinline__ void tiles_of(const ExpArgs& g) {
@@ -174,7 +212,8 @@ struct Walk {
             first = end;
             last = g.rows;
         }
-        here = (last - first + ROW_TILE - 1) / ROW_TILE * g.tiles_w;
+        along = (last - first + ROW_TILE - 1) / ROW_TILE;
+        here = along * g.tiles_w;
     }
     // Called by whole warps.
     __device__ __forceinline__ void init(const ExpArgs& g, int cluster, int clusters) {
@@ -198,18 +237,20 @@ struct Walk {
             }
             na += (g.rows - end + ROW_TILE - 1) / ROW_TILE * g.tiles_w;
         }
-        nb = g.experts * g.nb * g.tiles_mb * g.tiles_nb;
         const int r = na % P;
         mine = na / P + (c < r ? 1 : 0);
         light = r ? P - r : 0;
+        nb = B ? g.experts * g.nb * g.tiles_mb * g.tiles_nb : 0;
         // a tile's time in k-blocks; one of few costs what its results take to leave
         const int ca = max(8, g.segs * g.seg_blocks);
         const int cb = max(8, (g.rows / g.experts + GK - 1) / GK);
         extra = light ? min(nb / light, (ca + cb / 2) / cb) : 0;
         e = 0;
         base = 0;
+        ready = -1;
         tiles_of(g);
     }
+    // The next tile; t holds the one before.
     __device__ __forceinline__ bool next(const ExpArgs& g, Tile& t) {
         if (j < mine) {
             int l = c + j * P;
@@ -224,19 +265,23 @@ struct Walk {
                 t = Tile{};
                 return true;
             }
+            if (ready != e) {               // (not for the experts passed by)
+                ready = e;
+                per = extent((last - first + along - 1) / along);
+                rest.set(along % GROUP);
+            }
             t.family = 0;
             t.which = 0;
             t.e = e;
             t.first = first;
             t.last = last;
             t.blocks = e == g.experts ? 0 : g.segs * g.seg_blocks;
-            const int tiles = here / g.tiles_w;
-            place(l, tiles, g.tiles_w, t);
-            const int per = extent((last - first + tiles - 1) / tiles);
+            place(l, along, g.group_a, rest, t);
             t.r0 = first + t.tm * per;
             t.n = min(per, extent(last - t.r0));
             return true;
         }
+        if (!B) return false;
         const int k = j - mine;
         ++j;
         int id;
@@ -244,22 +289,29 @@ struct Walk {
         if (light && c >= P - light) id = k < extra ? (c - (P - light)) + k * light : lead + (c - (P - light)) + (k - extra) * P;
         else id = lead + (light ? light + c : c) + k * P;
         if (id >= nb) return false;
-        const int tiles = g.tiles_mb * g.tiles_nb;
+        const int matrix = g.matrix_b.of(id), expert = matrix >> (g.nb - 1);        // one or two of an expert
+        if (t.family == 0 || t.e != expert) {
+            expert_rows(g, expert, t.first, t.last);
+            t.blocks = (t.last - t.first + GK - 1) / GK;
+        }
         t.family = 1;
-        t.e = id / (g.nb * tiles);
-        id -= t.e * g.nb * tiles;
-        t.which = id / tiles;
-        expert_rows(g, t.e, t.first, t.last);
-        t.blocks = (t.last - t.first + GK - 1) / GK;
-        place(id - t.which * tiles, g.tiles_mb, g.tiles_nb, t);
+        t.e = expert;
+        t.which = matrix & (g.nb - 1);
+        place(id - matrix * (int)g.matrix_b.d, g.tiles_mb, g.group_b, g.rest_b, t);
         return true;
     }
     static __device__ __forceinline__ int extent(int rows) { return rows <= 32 ? 32 : (rows + 63) & ~63; }
-    __device__ __forceinline__ void place(int l, int tiles_m, int tiles_n, Tile& t) {
-        const int per = GROUP * tiles_n, grp = l / per, from = grp * GROUP, size = min(GROUP, tiles_m - from);
-        l -= grp * per;
-        t.tm = from + l % size;
-        t.tn = l / size;
+    // Tile l of tiles in groups of GROUP rows (the last one may have fewer, `rest`), down a group's columns.
+    static __device__ __forceinline__ void place(int l, int tiles_m, const Div& group, const Div& rest, Tile& t) {
+        const int grp = group.of(l), from = grp * GROUP;
+        l -= grp * (int)group.d;
+        if (tiles_m - from >= GROUP) {
+            t.tm = from + l % GROUP;
+            t.tn = l / GROUP;
+        } else {
+            t.tn = rest.of(l);
+            t.tm = from + l - t.tn * (int)rest.d;
+        }
     }
 };
 
@@ -308,26 +360,40 @@ __device__ __forceinline__ void store_rows(const ExpArgs& g, const GluOut& o, co
     }
 }
 
-// One warp's 32 x 32 chunk, a row per lane.
-__device__ __forceinline__ void store_chunk(const ExpArgs& g, const CUtensorMap* map, const GluOut& o, const Place& p,
-                                            const float (&v)[32], uint8_t* stage, int& groups) {
+// One warp's 32 rows x 64 columns of family b, a row per lane, in two steps of 32
+// columns: both into the warp's two buffers as 128-byte rows (swizzled: piece k of row
+// r at k ^ (r % 8)), then one store (32 columns per store: backward of the case above
+// 812 us instead of 783).  A cluster's tiles of family b come after those of a.
+__device__ __forceinline__ void put_half(const float (&v)[32], int step, bool f16, uint8_t* stage) {
     const int lane = threadIdx.x & 31;
-    const bool tile = as_tile(g, p);
-    uint8_t* buf = out_buffer(stage, groups, tile);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<uint4*>(buf + piece_at(lane, k)) = pack8_h(v + 8 * k, g.dtype == MUON_F16);
-    if (tile) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (tile) {
+        *reinterpret_cast<uint4*>(stage + lane * 128 + (((step * 4 + k) ^ (lane & 7)) << 4)) = pack8_h(v + 8 * k, f16);
+}
+
+__device__ __forceinline__ void store_wide(const ExpArgs& g, const CUtensorMap* map, const GluOut& o, const Place& p,
+                                           uint8_t* stage, int& groups) {
+    const int lane = threadIdx.x & 31;
+    if (g.tma_out) {                        // (a tile store ends with the expert's matrix)
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
         if (lane == 0) {
-            tma_store_3d(map, smem_u32(buf), p.c0, p.r0, p.z);
+            tma_store_3d(map, smem_u32(stage), p.c0, p.r0, p.z);
             bulk_commit();
         }
-        ++groups;
+        groups = 2;                         // both buffers are taken
         return;
     }
-    store_rows(g, o, p, buf);
+    __syncwarp();
+    const int n = min(32, p.rows - p.r0);
+    uint16_t* out = static_cast<uint16_t*>(o.p) + ((int64_t)p.z * p.z_rows + p.r0) * o.ld + p.c0;
+#pragma unroll
+    for (int c = lane; c < 64; c += 32) {
+        if (p.c0 + c >= p.cols) break;
+#pragma unroll 8
+        for (int i = 0; i < n; ++i)
+            out[(int64_t)i * o.ld + c] = *reinterpret_cast<const uint16_t*>(stage + i * 128 + (((c >> 3) ^ (i & 7)) << 4) + (c & 7) * 2);
+    }
     __syncwarp();
 }
 
@@ -380,17 +446,19 @@ __device__ __forceinline__ bool pair_all(int id, bool v) {
 
 // One copy of the loop per activation: chosen per element, the code of the other two
 // stands between the elements of the one, and an epilogue of 32 chunks spends
-// its time fetching it (64 experts, 512 rows each, 2048 x 1024: 383 us per call).
+// its time fetching it (64 experts, 512 rows each, 2048 x 1024: 383 us per call, 316
+// with one copy each).
 template <int ACT>
 __device__ __forceinline__ void times_act(const float (&gate)[16], float (&v)[32]) {
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-        if (ACT == ACT_GELU) {
+        if constexpr (ACT == ACT_GELU) {
             v[k] *= activate<false>(gate[k], ACT, nullptr);
             continue;
         }
         // g sigmoid(z), as activate() has it but for the quotient: two ulp instead of half
-        // of one, far below the results' rounding, for a third of the instructions
+        // of one, far below the results' rounding, for a third of the instructions (286 us
+        // -> 207 in the case above); a quotient by more than 2^126 is 0, for g below -87
         const float x = gate[k];
         const float z = ACT == ACT_SILU ? x : 1.5957691216057308f * x * fmaf(0.044715f * x, x, 1.0f);
         v[k] *= __fdividef(x, 1.0f + __expf(-z));
@@ -501,9 +569,9 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
     pdl_wait();
     pdl_trigger();
 
-    Walk w;
+    Walk<MODE == BACKWARD> w;
     w.init(g, (int)cluster_idx(), (int)cluster_count());
-    Tile t;
+    Tile t = {};
     if (warp == 0) {
         // ---------------- TMA producer ----------------
         if (lane == 0) {
@@ -675,12 +743,18 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
                 p = Place{t.last, g.cols_a, t.r0, c0, 0, g.rows};
                 chunks = c0 < p.cols ? t.n / 32 : 0;
             }
-            // chunk ch: rows 32 ch.. (family a) or columns 32 ch.. (family b)
+            // chunk ch: rows 32 ch.. (family a) or columns 32 ch.. (family b, which takes them by twos)
+            const int by = MODE == BACKWARD && t.family ? 2 : 1, first = half * by, step = 2 * by;
             auto chunk = [&](int ch, float(&v)[32]) {
                 Place c = p;
                 if (MODE == BACKWARD && t.family) {
-                    c.c0 += 32 * ch;
-                    store_chunk(g, &maps.out[o], g.out[o], c, v, stage, groups);
+                    c.c0 += 32 * (ch & ~1);
+                    if ((ch & 1) == 0 && groups > 0) {
+                        if (lane == 0) bulk_wait_read0();
+                        __syncwarp();
+                    }
+                    put_half(v, ch & 1, g.dtype == MUON_F16, stage);
+                    if ((ch & 1) || ch + 1 == chunks) store_wide(g, &maps.out[o], g.out[o], c, stage, groups);
                 } else {
                     c.r0 += 32 * ch;
                     if (MODE == FWD_GLU) store_gated(g, maps.out, c, q >= 2, pair, v, stage, others, groups);
@@ -691,11 +765,13 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
                 // nothing to sum (an expert without rows, rows behind the last expert)
                 float v[32];
 #pragma unroll 1
-                for (int ch = half; ch < chunks; ch += 2) {
+                for (int c0 = first; c0 < chunks; c0 += step)
+#pragma unroll 1
+                    for (int ch = c0; ch < min(c0 + by, chunks); ++ch) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] = 0.f;
-                    chunk(ch, v);
-                }
+                        for (int k = 0; k < 32; ++k) v[k] = 0.f;
+                        chunk(ch, v);
+                    }
                 continue;
             }
             for (int from = 0; from < t.blocks; from += MAX_BLOCKS) {
@@ -716,12 +792,14 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
                         else mbar_arrive(acce0 + 8 * acc);
                     }
                 };
-                if (half >= chunks) release();
+                if (first >= chunks) release();
+                int ch = first;
 #pragma unroll 1
-                for (int ch = half; ch < chunks; ch += 2) {
+                while (ch < chunks) {
                     float v[32];
                     tmem_ld32(lanes + (uint32_t)(ch * 32), v);
-                    if (ch + 2 >= chunks) release();
+                    const int next = by == 2 && (ch & 1) == 0 ? ch + 1 : ch + step - by + 1;
+                    if (next >= chunks) release();
                     float* at = part + ch * 32;
                     if (from) {
 #pragma unroll
@@ -740,6 +818,7 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
                     } else {
                         chunk(ch, v);
                     }
+                    ch = next;
                 }
                 acc ^= 1;
                 if (acc == 0) aphase ^= 1u;
@@ -874,10 +953,15 @@ int set_tiles(ExpArgs& g, int64_t cols_a, int tile_cols, int64_t k, int segs, in
     g.cols_b = (int)cols_b;
     g.tiles_mb = (int)((rows_b + 2 * GM - 1) / (2 * GM));
     g.tiles_nb = (int)((cols_b + 2 * GM - 1) / (2 * GM));
+    g.group_a.set(GROUP * g.tiles_w);
+    g.group_b.set(GROUP * g.tiles_nb);
+    g.rest_b.set(g.tiles_mb % GROUP);
     *most = (g.a_on ? ((int64_t)g.rows / ROW_TILE + g.experts + 1) * g.tiles_w : 0) +
             (int64_t)g.experts * nb * g.tiles_mb * g.tiles_nb;
     // (their results alone, 128 KB a tile, are more than the device holds)
-    return *most > 1 << 30 ? fail(MUON_ENOMEM, "products of more than 2^30 tiles") : MUON_OK;
+    if (*most > 1 << 30) return fail(MUON_ENOMEM, "products of more than 2^30 tiles");
+    g.matrix_b.set(g.tiles_mb * g.tiles_nb);
+    return MUON_OK;
 }
 
 // Whether a contraction of this launch can take more than one part.
@@ -923,6 +1007,11 @@ bool map_columns(CUtensorMap* m, const Operand& o, int dtype, int* whole, int64_
     return fn(m, dtype == MUON_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
               const_cast<void*>(o.p), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Family b's results, in boxes of 64 columns and 32 rows.
+bool map_wide(CUtensorMap* m, const GluOut& o, int dtype, int64_t rows, int64_t cols, int64_t batch) {
+    return map_in(m, Operand{o.p, rows, cols, o.ld}, dtype, 64, 32, batch);
 }
 
 // Bytes of the experts' last k-blocks of a matrix of pitch ld.
@@ -1155,8 +1244,8 @@ extern "C" int muon_expert_glu_backward(const void* x, const void* w_gate, const
               map_rows(maps.b[0], DG, dtype) && map_rows(maps.b[1], DU, dtype);
     if (ok && g.tma_out && dx) ok = map_out(&maps.out[0], g.out[0], dtype, rows, hidden);
     if (ok && g.tma_out && dw_gate)
-        ok = map_out(&maps.out[1], g.out[1], dtype, ffn, hidden, num_experts) &&
-             map_out(&maps.out[2], g.out[2], dtype, ffn, hidden, num_experts);
+        ok = map_wide(&maps.out[1], g.out[1], dtype, ffn, hidden, num_experts) &&
+             map_wide(&maps.out[2], g.out[2], dtype, ffn, hidden, num_experts);
     if (!ok) return fail(MUON_ECUDA, "tensor map creation failed");
     const Operand* const contracted[3] = {&DG, &DU, &X};
     if (dw_gate && (r = set_family_b(maps, g, contracted, 3, at + part + 2 * half + pads, dc.sms, s))) return r;
@@ -1225,7 +1314,7 @@ extern "C" int muon_expert_linear_backward(const void* x, const void* w, const v
     g.tma_out = tma_ok(dx, in) && tma_ok(dw, in);
     bool ok = map_columns(&maps.a[0], W, dtype, &g.whole_a, num_experts) && map_rows(maps.b[0], D, dtype);
     if (ok && g.tma_out && dx) ok = map_out(&maps.out[0], g.out[0], dtype, rows, in);
-    if (ok && g.tma_out && dw) ok = map_out(&maps.out[1], g.out[1], dtype, out, in, num_experts);
+    if (ok && g.tma_out && dw) ok = map_wide(&maps.out[1], g.out[1], dtype, out, in, num_experts);
     if (!ok) return fail(MUON_ECUDA, "tensor map creation failed");
     const Operand* const contracted[2] = {&D, &X};
     if (dw && (r = set_family_b(maps, g, contracted, 2, static_cast<char*>(scratch) + part + pads, dc.sms, s))) return r;

@@ -349,3 +349,38 @@ def test_scratch(mg):
     torch.cuda.synchronize()
     assert (guard[n:] == 7).all()
     assert torch.equal(y, mg.muon_expert_linear_forward(x, w, bounds))
+
+
+def test_input_gradients_alone(mg):
+    """Through the C ABI the weights' gradients may be left out too."""
+    import ctypes
+    args, (dx, _, _) = check_glu(mg, [40, 0, 100], 72, 136, "bf16", tail=4)
+    x, wg, wu, gate, up, dh, bounds = args
+    largs, (_, dlx, _) = check_linear(mg, [40, 0, 100], 72, 136, "bf16", tail=4)
+    lx, lw, ldy, lbounds = largs
+    s = torch.cuda.current_stream().cuda_stream
+
+    def call(name, *a):
+        need = ctypes.c_int64(0)
+        fn = getattr(mg.lib(), name)
+        st = fn(*a, None, ctypes.byref(need), s)
+        if st == mg.MUON_ENOMEM:
+            scratch = torch.empty(need.value, dtype=torch.uint8, device="cuda")
+            st = fn(*a, scratch.data_ptr(), ctypes.byref(need), s)
+        assert st == mg.MUON_OK
+        torch.cuda.synchronize()
+    got = torch.full_like(dx, NAN)
+    call("muon_expert_glu_backward", *[t.data_ptr() for t in (x, wg, wu, gate, up, dh, bounds)], got.data_ptr(), None, None,
+         144, 3, 72, 136, mg.MUON_BF16, 0)
+    assert torch.equal(got, dx)
+    got = torch.full_like(dlx, NAN)
+    call("muon_expert_linear_backward", *[t.data_ptr() for t in (lx, lw, ldy, lbounds)], got.data_ptr(), None, 144, 3, 72, 136,
+         mg.MUON_BF16)
+    assert torch.equal(got, dlx)
+
+
+def test_wide_and_narrow_experts(mg):
+    """Column counts around whole blocks of 64 and tiles of 256, where operands are copied in one piece or two."""
+    for hidden, ffn in ((64, 320), (320, 64), (448, 128), (127, 192), (192, 65)):
+        check_glu(mg, [33, 64, 0, 200], hidden, ffn, "bf16", tail=1)
+        check_linear(mg, [33, 64, 0, 200], hidden, ffn, "f16", tail=1)
