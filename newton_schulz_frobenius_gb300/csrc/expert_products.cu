@@ -171,11 +171,11 @@ struct ExpMaps {
     CUtensorMap out[3];
 };
 
-// [first, last) rows of expert e, within the matrix whatever the bounds hold.
-__device__ __forceinline__ void expert_rows(const ExpArgs& g, int e, int& first, int& last) {
-    const int lo = e == 0 ? 0 : g.bounds[e];
-    first = min(max(lo, 0), g.rows);
-    last = min(max(g.bounds[e + 1], first), g.rows);
+// [first, last) of `rows` rows that are expert e's, whatever the bounds hold.
+__device__ __forceinline__ void expert_rows(const int* bounds, int rows, int e, int& first, int& last) {
+    const int lo = e == 0 ? 0 : bounds[e];
+    first = min(max(lo, 0), rows);
+    last = min(max(bounds[e + 1], first), rows);
 }
 
 struct Tile {
@@ -207,7 +207,7 @@ struct Walk {
 
     __device__ __forceinline__ void tiles_of(const ExpArgs& g) {
         if (e < g.experts) {
-            expert_rows(g, e, first, last);
+            expert_rows(g.bounds, g.rows, e, first, last);
         } else {
             first = end;
             last = g.rows;
@@ -226,7 +226,7 @@ struct Walk {
         if (g.a_on) {
             for (int k = lane; k < g.experts; k += 32) {
                 int lo, hi;
-                expert_rows(g, k, lo, hi);
+                expert_rows(g.bounds, g.rows, k, lo, hi);
                 na += (hi - lo + ROW_TILE - 1) / ROW_TILE * g.tiles_w;
                 end = max(end, hi);
             }
@@ -291,7 +291,7 @@ struct Walk {
         if (id >= nb) return false;
         const int matrix = g.matrix_b.of(id), expert = matrix >> (g.nb - 1);        // one or two of an expert
         if (t.family == 0 || t.e != expert) {
-            expert_rows(g, expert, t.first, t.last);
+            expert_rows(g.bounds, g.rows, expert, t.first, t.last);
             t.blocks = (t.last - t.first + GK - 1) / GK;
         }
         t.family = 1;
@@ -840,12 +840,16 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
 // pitches of whole 16-byte pieces (zeros behind the columns).  A warp takes a row,
 // 128 pieces at a time: every lane loads four aligned vectors and shifts them into
 // place with its neighbours'.  Bound by HBM: the weights and rows of 20 experts of
-// 1001 x 2731 (285 MB read and written) 43 us.
+// 1001 x 2731 (285 MB read and written) 43 us.  Matrices of experts without rows are
+// left out: no product reads them.
 struct PadRows {
     const void* src[3];
     void* dst[3];
     int64_t rows[3];
     int cols[3];
+    Div each[3];                // rows of an expert's matrix; 0: the rows are not the experts'
+    const int* bounds;
+    int all;                    // sorted rows
 };
 
 __global__ void __launch_bounds__(256) pad_rows_kernel(const __grid_constant__ PadRows a) {
@@ -855,6 +859,11 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const __grid_constant__ P
     const int o = blockIdx.y, lane = threadIdx.x & 31, cols = a.cols[o], pieces = (cols + 7) / 8;
     const int64_t rows = a.rows[o], n = rows * cols, step = (int64_t)gridDim.x * 8;
     for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += step) {
+        if (a.each[o].d) {
+            int first, last;
+            expert_rows(a.bounds, a.all, a.each[o].of((int)row), first, last);
+            if (first == last) continue;
+        }
         const uint16_t* at = static_cast<const uint16_t*>(a.src[o]) + row * cols;
         const int off = (int)(reinterpret_cast<uintptr_t>(at) & 15) / 2;
         const int64_t e = row * cols - off;         // element of slot 0
@@ -919,7 +928,8 @@ __global__ void __launch_bounds__(256) tails_kernel(const __grid_constant__ Tail
     pdl_wait();
     pdl_trigger();
     const int m = blockIdx.z, e = blockIdx.x;
-    const int first = e == 0 ? 0 : min(max(a.bounds[e], 0), a.rows), last = min(max(a.bounds[e + 1], first), a.rows);
+    int first, last;
+    expert_rows(a.bounds, a.rows, e, first, last);
     const int left = (last - first) % GK;
     if (left == 0) return;
     const int pieces = (int)(a.ld[m] / 8);
@@ -969,22 +979,29 @@ bool in_parts(const ExpArgs& g) {
     return (g.a_on && g.segs * g.seg_blocks > MAX_BLOCKS) || (g.nb && blocks_of(g.rows) > MAX_BLOCKS);
 }
 
-// Points the operands that need it at padded copies from `at` on and makes these.
-int pad_rows(std::initializer_list<Operand*> ops, char* at, int sms, cudaStream_t s) {
+// Points the operands that need it at padded copies from `at` on and makes these;
+// `rows` are all experts', `weights` num_experts matrices each.
+int pad_rows(std::initializer_list<Operand*> rows, std::initializer_list<Operand*> weights, const ExpArgs& g, char* at,
+             int sms, cudaStream_t s) {
     PadRows p;
     std::memset(&p, 0, sizeof p);
+    p.bounds = g.bounds;
+    p.all = g.rows;
     int n = 0;
     int64_t most = 0;
-    for (Operand* o : ops) {
+    auto pad = [&](Operand* o, bool by_expert) {
         const size_t bytes = padded_bytes(*o);
-        if (!bytes) continue;
+        if (!bytes) return;
         p.src[n] = o->p; p.dst[n] = at; p.rows[n] = o->rows; p.cols[n] = (int)o->cols;
+        if (by_expert) p.each[n].set((int)(o->rows / g.experts));
         most = std::max(most, o->rows);
         o->p = at;
         o->ld = pad8(o->cols);
         at += bytes;
         ++n;
-    }
+    };
+    for (Operand* o : rows) pad(o, false);
+    for (Operand* o : weights) pad(o, true);
     if (n == 0) return MUON_OK;
     note_launch_begin(KC_OTHER, s);
     const cudaError_t e = launch_pdl(pad_rows_kernel, dim3((unsigned)std::min<int64_t>((most + 7) / 8, (int64_t)sms * 16), (unsigned)n),
@@ -1181,7 +1198,7 @@ extern "C" int muon_expert_glu_forward(const void* x, const void* w_gate, const 
     const size_t pads = padded_bytes(X) + padded_bytes(G) + padded_bytes(U);
     if ((r = scratch_check(scratch, scratch_bytes, part + pads))) return r;
     g.part = static_cast<float*>(scratch);
-    if ((r = pad_rows({&X, &G, &U}, static_cast<char*>(scratch) + part, dc.sms, s))) return r;
+    if ((r = pad_rows({&X}, {&G, &U}, g, static_cast<char*>(scratch) + part, dc.sms, s))) return r;
     G.rows = U.rows = ffn;
     ExpMaps maps;
     std::memset(&maps, 0, sizeof maps);
@@ -1232,8 +1249,8 @@ extern "C" int muon_expert_glu_backward(const void* x, const void* w_gate, const
     ga.rows = rows; ga.ffn = (int)ffn; ga.pieces = (int)(ldw / 8);
     ga.dtype = dtype; ga.act = act;
     ga.vec = tma_ok(dh, ffn) && tma_ok(gate, ffn) && tma_ok(up, ffn);
-    if ((r = pad_rows({&X, &G, &U}, at + part + 2 * half, dc.sms, s)) || (r = glu_prepare(nullptr, 0, nullptr, &ga, dc.sms, s)))
-        return r;
+    if ((r = pad_rows({&X}, {&G, &U}, g, at + part + 2 * half, dc.sms, s))) return r;
+    if ((r = glu_prepare(nullptr, 0, nullptr, &ga, dc.sms, s))) return r;
     G.rows = U.rows = ffn;
     const Operand DG{ga.dg, rows, ffn, ldw}, DU{ga.du, rows, ffn, ldw};
     ExpMaps maps;
@@ -1272,7 +1289,7 @@ extern "C" int muon_expert_linear_forward(const void* x, const void* w, const in
     const size_t pads = padded_bytes(X) + padded_bytes(W);
     if ((r = scratch_check(scratch, scratch_bytes, part + pads))) return r;
     g.part = static_cast<float*>(scratch);
-    if ((r = pad_rows({&X, &W}, static_cast<char*>(scratch) + part, dc.sms, s))) return r;
+    if ((r = pad_rows({&X}, {&W}, g, static_cast<char*>(scratch) + part, dc.sms, s))) return r;
     W.rows = out;
     ExpMaps maps;
     std::memset(&maps, 0, sizeof maps);
@@ -1306,7 +1323,7 @@ extern "C" int muon_expert_linear_backward(const void* x, const void* w, const v
     const size_t tails = tail_bytes(g, pad8(out)) + tail_bytes(g, pad8(in));
     if ((r = scratch_check(scratch, scratch_bytes, part + pads + tails))) return r;
     g.part = static_cast<float*>(scratch);
-    if ((r = pad_rows({&X, &W, &D}, static_cast<char*>(scratch) + part, dc.sms, s))) return r;
+    if ((r = pad_rows({&X, &D}, {&W}, g, static_cast<char*>(scratch) + part, dc.sms, s))) return r;
     W.rows = out;
     ExpMaps maps;
     std::memset(&maps, 0, sizeof maps);

@@ -224,3 +224,30 @@ def test_binding_refusals(mg):
     for n in (0, 1025, 1 << 40):
         with pytest.raises(mg.MuonError):
             mg.muon_expert_sort(choices(4, 2, 3), n)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(3, 100, 7, 65), (2, 1024, 1024, 8), (2, 3, 4, 1 << 20), (1, 2, 3, (1 << 20) - 1), (9, 33, 5, 127)],
+                         ids=str)
+def test_limits(mg, shape, dtype):
+    """More choices than a warp has lanes, the most choices and experts, the widest rows."""
+    check_rows(mg, *shape, dtype)
+
+
+def test_no_tokens(mg):
+    row_of, slot_of, bounds = mg.muon_expert_sort(torch.empty((0, 2), dtype=torch.int64, device="cuda"), 3)
+    x, w = torch.empty((0, 16), device="cuda"), torch.empty((0, 2), device="cuda")
+    assert mg.muon_expert_dispatch(x, row_of, bounds).shape == (0, 16)
+    assert mg.muon_expert_combine(x, row_of, bounds, weights=w, residual=x).shape == (0, 16)
+    dys, dw = mg.muon_expert_combine_backward(x, x, row_of, bounds, w)
+    assert dys.shape == (0, 16) and dw.shape == (0, 2)
+
+
+def test_large_values(mg):
+    """Infinities and NaN stay in their own token; a weight of 0 does not hide them (0 times infinity is no number)."""
+    row_of, _, bounds = mg.muon_expert_sort(torch.tensor([[0, 1], [1, 0], [0, -1]], dtype=torch.int32, device="cuda"), 2)
+    ys = torch.ones(6, 40, device="cuda")
+    ys[row_of[0, 0]] = float("inf")
+    ys[row_of[1, 1]] = float("nan")
+    y = mg.muon_expert_combine(ys, row_of, bounds, weights=torch.tensor([[1.0, 1.0], [1.0, 0.0], [2.0, 5.0]], device="cuda"))
+    assert torch.isinf(y[0]).all() and torch.isnan(y[1]).all() and (y[2] == 2).all()
