@@ -205,7 +205,8 @@ struct RowArgs {
     int k, hidden, experts_n;
     int dtype;
     int slots;                  // of a row: 16-byte pieces, or 4-byte words that it can touch
-    int span;                   // dispatch, combine: slots of a warp
+    int span;                   // dispatch, combine: slots of a warp; rings: chunks of a unit
+    int parts, units;           // rings: units of a token, of the call
     int group;                  // backward: warps that share a token's rows, a power of two
 };
 
@@ -415,7 +416,8 @@ __global__ void __launch_bounds__(RT) dispatch_kernel(const __grid_constant__ Ro
 // A warp takes one token and some runs of its slots and sums the token's k rows
 // there in fp32, in the order of the choices; one rounding.  Bound by latency, so
 // by warps: 8192 tokens, 8 rows of 2048 bf16 each onto a residual (336 MB): 60-63 us
-// at eight CTAs per SM, 69 at six, 71 at three with twice the loads in flight per warp.
+// at eight CTAs per SM, 69 at six, 71 at three with twice the loads in flight per warp
+// (such calls go by rings now, see below; few tokens, short rows and many choices here).
 template <int ES, bool VEC>
 __global__ void __launch_bounds__(RT, VEC ? 8 : ES == 4 ? 7 : 5) combine_kernel(const __grid_constant__ RowArgs a) {
     constexpr int V = VEC ? 16 / ES : 4 / ES, U = VEC ? 1 : 4;      // elements of a slot, slots of a lane
@@ -607,6 +609,142 @@ __global__ void __launch_bounds__(RT, 4) combine_backward_kernel(const __grid_co
     if (place == 0 && lane < some) a.dweights[s + lane] = lane == 0 ? dot[0] : lane == 1 ? dot[1] : lane == 2 ? dot[2] : dot[3];
 }
 
+// Copies of rows on their way to a warp's shared memory, RING_D slots of 128 pieces
+// (2 KB of one row): reads of a row stand together in DRAM, none waits for the sum of the one
+// before, none holds registers.  A warp takes units u, u + total ..: a token and some
+// chunks of its row; a unit's items are, chunk by chunk, the token's own row (if `own`)
+// and its k rows.  Each lane reads only what it copied itself, so it waits for nothing
+// but its own copies.  (8192 tokens, 8 rows of 2048 bf16 each onto a residual: slots of
+// 512 bytes 59-67 us, of 1 KB 57-61, of 2 KB 55-56.  combine_backward, which writes
+// beside its reads, was slower this way: 107 us against 97.)
+constexpr int RING_D = 4, RING_W = 4, RING_CTAS = 3;       // slots, pieces of a lane in one, CTAs per SM
+constexpr int RING_SMEM = RT / 32 * RING_D * RING_W * 32 * 16;
+
+template <int ES>
+struct Ring {
+    uint4* buf;                             // this lane's pieces: slot, then 32 apart
+    int64_t rows;                           // rows from here on are not read
+    int u, t, c, end, j, slot;              // the next copy: unit, token, chunk, item, its slot
+    int idx, next;                          // rows of that unit, of the one after, a lane each
+    int own;
+
+    static __device__ __forceinline__ int total() { return (int)gridDim.x * (RT / 32); }
+    static __device__ __forceinline__ int first() { return (int)blockIdx.x + (int)(threadIdx.x >> 5) * (int)gridDim.x; }
+    // Chunks [c, end) of token t.
+    static __device__ __forceinline__ void place(const RowArgs& a, int u, int& t, int& c, int& end) {
+        t = (int)((uint32_t)u / (uint32_t)a.parts);
+        c = (u - t * a.parts) * a.span;
+        end = min(c + a.span, (a.slots + 32 * RING_W - 1) / (32 * RING_W));
+    }
+    static __device__ __forceinline__ int token_rows(const RowArgs& a, int u, int64_t rows) {
+        return u < a.units ? rows_of(a, (uint32_t)u / (uint32_t)a.parts, 0, rows) : -1;
+    }
+    __device__ __forceinline__ void start(const RowArgs& a, uint4* smem, int64_t limit) {
+        buf = smem + (threadIdx.x >> 5) * (RING_D * RING_W * 32) + (threadIdx.x & 31);
+        rows = limit;
+        own = a.y != nullptr;
+        j = slot = 0;
+        u = first();
+        place(a, u, t, c, end);
+        idx = token_rows(a, u, rows);
+        next = token_rows(a, u + total(), rows);
+#pragma unroll
+        for (int i = 0; i < RING_D - 1; ++i) issue(a);
+    }
+    __device__ __forceinline__ void issue(const RowArgs& a) {
+        if (u < a.units) {
+            const bool mine = own && j == 0;
+            const int r = __shfl_sync(0xffffffffu, idx, j - own);
+            if (mine || r >= 0) {
+                const uint4* p = mine ? piece<ES>(a.y, t * a.ldy, 0) : piece<ES>(a.x, (int64_t)r * a.hidden, 0);
+                const uint32_t to = (uint32_t)__cvta_generic_to_shared(buf + slot * (RING_W * 32));
+#pragma unroll
+                for (int i = 0; i < RING_W; ++i) {
+                    const int at = (c * RING_W + i) * 32 + (threadIdx.x & 31);
+                    if (at < a.slots)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 512), "l"(p + at) : "memory");
+                }
+            }
+            if (++j == a.k + own) {
+                j = 0;
+                if (++c == end) {
+                    u += total();
+                    place(a, u, t, c, end);
+                    idx = next;
+                    next = token_rows(a, u + total(), rows);
+                }
+            }
+            if (++slot == RING_D) slot = 0;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // Makes the copy after those in flight and waits for the oldest of them.
+    __device__ __forceinline__ void turn(const RowArgs& a) {
+        issue(a);
+        asm volatile("cp.async.wait_group %0;" ::"n"(RING_D - 1) : "memory");
+    }
+};
+
+// combine_kernel for rows on 16 bytes that are not few, the same sums.  Bound by HBM:
+// 16384 tokens, 8 rows of 2048 bf16 each onto a residual (671 MB) 107 us, 6.3 TB/s
+// (combine_kernel 121); 8192 tokens 56 (61); 4096 tokens, 2 rows of 4096, 24.6 (29.9).
+template <int ES>
+__global__ void __launch_bounds__(RT, RING_CTAS) combine_ring_kernel(const __grid_constant__ RowArgs a) {
+    constexpr int V = 16 / ES;
+    extern __shared__ uint4 ring_smem[];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, live = live_rows(a);
+    const bool f16 = a.dtype == MUON_F16;
+    Ring<ES> ring;
+    int u = Ring<ES>::first(), slot = 0;
+    auto weights = [&](int of) {
+        return a.weights && of < a.units && lane < a.k ? a.weights[(int64_t)((uint32_t)of / (uint32_t)a.parts) * a.k + lane] : 1.f;
+    };
+    int next = Ring<ES>::token_rows(a, u, live);
+    float next_weight = weights(u);
+    ring.start(a, ring_smem, live);
+    for (; u < a.units; u += Ring<ES>::total()) {
+        const int mine = next;
+        const float weight = next_weight;
+        next = Ring<ES>::token_rows(a, u + Ring<ES>::total(), live);
+        next_weight = weights(u + Ring<ES>::total());
+        int t, c, end;
+        Ring<ES>::place(a, u, t, c, end);
+        for (; c < end; ++c) {
+            float acc[RING_W][V];
+#pragma unroll
+            for (int i = 0; i < RING_W; ++i)
+#pragma unroll
+                for (int k = 0; k < V; ++k) acc[i][k] = 0.f;
+            for (int j = -ring.own; j < a.k; ++j) {
+                ring.turn(a);
+                const uint4* from = ring.buf + slot * (RING_W * 32);
+                if (++slot == RING_D) slot = 0;
+                if (j < 0) {
+#pragma unroll
+                    for (int i = 0; i < RING_W; ++i) to_floats<ES>(from[32 * i], acc[i], f16);
+                    continue;
+                }
+                const float w = __shfl_sync(0xffffffffu, weight, j);
+                if (__shfl_sync(0xffffffffu, mine, j) < 0) continue;
+#pragma unroll
+                for (int i = 0; i < RING_W; ++i) {
+                    float v[V];
+                    to_floats<ES>(from[32 * i], v, f16);
+#pragma unroll
+                    for (int k = 0; k < V; ++k) acc[i][k] = fmaf(w, v[k], acc[i][k]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < RING_W; ++i) {
+                const int at = (c * RING_W + i) * 32 + lane;
+                if (at < a.slots) put_piece<ES>(a.out, (int64_t)t * a.hidden, at, from_floats<ES>(acc[i], f16));
+            }
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
@@ -658,6 +796,35 @@ int launch_token_rows(K kernel, RowArgs& a, int step, int sms, cudaStream_t s, c
     const int each = (int)std::max<int64_t>(1, std::min<int64_t>(steps, a.tokens * steps / ((int64_t)sms * 64)));
     a.span = each * step;
     return launch_rows(kernel, a, (a.tokens + RT / 32 - 1) / (RT / 32), (steps + each - 1) / each, s, what);
+}
+
+// Whether combine goes by rings, and the units then: whole tokens, or chunks of
+// them while that leaves warps without any.  Rows whose chunks are half empty gain
+// nothing (16384 x 512 bf16, 8 choices: 34 us against 33; x 1032 43 both ways), few
+// units neither (64 tokens of 2048: 5.2 against 3.5; 256: 5.5 against 5.9).
+bool set_ring(RowArgs& a, int sms) {
+    const int chunks = (a.slots + 32 * RING_W - 1) / (32 * RING_W);
+    if (a.k > 32 || a.slots <= chunks * 16 * RING_W || a.tokens * chunks < 4 * (int64_t)sms) return false;
+    const int64_t warps = (int64_t)sms * RING_CTAS * (RT / 32);
+    a.span = (int)std::max<int64_t>(1, std::min<int64_t>(chunks, a.tokens * chunks / (warps * 2)));
+    a.parts = (chunks + a.span - 1) / a.span;
+    a.units = (int)(a.tokens * a.parts);
+    return true;
+}
+
+template <typename K>
+int launch_ring(K kernel, const RowArgs& a, const DevCtx& dc, cudaStream_t s, const char* what) {
+    static OncePer<std::pair<int, int>, int> attr;          // by device and element's size
+    int set = 0;
+    cudaError_t e = attr.get({dc.device, (int)esize(a.dtype)}, &set, [&](int&) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_SMEM);
+    });
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+    const int64_t ctas = std::min<int64_t>((int64_t)dc.sms * RING_CTAS, (a.units + RT / 32 - 1) / (RT / 32));
+    note_launch_begin(KC_OTHER, s);
+    e = launch_pdl(kernel, dim3((unsigned)ctas), dim3(RT), RING_SMEM, s, a);
+    note_launch_end(KC_OTHER, 0.0, s);
+    return e == cudaSuccess ? MUON_OK : cuda_fail(e, what);
 }
 
 }  // namespace
@@ -756,6 +923,8 @@ extern "C" int muon_expert_combine(const void* ys, int64_t tokens, int64_t k, in
     const bool vec = aligned16(ys) && aligned16(y) && aligned16(residual) && (hidden * es) % 16 == 0 &&
                      (!residual || (ld_residual * es) % 16 == 0);
     a.slots = slots_of(a, vec);
+    if (vec && set_ring(a, dc.sms))
+        return launch_ring(es == 2 ? combine_ring_kernel<2> : combine_ring_kernel<4>, a, dc, s, "expert combine launch");
     auto kern = es == 2 ? (vec ? combine_kernel<2, true> : combine_kernel<2, false>)
                         : (vec ? combine_kernel<4, true> : combine_kernel<4, false>);
     return launch_token_rows(kern, a, vec ? 32 : 128, dc.sms, s, "expert combine launch");

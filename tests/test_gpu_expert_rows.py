@@ -251,3 +251,30 @@ def test_large_values(mg):
     ys[row_of[1, 1]] = float("nan")
     y = mg.muon_expert_combine(ys, row_of, bounds, weights=torch.tensor([[1.0, 1.0], [1.0, 0.0], [2.0, 5.0]], device="cuda"))
     assert torch.isinf(y[0]).all() and torch.isnan(y[1]).all() and (y[2] == 2).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("shape", [(4000, 1, 3, 520), (3700, 2, 8, 1032), (700, 32, 40, 1024), (700, 33, 40, 1024), (615, 3, 4, 4096),
+                                   (9001, 3, 5, 640)], ids=str)
+def test_rows_of_many_tokens(mg, shape, dtype):
+    """Tokens enough for combine's copies ahead: units of one chunk and of more, whole and ragged chunks, one choice to
+    as many as a warp has lanes, and one more."""
+    check_rows(mg, *shape, dtype)
+
+
+def test_many_tokens_outside_and_pitched(mg):
+    tokens, k, hidden = 2000, 4, 1048
+    check_rows(mg, tokens, k, 8, hidden, "bf16", dropped=0.0, pitch=hidden + 24)
+    check_rows(mg, tokens, k, 8, hidden, "f32", dropped=1.1)
+    ys = rand(tokens * k, hidden, "bf16", 2)
+    row_of = torch.randint(-50, tokens * k + 50, (tokens, k), generator=gen(3), device="cuda", dtype=torch.int32)
+    row_of[::7, 0] = 2 ** 31 - 1
+    live = tokens * k - 1000
+    bounds = torch.tensor([0, live], dtype=torch.int32, device="cuda")
+    ys[live:] = float("nan")
+    y = mg.muon_expert_combine(ys, row_of, bounds)
+    on = (row_of >= 0) & (row_of < live)
+    rows = torch.where(on, row_of, torch.zeros_like(row_of)).long()
+    part = ys[rows].double() * on[..., None]
+    size = f64(part.abs().sum(1))
+    close(y, f64(part.sum(1)), (k + 2) * E24 * size, "bf16", "y")
