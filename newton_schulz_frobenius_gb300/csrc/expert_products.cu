@@ -1233,7 +1233,9 @@ extern "C" int muon_expert_glu_backward(const void* x, const void* w_gate, const
         if ((r = zero_weights(dw_gate, bytes, s)) || (r = zero_weights(dw_up, bytes, s))) return r;
         return MUON_OK;
     }
-    Operand X{x, rows, hidden, hidden}, G{w_gate, num_experts * ffn, hidden, hidden}, U{w_up, num_experts * ffn, hidden, hidden};
+    // (operands of products that are not asked for have no rows to pad)
+    Operand X{x, dw_gate ? rows : 0, hidden, hidden}, G{w_gate, dx ? num_experts * ffn : 0, hidden, hidden}, U = G;
+    U.p = w_up;
     const int64_t ldw = pad8(ffn);
     const size_t half = align_up((size_t)rows * ldw * 2, 256);
     size_t part = 0;
@@ -1257,8 +1259,10 @@ extern "C" int muon_expert_glu_backward(const void* x, const void* w_gate, const
     std::memset(&maps, 0, sizeof maps);
     g.out[0] = GluOut{dx, hidden}; g.out[1] = GluOut{dw_gate, hidden}; g.out[2] = GluOut{dw_up, hidden};
     g.tma_out = tma_ok(dx, hidden) && tma_ok(dw_gate, hidden) && tma_ok(dw_up, hidden);
-    bool ok = map_columns(&maps.a[0], G, dtype, &g.whole_a, num_experts) && map_columns(&maps.a[1], U, dtype, &g.whole_a, num_experts) &&
-              map_rows(maps.b[0], DG, dtype) && map_rows(maps.b[1], DU, dtype);
+    bool ok = true;
+    if (dx)
+        ok = map_columns(&maps.a[0], G, dtype, &g.whole_a, num_experts) && map_columns(&maps.a[1], U, dtype, &g.whole_a, num_experts) &&
+             map_rows(maps.b[0], DG, dtype) && map_rows(maps.b[1], DU, dtype);
     if (ok && g.tma_out && dx) ok = map_out(&maps.out[0], g.out[0], dtype, rows, hidden);
     if (ok && g.tma_out && dw_gate)
         ok = map_wide(&maps.out[1], g.out[1], dtype, ffn, hidden, num_experts) &&
@@ -1316,7 +1320,7 @@ extern "C" int muon_expert_linear_backward(const void* x, const void* w, const v
     int64_t most = 0;
     if ((r = set_tiles(g, in, 2 * GM, out, 1, dw ? 1 : 0, out, in, &most))) return r;
     if (rows == 0) return zero_weights(dw, (size_t)(num_experts * in * out) * 2, s);
-    Operand X{x, rows, in, in}, W{w, num_experts * out, in, in}, D{dy, rows, out, out};
+    Operand X{x, dw ? rows : 0, in, in}, W{w, dx ? num_experts * out : 0, in, in}, D{dy, rows, out, out};
     size_t part = 0;
     if ((r = part_bytes<BACKWARD>(g, most, dc, &part))) return r;
     const size_t pads = padded_bytes(X) + padded_bytes(W) + padded_bytes(D);
@@ -1329,7 +1333,7 @@ extern "C" int muon_expert_linear_backward(const void* x, const void* w, const v
     std::memset(&maps, 0, sizeof maps);
     g.out[0] = GluOut{dx, in}; g.out[1] = GluOut{dw, in};
     g.tma_out = tma_ok(dx, in) && tma_ok(dw, in);
-    bool ok = map_columns(&maps.a[0], W, dtype, &g.whole_a, num_experts) && map_rows(maps.b[0], D, dtype);
+    bool ok = !dx || (map_columns(&maps.a[0], W, dtype, &g.whole_a, num_experts) && map_rows(maps.b[0], D, dtype));
     if (ok && g.tma_out && dx) ok = map_out(&maps.out[0], g.out[0], dtype, rows, in);
     if (ok && g.tma_out && dw) ok = map_wide(&maps.out[1], g.out[1], dtype, out, in, num_experts);
     if (!ok) return fail(MUON_ECUDA, "tensor map creation failed");

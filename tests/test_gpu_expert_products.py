@@ -384,3 +384,23 @@ def test_wide_and_narrow_experts(mg):
     for hidden, ffn in ((64, 320), (320, 64), (448, 128), (127, 192), (192, 65)):
         check_glu(mg, [33, 64, 0, 200], hidden, ffn, "bf16", tail=1)
         check_linear(mg, [33, 64, 0, 200], hidden, ffn, "f16", tail=1)
+
+
+def test_gradients_alone_of_odd_sizes(mg):
+    """Operands of the products that are not asked for are not copied; the others' results stay as they are."""
+    import ctypes
+    args, (dx, dwg, dwu) = check_glu(mg, [40, 0, 100], 73, 135, "f16", tail=4)
+    largs, (_, dlx, dw) = check_linear(mg, [40, 0, 100], 73, 135, "f16", tail=4)
+    none, *got = mg.muon_expert_glu_backward(*args, need_dx=False)
+    assert none is None and all(torch.equal(a, b) for a, b in zip(got, (dwg, dwu)))
+    none, got = mg.muon_expert_linear_backward(*largs, need_dx=False)
+    assert none is None and torch.equal(got, dw)
+    for name, ins, want, rest in (("muon_expert_glu_backward", args, dx, (None, None, 144, 3, 73, 135, mg.MUON_F16, 0)),
+                                  ("muon_expert_linear_backward", largs, dlx, (None, 144, 3, 73, 135, mg.MUON_F16))):
+        got, need, s = torch.full_like(want, NAN), ctypes.c_int64(0), torch.cuda.current_stream().cuda_stream
+        call = [t.data_ptr() for t in ins] + [got.data_ptr(), *rest]
+        assert getattr(mg.lib(), name)(*call, None, ctypes.byref(need), s) == mg.MUON_ENOMEM
+        scratch = torch.empty(need.value, dtype=torch.uint8, device="cuda")
+        assert getattr(mg.lib(), name)(*call, scratch.data_ptr(), ctypes.byref(need), s) == mg.MUON_OK
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
