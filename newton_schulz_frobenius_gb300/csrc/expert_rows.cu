@@ -27,18 +27,22 @@ constexpr int64_t MAX_HIDDEN = 1 << 20;
 // sort
 // ---------------------------------------------------------------------------
 //
-// A stable counting sort in one launch of one cluster.  Every warp takes a run
-// of consecutive slots and counts them by expert in its own row of a table;
-// columns are summed over the CTA's warps and, through distributed shared
+// A stable counting sort, up to 131072 slots in one launch of one cluster.  Every
+// warp takes a run of consecutive slots and counts them by expert in its own row of
+// a table; columns are summed over the CTA's warps and, through distributed shared
 // memory, over the cluster's CTAs before it, experts are summed in order, and a
 // second walk over the same slots hands out the places.  Within 32 slots equal
 // experts find each other by votes, so nothing depends on scheduling.  Bound by
-// latency: 4.8 us for 16384 slots and 64 experts, 8.0 for 65536, 12.6 for 131072
-// (back to back in a graph), beyond that by the sixteen SMs' scattered stores.
+// latency: 4.8 us for 16384 slots and 64 experts, 8.0 for 65536, 12.4 for 131072
+// (back to back in a graph).  More slots are sorted by the whole device in three
+// launches: the CTAs' counts (left in slot_of, which is not written until the last),
+// the places, and slot_of from them; 2^20 slots 26 us, 2^22 78 (one cluster, bound by
+// its SMs' instructions and scattered stores: 95 and 342; at 131072 both take 12.3).
 constexpr int SORT_T = 1024;
 constexpr int SORT_WARPS = SORT_T / 32;
 constexpr int SORT_CLUSTER = 16;
 constexpr int SORT_AHEAD = 8;       // loads of a warp in flight
+enum SortStep : int { SORTED = 0, COUNTS = 1, PLACES = 2 };        // all in one cluster; the first two of three launches
 
 struct SortArgs {
     const void* experts;
@@ -82,6 +86,7 @@ __device__ __forceinline__ int expert_of(const SortArgs& a, int64_t i, int64_t l
     return e >= 0 && e < a.experts_n ? e : a.experts_n;
 }
 
+template <int STEP>
 __global__ void __launch_bounds__(SORT_T, 1) expert_sort_kernel(const __grid_constant__ SortArgs a) {
     extern __shared__ uint32_t sort_smem[];
     const int E = a.experts_n, bins = E + 1;
@@ -89,7 +94,7 @@ __global__ void __launch_bounds__(SORT_T, 1) expert_sort_kernel(const __grid_con
     uint32_t* total = table + SORT_WARPS * bins;        // [bins] of this CTA, read by the others
     __shared__ uint32_t sums[SORT_WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)tc::cluster_ctarank(), C = (int)gridDim.x;
+    const int rank = (int)blockIdx.x, C = (int)gridDim.x;          // (in one cluster: the CTA's rank there)
     for (int i = threadIdx.x; i < SORT_WARPS * bins; i += SORT_T) table[i] = 0;
     __syncthreads();
     pdl_wait();
@@ -127,25 +132,32 @@ __global__ void __launch_bounds__(SORT_T, 1) expert_sort_kernel(const __grid_con
             table[w * bins + b] = n;
             n += c;
         }
-        total[b] = n;
+        if (STEP == COUNTS) a.slot_of[rank * bins + b] = (int)n;
+        else total[b] = n;
     }
-    tc::cluster_sync();
+    if (STEP == COUNTS) return;
+    if (STEP == SORTED) tc::cluster_sync();
     // all CTAs' counts of expert threadIdx.x, and those of the CTAs before this one
     uint32_t all = 0, before = 0, rest = 0, none = 0;
     auto counts = [&](int bin, uint32_t& upto_here, uint32_t& of_all) {
-        uint32_t n[SORT_CLUSTER];           // all on their way before the first is used
+        for (int c0 = 0; c0 < (STEP == SORTED ? 1 : C); c0 += SORT_CLUSTER) {
+            uint32_t n[SORT_CLUSTER];       // all on their way before the first is used
 #pragma unroll
-        for (int c = 0; c < SORT_CLUSTER; ++c) n[c] = c < C ? ld_cluster(total + bin, (uint32_t)c) : 0;
+            for (int c = 0; c < SORT_CLUSTER; ++c)
+                n[c] = c0 + c >= C ? 0
+                       : STEP == SORTED ? ld_cluster(total + bin, (uint32_t)c) : (uint32_t)a.slot_of[(c0 + c) * bins + bin];
 #pragma unroll
-        for (int c = 0; c < SORT_CLUSTER; ++c) {
-            if (c < rank) upto_here += n[c];
-            of_all += n[c];
+            for (int c = 0; c < SORT_CLUSTER; ++c) {
+                if (c0 + c < rank) upto_here += n[c];
+                of_all += n[c];
+            }
         }
     };
     if ((int)threadIdx.x < E) counts(threadIdx.x, before, all);
     if (threadIdx.x == SORT_T - 1) counts(E, rest, none);
     __syncwarp();
-    tc::cluster_sync();                 // the others have read this CTA's counts
+    if (STEP == SORTED) tc::cluster_sync();             // the others have read this CTA's counts
+    else __syncthreads();
     uint32_t upto = all;                // inclusive sum over experts
     for (int d = 1; d < 32; d <<= 1) {
         const uint32_t n = __shfl_up_sync(0xffffffffu, upto, d);
@@ -181,11 +193,18 @@ __global__ void __launch_bounds__(SORT_T, 1) expert_sort_kernel(const __grid_con
                 if (lane == __ffs((int)same[r]) - 1) mine[e[r]] = at + (uint32_t)__popc(same[r]);
                 const int row = (int)(total[e[r]] + at + (uint32_t)__popc(same[r] & ((1u << lane) - 1)));
                 a.row_of[i + 32 * r + lane] = row;
-                a.slot_of[row] = (int)(i + 32 * r + lane);
+                if (STEP == SORTED) a.slot_of[row] = (int)(i + 32 * r + lane);
             }
             __syncwarp();
         }
     }
+}
+
+// slot_of, after the launches of COUNTS and PLACES: every row has one slot.
+__global__ void __launch_bounds__(256) expert_invert_kernel(const int* row_of, int* slot_of, int slots) {
+    pdl_wait();
+    pdl_trigger();
+    for (int i = blockIdx.x * 1024 + threadIdx.x, n = 0; n < 4 && i < slots; i += 256, ++n) slot_of[row_of[i]] = i;
 }
 
 // ---------------------------------------------------------------------------
@@ -798,6 +817,40 @@ int launch_token_rows(K kernel, RowArgs& a, int step, int sms, cudaStream_t s, c
     return launch_rows(kernel, a, (a.tokens + RT / 32 - 1) / (RT / 32), (steps + each - 1) / each, s, what);
 }
 
+template <int STEP>
+int launch_sort(const SortArgs& a, int C, const DevCtx& dc, cudaStream_t s) {
+    static OncePer<int, int> attr;          // by device
+    int set = 0;
+    cudaError_t e = attr.get(dc.device, &set, [&](int&) {
+        cudaError_t r = cudaFuncSetAttribute(expert_sort_kernel<STEP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (SORT_WARPS + 1) * (MAX_EXPERTS + 1) * 4);
+        if (r == cudaSuccess && STEP == SORTED)
+            r = cudaFuncSetAttribute(expert_sort_kernel<STEP>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        return r;
+    });
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)C);
+    cfg.blockDim = dim3(SORT_T);
+    cfg.dynamicSmemBytes = (size_t)(SORT_WARPS + 1) * (size_t)(a.experts_n + 1) * 4;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = pdl_enabled() ? 1 : 0;
+    if (STEP == SORTED) {
+        cudaLaunchAttribute& c = at[cfg.numAttrs++];
+        c.id = cudaLaunchAttributeClusterDimension;
+        c.val.clusterDim.x = (unsigned)C;
+        c.val.clusterDim.y = c.val.clusterDim.z = 1;
+    }
+    note_launch_begin(KC_OTHER, s);
+    e = cudaLaunchKernelEx(&cfg, expert_sort_kernel<STEP>, a);
+    note_launch_end(KC_OTHER, 0.0, s);
+    return e == cudaSuccess ? MUON_OK : cuda_fail(e, "expert sort launch");
+}
+
 // Whether combine goes by rings, and the units then: whole tokens, or chunks of
 // them while that leaves warps without any.  Rows whose chunks are half empty gain
 // nothing (16384 x 512 bf16, 8 choices: 34 us against 33; x 1032 43 both ways), few
@@ -846,41 +899,29 @@ extern "C" int muon_expert_sort(const void* experts, int index_dtype, int64_t sl
     DevCtx dc;
     if ((r = get_dev(dc))) return r;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    int C = 1;                              // CTAs: a slot per thread until the cluster is full
-    while (C < SORT_CLUSTER && (int64_t)C * SORT_T < slots) C *= 2;
     SortArgs a;
     a.experts = experts;
     a.index64 = index_dtype == MUON_I64;
     a.slots = (int)slots;
     a.experts_n = (int)num_experts;
-    a.per_warp = (int)((slots + (int64_t)C * SORT_T - 1) / ((int64_t)C * SORT_T)) * 32;
     a.row_of = row_of; a.slot_of = slot_of; a.bounds = bounds;
-    static OncePer<int, int> attr;          // by device
-    int set = 0;
-    const size_t most = (size_t)(SORT_WARPS + 1) * (MAX_EXPERTS + 1) * 4;
-    cudaError_t e = attr.get(dc.device, &set, [&](int&) {
-        cudaError_t r = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
-        if (r == cudaSuccess) r = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        return r;
-    });
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)C);
-    cfg.blockDim = dim3(SORT_T);
-    cfg.dynamicSmemBytes = (size_t)(SORT_WARPS + 1) * (size_t)(num_experts + 1) * 4;
-    cfg.stream = s;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)C;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = pdl_enabled() ? 2 : 1;
-    note_launch_begin(KC_OTHER, s);
-    e = cudaLaunchKernelEx(&cfg, expert_sort_kernel, a);
-    note_launch_end(KC_OTHER, 0.0, s);
-    return e == cudaSuccess ? MUON_OK : cuda_fail(e, "expert sort launch");
+    if (slots > (int64_t)SORT_CLUSTER * SORT_T * SORT_AHEAD) {
+        // more than a cluster's warps keep in registers; 128 slots or more to a warp
+        // (262144 slots, 64 experts: 14.9 us, with 64 17.6, with 256 18.5), counts that slot_of has room for
+        int64_t C = std::min<int64_t>(dc.sms, std::min<int64_t>(slots / (128 * SORT_WARPS), slots / (num_experts + 1)));
+        a.per_warp = (int)((slots + C * SORT_T - 1) / (C * SORT_T)) * 32;
+        C = (slots + (int64_t)a.per_warp * SORT_WARPS - 1) / ((int64_t)a.per_warp * SORT_WARPS);
+        if ((r = launch_sort<COUNTS>(a, (int)C, dc, s)) || (r = launch_sort<PLACES>(a, (int)C, dc, s))) return r;
+        note_launch_begin(KC_OTHER, s);
+        const cudaError_t e = launch_pdl(expert_invert_kernel, dim3((unsigned)((slots + 1023) / 1024)), dim3(256), 0, s,
+                                         (const int*)row_of, slot_of, (int)slots);
+        note_launch_end(KC_OTHER, 0.0, s);
+        return e == cudaSuccess ? MUON_OK : cuda_fail(e, "expert sort launch");
+    }
+    int C = 1;                              // CTAs: a slot per thread until the cluster is full
+    while (C < SORT_CLUSTER && (int64_t)C * SORT_T < slots) C *= 2;
+    a.per_warp = (int)((slots + (int64_t)C * SORT_T - 1) / ((int64_t)C * SORT_T)) * 32;
+    return launch_sort<SORTED>(a, C, dc, s);
 } MUON_CATCH_ALL
 
 extern "C" int muon_expert_dispatch(const void* x, int64_t ldx, int64_t tokens, int64_t k, int64_t hidden, int dtype,

@@ -85,6 +85,43 @@ def test_sort_many_slots(mg):
     assert torch.equal(bounds.long(), torch.searchsorted(flat[want].contiguous(), torch.arange(1025, device="cuda")))
 
 
+@pytest.mark.parametrize("slots,experts", [(131072, 64), (131073, 64), (131073, 1024), (262144, 1), (700001, 8), (1 << 20, 257)])
+def test_sort_by_the_whole_device(mg, slots, experts):
+    """Around the most slots that one cluster sorts, and beyond; some experts empty, all slots in one, none in any."""
+    for e in (choices(slots, 1, experts, dropped=0.05), choices(slots, 1, max(1, experts // 3), seed=4, dtype=torch.int64),
+              torch.full((slots, 1), experts - 1, device="cuda"), torch.full((slots, 1), -1, device="cuda")):
+        row_of, slot_of, bounds = mg.muon_expert_sort(e, experts)
+        flat = e.reshape(-1).long()
+        flat = torch.where(flat < 0, torch.full_like(flat, experts), flat)
+        want = torch.argsort(flat, stable=True)
+        assert torch.equal(slot_of.long(), want)
+        assert torch.equal(row_of.reshape(-1)[want].long(), torch.arange(slots, device="cuda"))
+        assert torch.equal(bounds.long(), torch.searchsorted(flat[want].contiguous(), torch.arange(experts + 1, device="cuda")))
+
+
+def test_sorts_at_once_and_in_a_graph(mg):
+    """Large sorts on two streams at once, and replayed on new choices."""
+    a, b = choices(300000, 1, 64), choices(200000, 2, 9, seed=3)
+    want = mg.muon_expert_sort(a, 64), mg.muon_expert_sort(b, 9)
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, (e, n) in enumerate(((a, 64), (b, 9))):
+            got[i].append(mg.muon_expert_sort(e, n, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, y) for g in got[i] for x, y in zip(g, want[i]))
+    g = torch.cuda.CUDAGraph()
+    e = a.clone()
+    with torch.cuda.graph(g):
+        out = mg.muon_expert_sort(e, 64)
+    for seed in (11, 12):
+        e.copy_(choices(300000, 1, 64, seed=seed))
+        g.replay()
+        assert all(torch.equal(x, y) for x, y in zip(out, mg.muon_expert_sort(e, 64)))
+
+
 def test_sort_extremes(mg):
     check_sort(mg, torch.full((700, 3), 4, dtype=torch.int32, device="cuda"), 9)        # one expert takes all
     check_sort(mg, torch.full((700, 3), -1, dtype=torch.int32, device="cuda"), 9)       # nobody takes any
