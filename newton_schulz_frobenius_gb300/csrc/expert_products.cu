@@ -18,7 +18,7 @@
 // follows the expert (32, or in steps of 64).  An expert's rows are cut into
 // ceil(rows / 256) tiles of nearly equal extent, so that ragged or small experts
 // cost little more than their rows.  The epilogue turns 32 x 32 chunks
-// around through the neighbour lane.  In the gated forward pass each CTA's M side
+// around in shared memory.  In the gated forward pass each CTA's M side
 // is 64 rows of Wg and the same 64 of Wu: gate and value of a result are in two
 // warps, which exchange half of their rows through shared memory.  (Sixteen rows of
 // each in turn would put them in one warp, but eight copies of 2 KB per stage and
@@ -40,10 +40,14 @@
 // whose last tiles are smaller, 2.25-2.4, 1.1 and 2.35.  With short ones (64 experts of
 // 512 rows, 2048 x 1024) a tile's epilogue beside its 8 to 32 k-blocks, 55-65 % of the
 // product's floor; with few rows HBM (16 rows through 8 experts of 2048 x 8192: 75 us,
-// 6.4 TB/s).  An epilogue of sixteen warps (of 96 registers) and plain instead of tile
-// stores were built and were slower.
+// 6.4 TB/s), and in the weights' gradients of few rows HBM's rate of writes alone.  An
+// epilogue of sixteen warps (of 96 registers), plain instead of tile stores, and the weights'
+// tiles prefetched into L2 ahead of the ring (gated forward of the even experts above 2.1 ->
+// 2.5 ms) were built and were slower.
 #include "epilogue.cuh"
 #include "glu_parts.cuh"
+
+#include <climits>
 
 namespace muon {
 
@@ -142,7 +146,7 @@ struct Div {
 struct ExpArgs {
     int dtype, act;
     int save;                   // gated forward: G and U leave too
-    int tma_out;                // outputs leave through tile stores
+    int tma_out;                // outputs' rows start on 16 bytes
     int whole_a, whole_a2, whole_b2;        // MN-major operands' maps are by blocks of 64 columns
     int rows, experts;
     const int* bounds;
@@ -321,11 +325,9 @@ struct Place {
     int rows, cols, r0, c0, z, z_rows;
 };
 
-// Whether a chunk leaves as a tile: a tile store ends with the matrix, an
+// Whether a chunk of `n` rows leaves as a tile: a tile store ends with the matrix, an
 // expert's last rows leave row by row.
-__device__ __forceinline__ bool as_tile(const ExpArgs& g, const Place& p) {
-    return g.tma_out && (p.r0 + 32 <= p.rows || p.rows == p.z_rows);
-}
+__device__ __forceinline__ bool as_tile(const Place& p, int n) { return p.r0 + n <= p.rows || p.rows == p.z_rows; }
 
 // The warp's next output buffer, once the store that last used it has read it.
 __device__ __forceinline__ uint8_t* out_buffer(uint8_t* stage, int groups, bool tile) {
@@ -339,24 +341,40 @@ __device__ __forceinline__ uint8_t* out_buffer(uint8_t* stage, int groups, bool 
     return stage + (groups & 1) * OUT_BYTES;
 }
 
+__device__ __forceinline__ uint32_t pack2_h(float lo, float hi, bool f16) {
+    if (f16) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // Offset of 16-byte piece k of row r in a chunk: 64-byte swizzle, piece k at k ^ ((r / 2) % 4).
 __device__ __forceinline__ int piece_at(int r, int k) { return r * 64 + ((k ^ ((r >> 1) & 3)) << 4); }
 
-// A chunk that does not leave as a tile: rows up to p.rows.
-__device__ __forceinline__ void store_rows(const ExpArgs& g, const GluOut& o, const Place& p, const uint8_t* buf) {
-    const int lane = threadIdx.x & 31, n = min(32, p.rows - p.r0);
+// A chunk of a matrix whose rows start on 16 bytes that does not leave as a tile: rows up to
+// p.rows, eight of them per step.
+__device__ __forceinline__ void store_rows(const GluOut& o, const Place& p, const uint8_t* buf) {
+    const int lane = threadIdx.x & 31, n = min(32, p.rows - p.r0), k = lane & 3;
     uint16_t* out = static_cast<uint16_t*>(o.p) + ((int64_t)p.z * p.z_rows + p.r0) * o.ld + p.c0;
-    if (g.tma_out) {                        // rows start on 16 bytes: eight of them per step
-        const int k = lane & 3;
-        for (int i = lane >> 2; i < n; i += 8)
-            if (p.c0 + 8 * k < p.cols)
-                *reinterpret_cast<uint4*>(out + (int64_t)i * o.ld + 8 * k) =
-                    *reinterpret_cast<const uint4*>(buf + piece_at(i, k));
-    } else if (p.c0 + lane < p.cols) {      // a row's 32 columns per store
-#pragma unroll 8
-        for (int i = 0; i < n; ++i)
-            out[(int64_t)i * o.ld + lane] =
-                *reinterpret_cast<const uint16_t*>(buf + piece_at(i, lane >> 3) + (lane & 7) * 2);
+    for (int i = lane >> 2; i < n; i += 8)
+        if (p.c0 + 8 * k < p.cols)
+            *reinterpret_cast<uint4*>(out + (int64_t)i * o.ld + 8 * k) = *reinterpret_cast<const uint4*>(buf + piece_at(i, k));
+}
+
+// N rows of a chunk of other matrices, a column per lane: a row's 32 columns per store
+// (by way of shared memory 16 experts of 1001 x 2731, 16384 rows, took 305 us, so 249).
+template <int N>
+__device__ __forceinline__ void store_columns(const GluOut& o, const Place& p, const float (&v)[32], bool f16) {
+    const int lane = threadIdx.x & 31, n = p.rows - p.r0;
+    uint16_t* out = static_cast<uint16_t*>(o.p) + ((int64_t)p.z * p.z_rows + p.r0) * o.ld + p.c0 + lane;
+    if (p.c0 + lane >= p.cols) return;
+#pragma unroll
+    for (int k = 0; k < N; k += 2) {
+        const uint32_t q = pack2_h(v[k], v[k + 1], f16);
+        if (k < n) out[(int64_t)k * o.ld] = (uint16_t)q;
+        if (k + 1 < n) out[(int64_t)(k + 1) * o.ld] = (uint16_t)(q >> 16);
     }
 }
 
@@ -371,10 +389,11 @@ __device__ __forceinline__ void put_half(const float (&v)[32], int step, bool f1
         *reinterpret_cast<uint4*>(stage + lane * 128 + (((step * 4 + k) ^ (lane & 7)) << 4)) = pack8_h(v + 8 * k, f16);
 }
 
-__device__ __forceinline__ void store_wide(const ExpArgs& g, const CUtensorMap* map, const GluOut& o, const Place& p,
+template <bool TILES>
+__device__ __forceinline__ void store_wide(const CUtensorMap* map, const GluOut& o, const Place& p,
                                            uint8_t* stage, int& groups) {
     const int lane = threadIdx.x & 31;
-    if (g.tma_out) {                        // (a tile store ends with the expert's matrix)
+    if (TILES) {                            // (a tile store ends with the expert's matrix)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
@@ -397,28 +416,31 @@ __device__ __forceinline__ void store_wide(const ExpArgs& g, const CUtensorMap* 
     __syncwarp();
 }
 
-__device__ __forceinline__ uint32_t pack2_h(float lo, float hi, bool f16) {
-    if (f16) {
-        const __half2 h = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
+// Rows k and k + 1 (even k) of a warp's chunk, a column per lane.  (Neighbours that exchanged
+// a value of each pair and stored two columns took longer, for the instructions: 65536
+// rows, 256 experts of 1024 x 512: linear forward 168 us, 119 so; gated 275, 200.)
+__device__ __forceinline__ void put_rows(uint8_t* buf, int k, float lo, float hi, bool f16) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t q = pack2_h(lo, hi, f16);
+    uint16_t* at = reinterpret_cast<uint16_t*>(buf + k * 64 + (((lane >> 3) ^ ((k >> 1) & 3)) << 4) + (lane & 7) * 2);
+    at[0] = (uint16_t)q;
+    at[32] = (uint16_t)(q >> 16);
 }
 
-// One warp's 32 x 32 chunk, a column per lane: neighbours exchange one value of
-// each pair of rows and write two columns of one of them.
+// One warp's 32 x 32 chunk, a column per lane.
+template <bool TILES>
 __device__ __forceinline__ void store_turned(const ExpArgs& g, const CUtensorMap* map, const GluOut& o, const Place& p,
                                              const float (&v)[32], uint8_t* stage, int& groups) {
     const int lane = threadIdx.x & 31;
-    const bool tile = as_tile(g, p), odd = lane & 1, f16 = g.dtype == MUON_F16;
+    const bool tile = as_tile(p, 32), f16 = g.dtype == MUON_F16;
+    if (!TILES) {
+        store_columns<32>(o, p, v, f16);
+        __syncwarp();
+        return;
+    }
     uint8_t* buf = out_buffer(stage, groups, tile);
 #pragma unroll
-    for (int k = 0; k < 32; k += 2) {
-        const float got = __shfl_xor_sync(0xffffffffu, odd ? v[k] : v[k + 1], 1);
-        *reinterpret_cast<uint32_t*>(buf + (k + odd) * 64 + (((lane >> 3) ^ ((k >> 1) & 3)) << 4) + ((lane >> 1) & 3) * 4) =
-            odd ? pack2_h(got, v[k + 1], f16) : pack2_h(v[k], got, f16);
-    }
+    for (int k = 0; k < 32; k += 2) put_rows(buf, k, v[k], v[k + 1], f16);
     if (tile) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (tile) {
@@ -429,7 +451,7 @@ __device__ __forceinline__ void store_turned(const ExpArgs& g, const CUtensorMap
         ++groups;
         return;
     }
-    store_rows(g, o, p, buf);
+    store_rows(o, p, buf);
     __syncwarp();
 }
 
@@ -468,10 +490,11 @@ __device__ __forceinline__ void times_act(const float (&gate)[16], float (&v)[32
 // A pair's 32 x 32 chunk of the gated block, a column per lane, G in one warp and U
 // in the other.  Each stores its own matrix where it is kept; then they exchange half
 // of their rows through their second buffers and write the results of 16 rows each.
+template <bool TILES>
 __device__ __forceinline__ void store_gated(const ExpArgs& g, const CUtensorMap* maps, const Place& p, bool is_up, int id,
                                             float (&v)[32], uint8_t* stage, uint8_t* others, int& groups) {
     const int lane = threadIdx.x & 31;
-    const bool odd = lane & 1, f16 = g.dtype == MUON_F16;
+    const bool f16 = g.dtype == MUON_F16;
     if (g.save) {
         int own = 0;                        // (the first buffer, whatever was stored before)
         const int w = is_up ? 2 : 1;
@@ -479,24 +502,30 @@ __device__ __forceinline__ void store_gated(const ExpArgs& g, const CUtensorMap*
             if (lane == 0) bulk_wait_read0();
             __syncwarp();
         }
-        store_turned(g, &maps[w], g.out[w], p, v, stage, own);
+        store_turned<TILES>(g, &maps[w], g.out[w], p, v, stage, own);
         groups += own;
     } else if (groups > 0) {
         if (lane == 0) bulk_wait_read0();
         __syncwarp();
     }
     // rows 0 .. 15 are the G warp's, rows 16 .. 31 the U warp's
-    float* send = reinterpret_cast<float*>(stage + OUT_BYTES);
-    const float* got = reinterpret_cast<const float*>(others + OUT_BYTES);
+    float4* send = reinterpret_cast<float4*>(stage + OUT_BYTES);
+    const float4* got = reinterpret_cast<const float4*>(others + OUT_BYTES);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) send[k * 32 + lane] = is_up ? v[k] : v[16 + k];
+    for (int k = 0; k < 16; k += 4)
+        send[k * 8 + lane] = is_up ? make_float4(v[k], v[k + 1], v[k + 2], v[k + 3])
+                                   : make_float4(v[16 + k], v[17 + k], v[18 + k], v[19 + k]);
     pair_sync(id);
     float gate[16];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-        const float o = got[k * 32 + lane];
-        gate[k] = is_up ? o : v[k];
-        v[k] = is_up ? v[16 + k] : o;
+    for (int k = 0; k < 16; k += 4) {
+        const float4 q = got[k * 8 + lane];
+        const float o[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            gate[k + i] = is_up ? o[i] : v[k + i];
+            v[k + i] = is_up ? v[16 + k + i] : o[i];
+        }
     }
     pair_sync(id);                          // the other has read this warp's
     if (g.act == ACT_GELU) times_act<ACT_GELU>(gate, v);
@@ -505,14 +534,15 @@ __device__ __forceinline__ void store_gated(const ExpArgs& g, const CUtensorMap*
     Place mine = p;
     mine.r0 += is_up ? 16 : 0;
     if (mine.r0 >= p.rows) return;
-    const bool tile = g.tma_out && (mine.r0 + 16 <= p.rows || p.rows == p.z_rows);
+    if (!TILES) {
+        store_columns<16>(g.out[0], mine, v, f16);
+        __syncwarp();
+        return;
+    }
+    const bool tile = as_tile(mine, 16);
     uint8_t* buf = stage + OUT_BYTES;
 #pragma unroll
-    for (int k = 0; k < 16; k += 2) {
-        const float other = __shfl_xor_sync(0xffffffffu, odd ? v[k] : v[k + 1], 1);
-        *reinterpret_cast<uint32_t*>(buf + (k + odd) * 64 + (((lane >> 3) ^ ((k >> 1) & 3)) << 4) + ((lane >> 1) & 3) * 4) =
-            odd ? pack2_h(other, v[k + 1], f16) : pack2_h(v[k], other, f16);
-    }
+    for (int k = 0; k < 16; k += 2) put_rows(buf, k, v[k], v[k + 1], f16);
     if (tile) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (tile) {
@@ -524,11 +554,13 @@ __device__ __forceinline__ void store_gated(const ExpArgs& g, const CUtensorMap*
         return;
     }
     mine.rows = min(p.rows, mine.r0 + 16);
-    store_rows(g, g.out[0], mine, buf);
+    store_rows(g.out[0], mine, buf);
     __syncwarp();
 }
 
-template <int MODE>
+// TILES: the outputs' rows start on 16 bytes, so that chunks can leave by tile stores (a
+// form of its own: the code of the other between costs the gated forward pass 2 %).
+template <int MODE, bool TILES>
 __global__ void __launch_bounds__(GT, 1)
 expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpArgs g) {
     extern __shared__ uint8_t smem_raw[];
@@ -754,11 +786,11 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
                         __syncwarp();
                     }
                     put_half(v, ch & 1, g.dtype == MUON_F16, stage);
-                    if ((ch & 1) || ch + 1 == chunks) store_wide(g, &maps.out[o], g.out[o], c, stage, groups);
+                    if ((ch & 1) || ch + 1 == chunks) store_wide<TILES>(&maps.out[o], g.out[o], c, stage, groups);
                 } else {
                     c.r0 += 32 * ch;
-                    if (MODE == FWD_GLU) store_gated(g, maps.out, c, q >= 2, pair, v, stage, others, groups);
-                    else store_turned(g, &maps.out[0], g.out[0], c, v, stage, groups);
+                    if (MODE == FWD_GLU) store_gated<TILES>(g, maps.out, c, q >= 2, pair, v, stage, others, groups);
+                    else store_turned<TILES>(g, &maps.out[0], g.out[0], c, v, stage, groups);
                 }
             };
             if (t.blocks == 0) {
@@ -1071,22 +1103,28 @@ bool map_rows(CUtensorMap (&m)[BOXES], const Operand& o, int dtype) {
 
 template <int MODE>
 cudaError_t clusters_at_once(int device, int* n) {
-    static OncePer<int, int> fits;          // by device: pairs resident at once
+    static OncePer<int, int> fits;          // by device: pairs resident at once, of either form
     return fits.get(device, n, [&](int& v) {
-        cudaError_t e = cudaFuncSetAttribute(expert_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, EXP_SMEM);
-        if (e != cudaSuccess) return e;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2);
-        cfg.blockDim = dim3(GT);
-        cfg.dynamicSmemBytes = EXP_SMEM;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = 2;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&v, expert_kernel<MODE>, &cfg);
-        return e == cudaSuccess && v < 1 ? cudaErrorInvalidConfiguration : e;
+        v = INT_MAX;
+        for (auto kernel : {expert_kernel<MODE, false>, expert_kernel<MODE, true>}) {
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, EXP_SMEM);
+            if (e != cudaSuccess) return e;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(2);
+            cfg.blockDim = dim3(GT);
+            cfg.dynamicSmemBytes = EXP_SMEM;
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim.x = 2;
+            at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+            cfg.attrs = at;
+            cfg.numAttrs = 1;
+            int one = 0;
+            e = cudaOccupancyMaxActiveClusters(&one, kernel, &cfg);
+            if (e != cudaSuccess || one < 1) return e == cudaSuccess ? cudaErrorInvalidConfiguration : e;
+            v = std::min(v, one);
+        }
+        return cudaSuccess;
     });
 }
 
@@ -1109,7 +1147,7 @@ int launch_expert(const ExpMaps& maps, const ExpArgs& g, int64_t most, double wo
     cfg.attrs = at;
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
     note_launch_begin(KC_GLU, s);
-    e = cudaLaunchKernelEx(&cfg, expert_kernel<MODE>, maps, g);
+    e = cudaLaunchKernelEx(&cfg, g.tma_out ? expert_kernel<MODE, true> : expert_kernel<MODE, false>, maps, g);
     note_launch_end(KC_GLU, work, s);
     return e == cudaSuccess ? MUON_OK : cuda_fail(e, "expert products launch");
 }
