@@ -85,7 +85,7 @@ def test_sort_many_slots(mg):
     assert torch.equal(bounds.long(), torch.searchsorted(flat[want].contiguous(), torch.arange(1025, device="cuda")))
 
 
-@pytest.mark.parametrize("slots,experts", [(131072, 64), (131073, 64), (131073, 1024), (262144, 1), (700001, 8), (1 << 20, 257)])
+@pytest.mark.parametrize("slots,experts", [(131072, 64), (131073, 64), (131073, 1024), (262144, 1), (700001, 8), (1 << 20, 257), (1 << 24, 1024)])
 def test_sort_by_the_whole_device(mg, slots, experts):
     """Around the most slots that one cluster sorts, and beyond; some experts empty, all slots in one, none in any."""
     for e in (choices(slots, 1, experts, dropped=0.05), choices(slots, 1, max(1, experts // 3), seed=4, dtype=torch.int64),
