@@ -38,12 +38,12 @@
 // experts of 4096 x 14336, 16384 rows, even: gated forward 1.97-2.1 ms (1.83-1.95
 // PFLOP/s), linear forward 1.06 (1.81), linear backward 2.25 (1.71); uneven experts,
 // whose last tiles are smaller, 2.25-2.4, 1.1 and 2.35.  With short ones (64 experts of
-// 512 rows, 2048 x 1024) a tile's epilogue beside its 8 to 32 k-blocks, 55-65 % of the
+// 512 rows, 2048 x 1024) a tile's epilogue beside its 8 to 32 k-blocks, 60-70 % of the
 // product's floor; with few rows HBM (16 rows through 8 experts of 2048 x 8192: 75 us,
 // 6.4 TB/s), and in the weights' gradients of few rows HBM's rate of writes alone.  An
 // epilogue of sixteen warps (of 96 registers), plain instead of tile stores, and the weights'
-// tiles prefetched into L2 ahead of the ring (gated forward of the even experts above 2.1 ->
-// 2.5 ms) were built and were slower.
+// tiles prefetched into L2 ahead of the ring (gated forward of those uneven experts 2.1-2.2 ->
+// 2.55 ms) were built and were slower.
 #include "epilogue.cuh"
 #include "glu_parts.cuh"
 
