@@ -480,10 +480,13 @@ __device__ __forceinline__ void times_act(const float (&gate)[16], float (&v)[32
         }
         // g sigmoid(z), as activate() has it but for the quotient: two ulp instead of half
         // of one, far below the results' rounding, for a third of the instructions (286 us
-        // -> 207 in the case above); a quotient by more than 2^126 is 0, for g below -87
+        // -> 207 in the case above).  With e^-|z| the divisor is between 1 and 2: the fast
+        // quotient by more than 2^126 is 0, which e^-z reaches at z = -87, where bf16 still
+        // holds the result.
         const float x = gate[k];
         const float z = ACT == ACT_SILU ? x : 1.5957691216057308f * x * fmaf(0.044715f * x, x, 1.0f);
-        v[k] *= __fdividef(x, 1.0f + __expf(-z));
+        const float t = __expf(-fabsf(z));
+        v[k] *= __fdividef(z < 0.f ? x * t : x, 1.0f + t);
     }
 }
 
