@@ -523,9 +523,9 @@ int muon_expert_combine_backward(const void* dy, int64_t ld_dy, const void* ys, 
  *            over sides that are multiples of 8 and pointers on 16 bytes need
  *            none; other rows are copied there padded, the weights' too; the
  *            gated backward pass keeps dg and du there (4 bytes per row and ffn
- *            column), and both backward passes 64 rows per expert of what the
- *            weights' gradients contract.  Calls that can run at once, captured
- *            graphs among them, must not share it.
+ *            column), and both backward passes 64 rows per expert (per row, where
+ *            rows are fewer) of what the weights' gradients contract.  Calls that
+ *            can run at once, captured graphs among them, must not share it.
  */
 int muon_expert_glu_forward(const void* x, const void* w_gate, const void* w_up, const int* bounds, void* h,
                             void* gate, void* up, int64_t rows, int64_t num_experts, int64_t hidden, int64_t ffn,

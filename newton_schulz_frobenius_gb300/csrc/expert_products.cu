@@ -156,6 +156,7 @@ struct ExpArgs {
     // family b: the weights' gradients
     int nb;                     // results per expert: 0, 1 or 2
     int rows_b, cols_b, tiles_mb, tiles_nb;
+    int tails_by_row;           // tail_block()
     Div group_a, group_b, rest_b, matrix_b;     // tiles of a group of either family, rows of b's last group, tiles of a result of b
     GluOut out[3];              // H, G, U; Y; or dX, dW, dWu
     float* part;                // running sums of contractions in several parts
@@ -181,6 +182,11 @@ __device__ __forceinline__ void expert_rows(const int* bounds, int rows, int e, 
     first = min(max(lo, 0), rows);
     last = min(max(bounds[e + 1], first), rows);
 }
+
+// The block of the scratch that holds an expert's last k-block: its own, or, where rows
+// are fewer than experts, its first row's, so that no more blocks than rows are
+// kept (256 experts of 7168 x 2048, 64 rows: 92 MB, by experts 369).
+__device__ __forceinline__ int tail_block(bool by_row, int e, int first) { return by_row ? first : e; }
 
 struct Tile {
     int family, which;          // 0: a, 1: b; output index
@@ -647,7 +653,7 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
                                 // a last k-block of fewer rows stands padded with zeros in the scratch
                                 ma = &maps.a2_tail[t.which];
                                 mb = &maps.b2_tail;
-                                k0 = t.e * GK;
+                                k0 = tail_block(g.tails_by_row, t.e, t.first) * GK;
                             }
                             load_columns(a0 + at + i * OP_BYTES, ma, bar, m0, k0, 0, g.whole_a2);
                             load_columns(b0 + at + i * OP_BYTES, mb, bar, n0, k0, 0, g.whole_b2);
@@ -949,13 +955,13 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const __grid_constant__ P
 }
 
 // The experts' last k-blocks of up to three matrices (rows on 16 bytes, pitch ld):
-// block e of dst holds the rows of expert e's last, partial k-block, zeros behind
-// them; experts without one are left out (nothing reads theirs).
+// an expert's tail_block() of dst holds the rows of its last, partial k-block, zeros
+// behind them; experts without one are left out (nothing reads theirs).
 struct TailArgs {
     const void* src[3];
     void* dst[3];
     int64_t ld[3];              // of both
-    int rows;
+    int rows, by_row;
     const int* bounds;
 };
 
@@ -969,7 +975,7 @@ __global__ void __launch_bounds__(256) tails_kernel(const __grid_constant__ Tail
     if (left == 0) return;
     const int pieces = (int)(a.ld[m] / 8);
     const uint4* src = static_cast<const uint4*>(a.src[m]) + (int64_t)(last - left) * pieces;
-    uint4* dst = static_cast<uint4*>(a.dst[m]) + (int64_t)e * GK * pieces;
+    uint4* dst = static_cast<uint4*>(a.dst[m]) + (int64_t)tail_block(a.by_row, e, first) * GK * pieces;
     const int n = GK * pieces, live = left * pieces;
     for (int i = blockIdx.y * 256 + threadIdx.x; i < n; i += gridDim.y * 256)
         dst[i] = i < live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
@@ -1066,8 +1072,10 @@ bool map_wide(CUtensorMap* m, const GluOut& o, int dtype, int64_t rows, int64_t 
     return map_in(m, Operand{o.p, rows, cols, o.ld}, dtype, 64, 32, batch);
 }
 
-// Bytes of the experts' last k-blocks of a matrix of pitch ld.
-size_t tail_bytes(const ExpArgs& g, int64_t ld) { return g.nb ? align_up((size_t)g.experts * GK * ld * 2, 256) : 0; }
+// Rows and bytes of the experts' last k-blocks of a matrix of pitch ld: one block for
+// each expert that can have rows.
+int64_t tail_rows(const ExpArgs& g) { return (int64_t)std::min(g.experts, g.rows) * GK; }
+size_t tail_bytes(const ExpArgs& g, int64_t ld) { return g.nb ? align_up((size_t)tail_rows(g) * ld * 2, 256) : 0; }
 
 // Copies them for the matrices of family b to `at`, one after the other, and maps
 // both: which of ops is family b's B operand, the others are its A operands.
@@ -1075,13 +1083,14 @@ int set_family_b(ExpMaps& maps, ExpArgs& g, const Operand* const* ops, int n, ch
     TailArgs a;
     std::memset(&a, 0, sizeof a);
     a.rows = g.rows;
+    a.by_row = g.tails_by_row = g.rows < g.experts;
     a.bounds = g.bounds;
     int64_t widest = 1;
     for (int i = 0; i < n; ++i) {
         const Operand& o = *ops[i];
         CUtensorMap* whole = i < n - 1 ? &maps.a2[i] : &maps.b2;
         CUtensorMap* tail = i < n - 1 ? &maps.a2_tail[i] : &maps.b2_tail;
-        const Operand t{at, (int64_t)g.experts * GK, o.cols, o.ld};
+        const Operand t{at, tail_rows(g), o.cols, o.ld};
         int* by_blocks = i < n - 1 ? &g.whole_a2 : &g.whole_b2;         // (the A operands have one shape)
         if (!map_columns(whole, o, g.dtype, by_blocks) || !map_columns(tail, t, g.dtype, by_blocks))
             return fail(MUON_ECUDA, "tensor map creation failed");

@@ -36,3 +36,49 @@ def test_gates_far_below_zero(mg, act, lowest, step):
     z = gates if act == "silu" else 2 * np.sqrt(2 / np.pi) * (gates + 0.044715 * gates ** 3)
     want = (gates / (1 + torch.exp(-z)) * 2.0 ** 40)[:, None]
     assert ((h.double().cpu() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -13)).all()
+
+
+@pytest.mark.parametrize("seed", [0, 1])
+def test_fewer_rows_than_experts(mg, seed):
+    """Experts' last k-blocks stand by their first rows then: experts of one row, of whole blocks and one more,
+    beside experts without rows."""
+    from tests.test_gpu_expert_products import check_glu, check_linear
+    g = np.random.default_rng(seed)
+    counts = np.zeros(400, dtype=int)
+    for n, e in zip((1, 1, 1, 64, 65, 63, 2, 130), g.choice(400, 8, replace=False)):
+        counts[e] = n
+    check_glu(mg, counts.tolist(), 72, 40, "bf16", tail=3, seed=seed)
+    check_linear(mg, counts.tolist(), 136, 72, "f16", tail=3, seed=seed)
+    check_linear(mg, counts.tolist(), 73, 41, "bf16", seed=seed)
+    check_glu(mg, [0, 0, 1, 0], 64, 64, "f16", seed=seed)
+
+
+def test_scratch_of_fewer_rows_than_experts(mg):
+    """The call stays within the bytes that it asked for."""
+    import ctypes
+    rows, experts, cols, outs = 70, 500, 72, 200
+    g = torch.Generator(device="cuda").manual_seed(2)
+
+    def r(*s):
+        return torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+    x, dy, w = r(rows, cols), r(rows, outs), r(experts, outs, cols)
+    choice = torch.randint(0, experts, (rows, 1), generator=g, device="cuda")
+    _, _, bounds = mg.muon_expert_sort(choice, experts)
+    want = mg.muon_expert_linear_backward(x, w, dy, bounds)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    need, fn, s = ctypes.c_int64(0), mg.lib().muon_expert_linear_backward, torch.cuda.current_stream().cuda_stream
+    args = [t.data_ptr() for t in (x, w, dy, bounds, dx, dw)] + [rows, experts, cols, outs, mg.MUON_BF16]
+    assert fn(*args, None, ctypes.byref(need), s) == mg.MUON_ENOMEM
+    assert need.value <= rows * 64 * (cols + outs) * 2 + 512
+    guard = torch.full((need.value + 4096,), 7, dtype=torch.uint8, device="cuda")
+    assert fn(*args, guard.data_ptr(), ctypes.byref(need), s) == mg.MUON_OK
+    assert mg.muon_sync_status() == mg.MUON_OK
+    assert (guard[need.value:] == 7).all() and torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+    for e in torch.unique(choice).tolist():
+        a, b = bounds[e].item(), bounds[e + 1].item()
+        ref = dy[a:b].double().T @ x[a:b].double()
+        size = dy[a:b].double().abs().T @ x[a:b].double().abs()
+        assert ((dw[e].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -20 * size + 1e-37).all()
+    empty = torch.ones(experts, dtype=torch.bool, device="cuda")
+    empty[choice.reshape(-1)] = False
+    assert not dw[empty].any()
