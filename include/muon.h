@@ -519,10 +519,13 @@ int muon_expert_combine_backward(const void* dy, int64_t ld_dy, const void* ys, 
  *   scratch  device memory of the caller that the call may write until it has run
  *            (256-byte aligned); *scratch_bytes holds its size.  A call that needs
  *            more writes what it needs there, launches nothing and returns
- *            MUON_ENOMEM, so a first call with NULL and 0 asks.  Forward passes
- *            over sides that are multiples of 8 and pointers on 16 bytes need
- *            none; other rows are copied there padded, the weights' too; the
- *            gated backward pass keeps dg and du there (4 bytes per row and ffn
+ *            MUON_ENOMEM, so a first call with NULL and 0 asks.
+ *            Forward passes over sides that are multiples of 8, pointers on 16 bytes
+ *            and at most 65536 columns need none (scratch_bytes may be NULL then).
+ *            Rows of other sides or alignment are copied there padded, the weights'
+ *            too.  Contractions beyond 65536 terms, of any pass, keep running sums
+ *            there: 128 KB for each SM that the launch takes.  The gated
+ *            backward pass keeps dg and du there (4 bytes per row and ffn
  *            column), and both backward passes 64 rows per expert (per row, where
  *            rows are fewer) of what the weights' gradients contract.  Calls that
  *            can run at once, captured graphs among them, must not share it.
