@@ -839,14 +839,21 @@ def _sorted_rows(t, name, rows):
     return t.data_ptr()
 
 
+def _slot_weights(t, row_of, tokens, k):
+    """Pointer of a weight per slot: tokens x k, or a vector of them."""
+    import torch
+    if t is not None and t.dim() == 2 and t.shape != row_of.shape and 1 not in t.shape:
+        raise ValueError(f"weights must be {tokens} x {k}, got {t.shape[0]} x {t.shape[1]}")
+    return _vector(t, tokens * k, "weights", torch.float32)
+
+
 def muon_expert_combine(ys, row_of, bounds, weights=None, residual=None, stream=None):
     """Sums each token's sorted rows of ys, weighted (weights: tokens x k, fp32;
     None: 1), onto residual (tokens x hidden, contiguous rows; None: 0)."""
-    import torch
     _one_device(ys, row_of, bounds, weights, residual)
     tokens, k, experts, rp, bp = _route(row_of, bounds)
     yp, hidden = _sorted_rows(ys, "ys", tokens * k), ys.shape[1]
-    wp = _vector(weights, tokens * k, "weights", torch.float32)
+    wp = _slot_weights(weights, row_of, tokens, k)
     ap, lda = None, hidden
     if residual is not None:
         if residual.shape != (tokens, hidden) or residual.dtype is not ys.dtype:
@@ -863,7 +870,6 @@ def muon_expert_combine(ys, row_of, bounds, weights=None, residual=None, stream=
 def muon_expert_combine_backward(dy, ys, row_of, bounds, weights, stream=None):
     """Gradients (dys, dweights) of muon_expert_combine with weights; the
     residual's is dy itself."""
-    import torch
     _one_device(dy, ys, row_of, bounds, weights)
     tokens, k, experts, rp, bp = _route(row_of, bounds)
     yp, hidden = _sorted_rows(ys, "ys", tokens * k), ys.shape[1]
@@ -872,7 +878,7 @@ def muon_expert_combine_backward(dy, ys, row_of, bounds, weights, stream=None):
     dp, ldd = _rows_of(dy, "dy")
     if weights is None:
         raise ValueError("weights are required")
-    wp = _vector(weights, tokens * k, "weights", torch.float32)
+    wp = _slot_weights(weights, row_of, tokens, k)
     dys, dw = _new(stream, (ys.shape, ys), ((tokens, k), weights))
     st = lib().muon_expert_combine_backward(dp, ldd, yp, tokens, k, hidden, _dtype_code(ys), rp, bp, experts, wp,
                                             dys.data_ptr(), dw.data_ptr(), _stream_ptr(stream))
