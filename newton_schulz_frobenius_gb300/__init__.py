@@ -900,6 +900,15 @@ def _with_scratch(name, device, stream, *args):
         _check(st, name)
 
 
+def _apart(t, name, *others):
+    """Refuses a tensor to be written that shares memory with another of the call (all contiguous)."""
+    first = t.data_ptr()
+    end = first + t.numel() * t.element_size()
+    for o in others:
+        if o is not None and o.data_ptr() < end and first < o.data_ptr() + o.numel() * o.element_size():
+            raise ValueError(f"{name} overlaps another tensor of the call")
+
+
 def _matrix(t, shape, dtype, name):
     _cuda_contig(t, name)
     if tuple(t.shape) != tuple(shape):
@@ -947,8 +956,8 @@ def muon_expert_glu_forward(x, w_gate, w_up, bounds, act: str = "silu", save: bo
 def muon_expert_glu_backward(x, w_gate, w_up, gate, up, dh, bounds, act: str = "silu", need_dx: bool = True,
                              dw_gate=None, dw_up=None, stream=None):
     """Gradients (dx, dw_gate, dw_up) of muon_expert_glu_forward.  dw_gate and
-    dw_up may be tensors to write into (whose matrices a MuonGroup reads);
-    need_dx=False leaves dx out (None)."""
+    dw_up may be tensors to write into (whose matrices a MuonGroup reads), apart
+    from the call's others; need_dx=False leaves dx out (None)."""
     _one_device(x, w_gate, w_up, gate, up, dh, bounds, dw_gate, dw_up)
     rows, experts, hidden, ffn, dt, bp = _expert_args(x, (w_gate, w_up), bounds)
     code = _act_code(act)
@@ -956,6 +965,7 @@ def muon_expert_glu_backward(x, w_gate, w_up, gate, up, dh, bounds, act: str = "
     for t, nm in ((dw_gate, "dw_gate"), (dw_up, "dw_up")):
         if t is not None:
             _matrix(t, w_gate.shape, x.dtype, nm)
+            _apart(t, nm, x, w_gate, w_up, gate, up, dh, bounds, dw_gate if t is dw_up else None)
     dx, = _new(stream, (x.shape, x)) if need_dx else (None,)
     dw_gate, dw_up = _to_write(stream, w_gate, dw_gate, dw_up)
     _with_scratch("muon_expert_glu_backward", x.device, stream, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
@@ -985,12 +995,13 @@ def muon_expert_linear_forward(x, w, bounds, stream=None):
 
 def muon_expert_linear_backward(x, w, dy, bounds, need_dx: bool = True, dw=None, stream=None):
     """Gradients (dx, dw) of muon_expert_linear_forward; dw may be a tensor to
-    write into, need_dx=False leaves dx out (None)."""
+    write into, apart from the call's others, need_dx=False leaves dx out (None)."""
     _one_device(x, w, dy, bounds, dw)
     rows, experts, cols, out, dt, bp = _expert_args(x, (w,), bounds)
     dp = _matrix(dy, (rows, out), x.dtype, "dy")
     if dw is not None:
         _matrix(dw, w.shape, x.dtype, "dw")
+        _apart(dw, "dw", x, w, dy, bounds)
     dx, = _new(stream, (x.shape, x)) if need_dx else (None,)
     dw, = _to_write(stream, w, dw)
     _with_scratch("muon_expert_linear_backward", x.device, stream, x.data_ptr(), w.data_ptr(), dp, bp,
@@ -1008,7 +1019,8 @@ def muon_dropout(x, p: float, seed: int = 0, offset: int = 0, state=None, residu
     None: 0.  The mask follows from (seed, offset) and the element's index and is
     not stored: the gradient of x is muon_dropout(dy, p, ...) with the same two.
     state: an int64 CUDA tensor (seed, offset), read when the kernel runs, in
-    their place.  out: a tensor to write to, x and residual included."""
+    their place.  out: a tensor to write to, x and residual included (but not one
+    that overlaps them otherwise)."""
     import torch
     _one_device(x, state, residual, out)
     _cuda_contig(x, "x")
@@ -1018,6 +1030,9 @@ def muon_dropout(x, p: float, seed: int = 0, offset: int = 0, state=None, residu
             if t.shape != x.shape or t.dtype is not x.dtype:
                 raise ValueError(f"{nm} must have x's shape and dtype")
     sp = _vector(state, 2, "state", torch.int64)
+    if out is not None:                 # x and residual themselves, element for element, or none of their elements
+        at = out.data_ptr()
+        _apart(out, "out", state, *(t for t in (x, residual) if t is not None and t.data_ptr() != at))
     if out is None:
         out, = _new(stream, (x.shape, x))
     else:
