@@ -482,7 +482,8 @@ int muon_glu_backward(const void* x, const void* w_gate, const void* w_up, const
  * dweights are fp32.  Sums are fp32 in the order of the choices, rounded once.
  * row_of and bounds are read on the device: as muon_expert_sort wrote them, or
  * any rows; those outside [0, tokens k) are left out.  A row named twice by row_of
- * is written twice.  tokens k in [0, 2^24], k and num_experts in [1, 1024], hidden
+ * is written twice, in no order; rows of xs and dys that it does not name stay as they
+ * were.  tokens k in [0, 2^24], k and num_experts in [1, 1024], hidden
  * in [1, 2^20].  Outputs must not overlap anything else of the call.  No workspace.
  */
 int muon_expert_sort(const void* experts, int index_dtype, int64_t slots, int64_t num_experts, int* row_of,

@@ -817,8 +817,8 @@ def muon_expert_sort(experts, num_experts: int, stream=None):
 
 def muon_expert_dispatch(x, row_of, bounds, stream=None):
     """Copies each token's row of x to its k sorted rows: (tokens k) x hidden.
-    Rows behind the last expert are zero.  Its gradient is
-    muon_expert_combine(dxs, row_of, bounds)."""
+    Rows behind the last expert are zero, rows that row_of does not name (no
+    sort's) undefined.  Its gradient is muon_expert_combine(dxs, row_of, bounds)."""
     _one_device(x, row_of, bounds)
     xp, ld = _rows_of(x, "x")
     tokens, k, experts, rp, bp = _route(row_of, bounds)
@@ -869,7 +869,7 @@ def muon_expert_combine(ys, row_of, bounds, weights=None, residual=None, stream=
 
 def muon_expert_combine_backward(dy, ys, row_of, bounds, weights, stream=None):
     """Gradients (dys, dweights) of muon_expert_combine with weights; the
-    residual's is dy itself."""
+    residual's is dy itself.  Rows of dys that row_of does not name are undefined."""
     _one_device(dy, ys, row_of, bounds, weights)
     tokens, k, experts, rp, bp = _route(row_of, bounds)
     yp, hidden = _sorted_rows(ys, "ys", tokens * k), ys.shape[1]

@@ -82,3 +82,34 @@ def test_scratch_of_fewer_rows_than_experts(mg):
     empty = torch.ones(experts, dtype=torch.bool, device="cuda")
     empty[choice.reshape(-1)] = False
     assert not dw[empty].any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("hidden,off", [(64, 0), (33, 1)])
+def test_rows_that_are_not_named_stay(mg, hidden, off, dtype):
+    """dispatch and combine_backward write the rows that row_of names, and no byte beside them."""
+    tokens, k, rows = 5, 2, 10
+    row_of = torch.tensor([[0, 7], [-1, 3], [10, 4], [1 << 30, -5], [9, 2]], dtype=torch.int32, device="cuda")
+    bounds = torch.tensor([0, 8], dtype=torch.int32, device="cuda")         # row 9 is behind the last expert
+    g = torch.Generator(device="cuda").manual_seed(1)
+
+    def r(n):
+        return torch.randn(n * hidden + off, generator=g, device="cuda").to(dtype)[off:].view(n, hidden)
+    x, ys, w = r(tokens), r(rows), torch.rand(tokens, k, generator=g, device="cuda")
+    code = mg.MUON_F32 if dtype is torch.float32 else mg.MUON_BF16
+    s = torch.cuda.current_stream().cuda_stream
+    bufs = [torch.full((rows * hidden + off + 64,), 7.0, dtype=dtype, device="cuda") for _ in range(2)]
+    xs, dys = (b[off:off + rows * hidden].view(rows, hidden) for b in bufs)
+    dw = torch.full((tokens, k), 7.0, device="cuda")
+    assert mg.lib().muon_expert_dispatch(x.data_ptr(), hidden, tokens, k, hidden, code, row_of.data_ptr(),
+                                         bounds.data_ptr(), 1, xs.data_ptr(), s) == mg.MUON_OK
+    assert mg.lib().muon_expert_combine_backward(x.data_ptr(), hidden, ys.data_ptr(), tokens, k, hidden, code,
+                                                 row_of.data_ptr(), bounds.data_ptr(), 1, w.data_ptr(), dys.data_ptr(),
+                                                 dw.data_ptr(), s) == mg.MUON_OK
+    assert mg.muon_sync_status() == mg.MUON_OK
+    for t, j, row in ((0, 0, 0), (0, 1, 7), (1, 1, 3), (2, 1, 4), (4, 1, 2)):
+        assert torch.equal(xs[row], x[t]) and torch.equal(dys[row], (x[t].float() * w[t, j]).to(dtype))
+    for out, buf in zip((xs, dys), bufs):
+        assert not out[9].any() and (out[[1, 5, 6, 8]] == 7).all()
+        assert (buf[:off] == 7).all() and (buf[off + rows * hidden:] == 7).all()
+    assert not dw[row_of >= 8].any() and not dw[row_of < 0].any()
