@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(SORT_T, 1) expert_sort_kernel(const __grid_con
             if (e[r] >= 0 && lane == __ffs((int)same[r]) - 1) mine[e[r]] += (uint32_t)__popc(same[r]);
             __syncwarp();
         }
+        if (STEP == SORTED) break;          // a warp of a cluster has no more slots than one step takes
     }
     __syncthreads();
     // per expert: the warps' counts become the places before each warp's first
@@ -183,7 +184,8 @@ __global__ void __launch_bounds__(SORT_T, 1) expert_sort_kernel(const __grid_con
     if (threadIdx.x == 0 && rank == 0) a.bounds[0] = 0;
     __syncthreads();
     for (int64_t i = first; i < last; i += 32 * SORT_AHEAD) {
-        if (a.per_warp > 32 * SORT_AHEAD) read(i);      // else the first walk's are still here
+        // (else the first walk's are still here)
+        if (STEP == PLACES && a.per_warp > 32 * SORT_AHEAD) read(i);
 #pragma unroll
         for (int r = 0; r < SORT_AHEAD; ++r) {
             if (i + 32 * r >= last) break;
@@ -197,6 +199,7 @@ __global__ void __launch_bounds__(SORT_T, 1) expert_sort_kernel(const __grid_con
             }
             __syncwarp();
         }
+        if (STEP == SORTED) break;
     }
 }
 

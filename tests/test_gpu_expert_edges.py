@@ -113,3 +113,22 @@ def test_rows_that_are_not_named_stay(mg, hidden, off, dtype):
         assert not out[9].any() and (out[[1, 5, 6, 8]] == 7).all()
         assert (buf[:off] == 7).all() and (buf[off + rows * hidden:] == 7).all()
     assert not dw[row_of >= 8].any() and not dw[row_of < 0].any()
+
+
+@pytest.mark.parametrize("slots,experts", [(131072, 1024), (100003, 1000), (131071, 1023), (65537, 1024)])
+def test_sort_by_one_cluster_with_the_largest_tables(mg, slots, experts):
+    """All sixteen CTAs of a cluster with as many experts as there can be: some empty, some slots without one, all
+    slots in one expert, all in the last, none in any."""
+    g = torch.Generator(device="cuda").manual_seed(slots)
+    e = torch.randint(0, experts, (slots, 1), generator=g, device="cuda")
+    lost = torch.rand((slots, 1), generator=g, device="cuda") < 0.1
+    few = torch.randint(0, 7, (slots, 1), generator=g, device="cuda", dtype=torch.int32)
+    for c in (e, torch.where(lost, torch.full_like(e, experts), e), few, torch.full_like(few, experts - 1),
+              torch.zeros_like(few), torch.full_like(few, -1)):
+        row_of, slot_of, bounds = mg.muon_expert_sort(c, experts)
+        flat = c.reshape(-1).long()
+        flat = torch.where(flat < 0, torch.full_like(flat, experts), flat)
+        want = torch.argsort(flat, stable=True)
+        assert torch.equal(slot_of.long(), want)
+        assert torch.equal(row_of.reshape(-1)[want].long(), torch.arange(slots, device="cuda"))
+        assert torch.equal(bounds.long(), torch.searchsorted(flat[want].contiguous(), torch.arange(experts + 1, device="cuda")))
