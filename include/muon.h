@@ -580,6 +580,9 @@ int64_t muon_launch_count(void);
  *             tiles or pairing off): k-block `stage` of CTA 0's first tile
  *   kernel 2  the fused small-matrix kernel: prologue piece `stage` of CTA 0
  *             (16-byte aligned matrices)
+ *   kernel 4  the experts' products: the stage that CTA 0's producer fills as
+ *             number `stage` (two k-blocks each), whatever its tile; the other
+ *             CTA of the pair fills its half
  *   kernel 0  disarm.
  * MUON_EINVAL for another kernel or a stage outside [0, 2^20].
  */

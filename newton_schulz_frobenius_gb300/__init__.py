@@ -382,6 +382,7 @@ def muon_launch_count() -> int:
 #: kernels the bounded-wait test hook can stall
 STALL_PRODUCT = 1
 STALL_SMALL = 2
+STALL_EXPERT = 4
 
 
 def muon_debug_arm_stall(kernel: int, stage: int = 0) -> None:

@@ -161,6 +161,7 @@ struct ExpArgs {
     GluOut out[3];              // H, G, U; Y; or dX, dW, dWu
     float* part;                // running sums of contractions in several parts
     int* status;
+    int stall;                  // test hook: k + 1 = CTA 0 leaves the k-th stage that it comes to unfilled; 0 = off
 };
 
 // Extents of family a's tiles: 32, or multiples of 64 rows, half of them per CTA in
@@ -621,14 +622,18 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            // waits for a stage to be free and says how many bytes the pair's copies bring
+            int until_stall = blockIdx.x == 0 ? g.stall : 0;
+            // waits for a stage to be free and says how many bytes the pair's copies bring;
+            // false where this CTA brings none
             auto open = [&](uint32_t bytes) {
                 ok = wait_for(empty0 + 8 * stage, phase ^ 1u, abort_flag, g.status);
-                if (!ok) return;
+                if (!ok) return false;
+                if (until_stall && --until_stall == 0) return false;
                 if (rank == 0) mbar_expect_tx(full0 + 8 * stage, 2 * bytes);
                 else arrive_relaxed(full_pair + 8 * stage);
                 flight |= 1u << stage;
                 phases = (phases & ~(1u << stage)) | (phase << stage);
+                return true;
             };
             auto close = [&] {
                 if (++stage == STAGES) {
@@ -643,8 +648,11 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
                     const CUtensorMap *ma = &maps.a2[t.which], *mb = &maps.b2;
                     int k0 = t.first;
                     for (int left = t.blocks; left > 0; left -= SUB) {
-                        open((uint32_t)(min(left, SUB) * 2 * OP_BYTES));
-                        if (!ok) break;
+                        if (!open((uint32_t)(min(left, SUB) * 2 * OP_BYTES))) {
+                            if (!ok) break;
+                            close();
+                            continue;
+                        }
                         const uint32_t bar = full_pair + 8 * stage, at = (uint32_t)(stage * SUB * OP_BYTES);
 #pragma unroll
                         for (int i = 0; i < SUB; ++i) {
@@ -669,8 +677,11 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
                 const CUtensorMap *ma = &maps.a[0], *mb = &maps.b[0][hn / 32];
                 int k0 = 0;
                 for (int left = t.blocks; left > 0; left -= SUB) {
-                    open(min(left, SUB) * bytes);
-                    if (!ok) break;
+                    if (!open(min(left, SUB) * bytes)) {
+                        if (!ok) break;
+                        close();
+                        continue;
+                    }
                     const uint32_t bar = full_pair + 8 * stage, at = (uint32_t)(stage * SUB * OP_BYTES);
 #pragma unroll
                     for (int i = 0; i < SUB; ++i) {
@@ -696,11 +707,9 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
                 }
             }
             // copies still in flight (after an abort nobody consumes them): the even CTA
-            // sees those of both; the odd one, which may have issued some that the
-            // even one does not know of, waits out the limit on a barrier that nothing completes
+            // sees those of both in the stages that it has opened (see the end for others)
             for (int s = 0; s < STAGES; ++s)
                 if (rank == 0 && ((flight >> s) & 1)) wait_drain(full0 + 8 * s, (phases >> s) & 1);
-            if (rank == 1 && !ok) wait_drain(full0, 0);
         }
         __syncwarp();
     } else if (warp == 1 && rank == 1) {
@@ -870,6 +879,13 @@ expert_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpA
     }
     tc_fence_before();
     __syncthreads();
+    // After an abort the odd CTA may have copies in flight that the even one does not know
+    // of, also where its producer had come to its end: it waits out the limit on a
+    // barrier that nothing completes.  (Without one its epilogue has seen every product done.)
+    if (rank == 1 && warp == 0) {
+        if (lane == 0 && *abort_flag) wait_drain(full0, 0);
+        __syncwarp();
+    }
     cluster_sync();
     if (warp == 1) {
         tc_fence_after();
@@ -1141,7 +1157,7 @@ cudaError_t clusters_at_once(int device, int* n) {
 }
 
 template <int MODE>
-int launch_expert(const ExpMaps& maps, const ExpArgs& g, int64_t most, double work, const DevCtx& dc, cudaStream_t s) {
+int launch_expert(const ExpMaps& maps, ExpArgs& g, int64_t most, double work, const DevCtx& dc, cudaStream_t s) {
     int n = 0;
     cudaError_t e = clusters_at_once<MODE>(dc.device, &n);
     if (e != cudaSuccess) return cuda_fail(e, "expert products set-up");
@@ -1158,6 +1174,7 @@ int launch_expert(const ExpMaps& maps, const ExpArgs& g, int64_t most, double wo
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    g.stall = take_stall(STALL_EXPERT);
     note_launch_begin(KC_GLU, s);
     e = cudaLaunchKernelEx(&cfg, g.tma_out ? expert_kernel<MODE, true> : expert_kernel<MODE, false>, maps, g);
     note_launch_end(KC_GLU, work, s);

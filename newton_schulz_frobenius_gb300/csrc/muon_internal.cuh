@@ -290,7 +290,7 @@ void note_launch_end(int kclass, double work, cudaStream_t s);
 // Test hook of the bounded waits (muon_debug_arm_stall): the stage to leave
 // unfilled (+1) in the next launch of the given kernel kind, consumed by that
 // launch; 0 when nothing is armed.
-enum StallKind : int { STALL_NONE = 0, STALL_PRODUCT = 1, STALL_SMALL = 2 };
+enum StallKind : int { STALL_NONE = 0, STALL_PRODUCT = 1, STALL_SMALL = 2, STALL_EXPERT = 4 };
 int take_stall(int kind);
 
 }  // namespace muon

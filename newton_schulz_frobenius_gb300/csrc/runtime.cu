@@ -312,8 +312,8 @@ int muon_debug_arm_stall(int kernel, int stage) {
         g_stall.store(0);
         return MUON_OK;
     }
-    if ((kernel != STALL_PRODUCT && kernel != STALL_SMALL) || stage < 0 || stage > (1 << 20))
-        return fail(MUON_EINVAL, "kernel must be 0, 1 or 2 and stage in [0, 2^20]");
+    if ((kernel != STALL_PRODUCT && kernel != STALL_SMALL && kernel != STALL_EXPERT) || stage < 0 || stage > (1 << 20))
+        return fail(MUON_EINVAL, "kernel must be 0, 1, 2 or 4 and stage in [0, 2^20]");
     g_stall.store(((stage + 1) << 8) | kernel);
     return MUON_OK;
 }

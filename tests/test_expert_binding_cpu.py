@@ -105,3 +105,14 @@ def test_dropout_out_that_overlaps_is_refused(reached):
         assert mg.muon_dropout(x, 0.5, residual=residual, out=out) is out
     assert mg.muon_dropout(x, 0.5, residual=x, out=x) is x
     assert reached == ["muon_dropout"] * 5
+
+
+def test_the_experts_products_can_be_armed():
+    """The bounded-wait test hook knows their kernel; arming is host state only."""
+    from newton_schulz_frobenius_gb300 import _build
+    _build.build()
+    mg.muon_debug_arm_stall(mg.STALL_EXPERT, 1 << 20)
+    mg.muon_debug_arm_stall(0)
+    for kernel, stage in ((mg.STALL_EXPERT, -1), (mg.STALL_EXPERT, (1 << 20) + 1), (mg.STALL_EXPERT + 1, 0)):
+        with pytest.raises(mg.MuonError):
+            mg.muon_debug_arm_stall(kernel, stage)
