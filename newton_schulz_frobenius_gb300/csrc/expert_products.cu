@@ -1319,7 +1319,7 @@ extern "C" int muon_expert_glu_backward(const void* x, const void* w_gate, const
     ga.dtype = dtype; ga.act = act;
     ga.vec = tma_ok(dh, ffn) && tma_ok(gate, ffn) && tma_ok(up, ffn);
     if ((r = pad_rows({&X}, {&G, &U}, g, at + part + 2 * half, dc.sms, s))) return r;
-    if ((r = glu_prepare(nullptr, 0, nullptr, &ga, dc.sms, s))) return r;
+    if ((r = glu_prepare(nullptr, nullptr, &ga, dc.sms, s))) return r;
     G.rows = U.rows = ffn;
     const Operand DG{ga.dg, rows, ffn, ldw}, DU{ga.du, rows, ffn, ldw};
     ExpMaps maps;

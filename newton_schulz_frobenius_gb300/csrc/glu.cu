@@ -735,7 +735,7 @@ struct PadArgs {
     const void* src[3];
     void* dst[3];
     int64_t rows[3];
-    int cols[3], n;
+    int cols, n;                // the operands share their width
 };
 // What a call needs before its products, in one launch: operands blockIdx.y <
 // pads.n padded, and (backward) blockIdx.y == pads.n dG and dU.
@@ -749,13 +749,13 @@ __global__ void __launch_bounds__(256) glu_prepare_kernel(const __grid_constant_
         glu_grad<ACT>(g);
         return;
     }
-    const int cols = a.cols[o], pieces = (cols + 7) / 8;
-    const int64_t n = a.rows[o] * pieces, all = a.rows[o] * cols;
+    const int pieces = (a.cols + 7) / 8;
+    const int64_t n = a.rows[o] * pieces, all = a.rows[o] * a.cols;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int64_t row = row_of(i, n, pieces);
-        const int c = (int)(i - row * pieces) * 8, left = cols - c;
+        const int c = (int)(i - row * pieces) * 8, left = a.cols - c;
         Shifted v;
-        const bool in = v.at(a.src[o], all, row * cols + c);
+        const bool in = v.at(a.src[o], all, row * a.cols + c);
         if (in) v.load();
         static_cast<uint4*>(a.dst[o])[i] = in ? v.get(left) : v.by_elements(left);
     }
@@ -800,20 +800,20 @@ constexpr int MAX_BLOCKS = 1024;
 
 }  // namespace
 
-int glu_prepare(Operand* const* ops, int nops, char* at, const GluGradArgs* g, int sms, cudaStream_t s) {
+int glu_prepare(Operand* const* ops, char* at, const GluGradArgs* g, int sms, cudaStream_t s) {
     PadArgs p;
     GluGradArgs ga;
     std::memset(&p, 0, sizeof p);
     std::memset(&ga, 0, sizeof ga);
     int64_t blocks = 1;
-    for (int i = 0; i < nops; ++i) {
+    for (int i = 0; ops && i < 3; ++i) {
         Operand& o = *ops[i];
         const size_t b = padded_bytes(o);
         if (!b) continue;
         p.src[p.n] = o.p;
         p.dst[p.n] = at;
         p.rows[p.n] = o.rows;
-        p.cols[p.n] = (int)o.cols;
+        p.cols = (int)o.cols;
         ++p.n;
         o.ld = pad8(o.cols);
         blocks = std::max(blocks, (o.rows * (pad8(o.cols) / 8) + 255) / 256);
@@ -988,7 +988,7 @@ extern "C" int muon_glu_forward(const void* x, const void* w_gate, const void* w
         Workspace* w = nullptr;
         if ((r = ws_get(dc.device, s, need, &w))) return r;
         Operand* const ops[3] = {&X, &G, &U};
-        if ((r = glu_prepare(ops, 3, w->base, nullptr, dc.sms, s))) return r;
+        if ((r = glu_prepare(ops, w->base, nullptr, dc.sms, s))) return r;
     }
     if (tokens <= FEW_TOKENS) {
         FewArgs f;
@@ -1073,7 +1073,7 @@ extern "C" int muon_glu_backward(const void* x, const void* w_gate, const void* 
     ga.dtype = dtype; ga.act = act;
     ga.vec = tma_ok(dh, ffn) && tma_ok(gate, ffn) && tma_ok(up, ffn);
     Operand* const ops[3] = {&X, &G, &U};
-    if ((r = glu_prepare(ops, 3, w->base + 2 * half + parts, &ga, dc.sms, s))) return r;
+    if ((r = glu_prepare(ops, w->base + 2 * half + parts, &ga, dc.sms, s))) return r;
     const Operand DG{ga.dg, tokens, ffn, ldw}, DU{ga.du, tokens, ffn, ldw};
     GluMaps maps;
     std::memset(&maps, 0, sizeof maps);

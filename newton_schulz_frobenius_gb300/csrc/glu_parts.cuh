@@ -67,9 +67,11 @@ inline size_t padded_bytes(const Operand& o) {
     return tma_ok(o.p, o.ld) ? 0 : align_up((size_t)o.rows * pad8(o.cols) * 2, 256);
 }
 
-// Points the operands (up to three) that need it at padded copies and makes
-// these, with dG and dU where `g` is given, in one launch (glu.cu).
-int glu_prepare(Operand* const* ops, int nops, char* at, const GluGradArgs* g, int sms, cudaStream_t s);
+// Points those of the dense block's three operands (ops; null: none) that need it at
+// padded copies and makes these, with dG and dU where `g` is given, in one launch
+// (glu.cu).  The experts' operands, of different widths and counts, have a kernel of
+// their own.
+int glu_prepare(Operand* const* ops, char* at, const GluGradArgs* g, int sms, cudaStream_t s);
 
 // `batch` matrices of o.rows x o.cols, one after the other (o.rows * o.ld apart).
 inline bool map_in(CUtensorMap* m, const Operand& o, int dtype, uint32_t box_cols, uint32_t box_rows, int64_t batch = 1) {
