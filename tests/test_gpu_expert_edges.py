@@ -132,3 +132,64 @@ def test_sort_by_one_cluster_with_the_largest_tables(mg, slots, experts):
         assert torch.equal(slot_of.long(), want)
         assert torch.equal(row_of.reshape(-1)[want].long(), torch.arange(slots, device="cuda"))
         assert torch.equal(bounds.long(), torch.searchsorted(flat[want].contiguous(), torch.arange(experts + 1, device="cuda")))
+
+
+def whole(shape, seed, dtype=torch.bfloat16, top=2):
+    """Whole numbers, so that sums below 2^24 are exact in fp32 in any order."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(-top, top + 1, shape, generator=g, device="cuda", dtype=torch.int8).to(dtype)
+
+
+def test_the_most_rows(mg):
+    """2^24 rows, one expert with nearly all of them: results are exact whole numbers, rounded once."""
+    rows, cols, outs = 1 << 24, 8, 16
+    ends = [0, rows - 70100, rows - 100, rows - 100]
+    bounds = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    x, dy, w = whole((rows, cols), 1), whole((rows, outs), 2), whole((3, outs, cols), 3)
+    y = mg.muon_expert_linear_forward(x, w, bounds)
+    dx, dw = mg.muon_expert_linear_backward(x, w, dy, bounds)
+    assert mg.muon_sync_status() == mg.MUON_OK
+    for e in range(3):
+        a, b = ends[e], ends[e + 1]
+        want = dy[a:b].double().T @ x[a:b].double()
+        assert want.numel() == 0 or want.abs().max() < 2 ** 24
+        assert torch.equal(dw[e], want.to(dw.dtype))
+        for i in range(a, b, 1 << 22):
+            s = slice(i, min(b, i + (1 << 22)))
+            assert torch.equal(y[s], (x[s].double() @ w[e].double().T).to(y.dtype))
+            assert torch.equal(dx[s], (dy[s].double() @ w[e].double()).to(dx.dtype))
+    assert not y[ends[3]:].any() and not dx[ends[3]:].any()
+    row_of, slot_of, bounds = mg.muon_expert_sort((x[:, 0] + 1).int().reshape(-1, 1), 4)       # -1: no expert
+    xs = mg.muon_expert_dispatch(x, row_of, bounds)
+    live = int(bounds[-1])
+    assert torch.equal(xs[:live], x[slot_of[:live].long()]) and not xs[live:].any()
+    weights = whole((rows, 1), 4, torch.float32)
+    back = mg.muon_expert_combine(xs, row_of, bounds, weights=weights, residual=x)
+    on = (row_of < live).float()
+    assert torch.equal(back, (x.float() * (1 + on * weights)).to(x.dtype))
+    dys, dweights = mg.muon_expert_combine_backward(x, xs, row_of, bounds, weights)
+    assert torch.equal(dys[:live], (x.float() * weights).to(x.dtype)[slot_of[:live].long()]) and not dys[live:].any()
+    assert torch.equal(dweights, (x.float() ** 2).sum(1, keepdim=True) * on)
+
+
+@pytest.mark.parametrize("cols", [40000, 40001])
+def test_experts_matrices_beyond_31_bits(mg, cols):
+    """Weights of more than 2^31 elements, on 16 bytes and off: the last expert's results."""
+    outs, experts, rows = 20001, 3, 70
+    w = whole((experts, outs, cols), 1, top=1)
+    assert w.numel() > 1 << 31
+    x, dy = whole((rows, cols), 2, top=1), whole((rows, outs), 3, top=1)
+    ends = [0, 1, 3, rows]
+    bounds = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    y = mg.muon_expert_linear_forward(x, w, bounds)
+    dx, dw = mg.muon_expert_linear_backward(x, w, dy, bounds)
+    assert mg.muon_sync_status() == mg.MUON_OK
+    for e in range(experts):
+        a, b = ends[e], ends[e + 1]
+        assert torch.equal(dw[e], (dy[a:b].float().T @ x[a:b].float()).to(dw.dtype))
+        for i in range(0, outs, 4000):
+            s = slice(i, min(outs, i + 4000))
+            assert torch.equal(y[a:b, s], (x[a:b].double() @ w[e, s].double().T).to(y.dtype))
+        for i in range(0, cols, 4000):
+            s = slice(i, min(cols, i + 4000))
+            assert torch.equal(dx[a:b, s], (dy[a:b].double() @ w[e, :, s].double()).to(dx.dtype))
