@@ -10,7 +10,9 @@
 // 16 bits hides under the copies: 67 M bf16 elements onto a residual (403 MB) 58 us, at
 // the copy rate; without one (268 MB) 45 us, 0.89 of it, the generator's multiplications
 // showing.  One block per thread and step with the key's steps taken for each, the type
-// chosen per access, was 95 us.
+// chosen per access, was 95 us.  Tensors off 16 bytes go by elements, 16 bytes apart from
+// lane to lane: the same elements 128 us with or without a residual (fp32 179 and 200; on 16
+// bytes 76 and 113).
 #include "host.h"
 #include "epilogue.cuh"
 

@@ -9,8 +9,8 @@
 //
 // One persistent launch of 2-SM tcgen05 pairs covers all experts (M = 256, N up to
 // 256, fp32 accumulation in TMEM, two accumulators so that a tile's epilogue runs
-// under the next tile's products), fed by TMA through a ring of six 32 KB stages
-// per CTA.  Every warp finds its tiles from the bounds, so no host copy of them is
+// under the next tile's products), fed by TMA through a ring of three stages per CTA of
+// two k-blocks each (64 KB).  Every warp finds its tiles from the bounds, so no host copy of them is
 // needed and a captured call follows new ones.
 //
 // Results over sorted rows (family a: forward, dX) are computed transposed: 256
@@ -35,12 +35,12 @@
 //
 // What bounds it: with long contractions the rate at which L2 delivers operands, 64
 // bytes per cycle and SM, which a 256 x 256 tile takes in full, and the power cap: 8
-// experts of 4096 x 14336, 16384 rows, even: gated forward 1.97-2.1 ms (1.83-1.95
-// PFLOP/s), linear forward 1.06 (1.81), linear backward 2.25 (1.71); uneven experts,
-// whose last tiles are smaller, 2.25-2.4, 1.1 and 2.35.  With short ones (64 experts of
+// experts of 4096 x 14336, 16384 rows, even: gated forward 1.97-2.3 ms (1.67-1.95
+// PFLOP/s, by the card's temperature), linear forward 1.06-1.2, linear backward 2.25-2.4;
+// uneven experts, whose last tiles are smaller, 2.37-2.48, 1.1-1.3 and 2.28-2.5.  With short ones (64 experts of
 // 512 rows, 2048 x 1024) a tile's epilogue beside its 8 to 32 k-blocks, 60-70 % of the
-// product's floor; with few rows HBM (16 rows through 8 experts of 2048 x 8192: 75 us,
-// 6.4 TB/s), and in the weights' gradients of few rows HBM's rate of writes alone.  An
+// product's floor; with few rows HBM (16 rows through 8 experts of 2048 x 8192: 73 us where six
+// of them have any, 77 seven, 87 eight, 5.5-6.2 TB/s), and in the weights' gradients of few rows HBM's rate of writes alone.  An
 // epilogue of sixteen warps (of 96 registers), plain instead of tile stores, and the weights'
 // tiles prefetched into L2 ahead of the ring (gated forward of those uneven experts 2.1-2.2 ->
 // 2.55 ms) were built and were slower.

@@ -33,11 +33,15 @@ constexpr int64_t MAX_HIDDEN = 1 << 20;
 // memory, over the cluster's CTAs before it, experts are summed in order, and a
 // second walk over the same slots hands out the places.  Within 32 slots equal
 // experts find each other by votes, so nothing depends on scheduling.  Bound by
-// latency: 4.8 us for 16384 slots and 64 experts, 8.0 for 65536, 12.4 for 131072
+// latency: 4.5 us for 16384 slots and 64 experts, 7.7 for 65536, 12.0 for 131072
 // (back to back in a graph).  More slots are sorted by the whole device in three
 // launches: the CTAs' counts (left in slot_of, which is not written until the last),
 // the places, and slot_of from them; 2^20 slots 26 us, 2^22 78 (one cluster, bound by
-// its SMs' instructions and scattered stores: 95 and 342; at 131072 both take 12.3).
+// its SMs' instructions and scattered stores: 95 and 342; at 131072 three launches take
+// 12.3).  Each by itself, of 2^20 and 2^22 slots: counts 8 and 23 us, places 18 and 47,
+// slot_of 7 and 20: the walks issue a vote per bit of the expert for 32 slots, one CTA
+// to an SM, and slot_of is 4-byte stores a row apart, so that the floors of their bytes
+// (2 and 7 us) are out of reach in this form.
 constexpr int SORT_T = 1024;
 constexpr int SORT_WARPS = SORT_T / 32;
 constexpr int SORT_CLUSTER = 16;
@@ -440,8 +444,9 @@ __global__ void __launch_bounds__(RT) dispatch_kernel(const __grid_constant__ Ro
 // by warps: 8192 tokens, 8 rows of 2048 bf16 each onto a residual (336 MB): 60-63 us
 // at eight CTAs per SM, 69 at six, 71 at three with twice the loads in flight per warp
 // (such calls go by rings now, see below; few tokens, short rows and many choices here).
+// Eight CTAs leave 32 registers: 12 to 36 bytes per thread are spilled there.
 template <int ES, bool VEC>
-__global__ void __launch_bounds__(RT, VEC ? 8 : ES == 4 ? 7 : 5) combine_kernel(const __grid_constant__ RowArgs a) {
+__global__ void __launch_bounds__(RT, VEC || ES == 4 ? 8 : 5) combine_kernel(const __grid_constant__ RowArgs a) {
     constexpr int V = VEC ? 16 / ES : 4 / ES, U = VEC ? 1 : 4;      // elements of a slot, slots of a lane
     pdl_wait();
     pdl_trigger();
